@@ -15,18 +15,20 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
 __all__ = ["AttnError", "lib", "lib_path", "fwd", "fwd_split", "fwd_kv", "merge", "bwd", "fwd_varlen",
-           "bwd_varlen", "bwd_workspace_bytes", "quantize_fp8", "fwd_fp8", "poll_status", "set_wait_limit_us",
+           "bwd_varlen", "bwd_workspace_bytes", "rope_table", "rope", "rope_bwd", "append_kv", "fwd_paged",
+           "fwd_paged_workspace_bytes", "quantize_fp8", "fwd_fp8", "poll_status", "set_wait_limit_us",
            "selftest_wait_timeout", "num_sms", "STATUS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED",
           3: "ATTN_ERR_CUDA", 4: "ATTN_ERR_TIMEOUT"}
 _F16, _BF16 = 0, 1
+_MAX_AXES = 8  # position axes of a rotary table
 _lib = None
 
 
@@ -64,6 +66,10 @@ def lib() -> ctypes.CDLL:
         "attn_bwd_varlen": ([vp] * 10 + [sz, vp, i, i, i, i, i, i, i, f, i, vp], i),
         "attn_bwd_workspace_bytes": ([i, i, i, i], sz),
         "attn_bwd": ([vp] * 10 + [sz, i, i, i, i, i, f, i, vp], i),
+        "attn_rope": ([vp] * 6 + [i, i, vp] + [i] * 9 + [vp], i),
+        "attn_append_kv": ([vp] * 11 + [i, vp] + [i] * 11 + [vp], i),
+        "attn_fwd_paged_workspace_bytes": ([i, i, i, i], sz),
+        "attn_fwd_paged": ([vp] * 9 + [sz] + [i] * 10 + [f, i, vp], i),
         "attn_quantize_fp8": ([vp, vp, vp, i, i, i, i, i, vp, i, vp], i),
         "attn_fwd_fp8": ([vp] * 8 + [i, i, i, i, i, f, vp], i),
         "attn_poll_device_status": ([vp, u32p], i),
@@ -428,6 +434,268 @@ def bwd_varlen(q, k, v, o, do, lse, cu_seqlens: torch.Tensor, max_seqlen: int,
                                    _dtype_code(q), _stream(q))
     _check(st, "attn_bwd_varlen")
     return dq, dk, dv
+
+
+def rope_table(rot: int, theta: float = 10000.0, axes: Optional[Sequence[int]] = None,
+               inv_freq: Optional[Sequence[float]] = None, device="cuda") -> torch.Tensor:
+    """Table of rotary positions for ``rot`` turning channels (a multiple of
+    16): int64 [2, rot/2], made once per model.  Row 0: the angle of each
+    channel pair per position, in units of 2^-64 turns; row 1: the position
+    axis of the pair.  inv_freq (radians per position; default
+    theta^(-2p/rot)) and axes (default all 0) have one entry per pair."""
+    if rot < 16 or rot % 16 != 0:
+        raise ValueError("rot must be a positive multiple of 16")
+    half = rot // 2
+    freq = [theta ** (-2.0 * p / rot) for p in range(half)] if inv_freq is None \
+        else [float(x) for x in inv_freq]
+    axis = [0] * half if axes is None else [int(a) for a in axes]
+    if len(freq) != half or len(axis) != half:
+        raise ValueError("inv_freq and axes must have one entry per channel pair (rot/2)")
+    if not all(math.isfinite(x) for x in freq) or min(axis) < 0 or max(axis) >= _MAX_AXES:
+        raise ValueError(f"inv_freq must be finite and axes lie in [0, {_MAX_AXES})")
+    step = [round(x / (2.0 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for x in freq]
+    step = [x - 2 ** 64 if x >= 2 ** 63 else x for x in step]
+    return torch.tensor([step, axis], dtype=torch.int64).to(device)
+
+
+def _strides(t: torch.Tensor, dims: Sequence[int], what: str, written: bool = False):
+    """Element strides of the given dims (0 where the size is 1) of a tensor
+    whose rows are read or written 16 bytes at a time."""
+    got = [t.stride(i) if t.shape[i] > 1 else 0 for i in dims]
+    if t.stride(-1) != 1 or any(x % 8 for x in got):
+        raise ValueError(f"{what}: the last dimension must be contiguous and the other strides "
+                         "multiples of 8 elements")
+    if written and any(x == 0 for x, i in zip(got, dims) if t.shape[i] > 1):
+        raise ValueError(f"{what} must not be an expanded tensor")
+    return got
+
+
+def _check_table(table: torch.Tensor, d: int, device) -> int:
+    if (table.dtype != torch.int64 or table.dim() != 2 or table.shape[0] != 2
+            or not table.is_contiguous() or table.device != device):
+        raise ValueError("table must be a contiguous int64 [2, rot/2] tensor (rope_table) on the "
+                         "tensors' device")
+    rot = 2 * int(table.shape[1])
+    if rot < 16 or rot % 16 != 0 or rot > d:
+        raise ValueError("the table must turn a multiple of 16 channels, at most the head dim")
+    return rot
+
+
+def _rope(q, k, positions, table, interleaved, out_q, out_k, inverse):
+    what = "rope_bwd" if inverse else "rope"
+    packed = q.dim() == 3  # [H, total, d]: one batch
+    if q.dim() not in (3, 4):
+        raise ValueError("tensors must be [B, H, N, d] or packed [H, total, d]")
+    if not q.is_cuda:
+        raise ValueError("all tensors must be on the same CUDA device")
+    B = 1 if packed else int(q.shape[0])
+    H, N, d = (int(x) for x in q.shape[-3:])
+    if min(B, H, N) < 1:
+        raise ValueError("tensors must not be empty")
+    code = _dtype_code(q)
+    rot = _check_table(table, d, q.device)
+    if positions.dtype != torch.int32 or positions.device != q.device \
+            or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 tensor on the tensors' device")
+    if positions.dim() == 2:
+        n_axes, pos_batches = int(positions.shape[0]), 1
+    elif positions.dim() == 3:
+        n_axes, pos_batches = int(positions.shape[0]), int(positions.shape[1])
+    else:
+        raise ValueError("positions must be [axes, N] or [axes, B, N]")
+    if positions.shape[-1] != N or pos_batches not in (1, B) or not 1 <= n_axes <= _MAX_AXES:
+        raise ValueError(f"positions must be [axes, N] or [axes, B, N], at most {_MAX_AXES} axes")
+    dims = (0, 1) if packed else (0, 1, 2)
+    strides, outs = [], []
+    for x, out in ((q, out_q), (k, out_k)):
+        if x is None:
+            if out is not None:
+                raise ValueError("out_k without k")
+            outs.append(None)
+            continue
+        if x.dim() != q.dim() or x.dtype != q.dtype or x.device != q.device \
+                or x.shape[-2:] != q.shape[-2:] or (not packed and x.shape[0] != B) \
+                or x.shape[-3] < 1:
+            raise ValueError("q and k must share batch, length, head dim, dtype and device")
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+            raise ValueError("out_q, out_k must have the shape, dtype and device of q, k")
+        for t, written in ((x, False), (out, True)):
+            st = _strides(t, dims, "q, k" if t is x else "out_q, out_k", written)
+            strides += [0] + st if packed else st
+        outs.append(out)
+    arr = (ctypes.c_int64 * len(strides))(*strides)
+    with torch.cuda.device(q.device):
+        st = lib().attn_rope(_ptr(q), _ptr(k), _ptr(outs[0]), _ptr(outs[1]), arr,
+                             _ptr(positions), pos_batches, n_axes, _ptr(table), rot,
+                             int(bool(interleaved)), inverse, B, H,
+                             0 if k is None else int(k.shape[-3]), N, d, code, _stream(q))
+    _check(st, "attn_" + what)
+    return outs[0], outs[1]
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, table: torch.Tensor,
+         interleaved: bool = False, out_q: Optional[torch.Tensor] = None,
+         out_k: Optional[torch.Tensor] = None):
+    """Turns q and k (k may be None) by their positions: channel pair p of a
+    row by the angle positions[axis_p] f_p of ``table`` (see rope_table); the
+    pairs are (p, p + rot/2), or (2p, 2p + 1) if interleaved; channels past rot
+    pass through.  q [B,H,N,d], k [B,Hkv,N,d] (or packed [H,total,d]) may be
+    strided views with contiguous rows (a slice of a fused projection); new
+    outputs are contiguous, and out_q / out_k may be q / k themselves.
+    positions: int32 [axes, N] or [axes, B, N].  Returns (q', k')."""
+    return _rope(q, k, positions, table, interleaved, out_q, out_k, 0)
+
+
+def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor,
+             table: torch.Tensor, interleaved: bool = False,
+             out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None):
+    """Backward pass of rope: gradients with respect to q', k' in, with respect
+    to q, k out (the opposite turn); arguments as in rope."""
+    return _rope(dq, dk, positions, table, interleaved, out_q, out_k, 1)
+
+
+def _check_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens):
+    """Shapes of a paged cache [n_pages, Hkv, page, d] and its batch; q is a
+    packed [H, total, d] tensor of new tokens.  Returns n_seq, max_pages."""
+    if q.dim() != 3:
+        raise ValueError("packed tensors must be [H, total, d]")
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != q.shape[2]:
+        raise ValueError("k_pages, v_pages must be [n_pages, Hkv, page, d] with the tokens' d")
+    for t in (q, k_pages, v_pages):
+        if not t.is_cuda or t.device != q.device or t.dtype != q.dtype:
+            raise ValueError("tokens and pages must be CUDA tensors of one dtype on one device")
+    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("k_pages, v_pages must be contiguous")
+    n_seq = kv_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != n_seq or cu_seqlens.dim() != 1 \
+            or cu_seqlens.numel() != n_seq + 1 or kv_lens.dim() != 1 or n_seq < 1:
+        raise ValueError("block_table must be [n_seq, max_pages], cu_seqlens [n_seq + 1], "
+                         "kv_lens [n_seq]")
+    for t in (block_table, cu_seqlens, kv_lens):
+        if t.dtype != torch.int32 or t.device != q.device or not t.is_contiguous():
+            raise ValueError("block_table, cu_seqlens and kv_lens must be contiguous int32 "
+                             "tensors on the tokens' device")
+    return n_seq, int(block_table.shape[1])
+
+
+def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              block_table: torch.Tensor, cu_seqlens: torch.Tensor, kv_lens: torch.Tensor,
+              table: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              interleaved: bool = False, q: Optional[torch.Tensor] = None,
+              out_q: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Appends new keys and values to a paged cache, turning the keys (and the
+    new tokens' queries, if given) on the way.
+
+    k, v [Hkv,total,d] and q [Hq,total,d] are packed new tokens (strided views
+    with contiguous rows allowed): sequence b owns rows
+    cu_seqlens[b]..cu_seqlens[b+1], which become the last of its kv_lens[b]
+    cached positions (kv_lens counts them).  Position p of sequence b lies in
+    row p % page of page block_table[b, p // page] of k_pages, v_pages
+    [n_pages,Hkv,page,d].  table: see rope_table (None: no turn); positions:
+    int32 [axes, total] (None: the position in the cache on every axis).
+    Returns the turned queries (None without q); rows behind the last sequence
+    are left as they were."""
+    n_seq, max_pages = _check_paged(k, k_pages, v_pages, block_table, cu_seqlens, kv_lens)
+    Hkv, total, d = (int(x) for x in k.shape)
+    if k.shape[0] != k_pages.shape[1] or v.shape != k.shape or v.dtype != k.dtype \
+            or v.device != k.device:
+        raise ValueError("k and v must be [Hkv, total, d] with the cache's heads")
+    rot, n_axes = 0, 1
+    if table is not None:
+        rot = _check_table(table, d, k.device)
+    if positions is not None:
+        if table is None:
+            raise ValueError("positions without a table")
+        if positions.dtype != torch.int32 or positions.device != k.device \
+                or positions.dim() != 2 or positions.shape[1] != total \
+                or not 1 <= positions.shape[0] <= _MAX_AXES or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 [axes, total] tensor, at most "
+                             f"{_MAX_AXES} axes")
+        n_axes = int(positions.shape[0])
+    strides = _strides(k, (0, 1), "k") + _strides(v, (0, 1), "v")
+    Hq = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[1:] != k.shape[1:] or q.dtype != k.dtype \
+                or q.device != k.device or q.shape[0] < 1 or q.shape[0] % Hkv != 0:
+            raise ValueError("q must be [Hq, total, d] with k's total, d, dtype and device, "
+                             "Hq a multiple of Hkv")
+        Hq = int(q.shape[0])
+        strides += _strides(q, (0, 1), "q")
+        if out_q is None:
+            out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out_q.shape != q.shape or out_q.dtype != q.dtype or out_q.device != q.device \
+                or not out_q.is_contiguous():
+            raise ValueError("out_q must be contiguous with q's shape, dtype and device")
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    arr = (ctypes.c_int64 * len(strides))(*strides)
+    with torch.cuda.device(k.device):
+        st = lib().attn_append_kv(_ptr(k), _ptr(v), _ptr(q), _ptr(out_q), arr, _ptr(k_pages),
+                                  _ptr(v_pages), _ptr(block_table), _ptr(cu_seqlens),
+                                  _ptr(kv_lens), _ptr(positions), n_axes, _ptr(table), rot,
+                                  int(bool(interleaved)), n_seq, total, int(k_pages.shape[0]),
+                                  int(k_pages.shape[2]), max_pages, Hq, Hkv, d, _dtype_code(k),
+                                  _stream(k))
+    _check(st, "attn_append_kv")
+    return out_q
+
+
+def fwd_paged_workspace_bytes(max_q: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().attn_fwd_paged_workspace_bytes(max_q, Hq, Hkv, d))
+
+
+def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              block_table: torch.Tensor, cu_seqlens: torch.Tensor, kv_lens: torch.Tensor,
+              max_q: int, causal: bool = False, scale: Optional[float] = None,
+              out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """O [Hq,total,d], LSE [Hq,total] of new tokens against a paged key/value
+    cache (d in {64, 96, 128}): one token per sequence (decoding), chunks of a
+    prompt, or both together.  q [Hq,total,d] packed, sequence b owning rows
+    cu_seqlens[b]..cu_seqlens[b+1], at most max_q of them; its keys are the
+    kv_lens[b] positions of its pages (layouts as in append_kv; Hkv divides
+    Hq).  causal: the rows are the last positions, row i of n sees keys
+    j <= i + kv_lens[b] - n.  A row that sees no key gets O = 0, LSE = -inf;
+    rows behind the last sequence are left as they were.  workspace: uint8,
+    fwd_paged_workspace_bytes long; calls that may overlap need their own."""
+    n_seq, max_pages = _check_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens)
+    H, total, d = (int(x) for x in q.shape)
+    Hkv = int(k_pages.shape[1])
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous [Hq, total, d]")
+    if Hkv < 1 or H % Hkv != 0:
+        raise ValueError("the number of key/value heads must divide the query heads")
+    if not 1 <= int(max_q) <= total:
+        raise ValueError("max_q must lie in [1, total]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
+            or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
+    if lse is None:
+        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
+    elif tuple(lse.shape) != (H, total) or lse.dtype != torch.float32 \
+            or lse.device != q.device or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [Hq, total] tensor on q's device")
+    if workspace is None:
+        workspace = torch.empty(max(fwd_paged_workspace_bytes(int(max_q), H, Hkv, d), 256),
+                                dtype=torch.uint8, device=q.device)
+    elif workspace.dtype != torch.uint8 or workspace.device != q.device \
+            or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
+    with torch.cuda.device(q.device):
+        st = lib().attn_fwd_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse),
+                                  _ptr(block_table), _ptr(cu_seqlens), _ptr(kv_lens),
+                                  _ptr(workspace), workspace.numel(), n_seq, int(max_q), total,
+                                  int(k_pages.shape[0]), int(k_pages.shape[2]), max_pages, H,
+                                  Hkv, d, int(bool(causal)), float(scale), _dtype_code(q),
+                                  _stream(q))
+    _check(st, "attn_fwd_paged")
+    return out, lse
 
 
 def num_sms() -> int:

@@ -16,6 +16,8 @@
 #include "fp8.cuh"
 #include "fwd.cuh"
 #include "merge.cuh"
+#include "paged.cuh"
+#include "rotary.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {
@@ -406,6 +408,216 @@ size_t attn_bwd_workspace_bytes(int B, int H, int N, int d) {
   if (!shape_ok(B, H, N, d)) return 0;
   // D = rowsum(dO o O), fp32, then 256 bytes for the main kernels' work counters
   return bwd_delta_bytes(B, H, N) + 256;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool dtype_ok(attn_dtype t) { return t == ATTN_F16 || t == ATTN_BF16; }
+
+bool aligned(const void* p, uintptr_t n) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+// A rotary table of rot turning channels, positions on n_axes axes.
+bool rotary_ok(const int64_t* table, int rot, int n_axes, int d) {
+  return aligned(table, 8) && rot >= 16 && rot <= d && rot % 16 == 0 && n_axes >= 1 &&
+         n_axes <= kMaxAxes;
+}
+
+// Strides of a tensor read or written 16 bytes at a time.
+bool strides_ok(const int64_t* s, int n) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] < 0 || (s[i] & 7) != 0) return false;
+  return true;
+}
+
+// The cache and batch description the paged entry points share.
+attn_status paged_args(const void* k_pages, const void* v_pages, const int32_t* block_table,
+                       const int32_t* cu_seqlens, const int32_t* kv_lens, int n_seq, int total,
+                       int n_pages, int page, int max_pages, int Hq, int Hkv) {
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned(block_table, 4) ||
+      !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (n_seq < 1 || total < 1 || n_pages < 1 || max_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256)
+    return ATTN_ERR_UNSUPPORTED;
+  if ((int64_t)max_pages * page > 0x7FFFFF00 || (int64_t)n_pages * Hkv > 0x7FFFFFFF ||
+      (int64_t)n_seq * Hkv > 0x7FFFFFFF || (int64_t)Hq * total > 0x7FFFFFFF)
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
+                      const int64_t* strides, const int32_t* positions, int pos_batches,
+                      int n_axes, const int64_t* table, int rot, int interleaved, int inverse,
+                      int B, int Hq, int Hkv, int N, int d, attn_dtype dtype, void* stream) {
+  if (!aligned16(q) || !aligned16(q_out) || strides == nullptr || !aligned(positions, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if ((k == nullptr) != (k_out == nullptr) || (k == nullptr) != (Hkv == 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (k != nullptr && (!aligned16(k) || !aligned16(k_out))) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 0 || N < 1 || !dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
+  if ((interleaved | inverse) & ~1) return ATTN_ERR_INVALID_ARG;
+  if (!head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
+  if (!rotary_ok(table, rot, n_axes, d)) return ATTN_ERR_INVALID_ARG;
+  if (pos_batches != 1 && pos_batches != B) return ATTN_ERR_INVALID_ARG;
+  if (!strides_ok(strides, k != nullptr ? 12 : 6)) return ATTN_ERR_INVALID_ARG;
+  if (B > 65535 || (int64_t)Hq + Hkv > 65535 || N > (1 << 28)) return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  attn_status st = device_info(&di);
+  if (st != ATTN_OK) return st;
+  RopeLaunch a;
+  RopeParams& p = a.params;
+  const int64_t* s = strides;
+  p.x[0] = {const_cast<void*>(q), s[0], s[1], s[2]};
+  p.y[0] = {q_out, s[3], s[4], s[5]};
+  if (k != nullptr) {
+    p.x[1] = {const_cast<void*>(k), s[6], s[7], s[8]};
+    p.y[1] = {k_out, s[9], s[10], s[11]};
+  }
+  p.positions = positions;
+  p.table = table;
+  p.n_axes = n_axes;
+  p.pos_batches = pos_batches;
+  p.heads[0] = Hq;
+  p.heads[1] = Hkv;
+  p.N = N;
+  p.d = d;
+  p.rot = rot;
+  p.inverse = inverse != 0;
+  a.B = B;
+  a.bf16 = dtype == ATTN_BF16;
+  a.interleaved = interleaved != 0;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(launch_rope(a, di->num_sms));
+}
+
+attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_out,
+                           const int64_t* strides, void* k_pages, void* v_pages,
+                           const int32_t* block_table, const int32_t* cu_seqlens,
+                           const int32_t* kv_lens, const int32_t* positions, int n_axes,
+                           const int64_t* table, int rot, int interleaved, int n_seq, int total,
+                           int n_pages, int page, int max_pages, int Hq, int Hkv, int d,
+                           attn_dtype dtype, void* stream) {
+  if (!aligned16(k) || !aligned16(v) || strides == nullptr) return ATTN_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (q == nullptr) != (Hq == 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (q != nullptr && (!aligned16(q) || !aligned16(q_out))) return ATTN_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || (interleaved & ~1)) return ATTN_ERR_INVALID_ARG;
+  if (!head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
+  if (table != nullptr && !rotary_ok(table, rot, n_axes, d)) return ATTN_ERR_INVALID_ARG;
+  if (positions != nullptr && (table == nullptr || !aligned(positions, 4)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!strides_ok(strides, q != nullptr ? 6 : 4)) return ATTN_ERR_INVALID_ARG;
+  attn_status st = paged_args(k_pages, v_pages, block_table, cu_seqlens, kv_lens, n_seq, total,
+                              n_pages, page, max_pages, q != nullptr ? Hq : Hkv, Hkv);
+  if (st != ATTN_OK) return st;
+  if (2 * (int64_t)Hkv + Hq > 65535 || total > (1 << 28)) return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != ATTN_OK) return st;
+  AppendLaunch a;
+  AppendParams& p = a.params;
+  p.src[0] = k;
+  p.src[1] = v;
+  p.src[2] = q;
+  for (int i = 0; i < (q != nullptr ? 3 : 2); ++i) {
+    p.sh[i] = strides[2 * i];
+    p.sn[i] = strides[2 * i + 1];
+  }
+  p.q_out = q_out;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.block_table = block_table;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.positions = positions;
+  p.table = table;
+  p.status = di->status;
+  p.n_axes = n_axes;
+  p.n_seq = n_seq;
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.page = page;
+  p.total = total;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.rot = table != nullptr ? rot : 0;
+  a.bf16 = dtype == ATTN_BF16;
+  a.interleaved = interleaved != 0;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(launch_append(a, di->num_sms));
+}
+
+size_t attn_fwd_paged_workspace_bytes(int max_q, int Hq, int Hkv, int d) {
+  if (max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
+  if (d != 64 && d != 96 && d != 128) return 0;
+  return paged_workspace_bytes(d);
+}
+
+attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o,
+                           float* lse, const int32_t* block_table, const int32_t* cu_seqlens,
+                           const int32_t* kv_lens, void* workspace, size_t workspace_bytes,
+                           int n_seq, int max_q, int total, int n_pages, int page, int max_pages,
+                           int Hq, int Hkv, int d, int causal, float scale, attn_dtype dtype,
+                           void* stream) {
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  attn_status st = paged_args(k_pages, v_pages, block_table, cu_seqlens, kv_lens, n_seq, total,
+                              n_pages, page, max_pages, Hq, Hkv);
+  if (st != ATTN_OK) return st;
+  if (max_q < 1 || max_q > total) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 96 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (Hq / Hkv > kPagedMaxGroup) return ATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < attn_fwd_paged_workspace_bytes(max_q, Hq, Hkv, d))
+    return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != ATTN_OK) return st;
+  const CUtensorMapDataType dt =
+      dtype == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  PagedLaunch a;
+  PagedParams& p = a.params;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.status = di->status;
+  p.block_table = block_table;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.n_seq = n_seq;
+  p.total = total;
+  p.max_q = max_q;
+  p.n_pages = n_pages;
+  p.page = page;
+  p.page_log2 = 0;
+  while ((1 << p.page_log2) < page) ++p.page_log2;
+  p.max_pages = max_pages;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.causal = causal;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  paged_carve(&p, workspace, d);
+  a.num_sms = di->num_sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const int64_t heads = (int64_t)n_pages * Hkv;
+  if (!encode_3d(&a.tmK, k_pages, dt, 2, d, page, heads, 64, kPagedBlock) ||
+      !encode_3d(&a.tmV, v_pages, dt, 2, d, page, heads, 64, kPagedBlock))
+    return ATTN_ERR_CUDA;
+  p.min_share = 2;
+  return launch_result(launch_paged_decode(a, d, dtype == ATTN_BF16));
 }
 
 }  // extern "C"

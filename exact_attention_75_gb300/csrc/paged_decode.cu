@@ -1,0 +1,481 @@
+// Attention of a few new tokens per sequence over a paged key/value cache,
+// and the join of partial results.
+//
+// The mathematics is the decoding kernel's (online softmax over 16-key
+// blocks on the warp-level product, 16 query rows: the group's query heads x
+// the new tokens); what differs is where the keys lie.  A block of 16 keys
+// never crosses a page (pages hold a power of two of at least 16 rows), so
+// each TMA box takes one table entry.  A page number outside the cache, or a
+// box row past the cache, reads zeros.
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "mma16.cuh"
+#include "paged.cuh"
+#include "sm103_ptx.cuh"
+#include "smem_attr.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = kPagedBlock;
+constexpr int kBoxBytes = kKeys * 128;   // one 64-column chunk of a block's K or V
+
+template <int D>
+struct PagedDecodeLayout {
+  static constexpr int kChunks = (D + 63) / 64;
+  static constexpr int kSlotBytes = 2 * kChunks * kBoxBytes;  // K chunks, then V chunks
+  static constexpr int kSlots = D == 64 ? 6 : 3;              // ring depth of each warp
+  static constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
+  // After an item's keys the ring holds each warp's O (16 rows, padded), m and l.
+  static constexpr int kRowStride = D + 4;
+  static constexpr int kRedBytes = kWarps * 16 * (kRowStride + 2) * 4;
+  static_assert(kRingBytes >= kRedBytes && kRingBytes % 1024 == 0, "ring layout");
+  static constexpr int kBarOff = kRingBytes;  // one mbarrier per slot
+  static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;
+  static constexpr int kBytes = kFlagOff + 16 + 1024;  // + room to align the base
+  static_assert(kBytes <= 113 * 1024, "two CTAs per SM");
+};
+
+// Byte offset of 16-byte piece `piece` of row `row` in a staged block.
+__device__ __forceinline__ uint32_t sw_off(int row, int piece) {
+  return (uint32_t)((piece >> 3) * kBoxBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
+
+// An item's cost: its key units and one for its prologue and epilogue.
+__device__ __forceinline__ int key_units(const PagedSeq& s) {
+  return (s.klen + kPagedUnitKeys - 1) / kPagedUnitKeys;
+}
+__device__ __forceinline__ int row_groups(const PagedSeq& s, int G) {
+  return (s.qlen * G + kPagedRows - 1) / kPagedRows;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+  using L = PagedDecodeLayout<D>;
+  constexpr int KS = D / 16;      // k-steps of S = Q K^T
+  constexpr int NT = kKeys / 8;   // 8-key column tiles of S
+  constexpr int DN = D / 8;       // 8-column tiles of O
+  constexpr int NS = L::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlagOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int s) { return sbase + L::kBarOff + 8u * (uint32_t)(warp * NS + s); };
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kWarps * NS; ++i) mbar_init(sbase + L::kBarOff + 8u * i, 1);
+    mbar_fence_init();
+    p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  const PagedStart st = paged_partition<kThreads>(p, [&](const PagedSeq& s) {
+    return (long long)row_groups(s, p.G) * (key_units(s) + 1);
+  });
+  Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
+
+  long long left = st.left;
+  int b = st.b;
+  PagedSeq sq = paged_seq(p, b);
+  int nku = key_units(sq), ngr = row_groups(sq, p.G);
+  int head = 0, rg = 0, u0 = 0;
+  if (left > 0) {
+    const long long per_head = (long long)ngr * (nku + 1);
+    head = (int)(st.off / per_head);
+    const long long rem = st.off % per_head;
+    rg = (int)(rem / (nku + 1));
+    u0 = (int)(rem % (nku + 1));
+  }
+  uint32_t it = 0;  // blocks this warp has taken from its ring
+  const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
+
+  while (left > 0) {
+    const int take = (int)min((long long)(nku + 1 - u0), left);
+    const int u1 = min(u0 + take, nku);  // this share's key units [u0, u1)
+    left -= take;
+    if (u1 > u0 || nku == 0) {
+      const int k_lo = u0 * kPagedUnitKeys;
+      const int k_hi = min(u1 * kPagedUnitKeys, sq.klen);
+      const int nb = (k_hi - k_lo + kKeys - 1) / kKeys;
+      const int nbw = nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;  // this warp's blocks
+      const int R = sq.qlen * p.G;
+      const int row0 = rg * kPagedRows;
+      const int rows = min(kPagedRows, R - row0);
+      const int* pages = p.block_table + (size_t)b * p.max_pages;
+
+      // Block j of this warp in this item -> ring slot (it + j) % NS (lane 0 only).
+      auto issue = [&](int j) {
+        const int s = (int)((it + (uint32_t)j) % NS);
+        const uint32_t dk = ring + (uint32_t)(s * L::kSlotBytes);
+        const uint32_t dv = dk + L::kChunks * kBoxBytes;
+        const int key0 = k_lo + (warp + j * kWarps) * kKeys;
+        const int page = __ldg(pages + (key0 >> p.page_log2));
+        const bool ok = page >= 0 && page < p.n_pages;
+        if (!ok)
+          atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(b, 0xFFFF) << 16));
+        const int z = ok ? page * p.Hkv + head : -1;  // -1: the box reads zeros
+        const int y = key0 & (p.page - 1);
+        mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
+#pragma unroll
+        for (int c = 0; c < L::kChunks; ++c) {
+          tma_load_3d(dk + c * kBoxBytes, &tmK, bar(s), c * 64, y, z);
+          tma_load_3d(dv + c * kBoxBytes, &tmV, bar(s), c * 64, y, z);
+        }
+      };
+      int issued = min(nbw, NS);
+      if (lane == 0)
+        for (int j = 0; j < issued; ++j) issue(j);
+
+      // Row r of the item: new token (row0 + r) / G, query head (row0 + r) % G
+      // of the group.
+      auto grow = [&](int r) -> size_t {
+        const int i = (row0 + r) / p.G, h = (row0 + r) - i * p.G;
+        return (size_t)(head * p.G + h) * p.total + sq.s0 + i;
+      };
+      const int r0 = lane >> 2, cq = 2 * (lane & 3);
+      const uint16_t* qa_ = static_cast<const uint16_t*>(p.q) + (r0 < rows ? grow(r0) * D : 0);
+      const uint16_t* qb_ =
+          static_cast<const uint16_t*>(p.q) + (r0 + 8 < rows ? grow(r0 + 8) * D : 0);
+      uint32_t qa[KS][4];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int c = 16 * ks + cq;
+        qa[ks][0] = r0 < rows ? *reinterpret_cast<const uint32_t*>(qa_ + c) : 0u;
+        qa[ks][1] = r0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(qb_ + c) : 0u;
+        qa[ks][2] = r0 < rows ? *reinterpret_cast<const uint32_t*>(qa_ + c + 8) : 0u;
+        qa[ks][3] = r0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(qb_ + c + 8) : 0u;
+      }
+      // Last key each of the thread's two rows sees (-1: a padding row, or
+      // one before the first key).
+      auto last_key = [&](int r) {
+        if (r >= rows) return -1;
+        const int lim = p.causal ? (row0 + r) / p.G + sq.klen - sq.qlen : sq.klen - 1;
+        return min(lim, k_hi - 1);
+      };
+      const int limA = last_key(r0), limB = last_key(r0 + 8);
+      const bool hiB = rows > 8;
+
+      float o[DN][4];
+#pragma unroll
+      for (int dn = 0; dn < DN; ++dn) o[dn][0] = o[dn][1] = o[dn][2] = o[dn][3] = 0.f;
+      float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+      int j = 0;
+      bool aborted = false;
+#pragma unroll 1
+      for (; j < nbw; ++j) {
+        const uint32_t n = it + (uint32_t)j;
+        const int s = (int)(n % NS);
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(s), (n / NS) & 1, wd, 65))) {
+          aborted = true;
+          break;
+        }
+        const uint32_t tk = ring + (uint32_t)(s * L::kSlotBytes);
+        const uint32_t tv = tk + L::kChunks * kBoxBytes;
+        const int key0 = k_lo + (warp + j * kWarps) * kKeys;
+        if (key0 + kKeys > sq.klen) {
+          // Rows past the sequence's last key hold whatever the page held
+          // (P is 0 there, but 0 x NaN is not): zero those rows of V.
+          const int dead = key0 + kKeys - sq.klen;
+          for (int i = lane; i < dead * 8 * L::kChunks; i += 32) {
+            const int row = kKeys - 1 - i / (8 * L::kChunks), pc = i % (8 * L::kChunks);
+            *reinterpret_cast<uint4*>(smem + (tv - sbase) + sw_off(row, pc)) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+        }
+
+        float sc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t bm[4];
+            ldsm_x4(tk + sw_off(8 * nt + (lane & 7), 2 * ks + (lane >> 3)), bm);
+            mma16816<BF16>(sc[nt], qa[ks], bm[0], bm[1]);
+            mma16816<BF16>(sc[nt], qa[ks + 1], bm[2], bm[3]);
+          }
+        }
+
+        // Online softmax.  sc[nt][e]: row r0 (e < 2) or r0 + 8, key key0 + 8 nt + cq + e % 2.
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + 8 * nt + cq + (e & 1);
+            const float x = sc[nt][e] * p.scale_log2;
+            sc[nt][e] = key <= (e < 2 ? limA : limB) ? x : -INFINITY;
+          }
+        float bA = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+        bA = fmaxf(bA, __shfl_xor_sync(0xffffffffu, bA, 1));
+        bA = fmaxf(bA, __shfl_xor_sync(0xffffffffu, bA, 2));
+        const float nA = fmaxf(mA, bA);
+        const float alphaA = nA == mA ? 1.f : ex2_approx(mA - nA);
+        const float uA = nA == -INFINITY ? 0.f : nA;
+        mA = nA;
+        float psA = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sc[nt][e] = ex2_approx(sc[nt][e] - uA);
+            psA += sc[nt][e];
+          }
+        lA = lA * alphaA + psA;
+        float alphaB = 1.f;
+        if (hiB) {
+          float bB = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+          bB = fmaxf(bB, __shfl_xor_sync(0xffffffffu, bB, 1));
+          bB = fmaxf(bB, __shfl_xor_sync(0xffffffffu, bB, 2));
+          const float nB = fmaxf(mB, bB);
+          alphaB = nB == mB ? 1.f : ex2_approx(mB - nB);
+          const float uB = nB == -INFINITY ? 0.f : nB;
+          mB = nB;
+          float psB = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 2; e < 4; ++e) {
+              sc[nt][e] = ex2_approx(sc[nt][e] - uB);
+              psB += sc[nt][e];
+            }
+          lB = lB * alphaB + psB;
+        }
+        if (__any_sync(0xffffffffu, alphaA != 1.f || alphaB != 1.f)) {
+#pragma unroll
+          for (int dn = 0; dn < DN; ++dn) {
+            o[dn][0] *= alphaA;
+            o[dn][1] *= alphaA;
+            o[dn][2] *= alphaB;
+            o[dn][3] *= alphaB;
+          }
+        }
+
+        // O += P V
+        uint32_t pa[4];
+        pa[0] = pack2<BF16>(sc[0][0], sc[0][1]);
+        pa[1] = hiB ? pack2<BF16>(sc[0][2], sc[0][3]) : 0u;
+        pa[2] = pack2<BF16>(sc[1][0], sc[1][1]);
+        pa[3] = hiB ? pack2<BF16>(sc[1][2], sc[1][3]) : 0u;
+        const int vrow = 8 * ((lane >> 3) & 1) + (lane & 7);
+#pragma unroll
+        for (int dn = 0; dn < DN; dn += 2) {
+          uint32_t bm[4];
+          ldsm_x4_trans(tv + sw_off(vrow, dn + (lane >> 4)), bm);
+          mma16816<BF16>(o[dn], pa, bm[0], bm[1]);
+          mma16816<BF16>(o[dn + 1], pa, bm[2], bm[3]);
+        }
+
+        // The slot is read: refill it with this warp's block j + NS.
+        __syncwarp();
+        if (issued < nbw) {
+          if (lane == 0) {
+            fence_proxy_async_smem();
+            issue(issued);
+          }
+          ++issued;
+        }
+      }
+      if (aborted) {
+        // Every copy this warp issued must land before the CTA may exit or
+        // reuse the ring.
+        Watchdog dw = wd;
+        volatile int never = 0;
+        dw.abort_flag = &never;
+        dw.limit_ns = drain_limit_ns(wd.limit_ns);
+        for (int jj = j; jj < issued; ++jj) {
+          const uint32_t n = it + (uint32_t)jj;
+          mbar_wait(bar((int)(n % NS)), (n / NS) & 1, dw, 66);
+        }
+      }
+      it += (uint32_t)nbw;
+
+      lA += __shfl_xor_sync(0xffffffffu, lA, 1);
+      lA += __shfl_xor_sync(0xffffffffu, lA, 2);
+      lB += __shfl_xor_sync(0xffffffffu, lB, 1);
+      lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+
+      // Combine the warps: each writes its (O, m, l) over the (now idle) ring.
+      __syncthreads();
+      if (*abort_flag != 0) break;  // the same for every thread: no wait runs until the next item
+      float* red = reinterpret_cast<float*>(smem);
+      float* rm = red + kWarps * 16 * L::kRowStride;  // [kWarps][16]
+      float* rl = rm + kWarps * 16;                   // [kWarps][16]
+      {
+        float* ro = red + warp * 16 * L::kRowStride;
+#pragma unroll
+        for (int dn = 0; dn < DN; ++dn) {
+          *reinterpret_cast<float2*>(ro + r0 * L::kRowStride + 8 * dn + cq) =
+              make_float2(o[dn][0], o[dn][1]);
+          *reinterpret_cast<float2*>(ro + (r0 + 8) * L::kRowStride + 8 * dn + cq) =
+              make_float2(o[dn][2], o[dn][3]);
+        }
+        if ((lane & 3) == 0) {
+          rm[warp * 16 + r0] = mA;
+          rm[warp * 16 + r0 + 8] = mB;
+          rl[warp * 16 + r0] = lA;
+          rl[warp * 16 + r0 + 8] = lB;
+        }
+      }
+      __syncthreads();
+
+      const bool whole = u0 == 0 && u1 == nku;
+      const size_t slot = 2 * (size_t)blockIdx.x + (u0 == 0 ? 1 : 0);
+      if (!whole && u0 == 0 && threadIdx.x == 0)
+        p.desc[blockIdx.x] =
+            make_int4(b, head, rg, 1 + (int)((nku - u1 + st.share - 1) / st.share));
+      for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
+        const int r = idx / (D / 4), c4 = idx % (D / 4);
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, rm[w * 16 + r]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lsum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = rm[w * 16 + r];
+          const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+          lsum += f * rl[w * 16 + r];
+          const float4 x =
+              *reinterpret_cast<const float4*>(red + (w * 16 + r) * L::kRowStride + 4 * c4);
+          acc.x += f * x.x;
+          acc.y += f * x.y;
+          acc.z += f * x.z;
+          acc.w += f * x.w;
+        }
+        if (whole) {
+          const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+          const size_t gr = grow(r);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + 4 * c4) =
+              make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv),
+                         pack2<BF16>(acc.z * inv, acc.w * inv));
+          if (c4 == 0)
+            p.lse[gr] = lsum > 0.f ? (M + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + slot * 16 * D + part_at(c4, r, 16)) = acc;
+          if (c4 == 0)
+            *reinterpret_cast<float2*>(p.part_ml + (slot * 16 + r) * 2) = make_float2(M, lsum);
+        }
+      }
+      fence_proxy_async_smem();  // the ring is refilled by TMA in the next item
+      __syncthreads();
+    }
+    // the next item
+    u0 = 0;
+    if (left > 0 && ++rg == ngr) {
+      rg = 0;
+      if (++head == p.Hkv) {
+        head = 0;
+        do {
+          sq = paged_seq(p, ++b);
+        } while (sq.qlen == 0 && b + 1 < p.n_seq);
+        nku = key_units(sq);
+        ngr = row_groups(sq, p.G);
+      }
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// Joins the parts of the items that crossed shares: CTA (c, y) takes the
+// item that the main kernel's CTA c began and others continued, a slice y of
+// its rows and columns.  Per row, over the parts in key order,
+//   M = max m_k,  l = sum l_k 2^(m_k - M),  O = sum O_k 2^(m_k - M) / l.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 item = p.desc[blockIdx.x];
+  const int parts = item.w;
+  if (parts == 0) return;
+  constexpr int rows = 16;
+  const PagedSeq sq = paged_seq(p, item.x);
+  const int R = min(sq.qlen * p.G - item.z * kPagedRows, kPagedRows);
+  for (int idx = blockIdx.y * 128 + threadIdx.x; idx < rows * (D / 4); idx += 128 * gridDim.y) {
+    const int r = idx % rows, c4 = idx / rows;
+    if (r >= R) continue;
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+      const size_t slot = 2 * ((size_t)blockIdx.x + k) + (k == 0 ? 1 : 0);
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * rows + r) * 2);
+      const float4 x =
+          *reinterpret_cast<const float4*>(p.part_o + slot * rows * D + part_at(c4, r, rows));
+      if (ml.x == -INFINITY) continue;  // a row that sees no key of this part
+      const float N = fmaxf(M, ml.x);
+      const float f = exp2f(ml.x - N), g = exp2f(M - N);
+      M = N;
+      l = l * g + ml.y * f;
+      acc.x = acc.x * g + x.x * f;
+      acc.y = acc.y * g + x.y * f;
+      acc.z = acc.z * g + x.z * f;
+      acc.w = acc.w * g + x.w * f;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int i = (item.z * kPagedRows + r) / p.G, h = item.z * kPagedRows + r - i * p.G;
+    const size_t gr = (size_t)(item.y * p.G + h) * p.total + sq.s0 + i;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + 4 * c4) = make_uint2(
+        pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+    if (c4 == 0) p.lse[gr] = l > 0.f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_db(const PagedLaunch& a) {
+  using L = PagedDecodeLayout<D>;
+  static DeviceFlags configured;
+  cudaError_t e = ensure_dyn_smem(paged_decode_kernel<D, BF16>, L::kBytes, configured);
+  if (e != cudaSuccess) return e;
+  const int grid = 2 * a.num_sms < kPagedMaxCtas ? 2 * a.num_sms : kPagedMaxCtas;
+  paged_decode_kernel<D, BF16><<<grid, kThreads, L::kBytes, a.stream>>>(a.tmK, a.tmV, a.params);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 2);
+  cfg.blockDim = dim3(128);
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, BF16>, a.params);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedLaunch& a, bool bf16) {
+  return bf16 ? launch_db<D, true>(a) : launch_db<D, false>(a);
+}
+
+constexpr size_t kDescBytes = kPagedMaxCtas * sizeof(int4);
+constexpr size_t kMlBytes = (size_t)kPagedMaxCtas * 2 * kPagedRows * 2 * sizeof(float);
+
+}  // namespace
+
+size_t paged_workspace_bytes(int d) {
+  return kDescBytes + kMlBytes + (size_t)kPagedMaxCtas * 2 * kPagedRows * d * sizeof(float);
+}
+
+void paged_carve(PagedParams* p, void* workspace, int d) {
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p->desc = reinterpret_cast<int4*>(w);
+  p->part_ml = reinterpret_cast<float*>(w + kDescBytes);
+  p->part_o = reinterpret_cast<float*>(w + kDescBytes + kMlBytes);
+}
+
+cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16) {
+  switch (d) {
+    case 64: return launch_d<64>(a, bf16);
+    case 96: return launch_d<96>(a, bf16);
+    default: return launch_d<128>(a, bf16);
+  }
+}
+
+}  // namespace attn

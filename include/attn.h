@@ -243,6 +243,114 @@ attn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const v
                             int causal, float scale, attn_dtype dtype, void* stream);
 
 /*
+ * Rotary positions with one or several axes, on the way into attention (the
+ * pages name the rotary pre-pass that a Hadamard rotation would be fused
+ * with; the formulas are the usual ones).  Channel pair p of a row at
+ * position (pos_0, .., pos_{n_axes-1}) turns by the angle a = pos[axis_p] f_p:
+ *   y_a = x_a cos a - x_b sin a,   y_b = x_b cos a + x_a sin a
+ * with (a, b) = (p, p + rot/2), or (2p, 2p + 1) if interleaved = 1; channels
+ * rot..d-1 pass through.  inverse = 1 turns the other way: the backward pass
+ * (gradients of the outputs in, of the inputs out).
+ *   q, q_out  : [B,Hq,N,d];  k, k_out : [B,Hkv,N,d], or both NULL with Hkv = 0.
+ *               fp16/bf16, rows contiguous; in place (the same pointer and
+ *               strides) or without overlap.
+ *   strides   : HOST array of 12 (without k: 6) element strides of the batch,
+ *               head and token dimensions of q, q_out, k, k_out, each a
+ *               non-negative multiple of 8.
+ *   positions : DEVICE int32 [n_axes, pos_batches, N]; pos_batches = B, or 1
+ *               for one set of positions shared by the batch.  Any value.
+ *   table     : DEVICE int64 [2, rot/2]: f_p in units of 2^-64 turns (radians
+ *               / 2 pi, modulo 1 turn), then axis_p (clamped to [0, n_axes)).
+ *   rot       : a multiple of 16, 16 <= rot <= d;  1 <= n_axes <= 8.
+ * d in {64, 96, 128, 192, 256}; B, Hq + Hkv <= 65535.  Angles are formed
+ * modulo a turn in 64-bit integers, so they hold at any position; values are
+ * turned in fp32 and rounded once.
+ * Cite: "8.3 FlashAttention-3", section 5.2 (the rotary embedding as the
+ * pass before attention).
+ */
+attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
+                      const int64_t* strides, const int32_t* positions, int pos_batches,
+                      int n_axes, const int64_t* table, int rot, int interleaved, int inverse,
+                      int B, int Hq, int Hkv, int N, int d, attn_dtype dtype, void* stream);
+
+/*
+ * A paged key/value cache, shared by attn_append_kv and attn_fwd_paged:
+ *   k_pages, v_pages : [n_pages, Hkv, page, d] fp16/bf16; page in {16, 32, 64,
+ *                 128, 256} rows (ATTN_ERR_UNSUPPORTED otherwise).
+ *   block_table : DEVICE int32 [n_seq, max_pages]: position p of sequence b
+ *                 lies in row p % page of page block_table[b, p / page].
+ *                 Entries past a sequence's length are not read.
+ *   cu_seqlens  : DEVICE int32 [n_seq + 1], cu_seqlens[0] = 0, non-decreasing,
+ *                 the last at most total: sequence b's new tokens are rows
+ *                 [cu_seqlens[b], cu_seqlens[b+1]) of the packed [H, total, d]
+ *                 tensors (none: the sequence is skipped).  Rows behind the
+ *                 last sequence (padding) are neither read nor written.
+ *   kv_lens     : DEVICE int32 [n_seq]: positions of sequence b in the cache,
+ *                 its new tokens, the last ones, included.
+ * These arrays are read on the device, so a captured graph replays with new
+ * lengths and pages.  A value out of range (a length, an offset, a page
+ * number) records ATTN_ERR_INVALID_ARG in the status word
+ * (attn_poll_device_status; the block field holds the sequence) and is
+ * clamped or skipped: wrong results, but no access outside the tensors.
+ *
+ * attn_append_kv writes new keys and values to their places in the cache:
+ *   k, v      : [Hkv, total, d] new tokens, read only;  q [Hq, total, d] and
+ *               q_out, or both NULL with Hq = 0.  Row i of n of sequence b goes
+ *               to position kv_lens[b] - n + i.
+ *   strides   : HOST array of 6 (without q: 4) element strides of the head and
+ *               token dimensions of k, v, q, each a non-negative multiple of 8.
+ *   q_out     : [Hq, total, d] contiguous, written; may be q.
+ *   table     : NULL (no rotation; positions NULL, rot ignored), or as in
+ *               attn_rope: keys and queries are turned on the way.
+ *   positions : DEVICE int32 [n_axes, total], or NULL: the position in the
+ *               cache on every axis.
+ * Two new tokens with one place in the cache (a page shared by two
+ * sequences) leave the bytes of either.  d in {64, 96, 128, 192, 256}.
+ * Cite: the FlashAttention-2 review, "Insights" and "Discussion Points"
+ * (paged key/value caches and decoding from them are named there).
+ */
+attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_out,
+                           const int64_t* strides, void* k_pages, void* v_pages,
+                           const int32_t* block_table, const int32_t* cu_seqlens,
+                           const int32_t* kv_lens, const int32_t* positions, int n_axes,
+                           const int64_t* table, int rot, int interleaved, int n_seq, int total,
+                           int n_pages, int page, int max_pages, int Hq, int Hkv, int d,
+                           attn_dtype dtype, void* stream);
+
+/*
+ * Bytes of device workspace attn_fwd_paged needs for at most max_q new tokens
+ * per sequence (partial results of tiles whose keys are shared out over
+ * several CTAs).  Returns 0 for sizes it does not take.
+ */
+size_t attn_fwd_paged_workspace_bytes(int max_q, int Hq, int Hkv, int d);
+
+/*
+ * Forward pass of new tokens against a paged cache (see attn_append_kv):
+ * single tokens (decoding), chunks of a prompt, or both in one batch.
+ *   q, o      : [Hq, total, d], packed by cu_seqlens;  lse : [Hq, total] fp32.
+ *               Query head h uses key/value head h / (Hq/Hkv); Hq/Hkv <= 128.
+ *   max_q     : at least the new tokens of any sequence, <= total.
+ *   causal = 1: row i of a sequence's n rows sees keys j <= i + kv_lens[b] - n
+ *               (the rows are the last positions); causal = 0: all kv_lens[b].
+ *               A row that sees no key gets O = 0, LSE = -inf.
+ *   workspace : >= attn_fwd_paged_workspace_bytes bytes, 256-byte aligned,
+ *               caller-owned; contents on entry are ignored.  Calls in flight
+ *               at once need one each; calls in stream order may share one.
+ * Cache rows that no row of the batch sees may hold anything (NaN included).
+ * A value row that is infinite or NaN may reach every row of its sequence.
+ * Partial results are joined in key order: equal calls give equal bits (the
+ * split depends on all lengths of the batch).  d in {64, 96, 128}.
+ * Cite: the FlashAttention-2 review, "Insights" and "Discussion Points"
+ * (paged key/value caches; a decoding kernel that splits the keys).
+ */
+attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o,
+                           float* lse, const int32_t* block_table, const int32_t* cu_seqlens,
+                           const int32_t* kv_lens, void* workspace, size_t workspace_bytes,
+                           int n_seq, int max_q, int total, int n_pages, int page, int max_pages,
+                           int Hq, int Hkv, int d, int causal, float scale, attn_dtype dtype,
+                           void* stream);
+
+/*
  * Backward pass that allocates nothing (no counterpart on the pages: it is a
  * library convenience, not part of the method).
  *

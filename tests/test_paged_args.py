@@ -1,0 +1,113 @@
+"""Argument checks of rotary positions and the paged cache: refused on the
+host before anything is launched (CPU)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_attention_75_gb300 as attn
+
+P, BAD = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10008)
+INVALID, UNSUPPORTED = 1, 2
+
+
+@pytest.fixture(scope="module")
+def L():
+    from exact_attention_75_gb300 import build
+    build.build()
+    return attn.lib()
+
+
+def _strides(n, value=64):
+    return (ctypes.c_int64 * n)(*[value] * n)
+
+
+ROPE = dict(q=P, k=P, oq=P, ok=P, strides=_strides(12), pos=P, pos_batches=1, axes=1, table=P,
+            rot=64, inter=0, inverse=0, B=2, Hq=4, Hkv=2, N=8, d=64, dtype=1, stream=None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(q=BAD), INVALID), (dict(oq=None), INVALID), (dict(k=None), INVALID),
+    (dict(ok=None), INVALID), (dict(k=None, ok=None), INVALID), (dict(Hkv=0), INVALID),
+    (dict(table=None), INVALID), (dict(pos=None), INVALID), (dict(pos_batches=3), INVALID),
+    (dict(rot=0), INVALID), (dict(rot=24), INVALID), (dict(rot=80), INVALID),
+    (dict(axes=0), INVALID), (dict(axes=9), INVALID), (dict(strides=_strides(12, 63)), INVALID),
+    (dict(strides=_strides(12, -64)), INVALID), (dict(strides=None), INVALID),
+    (dict(B=0), INVALID), (dict(N=0), INVALID), (dict(d=80), UNSUPPORTED),
+    (dict(dtype=2), INVALID), (dict(inter=2), INVALID), (dict(inverse=-1), INVALID),
+    (dict(B=70000, pos_batches=1), INVALID)])
+def test_rope_refusals(L, change, want):
+    assert L.attn_rope(*dict(ROPE, **change).values()) == want
+
+
+APPEND = dict(k=P, v=P, q=P, oq=P, strides=_strides(6), kp=P, vp=P, table=P, cu=P, kv=P, pos=None,
+              axes=1, rtable=P, rot=64, inter=0, n_seq=2, total=9, n_pages=8, page=16, max_pages=4,
+              Hq=4, Hkv=2, d=64, dtype=0, stream=None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(k=BAD), INVALID), (dict(v=None), INVALID), (dict(q=None), INVALID),
+    (dict(oq=None), INVALID), (dict(Hq=0), INVALID), (dict(Hq=3), INVALID),
+    (dict(kp=None), INVALID), (dict(vp=BAD), INVALID), (dict(cu=None), INVALID),
+    (dict(kv=None), INVALID), (dict(table=None), INVALID), (dict(page=48), UNSUPPORTED),
+    (dict(page=8), UNSUPPORTED), (dict(d=72), UNSUPPORTED), (dict(rot=128), INVALID),
+    (dict(rtable=None, pos=P), INVALID), (dict(n_seq=0), INVALID), (dict(total=0), INVALID),
+    (dict(n_pages=0), INVALID), (dict(max_pages=0), INVALID), (dict(Hkv=0), INVALID),
+    (dict(max_pages=1 << 28), INVALID), (dict(n_pages=1 << 30), INVALID),
+    (dict(strides=_strides(6, 12)), INVALID), (dict(inter=3), INVALID)])
+def test_append_refusals(L, change, want):
+    assert L.attn_append_kv(*dict(APPEND, **change).values()) == want
+
+
+PAGED = dict(q=P, kp=P, vp=P, o=P, lse=P, table=P, cu=P, kv=P, ws=P, ws_bytes=1 << 40, n_seq=2,
+             max_q=4, total=9, n_pages=8, page=16, max_pages=4, Hq=4, Hkv=2, d=64, causal=1,
+             scale=0.1, dtype=1, stream=None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(q=BAD), INVALID), (dict(o=None), INVALID), (dict(lse=None), INVALID),
+    (dict(kp=BAD), INVALID), (dict(ws=BAD), INVALID), (dict(ws=None), INVALID),
+    (dict(ws_bytes=256), INVALID), (dict(max_q=0), INVALID), (dict(max_q=10), INVALID),
+    (dict(Hq=5), INVALID), (dict(Hq=258), UNSUPPORTED), (dict(d=192), UNSUPPORTED),
+    (dict(d=80), UNSUPPORTED), (dict(page=512), UNSUPPORTED), (dict(causal=2), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID),
+    (dict(dtype=5), INVALID), (dict(n_seq=0), INVALID)])
+def test_paged_refusals(L, change, want):
+    assert L.attn_fwd_paged(*dict(PAGED, **change).values()) == want
+
+
+def test_workspace_sizes(L):
+    assert attn.fwd_paged_workspace_bytes(1, 16, 4, 128) > 0
+    for bad in ((0, 16, 4, 128), (1, 16, 5, 128), (1, 16, 4, 192), (1, 0, 1, 64)):
+        assert attn.fwd_paged_workspace_bytes(*bad) == 0
+
+
+def test_rope_table_is_the_angle_per_position():
+    t = attn.rope_table(32, theta=500.0, axes=[0] * 4 + [1] * 6 + [2] * 6, device="cpu")
+    assert t.shape == (2, 16) and t.dtype == torch.int64
+    want = 500.0 ** (-np.arange(16) / 16) / (2 * math.pi)
+    assert np.allclose(t[0].numpy() / 2.0 ** 64, want, rtol=1e-15)
+    assert t[1].tolist() == [0] * 4 + [1] * 6 + [2] * 6
+    # whole turns drop out, a negative frequency is the opposite turn
+    t = attn.rope_table(16, inv_freq=[2 * math.pi * x for x in (0.75, -0.25, 5.25, 0, 1, 2, 3, 4)],
+                        device="cpu")
+    assert np.allclose(t[0].numpy() / 2.0 ** 64, [-0.25, -0.25, 0.25, 0, 0, 0, 0, 0], atol=1e-15)
+    for kw in (dict(rot=24), dict(rot=0), dict(rot=32, axes=[0] * 15), dict(rot=16, axes=[8] * 8),
+               dict(rot=16, axes=[-1] * 8), dict(rot=16, inv_freq=[math.nan] * 8)):
+        with pytest.raises(ValueError):
+            attn.rope_table(device="cpu", **kw)
+
+
+def test_binding_refuses_cpu_tensors():
+    t = attn.rope_table(64, device="cpu")
+    q = torch.zeros(2, 5, 64, dtype=torch.bfloat16)
+    pages = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError):
+        attn.rope(q, q, i(1, 5), t)
+    with pytest.raises(ValueError):
+        attn.append_kv(q, q, pages, pages, i(1, 2), i(2), i(1))
+    with pytest.raises(ValueError):
+        attn.fwd_paged(q, pages, pages, i(1, 2), i(2), i(1), 1)

@@ -1,0 +1,295 @@
+"""Attention over a paged cache: CUDA path vs the fp64 oracle.
+
+Tolerances, from the arithmetic.  The probabilities are rounded to 16 bits
+before the product with V (half a step u each, at most u * A with A = sum_j
+P_ij |v_j|) and the output once more (u |O|).  In fp32: a score is a sum of d
+exact products (d 2^-24 of its size, carried into P by the exponential), the
+sums over n keys lose at most n 2^-24, and the exponential and the joins a few
+2^-22.  So |O - O_ref| <= (u + e) A + u |O| and |LSE - LSE_ref| <= e + 2^-23
+|LSE| with e = 2^-20 + n 2^-24 + d 2^-24 max |S|, u = finfo.eps / 2.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from helpers import to64
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def cuda_i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def make(lens, Hq, Hkv, d, page, dtype, seed=0, pad=0, amp=1.0):
+    """A batch with (new, keys) per sequence; every cache row outside the
+    sequences, and every table entry past their lengths, is poison."""
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(seed)
+    new, keys = [n for n, _ in lens], [k for _, k in lens]
+    cu = np.concatenate([[0], np.cumsum(new)])
+    width = max(1, -(-max(keys) // page)) + 1
+    need = [-(-k // page) for k in keys]
+    n_pages = sum(need) + 2
+    order = torch.randperm(n_pages, generator=g).numpy()
+    table = np.full((len(lens), width), 0x7FFFFFFF, np.int64)
+    kp = torch.full((n_pages, Hkv, page, d), float("nan"), dtype=dt)
+    vp = torch.full((n_pages, Hkv, page, d), float("nan"), dtype=dt)
+    at = 0
+    for b, (m, k) in enumerate(zip(need, keys)):
+        table[b, :m] = order[at:at + m]
+        at += m
+        for j in range(m):
+            n = min(page, k - j * page)
+            kp[table[b, j], :, :n] = torch.randn((Hkv, n, d), generator=g).to(dt)
+            vp[table[b, j], :, :n] = torch.randn((Hkv, n, d), generator=g).to(dt)
+    q = (amp * torch.randn((Hq, int(cu[-1]) + pad, d), generator=g)).to(dt)
+    if pad:
+        q[:, int(cu[-1]):] = float("nan")
+    return dict(q=q.cuda(), k=kp.cuda(), v=vp.cuda(), table=cuda_i32(table), cu=cuda_i32(cu),
+                kv=cuda_i32(keys), max_q=max(max(new), 1))
+
+
+def run(attn, x, causal, **kw):
+    return attn.fwd_paged(x["q"], x["k"], x["v"], x["table"], x["cu"], x["kv"], x["max_q"],
+                          causal=causal, **kw)
+
+
+def check(x, o, lse, causal, scale=None):
+    d = x["q"].shape[2]
+    scale = d ** -0.5 if scale is None else scale
+    cu, kv = x["cu"].cpu().numpy(), x["kv"].cpu().numpy()
+    O, L, A, big = oracle.attention_paged(to64(x["q"]), to64(x["k"]), to64(x["v"]),
+                                          x["table"].cpu().numpy(), cu, kv, causal, scale)
+    live = slice(0, int(cu[-1]))
+    u = torch.finfo(x["q"].dtype).eps / 2
+    e = 2.0 ** -20 + int(kv.max()) * 2.0 ** -24 + d * 2.0 ** -24 * big
+    got, ref = to64(o)[:, live], O[:, live]
+    tiny = torch.finfo(x["q"].dtype).smallest_normal * u
+    tol = (u + e) * A[:, live] + u * np.abs(ref) + tiny
+    assert np.isfinite(got).all()
+    assert (np.abs(got - ref) <= tol).all(), float(np.max(np.abs(got - ref) - tol))
+    gl, rl = to64(lse)[:, live], L[:, live]
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(gl), empty)
+    assert (np.abs(gl[~empty] - rl[~empty]) <= e + 2.0 ** -23 * np.abs(rl[~empty])).all()
+
+
+DECODE = [(1, 1), (1, 15), (1, 16), (1, 17), (0, 40), (1, 64), (1, 65), (1, 300), (1, 129)]
+DRAFTS = [(3, 3), (1, 200), (0, 9), (2, 2), (3, 131), (2, 64)]
+CHUNKS = [(17, 17), (1, 90), (128, 128), (129, 300), (0, 5), (5, 400), (63, 64), (200, 777)]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("lens,Hq,Hkv,page", [
+    (DECODE, 4, 1, 16), (DECODE, 2, 2, 64), (DRAFTS, 10, 2, 32), (DRAFTS, 3, 1, 256),
+    ([(1, 5)], 1, 1, 16), ([(1, 2000)], 16, 1, 128)])
+def test_few_rows(attn_lib, causal, dtype, d, lens, Hq, Hkv, page):
+    x = make(lens, Hq, Hkv, d, page, dtype, seed=d + page, pad=2)
+    o, lse = run(attn_lib, x, causal)
+    assert attn_lib.poll_status() == (0, 0)
+    check(x, o, lse, causal)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("lens,Hq,Hkv,page", [
+    (CHUNKS, 4, 2, 16), (CHUNKS, 2, 2, 64), (CHUNKS, 3, 1, 32), (CHUNKS, 7, 1, 128),
+    ([(33, 1000)], 8, 1, 256), ([(1, 100), (1, 900)], 34, 1, 64), ([(9, 50), (2, 600)], 128, 1, 16),
+    ([(700, 700)], 1, 1, 64), ([(257, 1500)], 2, 1, 16), ([(18, 20)] * 40, 1, 1, 16)])
+def test_chunks(attn_lib, causal, dtype, d, lens, Hq, Hkv, page):
+    x = make(lens, Hq, Hkv, d, page, dtype, seed=d + page + len(lens), pad=3)
+    o, lse = run(attn_lib, x, causal)
+    assert attn_lib.poll_status() == (0, 0)
+    check(x, o, lse, causal)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([(4, 0), (3, 2), (1, 7)], 4, 2),
+                                         ([(150, 40), (30, 0), (200, 199)], 4, 2)])
+def test_rows_without_a_key(attn_lib, causal, lens, Hq, Hkv):
+    """Fewer keys than new tokens: causal rows before the first key, and all
+    rows of a sequence with an empty cache, give O = 0, LSE = -inf."""
+    x = make(lens, Hq, Hkv, 64, 16, "bf16", seed=5)
+    o, lse = run(attn_lib, x, causal)
+    assert attn_lib.poll_status() == (0, 0)
+    check(x, o, lse, causal)
+
+
+@pytest.mark.parametrize("lens,Hq", [(DECODE, 4), (CHUNKS, 4)])
+def test_padding_rows_are_left_alone_and_runs_repeat(attn_lib, lens, Hq):
+    x = make(lens, Hq, 2, 128, 16, "bf16", seed=8, pad=5)
+    live = int(x["cu"][-1])
+    outs = []
+    ws = torch.full((attn_lib.fwd_paged_workspace_bytes(x["max_q"], Hq, 2, 128),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    for fill in (3.0, -2.0):
+        o = torch.full_like(x["q"], fill)
+        lse = torch.full(x["q"].shape[:2], fill, device="cuda")
+        run(attn_lib, x, True, out=o, lse=lse, workspace=ws)
+        assert (o[:, live:] == fill).all() and (lse[:, live:] == fill).all()
+        outs.append((o[:, :live].clone(), lse[:, :live].clone()))
+    assert attn_lib.poll_status() == (0, 0)
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 64)], [(40, 700), (1, 64)]])
+@pytest.mark.parametrize("amp,scale", [(30.0, None), (1.0, 1e-4)])
+def test_large_and_small_logits(attn_lib, lens, amp, scale):
+    x = make(lens, 4, 2, 128, 32, "fp16", seed=11, amp=amp)
+    o, lse = run(attn_lib, x, True, scale=scale)
+    assert attn_lib.poll_status() == (0, 0)
+    check(x, o, lse, True, scale)
+
+
+@pytest.mark.parametrize("lens", [[(1, 50), (1, 40), (1, 30)], [(50, 50), (1, 40), (20, 30)]])
+def test_bad_pages_lengths_and_offsets_are_reported(attn_lib, lens):
+    """Out-of-range page numbers, lengths past the table and offsets past the
+    tensors: the call reports them and the other sequences keep their values."""
+    x = make(lens, 4, 2, 64, 16, "bf16", seed=13)
+    good, _ = run(attn_lib, x, True)
+    assert attn_lib.poll_status() == (0, 0)
+    cu = x["cu"].tolist()
+    cases = []
+    for page in (-1, 1 << 30, x["k"].shape[0]):
+        t = x["table"].clone()
+        t[1, 1] = page
+        cases.append(dict(x, table=t))
+    kv = x["kv"].clone()
+    kv[1] = x["table"].shape[1] * 16 + 1
+    cases.append(dict(x, kv=kv))
+    kv = x["kv"].clone()
+    kv[1] = -3
+    cases.append(dict(x, kv=kv))
+    for i, c in enumerate(cases):
+        o, _ = run(attn_lib, c, True)
+        st, detail = attn_lib.poll_status()
+        assert st == 1 and detail >> 16 == 1, (i, st, hex(detail))
+        for b in (0, 2):
+            assert torch.isfinite(o[:, cu[b]:cu[b + 1]]).all()
+            err = (o - good)[:, cu[b]:cu[b + 1]].float().abs().max()
+            assert err <= 2 ** -5 * good.float().abs().max(), (i, b)
+    for bad in ([0, cu[1], cu[1] - 1, cu[3]], [0, cu[1], cu[2], cu[3] + 9], [1] + cu[1:]):
+        run(attn_lib, dict(x, cu=cuda_i32(bad)), True)
+        assert attn_lib.poll_status()[0] == 1
+    o, _ = run(attn_lib, x, True)
+    assert attn_lib.poll_status() == (0, 0) and torch.equal(o, good)
+
+
+def test_many_sequences(attn_lib):
+    """More sequences than the CTA has threads, most of them without tokens."""
+    g = np.random.default_rng(3)
+    lens = [(int(g.integers(0, 2)), int(g.integers(1, 40))) for _ in range(1500)]
+    x = make(lens, 2, 1, 64, 16, "fp16", seed=17)
+    o, lse = run(attn_lib, x, True)
+    assert attn_lib.poll_status() == (0, 0)
+    check(x, o, lse, True)
+
+
+@pytest.mark.parametrize("chunk", [1, 50])
+def test_captured_call_replays_with_new_lengths(attn_lib, chunk):
+    """A graph of append + attention replays on new lengths, pages and tokens
+    written into the same tensors, on a side stream."""
+    Hq, Hkv, d, page, dt = 4, 2, 64, 16, torch.bfloat16
+    table = attn_lib.rope_table(d)
+    x = make([(chunk, chunk + 30), (1, 9)], Hq, Hkv, d, page, "bf16", seed=19)
+    y = make([(1, chunk + 29), (chunk, 2 * chunk + 3)], Hq, Hkv, d, page, "bf16", seed=23)
+    n = max(x["k"].shape[0], y["k"].shape[0])
+    wide = max(x["table"].shape[1], y["table"].shape[1])
+    pad = lambda t, size: torch.cat([t, t.new_zeros(size - t.shape[0], *t.shape[1:])])  # noqa: E731
+    for s in (x, y):
+        s["k"], s["v"] = pad(s["k"], n), pad(s["v"], n)
+        s["table"] = torch.cat([s["table"], s["table"].new_zeros(2, wide - s["table"].shape[1])], 1)
+        s["new"] = torch.randn(2, Hkv, s["q"].shape[1], d, device="cuda").to(dt)
+    hold = {k: v.clone() if torch.is_tensor(v) else v for k, v in x.items()}
+    ws = torch.empty(attn_lib.fwd_paged_workspace_bytes(chunk, Hq, Hkv, d), dtype=torch.uint8,
+                     device="cuda")
+
+    def step(s):
+        q = attn_lib.append_kv(s["new"][0], s["new"][1], s["k"], s["v"], s["table"], s["cu"],
+                               s["kv"], table=table, q=s["q"])
+        return attn_lib.fwd_paged(q, s["k"], s["v"], s["table"], s["cu"], s["kv"], chunk,
+                                  causal=True, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(hold)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        o, lse = step(hold)
+    for s in (x, y, x):
+        for key in ("q", "k", "v", "table", "cu", "kv", "new"):
+            hold[key].copy_(s[key])
+        graph.replay()
+        got = o.clone(), lse.clone()
+        want = step({k: v.clone() if torch.is_tensor(v) else v for k, v in s.items()})
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert attn_lib.poll_status() == (0, 0)
+
+
+@pytest.mark.parametrize("axes", [1, 3])
+def test_serving_run(attn_lib, axes):
+    """As a server uses them together: two prompts in chunks, then single
+    tokens, each step appending turned keys and attending over the cache; every
+    output row is the full causal attention of its sequence."""
+    Hq, Hkv, d, page, dt = 6, 2, 64, 16, torch.bfloat16
+    steps = [(70, 20), (50, 0), (1, 33), (1, 1), (1, 1), (4, 1)]  # new tokens of the two sequences
+    half = d // 2
+    axis = (np.arange(half) * axes // half)
+    inv = 10000.0 ** (-np.arange(half) / half)
+    rope = attn_lib.rope_table(d, axes=axis.tolist())
+    table = np.random.default_rng(0).permutation(24).reshape(2, 12)
+    kp = torch.full((24, Hkv, page, d), float("nan"), dtype=dt, device="cuda")
+    vp = torch.full_like(kp, float("nan"))
+    full = [np.zeros((n, 0, d)) for n in (Hkv, Hkv) * 2]  # k0, v0, k1, v1 as cached
+    kv = [0, 0]
+    g = torch.Generator().manual_seed(29)
+    for new in steps:
+        total = sum(new)
+        q, k, v = (torch.randn((h, total, d), generator=g).to(dt).cuda() for h in (Hq, Hkv, Hkv))
+        kv = [a + n for a, n in zip(kv, new)]
+        pos = torch.randint(0, 4000, (axes, total), generator=g).to(torch.int32).cuda()
+        cu = cuda_i32([0, new[0], total])
+        q2 = attn_lib.append_kv(k, v, kp, vp, cuda_i32(table), cu, cuda_i32(kv), table=rope,
+                                positions=pos, q=q)
+        ref_q, ref_k = attn_lib.rope(q, k, pos, rope)
+        assert torch.equal(q2, ref_q)
+        o, lse = attn_lib.fwd_paged(q2, kp, vp, cuda_i32(table), cu, cuda_i32(kv), max(new),
+                                    causal=True)
+        assert attn_lib.poll_status() == (0, 0)
+        turned = oracle.rotary(to64(q), pos.cpu().numpy(), inv, axis, False)
+        assert np.max(np.abs(to64(q2) - turned)) <= 2 ** -8 * np.abs(turned).max() + 1e-5
+        for b in range(2):
+            rows = slice(0, new[0]) if b == 0 else slice(new[0], total)
+            full[2 * b] = np.concatenate([full[2 * b], to64(ref_k)[:, rows]], 1)
+            full[2 * b + 1] = np.concatenate([full[2 * b + 1], to64(v)[:, rows]], 1)
+            assert np.array_equal(
+                oracle.paged_rows(to64(kp), table[b], kv[b]), full[2 * b])
+        x = dict(q=q2, k=kp, v=vp, table=cuda_i32(table), cu=cu, kv=cuda_i32(kv))
+        check(x, o, lse, True)
+
+
+def test_timeouts_wind_down(attn_lib):
+    """Waits that run out report ATTN_ERR_TIMEOUT and the next call is right."""
+    x = make([(1, 3000)] * 40, 16, 8, 128, 64, "bf16", seed=31)
+    y = make([(300, 3000)] * 3, 16, 8, 128, 64, "bf16", seed=37)
+    for s in (x, y):
+        run(attn_lib, s, True)
+        assert attn_lib.poll_status() == (0, 0)
+        want, _ = run(attn_lib, s, True)
+        attn_lib.set_wait_limit_us(1)
+        try:
+            for _ in range(3):
+                run(attn_lib, s, True)
+            st, _ = attn_lib.poll_status()
+        finally:
+            attn_lib.set_wait_limit_us(0)
+        assert st in (0, 4)
+        got, _ = run(attn_lib, s, True)
+        assert attn_lib.poll_status() == (0, 0) and torch.equal(got, want)
