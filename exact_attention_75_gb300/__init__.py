@@ -458,81 +458,104 @@ def rope_table(rot: int, theta: float = 10000.0, axes: Optional[Sequence[int]] =
     return torch.tensor([step, axis], dtype=torch.int64).to(device)
 
 
-def _strides(t: torch.Tensor, dims: Sequence[int], what: str, written: bool = False):
-    """Element strides of the given dims (0 where the size is 1) of a tensor
-    whose rows are read or written 16 bytes at a time."""
-    got = [t.stride(i) if t.shape[i] > 1 else 0 for i in dims]
-    if t.stride(-1) != 1 or any(x % 8 for x in got):
-        raise ValueError(f"{what}: the last dimension must be contiguous and the other strides "
-                         "multiples of 8 elements")
-    if written and any(x == 0 for x, i in zip(got, dims) if t.shape[i] > 1):
-        raise ValueError(f"{what} must not be an expanded tensor")
-    return got
+# The checks below run on every call of a decoding step, so they are written
+# for few attribute reads and no temporaries.
+
+_I64 = {n: ctypes.c_int64 * n for n in (4, 6, 12)}
+_CODES = {torch.float16: _F16, torch.bfloat16: _BF16}
 
 
-def _check_table(table: torch.Tensor, d: int, device) -> int:
-    if (table.dtype != torch.int64 or table.dim() != 2 or table.shape[0] != 2
-            or not table.is_contiguous() or table.device != device):
+def _row_strides(t: torch.Tensor, what: str, written: bool = False) -> Tuple[int, ...]:
+    """Strides of a tensor whose rows are read or written 16 bytes at a time
+    (0 for a dimension of size 1)."""
+    st = t.stride()
+    low = 0
+    for x in st[:-1]:
+        low |= x
+    if st[-1] != 1 or low & 7 or written:
+        st = tuple(x if n > 1 else 0 for x, n in zip(st[:-1], t.shape)) + (st[-1],)
+        if st[-1] != 1 or any(x & 7 for x in st[:-1]):
+            raise ValueError(f"{what}: the last dimension must be contiguous and the other "
+                             "strides multiples of 8 elements")
+        if written and any(x == 0 and n > 1 for x, n in zip(st, t.shape)):
+            raise ValueError(f"{what} must not be an expanded tensor")
+    return st
+
+
+def _call(fn, what: str, device: int, *args) -> None:
+    """fn(*args, stream) on the current stream of the tensors' device."""
+    if torch.cuda.current_device() == device:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if st != 0:
+        raise AttnError(what, st)
+
+
+def _check_table(table: torch.Tensor, d: int, device: int) -> int:
+    shape = table.shape
+    if (table.dtype != torch.int64 or len(shape) != 2 or shape[0] != 2
+            or not table.is_contiguous() or table.get_device() != device):
         raise ValueError("table must be a contiguous int64 [2, rot/2] tensor (rope_table) on the "
                          "tensors' device")
-    rot = 2 * int(table.shape[1])
-    if rot < 16 or rot % 16 != 0 or rot > d:
+    rot = 2 * shape[1]
+    if rot < 16 or rot & 15 or rot > d:
         raise ValueError("the table must turn a multiple of 16 channels, at most the head dim")
     return rot
 
 
 def _rope(q, k, positions, table, interleaved, out_q, out_k, inverse):
-    what = "rope_bwd" if inverse else "rope"
-    packed = q.dim() == 3  # [H, total, d]: one batch
-    if q.dim() not in (3, 4):
+    shape, code = q.shape, _CODES.get(q.dtype)
+    if len(shape) == 4:
+        B, H, N, d = shape
+    elif len(shape) == 3:  # packed: one batch
+        (H, N, d), B = shape, 1
+    else:
         raise ValueError("tensors must be [B, H, N, d] or packed [H, total, d]")
+    if code is None:
+        raise TypeError(f"q and k must be float16 or bfloat16, got {q.dtype}")
     if not q.is_cuda:
         raise ValueError("all tensors must be on the same CUDA device")
-    B = 1 if packed else int(q.shape[0])
-    H, N, d = (int(x) for x in q.shape[-3:])
-    if min(B, H, N) < 1:
+    if q.numel() == 0:
         raise ValueError("tensors must not be empty")
-    code = _dtype_code(q)
-    rot = _check_table(table, d, q.device)
-    if positions.dtype != torch.int32 or positions.device != q.device \
+    dev = q.get_device()
+    rot = _check_table(table, d, dev)
+    pshape = positions.shape
+    if positions.dtype != torch.int32 or positions.get_device() != dev \
             or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 tensor on the tensors' device")
-    if positions.dim() == 2:
-        n_axes, pos_batches = int(positions.shape[0]), 1
-    elif positions.dim() == 3:
-        n_axes, pos_batches = int(positions.shape[0]), int(positions.shape[1])
-    else:
-        raise ValueError("positions must be [axes, N] or [axes, B, N]")
-    if positions.shape[-1] != N or pos_batches not in (1, B) or not 1 <= n_axes <= _MAX_AXES:
+    n_axes = pshape[0] if len(pshape) in (2, 3) else 0
+    pos_batches = pshape[1] if len(pshape) == 3 else 1
+    if not 1 <= n_axes <= _MAX_AXES or pshape[-1] != N or (pos_batches != 1 and pos_batches != B):
         raise ValueError(f"positions must be [axes, N] or [axes, B, N], at most {_MAX_AXES} axes")
-    dims = (0, 1) if packed else (0, 1, 2)
-    strides, outs = [], []
-    for x, out in ((q, out_q), (k, out_k)):
-        if x is None:
-            if out is not None:
-                raise ValueError("out_k without k")
-            outs.append(None)
-            continue
-        if x.dim() != q.dim() or x.dtype != q.dtype or x.device != q.device \
-                or x.shape[-2:] != q.shape[-2:] or (not packed and x.shape[0] != B) \
-                or x.shape[-3] < 1:
+    if out_q is None:
+        out_q = q.new_empty(shape)
+    elif out_q.shape != shape or out_q.dtype != q.dtype or out_q.get_device() != dev:
+        raise ValueError("out_q must have the shape, dtype and device of q")
+    st = _row_strides(q, "q")[:-1] + _row_strides(out_q, "out_q", True)[:-1]
+    kp = okp = Hkv = 0
+    if k is not None:
+        kshape = k.shape
+        if len(kshape) != len(shape) or kshape[-2:] != shape[-2:] or k.dtype != q.dtype \
+                or k.get_device() != dev or (len(shape) == 4 and kshape[0] != B) \
+                or k.numel() == 0:
             raise ValueError("q and k must share batch, length, head dim, dtype and device")
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-            raise ValueError("out_q, out_k must have the shape, dtype and device of q, k")
-        for t, written in ((x, False), (out, True)):
-            st = _strides(t, dims, "q, k" if t is x else "out_q, out_k", written)
-            strides += [0] + st if packed else st
-        outs.append(out)
-    arr = (ctypes.c_int64 * len(strides))(*strides)
-    with torch.cuda.device(q.device):
-        st = lib().attn_rope(_ptr(q), _ptr(k), _ptr(outs[0]), _ptr(outs[1]), arr,
-                             _ptr(positions), pos_batches, n_axes, _ptr(table), rot,
-                             int(bool(interleaved)), inverse, B, H,
-                             0 if k is None else int(k.shape[-3]), N, d, code, _stream(q))
-    _check(st, "attn_" + what)
-    return outs[0], outs[1]
+        Hkv = kshape[-3]
+        if out_k is None:
+            out_k = k.new_empty(kshape)
+        elif out_k.shape != kshape or out_k.dtype != q.dtype or out_k.get_device() != dev:
+            raise ValueError("out_k must have the shape, dtype and device of k")
+        st += _row_strides(k, "k")[:-1] + _row_strides(out_k, "out_k", True)[:-1]
+        kp, okp = k.data_ptr(), out_k.data_ptr()
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    if len(shape) == 3:
+        st = tuple(x for i in range(0, len(st), 2) for x in (0, st[i], st[i + 1]))
+    _call(lib().attn_rope, "attn_rope_bwd" if inverse else "attn_rope", dev, q.data_ptr(), kp,
+          out_q.data_ptr(), okp, _I64[len(st)](*st), positions.data_ptr(), pos_batches, n_axes,
+          table.data_ptr(), rot, 1 if interleaved else 0, inverse, B, H, Hkv, N, d, code)
+    return out_q, out_k
 
 
 def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, table: torch.Tensor,
@@ -556,28 +579,32 @@ def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tens
     return _rope(dq, dk, positions, table, interleaved, out_q, out_k, 1)
 
 
-def _check_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens):
+def _check_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens) -> int:
     """Shapes of a paged cache [n_pages, Hkv, page, d] and its batch; q is a
-    packed [H, total, d] tensor of new tokens.  Returns n_seq, max_pages."""
-    if q.dim() != 3:
+    packed [H, total, d] tensor of new tokens.  Returns the device."""
+    qshape, kshape, bshape = q.shape, k_pages.shape, block_table.shape
+    if len(qshape) != 3:
         raise ValueError("packed tensors must be [H, total, d]")
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[3] != q.shape[2]:
+    if len(kshape) != 4 or kshape != v_pages.shape or kshape[3] != qshape[2]:
         raise ValueError("k_pages, v_pages must be [n_pages, Hkv, page, d] with the tokens' d")
-    for t in (q, k_pages, v_pages):
-        if not t.is_cuda or t.device != q.device or t.dtype != q.dtype:
-            raise ValueError("tokens and pages must be CUDA tensors of one dtype on one device")
-    if not k_pages.is_contiguous() or not v_pages.is_contiguous():
+    dev, dt = q.get_device(), q.dtype
+    if dt not in _CODES:
+        raise TypeError(f"tokens must be float16 or bfloat16, got {dt}")
+    if not q.is_cuda or k_pages.get_device() != dev or v_pages.get_device() != dev \
+            or k_pages.dtype != dt or v_pages.dtype != dt:
+        raise ValueError("tokens and pages must be CUDA tensors of one dtype on one device")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages, v_pages must be contiguous")
-    n_seq = kv_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != n_seq or cu_seqlens.dim() != 1 \
-            or cu_seqlens.numel() != n_seq + 1 or kv_lens.dim() != 1 or n_seq < 1:
+    n = kv_lens.shape
+    if len(bshape) != 2 or len(n) != 1 or bshape[0] != n[0] or n[0] < 1 \
+            or cu_seqlens.shape != (n[0] + 1,):
         raise ValueError("block_table must be [n_seq, max_pages], cu_seqlens [n_seq + 1], "
                          "kv_lens [n_seq]")
     for t in (block_table, cu_seqlens, kv_lens):
-        if t.dtype != torch.int32 or t.device != q.device or not t.is_contiguous():
+        if t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous():
             raise ValueError("block_table, cu_seqlens and kv_lens must be contiguous int32 "
                              "tensors on the tokens' device")
-    return n_seq, int(block_table.shape[1])
+    return dev
 
 
 def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -597,48 +624,47 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
     int32 [axes, total] (None: the position in the cache on every axis).
     Returns the turned queries (None without q); rows behind the last sequence
     are left as they were."""
-    n_seq, max_pages = _check_paged(k, k_pages, v_pages, block_table, cu_seqlens, kv_lens)
-    Hkv, total, d = (int(x) for x in k.shape)
-    if k.shape[0] != k_pages.shape[1] or v.shape != k.shape or v.dtype != k.dtype \
-            or v.device != k.device:
+    dev = _check_paged(k, k_pages, v_pages, block_table, cu_seqlens, kv_lens)
+    shape, dt = k.shape, k.dtype
+    Hkv, total, d = shape
+    n_pages, cache_heads, page, _ = k_pages.shape
+    n_seq, max_pages = block_table.shape
+    if Hkv != cache_heads or v.shape != shape or v.dtype != dt or v.get_device() != dev:
         raise ValueError("k and v must be [Hkv, total, d] with the cache's heads")
-    rot, n_axes = 0, 1
-    if table is not None:
-        rot = _check_table(table, d, k.device)
+    rot, tp = (0, 0) if table is None else (_check_table(table, d, dev), table.data_ptr())
+    pp, n_axes = 0, 1
     if positions is not None:
+        pshape = positions.shape
         if table is None:
             raise ValueError("positions without a table")
-        if positions.dtype != torch.int32 or positions.device != k.device \
-                or positions.dim() != 2 or positions.shape[1] != total \
-                or not 1 <= positions.shape[0] <= _MAX_AXES or not positions.is_contiguous():
+        if positions.dtype != torch.int32 or positions.get_device() != dev or len(pshape) != 2 \
+                or pshape[1] != total or not 1 <= pshape[0] <= _MAX_AXES \
+                or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous int32 [axes, total] tensor, at most "
                              f"{_MAX_AXES} axes")
-        n_axes = int(positions.shape[0])
-    strides = _strides(k, (0, 1), "k") + _strides(v, (0, 1), "v")
-    Hq = 0
+        pp, n_axes = positions.data_ptr(), pshape[0]
+    st = _row_strides(k, "k")[:-1] + _row_strides(v, "v")[:-1]
+    Hq = qp = op = 0
     if q is not None:
-        if q.dim() != 3 or q.shape[1:] != k.shape[1:] or q.dtype != k.dtype \
-                or q.device != k.device or q.shape[0] < 1 or q.shape[0] % Hkv != 0:
+        qshape = q.shape
+        Hq = qshape[0]
+        if len(qshape) != 3 or qshape[1:] != shape[1:] or q.dtype != dt \
+                or q.get_device() != dev or Hq < 1 or Hq % Hkv != 0:
             raise ValueError("q must be [Hq, total, d] with k's total, d, dtype and device, "
                              "Hq a multiple of Hkv")
-        Hq = int(q.shape[0])
-        strides += _strides(q, (0, 1), "q")
+        st += _row_strides(q, "q")[:-1]
         if out_q is None:
-            out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif out_q.shape != q.shape or out_q.dtype != q.dtype or out_q.device != q.device \
+            out_q = q.new_empty(qshape)
+        elif out_q.shape != qshape or out_q.dtype != dt or out_q.get_device() != dev \
                 or not out_q.is_contiguous():
             raise ValueError("out_q must be contiguous with q's shape, dtype and device")
+        qp, op = q.data_ptr(), out_q.data_ptr()
     elif out_q is not None:
         raise ValueError("out_q without q")
-    arr = (ctypes.c_int64 * len(strides))(*strides)
-    with torch.cuda.device(k.device):
-        st = lib().attn_append_kv(_ptr(k), _ptr(v), _ptr(q), _ptr(out_q), arr, _ptr(k_pages),
-                                  _ptr(v_pages), _ptr(block_table), _ptr(cu_seqlens),
-                                  _ptr(kv_lens), _ptr(positions), n_axes, _ptr(table), rot,
-                                  int(bool(interleaved)), n_seq, total, int(k_pages.shape[0]),
-                                  int(k_pages.shape[2]), max_pages, Hq, Hkv, d, _dtype_code(k),
-                                  _stream(k))
-    _check(st, "attn_append_kv")
+    _call(lib().attn_append_kv, "attn_append_kv", dev, k.data_ptr(), v.data_ptr(), qp, op,
+          _I64[len(st)](*st), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+          cu_seqlens.data_ptr(), kv_lens.data_ptr(), pp, n_axes, tp, rot,
+          1 if interleaved else 0, n_seq, total, n_pages, page, max_pages, Hq, Hkv, d, _CODES[dt])
     return out_q
 
 
@@ -660,41 +686,40 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     j <= i + kv_lens[b] - n.  A row that sees no key gets O = 0, LSE = -inf;
     rows behind the last sequence are left as they were.  workspace: uint8,
     fwd_paged_workspace_bytes long; calls that may overlap need their own."""
-    n_seq, max_pages = _check_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens)
-    H, total, d = (int(x) for x in q.shape)
-    Hkv = int(k_pages.shape[1])
+    dev = _check_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens)
+    shape, dt = q.shape, q.dtype
+    H, total, d = shape
+    n_pages, Hkv, page, _ = k_pages.shape
+    n_seq, max_pages = block_table.shape
     if not q.is_contiguous():
         raise ValueError("q must be contiguous [Hq, total, d]")
     if Hkv < 1 or H % Hkv != 0:
         raise ValueError("the number of key/value heads must divide the query heads")
-    if not 1 <= int(max_q) <= total:
+    max_q = int(max_q)
+    if not 1 <= max_q <= total:
         raise ValueError("max_q must lie in [1, total]")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
+        out = q.new_empty(shape)
+    elif out.shape != shape or out.dtype != dt or out.get_device() != dev \
             or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
     if lse is None:
-        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
-    elif tuple(lse.shape) != (H, total) or lse.dtype != torch.float32 \
-            or lse.device != q.device or not lse.is_contiguous():
+        lse = q.new_empty((H, total), dtype=torch.float32)
+    elif lse.shape != (H, total) or lse.dtype != torch.float32 or lse.get_device() != dev \
+            or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [Hq, total] tensor on q's device")
+    L = lib()
     if workspace is None:
-        workspace = torch.empty(max(fwd_paged_workspace_bytes(int(max_q), H, Hkv, d), 256),
-                                dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8 or workspace.device != q.device \
+        workspace = q.new_empty(max(L.attn_fwd_paged_workspace_bytes(max_q, H, Hkv, d), 256),
+                                dtype=torch.uint8)
+    elif workspace.dtype != torch.uint8 or workspace.get_device() != dev \
             or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    with torch.cuda.device(q.device):
-        st = lib().attn_fwd_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse),
-                                  _ptr(block_table), _ptr(cu_seqlens), _ptr(kv_lens),
-                                  _ptr(workspace), workspace.numel(), n_seq, int(max_q), total,
-                                  int(k_pages.shape[0]), int(k_pages.shape[2]), max_pages, H,
-                                  Hkv, d, int(bool(causal)), float(scale), _dtype_code(q),
-                                  _stream(q))
-    _check(st, "attn_fwd_paged")
+    _call(L.attn_fwd_paged, "attn_fwd_paged", dev, q.data_ptr(), k_pages.data_ptr(),
+          v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
+          cu_seqlens.data_ptr(), kv_lens.data_ptr(), workspace.data_ptr(), workspace.numel(),
+          n_seq, max_q, total, n_pages, page, max_pages, H, Hkv, d, 1 if causal else 0,
+          1.0 / math.sqrt(d) if scale is None else float(scale), _CODES[dt])
     return out, lse
 
 

@@ -90,13 +90,13 @@ attn_status launch_result(cudaError_t e) {
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // 3-D tiled map over a contiguous [outer, rows, inner] tensor with the
-// 128-byte swizzle; box = [1, box_rows, box_inner].
+// 128-byte swizzle; box = [box_outer, box_rows, box_inner].
 bool encode_3d(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int esize, int64_t inner,
                int64_t rows, int64_t outer, int box_inner, int box_rows,
-               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
+               CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B, int box_outer = 1) {
   cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)outer};
   cuuint64_t strides[2] = {(cuuint64_t)(inner * esize), (cuuint64_t)(inner * rows * esize)};
-  cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, (cuuint32_t)box_outer};
   cuuint32_t es[3] = {1, 1, 1};
   return g_encode(m, dt, 3, const_cast<void*>(ptr), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -450,6 +450,23 @@ attn_status paged_args(const void* k_pages, const void* v_pages, const int32_t* 
   return ATTN_OK;
 }
 
+// At most 16 query rows per sequence and key/value head run on the decoding
+// kernel (16 rows of the warp-level product, two CTAs per SM), more on the
+// tile kernel.
+bool paged_decode(int max_q, int group) { return (int64_t)max_q * group <= kPagedRows; }
+
+// The partial results of a grid in the workspace: desc, (m, l), O.
+struct PagedWorkspace {
+  size_t ml, o, bytes;
+  PagedWorkspace(bool decode, int d) {
+    const size_t ctas = decode ? 2 * kPagedMaxSms : kPagedMaxSms;
+    const size_t rows = 2 * ctas * (decode ? kPagedRows : kPagedTileRows);
+    ml = ctas * sizeof(int4);
+    o = ml + rows * sizeof(float2);
+    bytes = o + rows * d * sizeof(float);
+  }
+};
+
 }  // namespace
 
 extern "C" {
@@ -560,7 +577,7 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
 size_t attn_fwd_paged_workspace_bytes(int max_q, int Hq, int Hkv, int d) {
   if (max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
   if (d != 64 && d != 96 && d != 128) return 0;
-  return paged_workspace_bytes(d);
+  return PagedWorkspace(paged_decode(max_q, Hq / Hkv), d).bytes;
 }
 
 attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o,
@@ -609,15 +626,32 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   p.causal = causal;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = g_wait_limit_ns.load();
-  paged_carve(&p, workspace, d);
-  a.num_sms = di->num_sms;
-  a.stream = static_cast<cudaStream_t>(stream);
-  const int64_t heads = (int64_t)n_pages * Hkv;
-  if (!encode_3d(&a.tmK, k_pages, dt, 2, d, page, heads, 64, kPagedBlock) ||
-      !encode_3d(&a.tmV, v_pages, dt, 2, d, page, heads, 64, kPagedBlock))
-    return ATTN_ERR_CUDA;
+  const bool decode = paged_decode(max_q, p.G);
+  const PagedWorkspace ws(decode, d);
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p.desc = reinterpret_cast<int4*>(w);
+  p.part_ml = reinterpret_cast<float*>(w + ws.ml);
+  p.part_o = reinterpret_cast<float*>(w + ws.o);
   p.min_share = 2;
-  return launch_result(launch_paged_decode(a, d, dtype == ATTN_BF16));
+  const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
+  a.grid = decode ? 2 * sms : sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  // the units of the largest batch of these sizes, per CTA, stay in 31 bits
+  const int64_t blocks = (int64_t)max_pages * page / kPagedUnitKeys + 2;
+  const int64_t items = (((int64_t)total * p.G) / 64 + n_seq) * Hkv;
+  if (blocks > ((int64_t)a.grid << 31) / items) return ATTN_ERR_INVALID_ARG;
+  const int64_t heads = (int64_t)n_pages * Hkv;
+  const int box = decode ? kPagedBlock : (page < 128 ? page : 128);
+  if (!encode_3d(&a.tmK, k_pages, dt, 2, d, page, heads, 64, box) ||
+      !encode_3d(&a.tmV, v_pages, dt, 2, d, page, heads, 64, box))
+    return ATTN_ERR_CUDA;
+  if (!decode && !encode_3d(&a.tmQ, q, dt, 2, d, total, Hq, 64, 128 / p.G,
+                            CU_TENSOR_MAP_SWIZZLE_128B, p.G))
+    return ATTN_ERR_CUDA;
+  const bool bf16 = dtype == ATTN_BF16;
+  cudaError_t e = decode ? launch_paged_decode(a, d, bf16) : launch_paged_tile(a, d, bf16);
+  if (e == cudaSuccess) e = launch_paged_join(a, d, bf16, decode);
+  return launch_result(e);
 }
 
 }  // extern "C"

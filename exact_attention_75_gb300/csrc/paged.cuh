@@ -27,10 +27,12 @@
 
 namespace attn {
 
-constexpr int kPagedMaxCtas = 320;  // bound of the grids, sizes the workspace
+constexpr int kPagedMaxSms = 160;  // bound of the grids (two CTAs per SM at most)
 // Query rows (query heads of a group x new tokens) of an item on the
 // warp-level kernel: the M = 16 of its product.
 constexpr int kPagedRows = 16;
+// Rows of an item of the tile kernel (two query tiles).
+constexpr int kPagedTileRows = 256;
 // Keys of a block there (rows of the tensor-map box).
 constexpr int kPagedBlock = 16;
 // Query heads per key/value head at most.
@@ -57,17 +59,19 @@ struct PagedParams {
 };
 
 struct PagedLaunch {
+  CUtensorMap tmQ;          // [Hkv * G, total, D] (tile kernel)
   CUtensorMap tmK, tmV;     // [n_pages * Hkv, page, D]
   PagedParams params;
-  int num_sms;
+  int grid;                 // CTAs of the main kernel
   cudaStream_t stream;
 };
 
-size_t paged_workspace_bytes(int d);
-// Places desc, part_ml and part_o in a workspace.
-void paged_carve(PagedParams* p, void* workspace, int d);
-// d in {64, 96, 128}.
+// d in {64, 96, 128}.  The decoding kernel takes at most kPagedRows query
+// rows per sequence and key/value head, the tile kernel any number; the join
+// follows either with the same grid.
 cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16);
+cudaError_t launch_paged_tile(const PagedLaunch& a, int d, bool bf16);
+cudaError_t launch_paged_join(const PagedLaunch& a, int d, bool bf16, bool decode);
 
 #ifdef __CUDACC__
 
@@ -95,21 +99,24 @@ __device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
     atomicCAS(p.status, 0u, 1u | (63u << 8) | ((uint32_t)min(b, 0xFFFF) << 16));
 }
 
-// Where a CTA's share begins: sequence b, units into its line, and the units
-// of the share (0: none).
+// Where a CTA's share begins (sequence b, its item counted over the key/value
+// heads, the unit in the item), its units (left 0: none), and the units of a
+// full share.
 struct PagedStart {
   int b;
-  long long off;
+  int item, items_per_head, unit;
   long long left;
   long long share;
 };
 
-// Every thread of the CTA calls this; head_cost(seq) gives the cost units of
-// one key/value head of a sequence (a long long).  The threads take runs of sequences, a
-// scan over the threads' sums places the share, and the thread whose run
-// holds its start walks there.
-template <int THREADS, typename HeadCost>
-__device__ __forceinline__ PagedStart paged_partition(const PagedParams& p, HeadCost head_cost) {
+// Every thread of the CTA calls this.  head_cost(seq) gives the cost units of
+// one key/value head of a sequence (a long long); place(seq, off, start) turns
+// an offset into a sequence's line into item, items_per_head and unit.  The
+// threads take runs of sequences, a scan over the threads' sums places the
+// share, and the thread whose run holds its start walks there.
+template <int THREADS, typename HeadCost, typename Place>
+__device__ __forceinline__ PagedStart paged_partition(const PagedParams& p, HeadCost head_cost,
+                                                      Place place) {
   __shared__ long long warp_sum[THREADS / 32];
   __shared__ PagedStart start;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -137,13 +144,14 @@ __device__ __forceinline__ PagedStart paged_partition(const PagedParams& p, Head
   long long share = (all + gridDim.x - 1) / gridDim.x;
   if (share < p.min_share) share = p.min_share;
   const long long s = share * blockIdx.x;
-  if (tid == 0 && s >= all) start = PagedStart{0, 0, 0, share};
+  if (tid == 0 && s >= all) start = PagedStart{0, 0, 1, 0, 0, share};
   long long at = before + incl - sum;
   if (s >= at && s < at + sum) {
     for (int b = b0; b < b1; ++b) {
       const long long c = head_cost(paged_seq(p, b)) * p.Hkv;
       if (s < at + c) {
-        start = PagedStart{b, s - at, min(share, all - s), share};
+        start = PagedStart{b, 0, 1, 0, min(share, all - s), share};
+        place(paged_seq(p, b), s - at, start);
         break;
       }
       at += c;

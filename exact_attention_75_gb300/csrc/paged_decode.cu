@@ -1,5 +1,5 @@
-// Attention of a few new tokens per sequence over a paged key/value cache,
-// and the join of partial results.
+// Attention of a few new tokens per sequence (at most 16 query rows per
+// key/value head) over a paged key/value cache.
 //
 // The mathematics is the decoding kernel's (online softmax over 16-key
 // blocks on the warp-level product, 16 query rows: the group's query heads x
@@ -45,12 +45,10 @@ __device__ __forceinline__ uint32_t sw_off(int row, int piece) {
   return (uint32_t)((piece >> 3) * kBoxBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// An item's cost: its key units and one for its prologue and epilogue.
+// An item is a sequence's key/value head; its cost: the key units and one for
+// its prologue and epilogue.
 __device__ __forceinline__ int key_units(const PagedSeq& s) {
   return (s.klen + kPagedUnitKeys - 1) / kPagedUnitKeys;
-}
-__device__ __forceinline__ int row_groups(const PagedSeq& s, int G) {
-  return (s.qlen * G + kPagedRows - 1) / kPagedRows;
 }
 
 template <int D, bool BF16>
@@ -76,23 +74,19 @@ __global__ void __launch_bounds__(kThreads)
     mbar_fence_init();
     p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  const PagedStart st = paged_partition<kThreads>(p, [&](const PagedSeq& s) {
-    return (long long)row_groups(s, p.G) * (key_units(s) + 1);
-  });
+  const PagedStart st = paged_partition<kThreads>(
+      p, [&](const PagedSeq& s) { return s.qlen == 0 ? 0LL : key_units(s) + 1LL; },
+      [&](const PagedSeq& s, long long off, PagedStart& at) {
+        at.item = (int)(off / (key_units(s) + 1));
+        at.unit = (int)(off % (key_units(s) + 1));
+      });
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
 
   long long left = st.left;
   int b = st.b;
   PagedSeq sq = paged_seq(p, b);
-  int nku = key_units(sq), ngr = row_groups(sq, p.G);
-  int head = 0, rg = 0, u0 = 0;
-  if (left > 0) {
-    const long long per_head = (long long)ngr * (nku + 1);
-    head = (int)(st.off / per_head);
-    const long long rem = st.off % per_head;
-    rg = (int)(rem / (nku + 1));
-    u0 = (int)(rem % (nku + 1));
-  }
+  int nku = key_units(sq);
+  int head = st.item, u0 = st.unit;
   uint32_t it = 0;  // blocks this warp has taken from its ring
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
@@ -105,9 +99,7 @@ __global__ void __launch_bounds__(kThreads)
       const int k_hi = min(u1 * kPagedUnitKeys, sq.klen);
       const int nb = (k_hi - k_lo + kKeys - 1) / kKeys;
       const int nbw = nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;  // this warp's blocks
-      const int R = sq.qlen * p.G;
-      const int row0 = rg * kPagedRows;
-      const int rows = min(kPagedRows, R - row0);
+      const int rows = min(kPagedRows, sq.qlen * p.G);
       const int* pages = p.block_table + (size_t)b * p.max_pages;
 
       // Block j of this warp in this item -> ring slot (it + j) % NS (lane 0 only).
@@ -133,10 +125,9 @@ __global__ void __launch_bounds__(kThreads)
       if (lane == 0)
         for (int j = 0; j < issued; ++j) issue(j);
 
-      // Row r of the item: new token (row0 + r) / G, query head (row0 + r) % G
-      // of the group.
+      // Row r of the item: new token r / G, query head r % G of the group.
       auto grow = [&](int r) -> size_t {
-        const int i = (row0 + r) / p.G, h = (row0 + r) - i * p.G;
+        const int i = r / p.G, h = r - i * p.G;
         return (size_t)(head * p.G + h) * p.total + sq.s0 + i;
       };
       const int r0 = lane >> 2, cq = 2 * (lane & 3);
@@ -156,7 +147,7 @@ __global__ void __launch_bounds__(kThreads)
       // one before the first key).
       auto last_key = [&](int r) {
         if (r >= rows) return -1;
-        const int lim = p.causal ? (row0 + r) / p.G + sq.klen - sq.qlen : sq.klen - 1;
+        const int lim = p.causal ? r / p.G + sq.klen - sq.qlen : sq.klen - 1;
         return min(lim, k_hi - 1);
       };
       const int limA = last_key(r0), limB = last_key(r0 + 8);
@@ -331,7 +322,7 @@ __global__ void __launch_bounds__(kThreads)
       const size_t slot = 2 * (size_t)blockIdx.x + (u0 == 0 ? 1 : 0);
       if (!whole && u0 == 0 && threadIdx.x == 0)
         p.desc[blockIdx.x] =
-            make_int4(b, head, rg, 1 + (int)((nku - u1 + st.share - 1) / st.share));
+            make_int4(b, head, 0, 1 + (int)((nku - u1 + st.share - 1) / st.share));
       for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
         const int r = idx / (D / 4), c4 = idx % (D / 4);
         float M = -INFINITY;
@@ -370,61 +361,15 @@ __global__ void __launch_bounds__(kThreads)
     }
     // the next item
     u0 = 0;
-    if (left > 0 && ++rg == ngr) {
-      rg = 0;
-      if (++head == p.Hkv) {
-        head = 0;
-        do {
-          sq = paged_seq(p, ++b);
-        } while (sq.qlen == 0 && b + 1 < p.n_seq);
-        nku = key_units(sq);
-        ngr = row_groups(sq, p.G);
-      }
+    if (left > 0 && ++head == p.Hkv) {
+      head = 0;
+      do {
+        sq = paged_seq(p, ++b);
+      } while (sq.qlen == 0 && b + 1 < p.n_seq);
+      nku = key_units(sq);
     }
   }
   asm volatile("griddepcontrol.launch_dependents;");
-}
-
-// Joins the parts of the items that crossed shares: CTA (c, y) takes the
-// item that the main kernel's CTA c began and others continued, a slice y of
-// its rows and columns.  Per row, over the parts in key order,
-//   M = max m_k,  l = sum l_k 2^(m_k - M),  O = sum O_k 2^(m_k - M) / l.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 item = p.desc[blockIdx.x];
-  const int parts = item.w;
-  if (parts == 0) return;
-  constexpr int rows = 16;
-  const PagedSeq sq = paged_seq(p, item.x);
-  const int R = min(sq.qlen * p.G - item.z * kPagedRows, kPagedRows);
-  for (int idx = blockIdx.y * 128 + threadIdx.x; idx < rows * (D / 4); idx += 128 * gridDim.y) {
-    const int r = idx % rows, c4 = idx / rows;
-    if (r >= R) continue;
-    float M = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < parts; ++k) {
-      const size_t slot = 2 * ((size_t)blockIdx.x + k) + (k == 0 ? 1 : 0);
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * rows + r) * 2);
-      const float4 x =
-          *reinterpret_cast<const float4*>(p.part_o + slot * rows * D + part_at(c4, r, rows));
-      if (ml.x == -INFINITY) continue;  // a row that sees no key of this part
-      const float N = fmaxf(M, ml.x);
-      const float f = exp2f(ml.x - N), g = exp2f(M - N);
-      M = N;
-      l = l * g + ml.y * f;
-      acc.x = acc.x * g + x.x * f;
-      acc.y = acc.y * g + x.y * f;
-      acc.z = acc.z * g + x.z * f;
-      acc.w = acc.w * g + x.w * f;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int i = (item.z * kPagedRows + r) / p.G, h = item.z * kPagedRows + r - i * p.G;
-    const size_t gr = (size_t)(item.y * p.G + h) * p.total + sq.s0 + i;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + 4 * c4) = make_uint2(
-        pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-    if (c4 == 0) p.lse[gr] = l > 0.f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
-  }
 }
 
 template <int D, bool BF16>
@@ -433,20 +378,9 @@ cudaError_t launch_db(const PagedLaunch& a) {
   static DeviceFlags configured;
   cudaError_t e = ensure_dyn_smem(paged_decode_kernel<D, BF16>, L::kBytes, configured);
   if (e != cudaSuccess) return e;
-  const int grid = 2 * a.num_sms < kPagedMaxCtas ? 2 * a.num_sms : kPagedMaxCtas;
-  paged_decode_kernel<D, BF16><<<grid, kThreads, L::kBytes, a.stream>>>(a.tmK, a.tmV, a.params);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, 2);
-  cfg.blockDim = dim3(128);
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, BF16>, a.params);
+  paged_decode_kernel<D, BF16>
+      <<<a.grid, kThreads, L::kBytes, a.stream>>>(a.tmK, a.tmV, a.params);
+  return cudaGetLastError();
 }
 
 template <int D>
@@ -454,21 +388,7 @@ cudaError_t launch_d(const PagedLaunch& a, bool bf16) {
   return bf16 ? launch_db<D, true>(a) : launch_db<D, false>(a);
 }
 
-constexpr size_t kDescBytes = kPagedMaxCtas * sizeof(int4);
-constexpr size_t kMlBytes = (size_t)kPagedMaxCtas * 2 * kPagedRows * 2 * sizeof(float);
-
 }  // namespace
-
-size_t paged_workspace_bytes(int d) {
-  return kDescBytes + kMlBytes + (size_t)kPagedMaxCtas * 2 * kPagedRows * d * sizeof(float);
-}
-
-void paged_carve(PagedParams* p, void* workspace, int d) {
-  uint8_t* w = static_cast<uint8_t*>(workspace);
-  p->desc = reinterpret_cast<int4*>(w);
-  p->part_ml = reinterpret_cast<float*>(w + kDescBytes);
-  p->part_o = reinterpret_cast<float*>(w + kDescBytes + kMlBytes);
-}
 
 cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16) {
   switch (d) {
