@@ -433,6 +433,12 @@ bool strides_ok(const int64_t* s, int n) {
   return true;
 }
 
+int log2_of(int pow2) {
+  int n = 0;
+  while ((1 << n) < pow2) ++n;
+  return n;
+}
+
 // The cache and batch description the paged entry points share.
 attn_status paged_args(const void* k_pages, const void* v_pages, const int32_t* block_table,
                        const int32_t* cu_seqlens, const int32_t* kv_lens, int n_seq, int total,
@@ -461,7 +467,7 @@ struct PagedWorkspace {
   PagedWorkspace(bool decode, int d) {
     const size_t ctas = decode ? 2 * kPagedMaxSms : kPagedMaxSms;
     const size_t rows = 2 * ctas * (decode ? kPagedRows : kPagedTileRows);
-    ml = ctas * sizeof(int4);
+    ml = 2 * ctas * sizeof(int4);
     o = ml + rows * sizeof(float2);
     bytes = o + rows * d * sizeof(float);
   }
@@ -486,7 +492,7 @@ attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
   if (!rotary_ok(table, rot, n_axes, d)) return ATTN_ERR_INVALID_ARG;
   if (pos_batches != 1 && pos_batches != B) return ATTN_ERR_INVALID_ARG;
   if (!strides_ok(strides, k != nullptr ? 12 : 6)) return ATTN_ERR_INVALID_ARG;
-  if (B > 65535 || (int64_t)Hq + Hkv > 65535 || N > (1 << 28)) return ATTN_ERR_INVALID_ARG;
+  if (B > 65535 || ((int64_t)Hq + Hkv) * N > 0x7FFFFFFF) return ATTN_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;
   attn_status st = device_info(&di);
   if (st != ATTN_OK) return st;
@@ -536,7 +542,7 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
   attn_status st = paged_args(k_pages, v_pages, block_table, cu_seqlens, kv_lens, n_seq, total,
                               n_pages, page, max_pages, q != nullptr ? Hq : Hkv, Hkv);
   if (st != ATTN_OK) return st;
-  if (2 * (int64_t)Hkv + Hq > 65535 || total > (1 << 28)) return ATTN_ERR_INVALID_ARG;
+  if ((2 * (int64_t)Hkv + Hq) * total > 0x7FFFFFFF) return ATTN_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
   if (st != ATTN_OK) return st;
@@ -562,7 +568,7 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
   p.n_seq = n_seq;
   p.max_pages = max_pages;
   p.n_pages = n_pages;
-  p.page = page;
+  p.page_log2 = log2_of(page);
   p.total = total;
   p.Hq = Hq;
   p.Hkv = Hkv;
@@ -618,8 +624,7 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   p.max_q = max_q;
   p.n_pages = n_pages;
   p.page = page;
-  p.page_log2 = 0;
-  while ((1 << p.page_log2) < page) ++p.page_log2;
+  p.page_log2 = log2_of(page);
   p.max_pages = max_pages;
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
@@ -635,6 +640,7 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   p.min_share = 2;
   const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
   a.grid = decode ? 2 * sms : sms;
+  a.rows = decode ? max_q * p.G : kPagedTileRows;
   a.stream = static_cast<cudaStream_t>(stream);
   // the units of the largest batch of these sizes, per CTA, stay in 31 bits
   const int64_t blocks = (int64_t)max_pages * page / kPagedUnitKeys + 2;

@@ -48,9 +48,10 @@ struct PagedParams {
   const int* block_table;   // [n_seq, max_pages]
   const int* cu_seqlens;    // [n_seq + 1]
   const int* kv_lens;       // [n_seq], new tokens included
-  int4* desc;               // [grid] (sequence, key/value head, tile, parts); parts 0: none
+  int4* desc;               // [grid][2] of the item the CTA began and others continue: parts
+                            // (0: none), key/value head, first token; s0, qlen of its sequence
   float* part_ml;           // [grid][2][rows][2]
-  float* part_o;            // [grid][2][D / 4][rows][4]
+  float* part_o;            // [grid][2][rows][D], of the tile kernel [grid][2][D / 4][rows][4]
   int n_seq, total, max_q, n_pages, page, page_log2, max_pages, Hkv, G;
   int causal;               // query i of n sees keys j <= i + kv_len - n
   int min_share;            // least cost units per CTA
@@ -63,6 +64,7 @@ struct PagedLaunch {
   CUtensorMap tmK, tmV;     // [n_pages * Hkv, page, D]
   PagedParams params;
   int grid;                 // CTAs of the main kernel
+  int rows;                 // rows of an item at most
   cudaStream_t stream;
 };
 
@@ -159,11 +161,6 @@ __device__ __forceinline__ PagedStart paged_partition(const PagedParams& p, Head
   }
   __syncthreads();
   return start;
-}
-
-// Element offset of a row's four columns 4 c4.. in a partial O of `rows` rows.
-__device__ __forceinline__ size_t part_at(int c4, int r, int rows) {
-  return ((size_t)c4 * rows + r) * 4;
 }
 
 #endif  // __CUDACC__

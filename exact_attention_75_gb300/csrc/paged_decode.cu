@@ -22,7 +22,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = kPagedBlock;
-constexpr int kBoxBytes = kKeys * 128;   // one 64-column chunk of a block's K or V
+constexpr int kMeet = 4;                // rows that meet in shared memory at a time
+constexpr int kBoxBytes = kKeys * 128;  // one 64-column chunk of a block's K or V
 
 template <int D>
 struct PagedDecodeLayout {
@@ -30,14 +31,14 @@ struct PagedDecodeLayout {
   static constexpr int kSlotBytes = 2 * kChunks * kBoxBytes;  // K chunks, then V chunks
   static constexpr int kSlots = D == 64 ? 6 : 3;              // ring depth of each warp
   static constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
-  // After an item's keys the ring holds each warp's O (16 rows, padded), m and l.
+  // Where the warps' results meet: kMeet rows of O each (padded), m and l.
   static constexpr int kRowStride = D + 4;
-  static constexpr int kRedBytes = kWarps * 16 * (kRowStride + 2) * 4;
-  static_assert(kRingBytes >= kRedBytes && kRingBytes % 1024 == 0, "ring layout");
-  static constexpr int kBarOff = kRingBytes;  // one mbarrier per slot
+  static constexpr int kMeetOff = kRingBytes;
+  static constexpr int kMlOff = kMeetOff + kWarps * kMeet * kRowStride * 4;
+  static constexpr int kBarOff = kMlOff + kWarps * kMeet * 8;  // one mbarrier per slot
   static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;
   static constexpr int kBytes = kFlagOff + 16 + 1024;  // + room to align the base
-  static_assert(kBytes <= 113 * 1024, "two CTAs per SM");
+  static_assert(kRingBytes % 1024 == 0 && kBytes + 256 <= 113 * 1024, "two CTAs per SM");
 };
 
 // Byte offset of 16-byte piece `piece` of row `row` in a staged block.
@@ -51,8 +52,54 @@ __device__ __forceinline__ int key_units(const PagedSeq& s) {
   return (s.klen + kPagedUnitKeys - 1) / kPagedUnitKeys;
 }
 
+// A walk along the CTA's share, one piece (an item, or the part of one that
+// the share holds) at a time.
+struct Walk {
+  int left;       // units still to take, the current piece included
+  int b, head;    // item: sequence, key/value head
+  PagedSeq sq;
+  int nku;        // the item's key units
+  int u0, u1;     // those of the piece
+  int take;       // units of the piece
+  int nbw;        // 16-key blocks of the piece that this warp takes
+
+  __device__ __forceinline__ void piece(int warp) {
+    take = min(nku + 1 - u0, left);
+    u1 = min(u0 + take, nku);
+    const int keys = min(u1 * kPagedUnitKeys, sq.klen) - u0 * kPagedUnitKeys;
+    const int nb = (max(keys, 0) + kKeys - 1) / kKeys;
+    nbw = nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;
+  }
+  __device__ __forceinline__ void start(const PagedParams& p, const PagedStart& st, int warp) {
+    left = (int)st.left;
+    b = st.b;
+    head = st.item;
+    u0 = st.unit;
+    sq = paged_seq(p, b);
+    nku = key_units(sq);
+    piece(warp);
+  }
+  __device__ __forceinline__ void advance(const PagedParams& p, int warp) {
+    left -= take;
+    if (left <= 0) return;
+    u0 = 0;
+    if (++head == p.Hkv) {
+      head = 0;
+      do {
+        sq = paged_seq(p, ++b);
+      } while (sq.qlen == 0 && b + 1 < p.n_seq);
+      nku = key_units(sq);
+    }
+    piece(warp);
+  }
+  // First key of the warp's block j.
+  __device__ __forceinline__ int key0(int warp, int j) const {
+    return u0 * kPagedUnitKeys + (warp + j * kWarps) * kKeys;
+  }
+};
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
   using L = PagedDecodeLayout<D>;
@@ -72,7 +119,9 @@ __global__ void __launch_bounds__(kThreads)
     *abort_flag = 0;
     for (int i = 0; i < kWarps * NS; ++i) mbar_init(sbase + L::kBarOff + 8u * i, 1);
     mbar_fence_init();
-    p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   const PagedStart st = paged_partition<kThreads>(
       p, [&](const PagedSeq& s) { return s.qlen == 0 ? 0LL : key_units(s) + 1LL; },
@@ -81,262 +130,248 @@ __global__ void __launch_bounds__(kThreads)
         at.unit = (int)(off % (key_units(s) + 1));
       });
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
-
-  long long left = st.left;
-  int b = st.b;
-  PagedSeq sq = paged_seq(p, b);
-  int nku = key_units(sq);
-  int head = st.item, u0 = st.unit;
-  uint32_t it = 0;  // blocks this warp has taken from its ring
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
-  while (left > 0) {
-    const int take = (int)min((long long)(nku + 1 - u0), left);
-    const int u1 = min(u0 + take, nku);  // this share's key units [u0, u1)
-    left -= take;
-    if (u1 > u0 || nku == 0) {
-      const int k_lo = u0 * kPagedUnitKeys;
-      const int k_hi = min(u1 * kPagedUnitKeys, sq.klen);
-      const int nb = (k_hi - k_lo + kKeys - 1) / kKeys;
-      const int nbw = nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;  // this warp's blocks
-      const int rows = min(kPagedRows, sq.qlen * p.G);
-      const int* pages = p.block_table + (size_t)b * p.max_pages;
+  Walk w;
+  w.left = 0;
+  if (st.left > 0) w.start(p, st, warp);
 
-      // Block j of this warp in this item -> ring slot (it + j) % NS (lane 0 only).
-      auto issue = [&](int j) {
-        const int s = (int)((it + (uint32_t)j) % NS);
-        const uint32_t dk = ring + (uint32_t)(s * L::kSlotBytes);
-        const uint32_t dv = dk + L::kChunks * kBoxBytes;
-        const int key0 = k_lo + (warp + j * kWarps) * kKeys;
-        const int page = __ldg(pages + (key0 >> p.page_log2));
-        const bool ok = page >= 0 && page < p.n_pages;
-        if (!ok)
-          atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(b, 0xFFFF) << 16));
-        const int z = ok ? page * p.Hkv + head : -1;  // -1: the box reads zeros
-        const int y = key0 & (p.page - 1);
-        mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
+  // The warp's stream of blocks runs over the pieces without a break: ahead
+  // walks it as far as the ring reaches, the page of its next block already
+  // read.  issued, it: blocks issued to and taken from the ring.
+  Walk ahead = w;
+  int aj = 0, apage = -1;
+  uint32_t issued = 0, it = 0;
+  auto find_next = [&]() {  // settles ahead on its next block, or on left <= 0
+    while (ahead.left > 0 && aj >= ahead.nbw) {
+      ahead.advance(p, warp);
+      aj = 0;
+    }
+    if (ahead.left > 0)
+      apage = __ldg(p.block_table + (size_t)ahead.b * p.max_pages +
+                    (ahead.key0(warp, aj) >> p.page_log2));
+  };
+  auto issue = [&]() {
+    if (ahead.left <= 0) return;
+    if (lane == 0) {
+      const int s = (int)(issued % NS);
+      const uint32_t dk = ring + (uint32_t)(s * L::kSlotBytes);
+      const uint32_t dv = dk + L::kChunks * kBoxBytes;
+      const bool ok = apage >= 0 && apage < p.n_pages;
+      if (!ok)
+        atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(ahead.b, 0xFFFF) << 16));
+      const int z = ok ? apage * p.Hkv + ahead.head : -1;  // -1: the box reads zeros
+      const int y = ahead.key0(warp, aj) & (p.page - 1);
+      mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
 #pragma unroll
-        for (int c = 0; c < L::kChunks; ++c) {
-          tma_load_3d(dk + c * kBoxBytes, &tmK, bar(s), c * 64, y, z);
-          tma_load_3d(dv + c * kBoxBytes, &tmV, bar(s), c * 64, y, z);
-        }
-      };
-      int issued = min(nbw, NS);
-      if (lane == 0)
-        for (int j = 0; j < issued; ++j) issue(j);
-
-      // Row r of the item: new token r / G, query head r % G of the group.
-      auto grow = [&](int r) -> size_t {
-        const int i = r / p.G, h = r - i * p.G;
-        return (size_t)(head * p.G + h) * p.total + sq.s0 + i;
-      };
-      const int r0 = lane >> 2, cq = 2 * (lane & 3);
-      const uint16_t* qa_ = static_cast<const uint16_t*>(p.q) + (r0 < rows ? grow(r0) * D : 0);
-      const uint16_t* qb_ =
-          static_cast<const uint16_t*>(p.q) + (r0 + 8 < rows ? grow(r0 + 8) * D : 0);
-      uint32_t qa[KS][4];
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int c = 16 * ks + cq;
-        qa[ks][0] = r0 < rows ? *reinterpret_cast<const uint32_t*>(qa_ + c) : 0u;
-        qa[ks][1] = r0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(qb_ + c) : 0u;
-        qa[ks][2] = r0 < rows ? *reinterpret_cast<const uint32_t*>(qa_ + c + 8) : 0u;
-        qa[ks][3] = r0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(qb_ + c + 8) : 0u;
+      for (int c = 0; c < L::kChunks; ++c) {
+        tma_load_3d(dk + c * kBoxBytes, &tmK, bar(s), c * 64, y, z);
+        tma_load_3d(dv + c * kBoxBytes, &tmV, bar(s), c * 64, y, z);
       }
-      // Last key each of the thread's two rows sees (-1: a padding row, or
-      // one before the first key).
-      auto last_key = [&](int r) {
-        if (r >= rows) return -1;
-        const int lim = p.causal ? r / p.G + sq.klen - sq.qlen : sq.klen - 1;
-        return min(lim, k_hi - 1);
-      };
-      const int limA = last_key(r0), limB = last_key(r0 + 8);
-      const bool hiB = rows > 8;
+    }
+    ++issued;
+    ++aj;
+    find_next();
+  };
+  find_next();
+  for (int i = 0; i < NS; ++i) issue();
 
-      float o[DN][4];
+  float* meet = reinterpret_cast<float*>(smem + L::kMeetOff);
+  float2* meet_ml = reinterpret_cast<float2*>(smem + L::kMlOff);  // [kWarps][kMeet]
+
+  for (; w.left > 0; w.advance(p, warp)) {
+    if (w.u1 == w.u0 && w.nku > 0) continue;  // the item's last unit alone: no keys
+    const PagedSeq sq = w.sq;
+    const int rows = min(kPagedRows, sq.qlen * p.G);
+    // Row r of the item: new token r / G, query head r % G of the group.
+    auto grow = [&](int r) -> size_t {
+      const int i = r / p.G, h = r - i * p.G;
+      return (size_t)(w.head * p.G + h) * p.total + sq.s0 + i;
+    };
+    const int r0 = lane >> 2, cq = 2 * (lane & 3);
+    const uint16_t* qa_ = static_cast<const uint16_t*>(p.q) + (r0 < rows ? grow(r0) * D : 0);
+    const uint16_t* qb_ =
+        static_cast<const uint16_t*>(p.q) + (r0 + 8 < rows ? grow(r0 + 8) * D : 0);
+    uint32_t qa[KS][4];
 #pragma unroll
-      for (int dn = 0; dn < DN; ++dn) o[dn][0] = o[dn][1] = o[dn][2] = o[dn][3] = 0.f;
-      float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
-      int j = 0;
-      bool aborted = false;
+    for (int ks = 0; ks < KS; ++ks) {
+      const int c = 16 * ks + cq;
+      qa[ks][0] = r0 < rows ? *reinterpret_cast<const uint32_t*>(qa_ + c) : 0u;
+      qa[ks][1] = r0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(qb_ + c) : 0u;
+      qa[ks][2] = r0 < rows ? *reinterpret_cast<const uint32_t*>(qa_ + c + 8) : 0u;
+      qa[ks][3] = r0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(qb_ + c + 8) : 0u;
+    }
+    // Last key each of the thread's two rows sees (-1: a padding row, or one
+    // before the first key).
+    auto last_key = [&](int r) {
+      if (r >= rows) return -1;
+      return min(p.causal ? r / p.G + sq.klen - sq.qlen : sq.klen, sq.klen - 1);
+    };
+    const int limA = last_key(r0), limB = last_key(r0 + 8);
+    const bool hiB = rows > 8;
+
+    float o[DN][4];
+#pragma unroll
+    for (int dn = 0; dn < DN; ++dn) o[dn][0] = o[dn][1] = o[dn][2] = o[dn][3] = 0.f;
+    float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+    bool aborted = false;
 #pragma unroll 1
-      for (; j < nbw; ++j) {
-        const uint32_t n = it + (uint32_t)j;
-        const int s = (int)(n % NS);
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(s), (n / NS) & 1, wd, 65))) {
-          aborted = true;
-          break;
+    for (int j = 0; j < w.nbw; ++j) {
+      const int s = (int)(it % NS);
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(s), (it / NS) & 1, wd, 65))) {
+        aborted = true;
+        break;
+      }
+      ++it;
+      const uint32_t tk = ring + (uint32_t)(s * L::kSlotBytes);
+      const uint32_t tv = tk + L::kChunks * kBoxBytes;
+      const int key0 = w.key0(warp, j);
+      if (key0 + kKeys > sq.klen) {
+        // Rows past the sequence's last key hold whatever the page held (P is
+        // 0 there, but 0 x NaN is not): zero those rows of V.
+        const int dead = key0 + kKeys - sq.klen;
+        for (int i = lane; i < dead * 8 * L::kChunks; i += 32) {
+          const int row = kKeys - 1 - i / (8 * L::kChunks), pc = i % (8 * L::kChunks);
+          *reinterpret_cast<uint4*>(smem + (tv - sbase) + sw_off(row, pc)) =
+              make_uint4(0u, 0u, 0u, 0u);
         }
-        const uint32_t tk = ring + (uint32_t)(s * L::kSlotBytes);
-        const uint32_t tv = tk + L::kChunks * kBoxBytes;
-        const int key0 = k_lo + (warp + j * kWarps) * kKeys;
-        if (key0 + kKeys > sq.klen) {
-          // Rows past the sequence's last key hold whatever the page held
-          // (P is 0 there, but 0 x NaN is not): zero those rows of V.
-          const int dead = key0 + kKeys - sq.klen;
-          for (int i = lane; i < dead * 8 * L::kChunks; i += 32) {
-            const int row = kKeys - 1 - i / (8 * L::kChunks), pc = i % (8 * L::kChunks);
-            *reinterpret_cast<uint4*>(smem + (tv - sbase) + sw_off(row, pc)) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          __syncwarp();
-        }
-
-        float sc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ks += 2) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            uint32_t bm[4];
-            ldsm_x4(tk + sw_off(8 * nt + (lane & 7), 2 * ks + (lane >> 3)), bm);
-            mma16816<BF16>(sc[nt], qa[ks], bm[0], bm[1]);
-            mma16816<BF16>(sc[nt], qa[ks + 1], bm[2], bm[3]);
-          }
-        }
-
-        // Online softmax.  sc[nt][e]: row r0 (e < 2) or r0 + 8, key key0 + 8 nt + cq + e % 2.
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = key0 + 8 * nt + cq + (e & 1);
-            const float x = sc[nt][e] * p.scale_log2;
-            sc[nt][e] = key <= (e < 2 ? limA : limB) ? x : -INFINITY;
-          }
-        float bA = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-        bA = fmaxf(bA, __shfl_xor_sync(0xffffffffu, bA, 1));
-        bA = fmaxf(bA, __shfl_xor_sync(0xffffffffu, bA, 2));
-        const float nA = fmaxf(mA, bA);
-        const float alphaA = nA == mA ? 1.f : ex2_approx(mA - nA);
-        const float uA = nA == -INFINITY ? 0.f : nA;
-        mA = nA;
-        float psA = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            sc[nt][e] = ex2_approx(sc[nt][e] - uA);
-            psA += sc[nt][e];
-          }
-        lA = lA * alphaA + psA;
-        float alphaB = 1.f;
-        if (hiB) {
-          float bB = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-          bB = fmaxf(bB, __shfl_xor_sync(0xffffffffu, bB, 1));
-          bB = fmaxf(bB, __shfl_xor_sync(0xffffffffu, bB, 2));
-          const float nB = fmaxf(mB, bB);
-          alphaB = nB == mB ? 1.f : ex2_approx(mB - nB);
-          const float uB = nB == -INFINITY ? 0.f : nB;
-          mB = nB;
-          float psB = 0.f;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 2; e < 4; ++e) {
-              sc[nt][e] = ex2_approx(sc[nt][e] - uB);
-              psB += sc[nt][e];
-            }
-          lB = lB * alphaB + psB;
-        }
-        if (__any_sync(0xffffffffu, alphaA != 1.f || alphaB != 1.f)) {
-#pragma unroll
-          for (int dn = 0; dn < DN; ++dn) {
-            o[dn][0] *= alphaA;
-            o[dn][1] *= alphaA;
-            o[dn][2] *= alphaB;
-            o[dn][3] *= alphaB;
-          }
-        }
-
-        // O += P V
-        uint32_t pa[4];
-        pa[0] = pack2<BF16>(sc[0][0], sc[0][1]);
-        pa[1] = hiB ? pack2<BF16>(sc[0][2], sc[0][3]) : 0u;
-        pa[2] = pack2<BF16>(sc[1][0], sc[1][1]);
-        pa[3] = hiB ? pack2<BF16>(sc[1][2], sc[1][3]) : 0u;
-        const int vrow = 8 * ((lane >> 3) & 1) + (lane & 7);
-#pragma unroll
-        for (int dn = 0; dn < DN; dn += 2) {
-          uint32_t bm[4];
-          ldsm_x4_trans(tv + sw_off(vrow, dn + (lane >> 4)), bm);
-          mma16816<BF16>(o[dn], pa, bm[0], bm[1]);
-          mma16816<BF16>(o[dn + 1], pa, bm[2], bm[3]);
-        }
-
-        // The slot is read: refill it with this warp's block j + NS.
+        fence_proxy_async_smem();  // before the slot's next copy
         __syncwarp();
-        if (issued < nbw) {
-          if (lane == 0) {
-            fence_proxy_async_smem();
-            issue(issued);
+      }
+
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks += 2) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t bm[4];
+          ldsm_x4(tk + sw_off(8 * nt + (lane & 7), 2 * ks + (lane >> 3)), bm);
+          mma16816<BF16>(sc[nt], qa[ks], bm[0], bm[1]);
+          mma16816<BF16>(sc[nt], qa[ks + 1], bm[2], bm[3]);
+        }
+      }
+
+      // Online softmax.  sc[nt][e]: row r0 (e < 2) or r0 + 8, key key0 + 8 nt + cq + e % 2.
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + 8 * nt + cq + (e & 1);
+          const float x = sc[nt][e] * p.scale_log2;
+          sc[nt][e] = key <= (e < 2 ? limA : limB) ? x : -INFINITY;
+        }
+      float bA = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      bA = fmaxf(bA, __shfl_xor_sync(0xffffffffu, bA, 1));
+      bA = fmaxf(bA, __shfl_xor_sync(0xffffffffu, bA, 2));
+      const float nA = fmaxf(mA, bA);
+      const float alphaA = nA == mA ? 1.f : ex2_approx(mA - nA);
+      const float uA = nA == -INFINITY ? 0.f : nA;
+      mA = nA;
+      float psA = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sc[nt][e] = ex2_approx(sc[nt][e] - uA);
+          psA += sc[nt][e];
+        }
+      lA = lA * alphaA + psA;
+      float alphaB = 1.f;
+      if (hiB) {
+        float bB = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+        bB = fmaxf(bB, __shfl_xor_sync(0xffffffffu, bB, 1));
+        bB = fmaxf(bB, __shfl_xor_sync(0xffffffffu, bB, 2));
+        const float nB = fmaxf(mB, bB);
+        alphaB = nB == mB ? 1.f : ex2_approx(mB - nB);
+        const float uB = nB == -INFINITY ? 0.f : nB;
+        mB = nB;
+        float psB = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 2; e < 4; ++e) {
+            sc[nt][e] = ex2_approx(sc[nt][e] - uB);
+            psB += sc[nt][e];
           }
-          ++issued;
-        }
+        lB = lB * alphaB + psB;
       }
-      if (aborted) {
-        // Every copy this warp issued must land before the CTA may exit or
-        // reuse the ring.
-        Watchdog dw = wd;
-        volatile int never = 0;
-        dw.abort_flag = &never;
-        dw.limit_ns = drain_limit_ns(wd.limit_ns);
-        for (int jj = j; jj < issued; ++jj) {
-          const uint32_t n = it + (uint32_t)jj;
-          mbar_wait(bar((int)(n % NS)), (n / NS) & 1, dw, 66);
-        }
-      }
-      it += (uint32_t)nbw;
-
-      lA += __shfl_xor_sync(0xffffffffu, lA, 1);
-      lA += __shfl_xor_sync(0xffffffffu, lA, 2);
-      lB += __shfl_xor_sync(0xffffffffu, lB, 1);
-      lB += __shfl_xor_sync(0xffffffffu, lB, 2);
-
-      // Combine the warps: each writes its (O, m, l) over the (now idle) ring.
-      __syncthreads();
-      if (*abort_flag != 0) break;  // the same for every thread: no wait runs until the next item
-      float* red = reinterpret_cast<float*>(smem);
-      float* rm = red + kWarps * 16 * L::kRowStride;  // [kWarps][16]
-      float* rl = rm + kWarps * 16;                   // [kWarps][16]
-      {
-        float* ro = red + warp * 16 * L::kRowStride;
+      if (__any_sync(0xffffffffu, alphaA != 1.f || alphaB != 1.f)) {
 #pragma unroll
         for (int dn = 0; dn < DN; ++dn) {
-          *reinterpret_cast<float2*>(ro + r0 * L::kRowStride + 8 * dn + cq) =
-              make_float2(o[dn][0], o[dn][1]);
-          *reinterpret_cast<float2*>(ro + (r0 + 8) * L::kRowStride + 8 * dn + cq) =
-              make_float2(o[dn][2], o[dn][3]);
-        }
-        if ((lane & 3) == 0) {
-          rm[warp * 16 + r0] = mA;
-          rm[warp * 16 + r0 + 8] = mB;
-          rl[warp * 16 + r0] = lA;
-          rl[warp * 16 + r0 + 8] = lB;
+          o[dn][0] *= alphaA;
+          o[dn][1] *= alphaA;
+          o[dn][2] *= alphaB;
+          o[dn][3] *= alphaB;
         }
       }
-      __syncthreads();
 
-      const bool whole = u0 == 0 && u1 == nku;
-      const size_t slot = 2 * (size_t)blockIdx.x + (u0 == 0 ? 1 : 0);
-      if (!whole && u0 == 0 && threadIdx.x == 0)
-        p.desc[blockIdx.x] =
-            make_int4(b, head, 0, 1 + (int)((nku - u1 + st.share - 1) / st.share));
-      for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
-        const int r = idx / (D / 4), c4 = idx % (D / 4);
+      // O += P V
+      uint32_t pa[4];
+      pa[0] = pack2<BF16>(sc[0][0], sc[0][1]);
+      pa[1] = hiB ? pack2<BF16>(sc[0][2], sc[0][3]) : 0u;
+      pa[2] = pack2<BF16>(sc[1][0], sc[1][1]);
+      pa[3] = hiB ? pack2<BF16>(sc[1][2], sc[1][3]) : 0u;
+      const int vrow = 8 * ((lane >> 3) & 1) + (lane & 7);
+#pragma unroll
+      for (int dn = 0; dn < DN; dn += 2) {
+        uint32_t bm[4];
+        ldsm_x4_trans(tv + sw_off(vrow, dn + (lane >> 4)), bm);
+        mma16816<BF16>(o[dn], pa, bm[0], bm[1]);
+        mma16816<BF16>(o[dn + 1], pa, bm[2], bm[3]);
+      }
+
+      // The slot is read: refill it with the next block of the stream.
+      __syncwarp();
+      if (lane == 0) fence_proxy_async_smem();
+      issue();
+    }
+    // The warps leave together when one has given up; the barrier also frees
+    // the meeting place from the piece before.
+    if (__syncthreads_or(aborted)) break;
+
+    lA += __shfl_xor_sync(0xffffffffu, lA, 1);
+    lA += __shfl_xor_sync(0xffffffffu, lA, 2);
+    lB += __shfl_xor_sync(0xffffffffu, lB, 1);
+    lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+
+    // The warps' (O, m, l) meet in shared memory, kMeet rows at a time.
+    const bool whole = w.u0 == 0 && w.u1 == w.nku;
+    const size_t slot = 2 * (size_t)blockIdx.x + (w.u0 == 0 ? 1 : 0);
+    if (!whole && w.u0 == 0 && threadIdx.x == 0) {
+      p.desc[2 * blockIdx.x] =
+          make_int4(1 + (int)((w.nku - w.u1 + st.share - 1) / st.share), w.head, 0, 0);
+      p.desc[2 * blockIdx.x + 1] = make_int4(sq.s0, sq.qlen, 0, 0);
+    }
+    for (int pass = 0; pass * kMeet < rows; ++pass) {
+      if (pass > 0) __syncthreads();
+      if ((r0 >> 2) == (pass & 1)) {
+        float* ro = meet + (warp * kMeet + (r0 & 3)) * L::kRowStride + cq;
+#pragma unroll
+        for (int dn = 0; dn < DN; ++dn)
+          *reinterpret_cast<float2*>(ro + 8 * dn) =
+              pass < 2 ? make_float2(o[dn][0], o[dn][1]) : make_float2(o[dn][2], o[dn][3]);
+        if ((lane & 3) == 0)
+          meet_ml[warp * kMeet + (r0 & 3)] = pass < 2 ? make_float2(mA, lA) : make_float2(mB, lB);
+      }
+      __syncthreads();
+      for (int idx = threadIdx.x; idx < kMeet * (D / 4); idx += kThreads) {
+        const int mr = idx / (D / 4), c = idx % (D / 4) * 4;
+        const int r = pass * kMeet + mr;
+        if (r >= rows) break;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, rm[w * 16 + r]);
+        for (int k = 0; k < kWarps; ++k) M = fmaxf(M, meet_ml[k * kMeet + mr].x);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float lsum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = rm[w * 16 + r];
-          const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-          lsum += f * rl[w * 16 + r];
+        for (int k = 0; k < kWarps; ++k) {
+          const float2 ml = meet_ml[k * kMeet + mr];
+          const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+          lsum += f * ml.y;
           const float4 x =
-              *reinterpret_cast<const float4*>(red + (w * 16 + r) * L::kRowStride + 4 * c4);
+              *reinterpret_cast<const float4*>(meet + (k * kMeet + mr) * L::kRowStride + c);
           acc.x += f * x.x;
           acc.y += f * x.y;
           acc.z += f * x.z;
@@ -345,30 +380,24 @@ __global__ void __launch_bounds__(kThreads)
         if (whole) {
           const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
           const size_t gr = grow(r);
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + 4 * c4) =
-              make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv),
-                         pack2<BF16>(acc.z * inv, acc.w * inv));
-          if (c4 == 0)
-            p.lse[gr] = lsum > 0.f ? (M + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + c) = make_uint2(
+              pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+          if (c == 0) p.lse[gr] = lsum > 0.f ? (M + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
         } else {
-          *reinterpret_cast<float4*>(p.part_o + slot * 16 * D + part_at(c4, r, 16)) = acc;
-          if (c4 == 0)
-            *reinterpret_cast<float2*>(p.part_ml + (slot * 16 + r) * 2) = make_float2(M, lsum);
+          *reinterpret_cast<float4*>(p.part_o + (slot * kPagedRows + r) * D + c) = acc;
+          if (c == 0)
+            *reinterpret_cast<float2*>(p.part_ml + (slot * kPagedRows + r) * 2) =
+                make_float2(M, lsum);
         }
       }
-      fence_proxy_async_smem();  // the ring is refilled by TMA in the next item
-      __syncthreads();
-    }
-    // the next item
-    u0 = 0;
-    if (left > 0 && ++head == p.Hkv) {
-      head = 0;
-      do {
-        sq = paged_seq(p, ++b);
-      } while (sq.qlen == 0 && b + 1 < p.n_seq);
-      nku = key_units(sq);
     }
   }
+  // After an abort, copies still on their way must land before the CTA exits.
+  Watchdog dw = wd;
+  volatile int never = 0;
+  dw.abort_flag = &never;
+  dw.limit_ns = drain_limit_ns(wd.limit_ns);
+  for (; it < issued; ++it) mbar_wait(bar((int)(it % NS)), (it / NS) & 1, dw, 66);
   asm volatile("griddepcontrol.launch_dependents;");
 }
 

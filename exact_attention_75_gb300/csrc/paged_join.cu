@@ -41,66 +41,74 @@ __device__ __forceinline__ void add(Sum& s, float m, float l, const float4& o) {
 }
 
 // ROWS: rows of an item's partial result (kPagedRows: the decoding kernel;
-// 256: a pair of query tiles).
+// kPagedTileRows: a pair of query tiles).
 template <int D, bool BF16, int ROWS>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr bool kDecode = ROWS == kPagedRows;
   constexpr int kWays = kDecode ? 4 : 1;  // warps that share a segment's parts
   constexpr int kSegs = ROWS * (D / 4) / 32;
-  const int4 item = p.desc[blockIdx.x];
-  const int parts = item.w;
-  if (parts == 0) return;
   __shared__ Sum meet[kDecode ? kThreads : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const PagedSeq sq = paged_seq(p, item.x);
   const int way = warp % kWays;
-  for (int s0 = blockIdx.y * (kWarps / kWays); s0 < kSegs; s0 += gridDim.y * (kWarps / kWays)) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 item = p.desc[2 * blockIdx.x], seq = p.desc[2 * blockIdx.x + 1];
+  const int parts = item.x;
+  if (parts == 0) return;
+  // decoding: the grid covers the live segments in one round
+  const int segs = kDecode ? (int)gridDim.y * (kWarps / kWays) : kSegs;
+  for (int s0 = blockIdx.y * (kWarps / kWays); s0 < segs; s0 += gridDim.y * (kWarps / kWays)) {
     const int seg = s0 + warp / kWays;
     const int e = min(seg, kSegs - 1) * 32 + lane;
-    const int r = e % ROWS, c4 = e / ROWS;
+    int r, c4, token, head;  // row of the item, columns; token of the sequence, head of the group
+    if constexpr (kDecode) {
+      r = e / (D / 4);
+      c4 = e % (D / 4);
+      token = r / p.G;
+      head = r - token * p.G;
+    } else {
+      r = e % ROWS;
+      c4 = e / ROWS;
+      const int TT = 128 / p.G;
+      head = (r & 127) / TT;
+      token = item.z + (r >> 7) * TT + (r & 127) - head * TT;
+    }
+    const bool live = seg < kSegs && head < p.G && token < seq.y;
     Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int k0 = way * kFlight; k0 < parts; k0 += kWays * kFlight) {
+    for (int k0 = way * kFlight; live && k0 < parts; k0 += kWays * kFlight) {
       float2 ml[kFlight];
       float4 o[kFlight];
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
-        const int k = min(k0 + i, parts - 1);
+        if (k0 + i >= parts) break;
+        const int k = k0 + i;
         const size_t slot = 2 * ((size_t)blockIdx.x + k) + (k == 0 ? 1 : 0);
         ml[i] = *reinterpret_cast<const float2*>(p.part_ml + (slot * ROWS + r) * 2);
         o[i] = *reinterpret_cast<const float4*>(p.part_o + slot * ROWS * D + (size_t)e * 4);
       }
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i)
+      for (int i = 0; i < kFlight; ++i) {
+        if (k0 + i >= parts) break;
         // a part with no key for the row holds no O
-        if (k0 + i < parts && ml[i].x != -INFINITY) add(s, ml[i].x, ml[i].y, o[i]);
+        if (ml[i].x != -INFINITY) add(s, ml[i].x, ml[i].y, o[i]);
+      }
     }
     if constexpr (kDecode) {
-      meet[threadIdx.x] = s;
-      __syncthreads();
-      if (way == 0) {
+      if (parts > kFlight) {  // the other warps have some
+        meet[threadIdx.x] = s;
+        __syncthreads();
+        if (way == 0) {
 #pragma unroll
-        for (int w = 1; w < kWays; ++w) {
-          const Sum& x = meet[threadIdx.x + 32 * w];
-          add(s, x.m, x.l, x.o);
+          for (int w = 1; w < kWays; ++w) {
+            const Sum& x = meet[threadIdx.x + 32 * w];
+            add(s, x.m, x.l, x.o);
+          }
         }
+        __syncthreads();
       }
-      __syncthreads();
       if (way != 0) continue;
     }
-    int token, head;  // of the sequence, of the group
-    bool live = seg < kSegs;
-    if constexpr (kDecode) {
-      token = r / p.G;
-      head = r - token * p.G;
-    } else {
-      const int TT = 128 / p.G;
-      head = (r & 127) / TT;
-      token = (2 * item.z + (r >> 7)) * TT + (r & 127) - head * TT;
-      live = live && head < p.G;
-    }
-    if (!live || token >= sq.qlen) continue;
-    const size_t gr = (size_t)(item.y * p.G + head) * p.total + sq.s0 + token;
+    if (!live) continue;
+    const size_t gr = (size_t)(item.y * p.G + head) * p.total + seq.x + token;
     const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + 4 * c4) = make_uint2(
         pack2<BF16>(s.o.x * inv, s.o.y * inv), pack2<BF16>(s.o.z * inv, s.o.w * inv));
@@ -111,8 +119,9 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedParams 
 template <int D, bool BF16, int ROWS>
 cudaError_t launch_dbr(const PagedLaunch& a) {
   cudaLaunchConfig_t cfg = {};
-  // decoding: every segment at once; tiles: two rounds of segments per CTA
-  const unsigned y = ROWS == kPagedRows ? D / 32 : D / 16;
+  // decoding: every live segment at once, four warps each; tiles: two rounds
+  // of 16 segments per CTA
+  const unsigned y = ROWS == kPagedRows ? (unsigned)(a.rows * (D / 4) + 127) / 128 : D / 16;
   cfg.gridDim = dim3((unsigned)a.grid, y);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = a.stream;

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(L::kKvEmpty + s), 1);
     }
     mbar_fence_init();
-    p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(tmem_holder), 512);
@@ -311,9 +311,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (; w.left > 0; w.advance(p, TT)) {
       const int nbmax = max(w.n[0], w.n[1]);
-      if (nbmax > 0 && w.u0 == 0 && !w.whole() && lane == 0)
-        p.desc[blockIdx.x] = make_int4(w.b, w.head, w.qp,
-                                       1 + (int)((w.nb - w.u1 + st.share - 1) / st.share));
+      if (nbmax > 0 && w.u0 == 0 && !w.whole() && lane == 0) {
+        p.desc[2 * blockIdx.x] = make_int4(1 + (int)((w.nb - w.u1 + st.share - 1) / st.share),
+                                           w.head, 2 * w.qp * TT, 0);
+        p.desc[2 * blockIdx.x + 1] = make_int4(w.sq.s0, w.sq.qlen, 0, 0);
+      }
       if (nbmax == 0) continue;  // the same skip in every role
 #pragma unroll
       for (int t = 0; t < 2; ++t) {

@@ -23,7 +23,7 @@ struct RopeParams {
   const int64_t* table;    // [2, rot / 2]: angle per position (2^-64 turns), axis
   int n_axes, pos_batches; // pos_batches 1: one set of positions for every batch
   int heads[2], N, d, rot;
-  int group_heads;         // heads one block turns
+  int group_heads, head_groups;  // heads one block turns, blocks per run of tokens
   bool inverse;
 };
 
@@ -49,8 +49,8 @@ struct AppendParams {
   const int* positions;    // [n_axes, total]; null: the position in the cache on every axis
   const int64_t* table;    // null: no rotation
   uint32_t* status;
-  int n_axes, n_seq, max_pages, n_pages, page, total, Hq, Hkv, d, rot;
-  int group_heads;
+  int n_axes, n_seq, max_pages, n_pages, page_log2, total, Hq, Hkv, d, rot;
+  int group_heads, head_groups;
 };
 
 struct AppendLaunch {

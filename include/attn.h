@@ -262,7 +262,7 @@ attn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const v
  *   table     : DEVICE int64 [2, rot/2]: f_p in units of 2^-64 turns (radians
  *               / 2 pi, modulo 1 turn), then axis_p (clamped to [0, n_axes)).
  *   rot       : a multiple of 16, 16 <= rot <= d;  1 <= n_axes <= 8.
- * d in {64, 96, 128, 192, 256}; B, Hq + Hkv <= 65535.  Angles are formed
+ * d in {64, 96, 128, 192, 256}; B <= 65535, (Hq + Hkv) * N < 2^31.  Angles are formed
  * modulo a turn in 64-bit integers, so they hold at any position; values are
  * turned in fp32 and rounded once.
  * Cite: "8.3 FlashAttention-3", section 5.2 (the rotary embedding as the
@@ -305,7 +305,8 @@ attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
  *   positions : DEVICE int32 [n_axes, total], or NULL: the position in the
  *               cache on every axis.
  * Two new tokens with one place in the cache (a page shared by two
- * sequences) leave the bytes of either.  d in {64, 96, 128, 192, 256}.
+ * sequences) leave the bytes of either.  d in {64, 96, 128, 192, 256};
+ * (Hq + 2 Hkv) * total < 2^31.
  * Cite: the FlashAttention-2 review, "Insights" and "Discussion Points"
  * (paged key/value caches and decoding from them are named there).
  */

@@ -102,6 +102,21 @@ def test_rope_holds_at_far_positions(attn_lib):
     assert err.max() <= 2 ** -11 * np.abs(ref).max() + 2 ** -20 * 2 * np.abs(to64(q)).max()
 
 
+def test_rope_of_many_rows(attn_lib):
+    """More blocks of rows than a grid's second dimension holds, elements past
+    2^31 bytes; the first, last and some middle rows against the oracle."""
+    N, d, H = 600_000, 256, 4
+    q = torch.empty(1, H, N, d, dtype=torch.bfloat16, device="cuda")
+    q.normal_(generator=torch.Generator("cuda").manual_seed(3))
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")[None]
+    inv, axis = _freq(d, 1)
+    y, _ = attn_lib.rope(q, None, pos, _table(attn_lib, d, 1))
+    at = torch.tensor([0, 1, 524_287, 524_288, 524_300, N - 2, N - 1], device="cuda")
+    for h in (0, H - 1):
+        ref = oracle.rotary(to64(q[0, h, at]), at.cpu().numpy()[None], inv, axis, False)
+        _close(y[0, h, at], ref, q[0, h, at], torch.bfloat16)
+
+
 def test_rope_gradient_by_differences(attn_lib):
     """<dy, rope(x + e) - rope(x - e)> against <rope_bwd(dy), 2 e>: the map is
     linear, so large steps are exact up to the fp16 roundings (2^-11 each)."""
