@@ -450,7 +450,7 @@ attn_status paged_args(const void* k_pages, const void* v_pages, const int32_t* 
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256)
     return ATTN_ERR_UNSUPPORTED;
-  if ((int64_t)max_pages * page > 0x7FFFFF00 || (int64_t)n_pages * Hkv > 0x7FFFFFFF ||
+  if ((int64_t)max_pages * page > 0x7FFF0000 || (int64_t)n_pages * Hkv > 0x7FFFFFFF ||
       (int64_t)n_seq * Hkv > 0x7FFFFFFF || (int64_t)Hq * total > 0x7FFFFFFF)
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
@@ -637,15 +637,15 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   p.desc = reinterpret_cast<int4*>(w);
   p.part_ml = reinterpret_cast<float*>(w + ws.ml);
   p.part_o = reinterpret_cast<float*>(w + ws.o);
-  p.min_share = 2;
+  p.min_share = decode ? 128 : 256;
   const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
   a.grid = decode ? 2 * sms : sms;
   a.rows = decode ? max_q * p.G : kPagedTileRows;
   a.stream = static_cast<cudaStream_t>(stream);
-  // the units of the largest batch of these sizes, per CTA, stay in 31 bits
-  const int64_t blocks = (int64_t)max_pages * page / kPagedUnitKeys + 2;
+  // the largest batch of these sizes stays in 63 bits of keys
+  const int64_t keys = (int64_t)max_pages * page + kPagedOverhead;
   const int64_t items = (((int64_t)total * p.G) / 64 + n_seq) * Hkv;
-  if (blocks > ((int64_t)a.grid << 31) / items) return ATTN_ERR_INVALID_ARG;
+  if (keys > INT64_MAX / items) return ATTN_ERR_INVALID_ARG;
   const int64_t heads = (int64_t)n_pages * Hkv;
   const int box = decode ? kPagedBlock : (page < 128 ? page : 128);
   if (!encode_3d(&a.tmK, k_pages, dt, 2, d, page, heads, 64, box) ||

@@ -3,14 +3,16 @@
 // over a persistent grid, and the partial results).
 //
 // Work.  A sequence with new tokens gives each of its key/value heads a run
-// of items; an item is a tile of query rows, and costs its key blocks plus
-// one (its prologue and epilogue).  All items of the batch laid end to end
-// (sequence, key/value head, tile) form one line of cost units, and CTA c of
-// the grid takes units [c w, (c + 1) w): equal shares whatever the lengths
-// are, so one long sequence spreads over every SM and a ragged batch
-// balances itself.  The lengths live on the device (a captured graph replays
-// with new ones), so each CTA finds its own start by a prefix sum over the
-// sequences.
+// of items; an item is a tile of query rows, and costs the keys they see plus
+// kPagedOverhead (its prologue and epilogue).  All items of the batch laid end
+// to end (sequence, key/value head, tile) form one line, and CTA c of the grid
+// takes [c w, (c + 1) w) of it: equal shares whatever the lengths are, so one
+// long sequence spreads over every SM and a ragged batch balances itself.  A
+// key block belongs to the share that its first key falls in.  The lengths
+// live on the device (a captured graph replays with new ones), so each CTA
+// finds its own start: costs in keys make an item run's cost an arithmetic
+// series (no loop over tiles), and a prefix sum over the sequences does the
+// rest.
 //
 // An item that lies in one CTA's share is finished there.  One that crosses
 // shares leaves a partial result per share: an unnormalised O and the (m, l)
@@ -37,8 +39,8 @@ constexpr int kPagedTileRows = 256;
 constexpr int kPagedBlock = 16;
 // Query heads per key/value head at most.
 constexpr int kPagedMaxGroup = 128;
-// Keys of one cost unit there (16 for each of the four warps).
-constexpr int kPagedUnitKeys = 64;
+// Keys an item's prologue and epilogue cost as much as.
+constexpr int kPagedOverhead = 128;
 
 struct PagedParams {
   const void* q;            // [Hkv * G, total, D]
@@ -54,7 +56,7 @@ struct PagedParams {
   float* part_o;            // [grid][2][rows][D], of the tile kernel [grid][2][D / 4][rows][4]
   int n_seq, total, max_q, n_pages, page, page_log2, max_pages, Hkv, G;
   int causal;               // query i of n sees keys j <= i + kv_len - n
-  int min_share;            // least cost units per CTA
+  int min_share;            // least share, at least one key block
   float scale_log2;         // scale * log2(e)
   unsigned long long wait_limit_ns;
 };
@@ -101,32 +103,90 @@ __device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
     atomicCAS(p.status, 0u, 1u | (63u << 8) | ((uint32_t)min(b, 0xFFFF) << 16));
 }
 
-// Where a CTA's share begins (sequence b, its item counted over the key/value
-// heads, the unit in the item), its units (left 0: none), and the units of a
-// full share.
-struct PagedStart {
-  int b;
-  int item, items_per_head, unit;
-  long long left;
+// Items of one key/value head of a sequence: W new tokens each.
+__device__ __forceinline__ int paged_items(const PagedSeq& s, int W) {
+  return (s.qlen + W - 1) / W;
+}
+
+// Keys that item i's rows see: all klen in the last item (and without causal
+// masking in every one), fewer by the tokens that follow in the others.
+__device__ __forceinline__ int paged_keys(const PagedSeq& s, int W, int causal, int i) {
+  return causal ? max(min((i + 1) * W, s.qlen) + s.klen - s.qlen, 0) : s.klen;
+}
+
+// Cost of a head's items 0 .. q-1, q at most their number.
+__device__ __forceinline__ long long paged_line(const PagedSeq& s, int W, int causal, int q) {
+  long long sum = (long long)q * kPagedOverhead;
+  if (q == 0) return sum;
+  if (!causal) return sum + (long long)q * s.klen;
+  const int koff = s.klen - s.qlen;
+  const int i0 = koff + W > 0 ? 0 : -koff / W;  // the first item that sees a key
+  const long long n = q - 1 - i0;               // items from it up to the one before the last
+  if (n > 0) sum += n * ((long long)(i0 + 1) * W + koff) + n * (n - 1) / 2 * W;
+  return sum + paged_keys(s, W, causal, q - 1);
+}
+
+// A CTA's walk along its share, one piece (an item, or the part of one that
+// the share holds) at a time.  UNIT: keys of a block.
+template <int UNIT>
+struct PagedWalk {
+  long long left;     // of the share, the current piece included
   long long share;
+  int b, head, item;  // sequence, key/value head, tile of rows
+  PagedSeq sq;
+  int x0, take;       // the piece: [x0, x0 + take) of the item's cost
+  int nb;             // the item's key blocks
+  int u0, u1;         // those of the piece
+
+  __device__ __forceinline__ void piece(const PagedParams& p, int W) {
+    const int keys = paged_keys(sq, W, p.causal, item);
+    nb = (keys + UNIT - 1) / UNIT;
+    take = (int)min((long long)(keys + kPagedOverhead - x0), left);
+    u0 = min((x0 + UNIT - 1) / UNIT, nb);
+    u1 = min((x0 + take + UNIT - 1) / UNIT, nb);
+  }
+  // The item is finished here.
+  __device__ __forceinline__ bool whole() const { return x0 == 0 && u1 == nb; }
+  // No block of the item starts in this share (and if it has none at all, the
+  // share that begins it sees to its rows).
+  __device__ __forceinline__ bool nothing() const { return u0 == u1 && (nb > 0 || x0 > 0); }
+  // Parts of an item that this share begins and others continue.
+  __device__ __forceinline__ int parts() const {
+    return (int)((share - left + (long long)(nb - 1) * UNIT) / share) + 1;
+  }
+  __device__ __forceinline__ void advance(const PagedParams& p, int W) {
+    left -= take;
+    if (left <= 0) return;
+    x0 = 0;
+    if (++item * W >= sq.qlen) {
+      item = 0;
+      if (++head == p.Hkv) {
+        head = 0;
+        do {
+          sq = paged_seq(p, ++b);
+        } while (sq.qlen == 0 && b + 1 < p.n_seq);
+      }
+    }
+    piece(p, W);
+  }
 };
 
-// Every thread of the CTA calls this.  head_cost(seq) gives the cost units of
-// one key/value head of a sequence (a long long); place(seq, off, start) turns
-// an offset into a sequence's line into item, items_per_head and unit.  The
-// threads take runs of sequences, a scan over the threads' sums places the
-// share, and the thread whose run holds its start walks there.
-template <int THREADS, typename HeadCost, typename Place>
-__device__ __forceinline__ PagedStart paged_partition(const PagedParams& p, HeadCost head_cost,
-                                                      Place place) {
+// Places the CTA at the start of its share (left 0: it has none).  Every
+// thread calls this.  The threads take runs of sequences, a scan over their
+// sums places the share, and the thread whose run holds its start walks there.
+template <int UNIT, int THREADS>
+__device__ __forceinline__ PagedWalk<UNIT> paged_start(const PagedParams& p, int W) {
   __shared__ long long warp_sum[THREADS / 32];
-  __shared__ PagedStart start;
+  __shared__ PagedWalk<UNIT> start;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.n_seq + THREADS - 1) / THREADS;
   const int b0 = min(tid * run, p.n_seq), b1 = min(b0 + run, p.n_seq);
-  long long sum = 0;
+  long long sum = 0, line = 0;  // of the run, of a head of its last sequence
+  PagedSeq sq = {0, 0, 0};
   for (int b = b0; b < b1; ++b) {
-    sum += head_cost(paged_seq(p, b)) * p.Hkv;
+    sq = paged_seq(p, b);
+    line = paged_line(sq, W, p.causal, paged_items(sq, W));
+    sum += line * p.Hkv;
     if (blockIdx.x == 0) paged_check(p, b);
   }
   long long incl = sum;
@@ -136,6 +196,7 @@ __device__ __forceinline__ PagedStart paged_partition(const PagedParams& p, Head
     if (lane >= off) incl += up;
   }
   if (lane == 31) warp_sum[warp] = incl;
+  if (tid == 0) start.left = 0;
   __syncthreads();
   long long before = 0, all = 0;
 #pragma unroll
@@ -143,21 +204,36 @@ __device__ __forceinline__ PagedStart paged_partition(const PagedParams& p, Head
     if (w < warp) before += warp_sum[w];
     all += warp_sum[w];
   }
-  long long share = (all + gridDim.x - 1) / gridDim.x;
-  if (share < p.min_share) share = p.min_share;
+  const long long share = max((all + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
   const long long s = share * blockIdx.x;
-  if (tid == 0 && s >= all) start = PagedStart{0, 0, 1, 0, 0, share};
   long long at = before + incl - sum;
-  if (s >= at && s < at + sum) {
-    for (int b = b0; b < b1; ++b) {
-      const long long c = head_cost(paged_seq(p, b)) * p.Hkv;
-      if (s < at + c) {
-        start = PagedStart{b, 0, 1, 0, min(share, all - s), share};
-        place(paged_seq(p, b), s - at, start);
-        break;
+  if (s < all && s >= at && s < at + sum) {
+    int b = b1 - 1;
+    if (run > 1) {  // the last sequence's line is known, the others' not
+      for (b = b0; b < b1; ++b) {
+        sq = paged_seq(p, b);
+        line = paged_line(sq, W, p.causal, paged_items(sq, W));
+        if (s < at + line * p.Hkv) break;
+        at += line * p.Hkv;
       }
-      at += c;
     }
+    PagedWalk<UNIT> w;
+    w.b = b;
+    w.sq = sq;
+    w.share = share;
+    w.left = min(share, all - s);
+    w.head = (int)((s - at) / line);
+    const long long off = s - at - w.head * line;
+    int lo = 0, hi = paged_items(sq, W) - 1;  // the last item that starts at or before off
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (paged_line(sq, W, p.causal, mid) <= off) lo = mid;
+      else hi = mid - 1;
+    }
+    w.item = lo;
+    w.x0 = (int)(off - paged_line(sq, W, p.causal, lo));
+    w.piece(p, W);
+    start = w;
   }
   __syncthreads();
   return start;

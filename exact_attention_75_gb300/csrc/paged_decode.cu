@@ -46,57 +46,20 @@ __device__ __forceinline__ uint32_t sw_off(int row, int piece) {
   return (uint32_t)((piece >> 3) * kBoxBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-// An item is a sequence's key/value head; its cost: the key units and one for
-// its prologue and epilogue.
-__device__ __forceinline__ int key_units(const PagedSeq& s) {
-  return (s.klen + kPagedUnitKeys - 1) / kPagedUnitKeys;
+// An item is a sequence's key/value head; the warps take the 16-key blocks of
+// its kUnit-key cost blocks in turn.
+constexpr int kUnit = kWarps * kKeys;
+using Walk = PagedWalk<kUnit>;
+
+__device__ __forceinline__ int warp_blocks(const Walk& w, int warp) {
+  const int keys = min(w.u1 * kUnit, w.sq.klen) - w.u0 * kUnit;
+  const int nb = (max(keys, 0) + kKeys - 1) / kKeys;
+  return nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;
 }
-
-// A walk along the CTA's share, one piece (an item, or the part of one that
-// the share holds) at a time.
-struct Walk {
-  int left;       // units still to take, the current piece included
-  int b, head;    // item: sequence, key/value head
-  PagedSeq sq;
-  int nku;        // the item's key units
-  int u0, u1;     // those of the piece
-  int take;       // units of the piece
-  int nbw;        // 16-key blocks of the piece that this warp takes
-
-  __device__ __forceinline__ void piece(int warp) {
-    take = min(nku + 1 - u0, left);
-    u1 = min(u0 + take, nku);
-    const int keys = min(u1 * kPagedUnitKeys, sq.klen) - u0 * kPagedUnitKeys;
-    const int nb = (max(keys, 0) + kKeys - 1) / kKeys;
-    nbw = nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;
-  }
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedStart& st, int warp) {
-    left = (int)st.left;
-    b = st.b;
-    head = st.item;
-    u0 = st.unit;
-    sq = paged_seq(p, b);
-    nku = key_units(sq);
-    piece(warp);
-  }
-  __device__ __forceinline__ void advance(const PagedParams& p, int warp) {
-    left -= take;
-    if (left <= 0) return;
-    u0 = 0;
-    if (++head == p.Hkv) {
-      head = 0;
-      do {
-        sq = paged_seq(p, ++b);
-      } while (sq.qlen == 0 && b + 1 < p.n_seq);
-      nku = key_units(sq);
-    }
-    piece(warp);
-  }
-  // First key of the warp's block j.
-  __device__ __forceinline__ int key0(int warp, int j) const {
-    return u0 * kPagedUnitKeys + (warp + j * kWarps) * kKeys;
-  }
-};
+// First key of the warp's block j.
+__device__ __forceinline__ int first_key(const Walk& w, int warp, int j) {
+  return w.u0 * kUnit + (warp + j * kWarps) * kKeys;
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -121,35 +84,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_fence_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  const PagedStart st = paged_partition<kThreads>(
-      p, [&](const PagedSeq& s) { return s.qlen == 0 ? 0LL : key_units(s) + 1LL; },
-      [&](const PagedSeq& s, long long off, PagedStart& at) {
-        at.item = (int)(off / (key_units(s) + 1));
-        at.unit = (int)(off % (key_units(s) + 1));
-      });
+  grid_wait();
+  if (threadIdx.x == 0) p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  Walk w = paged_start<kUnit, kThreads>(p, p.max_q);
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
-
-  Walk w;
-  w.left = 0;
-  if (st.left > 0) w.start(p, st, warp);
 
   // The warp's stream of blocks runs over the pieces without a break: ahead
   // walks it as far as the ring reaches, the page of its next block already
   // read.  issued, it: blocks issued to and taken from the ring.
   Walk ahead = w;
-  int aj = 0, apage = -1;
+  int aj = 0, an = w.left > 0 ? warp_blocks(w, warp) : 0, apage = -1;
   uint32_t issued = 0, it = 0;
   auto find_next = [&]() {  // settles ahead on its next block, or on left <= 0
-    while (ahead.left > 0 && aj >= ahead.nbw) {
-      ahead.advance(p, warp);
+    while (ahead.left > 0 && aj >= an) {
+      ahead.advance(p, p.max_q);
+      an = warp_blocks(ahead, warp);
       aj = 0;
     }
     if (ahead.left > 0)
       apage = __ldg(p.block_table + (size_t)ahead.b * p.max_pages +
-                    (ahead.key0(warp, aj) >> p.page_log2));
+                    (first_key(ahead, warp, aj) >> p.page_log2));
   };
   auto issue = [&]() {
     if (ahead.left <= 0) return;
@@ -161,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok)
         atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(ahead.b, 0xFFFF) << 16));
       const int z = ok ? apage * p.Hkv + ahead.head : -1;  // -1: the box reads zeros
-      const int y = ahead.key0(warp, aj) & (p.page - 1);
+      const int y = first_key(ahead, warp, aj) & (p.page - 1);
       mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
 #pragma unroll
       for (int c = 0; c < L::kChunks; ++c) {
@@ -179,8 +135,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* meet = reinterpret_cast<float*>(smem + L::kMeetOff);
   float2* meet_ml = reinterpret_cast<float2*>(smem + L::kMlOff);  // [kWarps][kMeet]
 
-  for (; w.left > 0; w.advance(p, warp)) {
-    if (w.u1 == w.u0 && w.nku > 0) continue;  // the item's last unit alone: no keys
+  for (; w.left > 0; w.advance(p, p.max_q)) {
+    if (w.nothing()) continue;
+    const int nbw = warp_blocks(w, warp);
     const PagedSeq sq = w.sq;
     const int rows = min(kPagedRows, sq.qlen * p.G);
     // Row r of the item: new token r / G, query head r % G of the group.
@@ -216,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
     bool aborted = false;
 #pragma unroll 1
-    for (int j = 0; j < w.nbw; ++j) {
+    for (int j = 0; j < nbw; ++j) {
       const int s = (int)(it % NS);
       if (!__all_sync(0xffffffffu, mbar_wait(bar(s), (it / NS) & 1, wd, 65))) {
         aborted = true;
@@ -225,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++it;
       const uint32_t tk = ring + (uint32_t)(s * L::kSlotBytes);
       const uint32_t tv = tk + L::kChunks * kBoxBytes;
-      const int key0 = w.key0(warp, j);
+      const int key0 = first_key(w, warp, j);
       if (key0 + kKeys > sq.klen) {
         // Rows past the sequence's last key hold whatever the page held (P is
         // 0 there, but 0 x NaN is not): zero those rows of V.
@@ -337,11 +294,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     lB += __shfl_xor_sync(0xffffffffu, lB, 2);
 
     // The warps' (O, m, l) meet in shared memory, kMeet rows at a time.
-    const bool whole = w.u0 == 0 && w.u1 == w.nku;
-    const size_t slot = 2 * (size_t)blockIdx.x + (w.u0 == 0 ? 1 : 0);
-    if (!whole && w.u0 == 0 && threadIdx.x == 0) {
-      p.desc[2 * blockIdx.x] =
-          make_int4(1 + (int)((w.nku - w.u1 + st.share - 1) / st.share), w.head, 0, 0);
+    const bool whole = w.whole();
+    const size_t slot = 2 * (size_t)blockIdx.x + (w.x0 == 0 ? 1 : 0);
+    if (!whole && w.x0 == 0 && threadIdx.x == 0) {
+      p.desc[2 * blockIdx.x] = make_int4(w.parts(), w.head, 0, 0);
       p.desc[2 * blockIdx.x + 1] = make_int4(sq.s0, sq.qlen, 0, 0);
     }
     for (int pass = 0; pass * kMeet < rows; ++pass) {
@@ -398,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   dw.abort_flag = &never;
   dw.limit_ns = drain_limit_ns(wd.limit_ns);
   for (; it < issued; ++it) mbar_wait(bar((int)(it % NS)), (it / NS) & 1, dw, 66);
-  asm volatile("griddepcontrol.launch_dependents;");
+  grid_release();
 }
 
 template <int D, bool BF16>
@@ -407,9 +363,8 @@ cudaError_t launch_db(const PagedLaunch& a) {
   static DeviceFlags configured;
   cudaError_t e = ensure_dyn_smem(paged_decode_kernel<D, BF16>, L::kBytes, configured);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D, BF16>
-      <<<a.grid, kThreads, L::kBytes, a.stream>>>(a.tmK, a.tmV, a.params);
-  return cudaGetLastError();
+  return launch_dependent(paged_decode_kernel<D, BF16>, dim3((unsigned)a.grid), kThreads,
+                          L::kBytes, a.stream, a.tmK, a.tmV, a.params);
 }
 
 template <int D>

@@ -3,7 +3,7 @@
 //   M = max m_k,  l = sum l_k 2^(m_k - M),  O = sum O_k 2^(m_k - M) / l.
 //
 // A warp takes a segment of 32 (row, four columns) elements, contiguous in
-// every part (512 bytes a read), eight parts in flight at a time.  The
+// every part (512 bytes a read), four parts in flight at a time.  The
 // decoding kernel's items are small and may be spread over every CTA (one
 // sequence with a long cache), so four warps share the parts of a segment and
 // meet in shared memory; a pair of query tiles has enough segments.  Launched
@@ -14,14 +14,15 @@
 #include "mma16.cuh"
 #include "paged.cuh"
 #include "sm103_ptx.cuh"
+#include "smem_attr.cuh"
 
 namespace attn {
 
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kFlight = 8;  // parts read together
+constexpr int kFlight = 4;  // parts read together
 
 struct Sum {
   float m, l;
@@ -43,14 +44,15 @@ __device__ __forceinline__ void add(Sum& s, float m, float l, const float4& o) {
 // ROWS: rows of an item's partial result (kPagedRows: the decoding kernel;
 // kPagedTileRows: a pair of query tiles).
 template <int D, bool BF16, int ROWS>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kThreads, 4) paged_join_kernel(const PagedParams p) {
   constexpr bool kDecode = ROWS == kPagedRows;
   constexpr int kWays = kDecode ? 4 : 1;  // warps that share a segment's parts
   constexpr int kSegs = ROWS * (D / 4) / 32;
   __shared__ Sum meet[kDecode ? kThreads : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int way = warp % kWays;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
+  grid_release();
   const int4 item = p.desc[2 * blockIdx.x], seq = p.desc[2 * blockIdx.x + 1];
   const int parts = item.x;
   if (parts == 0) return;
@@ -118,19 +120,11 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedParams 
 
 template <int D, bool BF16, int ROWS>
 cudaError_t launch_dbr(const PagedLaunch& a) {
-  cudaLaunchConfig_t cfg = {};
-  // decoding: every live segment at once, four warps each; tiles: two rounds
-  // of 16 segments per CTA
-  const unsigned y = ROWS == kPagedRows ? (unsigned)(a.rows * (D / 4) + 127) / 128 : D / 16;
-  cfg.gridDim = dim3((unsigned)a.grid, y);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, BF16, ROWS>, a.params);
+  // decoding: every live segment at once, kWarps / 4 in a CTA; tiles: two
+  // rounds of kWarps segments per CTA
+  const unsigned y = ROWS == kPagedRows ? (unsigned)(a.rows * (D / 4) + 63) / 64 : D / 8;
+  return launch_dependent(paged_join_kernel<D, BF16, ROWS>, dim3((unsigned)a.grid, y), kThreads, 0,
+                          a.stream, a.params);
 }
 
 template <int D>

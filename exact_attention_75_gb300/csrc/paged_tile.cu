@@ -33,15 +33,17 @@ constexpr int kWarpMma = 9;
 constexpr int kWarpRelay = 10;
 constexpr uint32_t kBarKv = 1, kBarP = 2;  // issuer <-> relay, issuer <-> softmax t
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
-constexpr int kRows = 2 * 128;             // rows of a partial result
+constexpr int kRows = kPagedTileRows;
+constexpr int kStageBytes = 32 * 128;      // a softmax warp's rows on their way out
 
 template <int D>
 struct PagedTileLayout {
   static constexpr int kTileBytes = 128 * kPaddedD<D> * 2;
-  static constexpr int kSlots = D == 64 ? 8 : (D == 96 ? 5 : 4);  // K/V ring, as in the forward
+  static constexpr int kSlots = D == 64 ? 8 : 4;  // K/V ring
   static constexpr int kQOff = 0;
   static constexpr int kKvOff = 2 * kTileBytes;
-  static constexpr int kBarOff = kKvOff + kSlots * kTileBytes;
+  static constexpr int kStageOff = kKvOff + kSlots * kTileBytes;
+  static constexpr int kBarOff = kStageOff + 8 * kStageBytes;
   static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kOFull = 6, kDrain = 8;
   static constexpr int kKvFull = 9, kKvEmpty = 9 + kSlots;
   static constexpr int kNumBars = 9 + 2 * kSlots;
@@ -51,99 +53,22 @@ struct PagedTileLayout {
   static_assert(kDynSmem + 256 <= 232448, "shared memory budget (227 KB) exceeded");
 };
 
-// Key blocks the rows of a query tile see (-1: no such tile).
-__device__ __forceinline__ int tile_blocks(const PagedSeq& s, int tile, int TT, int causal) {
-  const int first = tile * TT;
-  if (first >= s.qlen) return -1;
-  const int last = min(first + TT, s.qlen) - 1;
-  const int seen = causal ? max(last + s.klen - s.qlen + 1, 0) : s.klen;
-  return (seen + 127) >> 7;
-}
+// A walk along the CTA's share; an item is a pair of tiles of TT tokens each.
+struct Walk : PagedWalk<128> {
+  int n[2];  // key blocks of the piece that tile 0 / 1 sees
+  bool two;  // tile 1 has rows
 
-// sum over i in [0, n) of floor((a i + b) / m).
-__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  long long sum = 0;
-  while (n > 0) {
-    sum += (long long)(n - 1) * n / 2 * (a / m) + (long long)n * (b / m);
-    a %= m;
-    b %= m;
-    const uint32_t top = a * n + b;  // < 2^31: a key position
-    n = top / m;
-    b = top % m;
-    const uint32_t t = m;
-    m = a;
-    a = t;
-    if (m == 0) break;
-  }
-  return sum;
-}
-
-// Cost units of one key/value head of a sequence: its pairs' key blocks and
-// one per pair.  Pair i of W = 2 TT tokens sees (i + 1) W + klen - qlen keys
-// when causal (the last pair all klen), none where that is negative.
-__device__ __forceinline__ long long head_units(const PagedSeq& s, int W, int causal) {
-  if (s.qlen == 0) return 0;
-  const int pairs = (s.qlen + W - 1) / W;
-  const int all = (s.klen + 127) >> 7;
-  if (!causal) return (long long)pairs * (all + 1);
-  const int koff = s.klen - s.qlen;
-  const int i0 = koff + W > 0 ? 0 : -koff / W;  // the first pair that sees a key
-  long long sum = pairs + all;
-  if (pairs - 1 > i0)
-    sum += floor_sum((uint32_t)(pairs - 1 - i0), 128u, (uint32_t)W,
-                     (uint32_t)((i0 + 1) * W + koff + 127));
-  return sum;
-}
-
-// A CTA's walk along its share; every role walks it alike.
-struct Walk {
-  int left;          // units still to take, the current piece included
-  int b, head, qp;   // item: sequence, key/value head, pair of query tiles
-  PagedSeq sq;
-  int u0, u1;        // its key blocks [u0, u1) in this share
-  int nb;            // all of its key blocks
-  int take;          // units of the piece
-  int n[2];          // key blocks of [u0, u1) that tile 0 / 1 sees
-  bool here[2];      // the tile has rows
-
-  __device__ __forceinline__ void piece(const PagedParams& p, int TT) {
-    const int k0 = tile_blocks(sq, 2 * qp, TT, p.causal);
-    const int k1 = tile_blocks(sq, 2 * qp + 1, TT, p.causal);
-    here[0] = k0 >= 0;
-    here[1] = k1 >= 0;
-    nb = max(max(k0, k1), 0);
-    take = min(nb + 1 - u0, left);
-    u1 = min(u0 + take, nb);
+  __device__ __forceinline__ void tiles(const PagedParams& p, int TT) {
+    two = (2 * item + 1) * TT < sq.qlen;
+    int k0 = nb;  // key blocks of tile 0: fewer than tile 1's under causal masking
+    if (two && p.causal)
+      k0 = (max((2 * item + 1) * TT + sq.klen - sq.qlen, 0) + 127) >> 7;
     n[0] = max(min(u1, k0) - u0, 0);
-    n[1] = max(min(u1, k1) - u0, 0);
+    n[1] = two ? u1 - u0 : 0;
   }
-  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == nb; }
-  // Only the item's last unit (it costs, but holds no work of its own).
-  __device__ __forceinline__ bool nothing() const { return u1 == u0 && nb > 0; }
-
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedStart& st, int TT) {
-    left = (int)st.left;
-    b = st.b;
-    sq = paged_seq(p, b);
-    head = st.item / st.items_per_head;
-    qp = st.item % st.items_per_head;
-    u0 = st.unit;
-    piece(p, TT);
-  }
-  __device__ __forceinline__ void advance(const PagedParams& p, int TT) {
-    left -= take;
-    if (left <= 0) return;
-    u0 = 0;
-    if (++qp * 2 * TT >= sq.qlen) {
-      qp = 0;
-      if (++head == p.Hkv) {
-        head = 0;
-        do {
-          sq = paged_seq(p, ++b);
-        } while (sq.qlen == 0 && b + 1 < p.n_seq);
-      }
-    }
-    piece(p, TT);
+  __device__ __forceinline__ void next(const PagedParams& p, int TT) {
+    advance(p, 2 * TT);
+    if (left > 0) tiles(p, TT);
   }
 };
 
@@ -182,37 +107,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(L::kKvEmpty + s), 1);
     }
     mbar_fence_init();
-    p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  const PagedStart st = paged_partition<kThreads>(
-      p, [&](const PagedSeq& s) { return head_units(s, 2 * TT, p.causal); },
-      [&](const PagedSeq& s, long long off, PagedStart& at) {
-        const long long per_head = head_units(s, 2 * TT, p.causal);
-        const int pairs = (s.qlen + 2 * TT - 1) / (2 * TT);
-        long long rem = off % per_head;
-        int qp = 0;
-        for (;; ++qp) {
-          const int nb = max(max(tile_blocks(s, 2 * qp, TT, p.causal),
-                                 tile_blocks(s, 2 * qp + 1, TT, p.causal)), 0);
-          if (rem <= nb || qp + 1 == pairs) break;
-          rem -= nb + 1;
-        }
-        at.items_per_head = pairs;
-        at.item = (int)(off / per_head) * pairs + qp;
-        at.unit = (int)rem;
-      });
-  __syncthreads();
+  grid_wait();
+  if (threadIdx.x == 0) p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  Walk w;
+  static_cast<PagedWalk<128>&>(w) = paged_start<128, kThreads>(p, 2 * TT);  // a CTA barrier
+  if (w.left > 0) w.tiles(p, TT);
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
-
-  Walk w;
-  w.left = 0;
-  if (st.left > 0) w.start(p, st, TT);
 
   if (warp == kWarpProducer) {
     // ------------------------------------------------------ TMA producer ---
@@ -225,23 +132,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    for (; w.left > 0 && ok; w.advance(p, TT)) {
+    for (; w.left > 0 && ok; w.next(p, TT)) {
       const int nbmax = max(w.n[0], w.n[1]);
       if (nbmax == 0) continue;
-      // The lane's box of key block kb: tensor-map page index, -1 (zeros) past
-      // the sequence or for a page outside the cache.
+      // The page of the lane's box of key block kb, read ahead of its use: -2
+      // past the sequence.
       auto box_page = [&](int kb) {
         const int key0 = kb * 128 + lane * box_rows;
-        if (lane >= boxes || key0 >= w.sq.klen) return -1;
-        const int page =
-            __ldg(p.block_table + (size_t)w.b * p.max_pages + (key0 >> p.page_log2));
-        if (page < 0 || page >= p.n_pages) {
-          atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(w.b, 0xFFFF) << 16));
-          return -1;
-        }
-        return page * p.Hkv + w.head;
+        return lane < boxes && key0 < w.sq.klen
+                   ? __ldg(p.block_table + (size_t)w.b * p.max_pages + (key0 >> p.page_log2))
+                   : -2;
       };
-      int z = box_page(w.u0);
+      int page = box_page(w.u0);
       for (int t = 0; t < 2 && ok; ++t) {
         if (w.n[t] == 0) continue;
         ok = __all_sync(0xffffffffu,
@@ -253,13 +155,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < kChunks; ++h)
             tma_load_3d(dst + h * 16384, &tmQ, bar(L::kQFull + t), h * 64,
-                        w.sq.s0 + (2 * w.qp + t) * TT, w.head * p.G);
+                        w.sq.s0 + (2 * w.item + t) * TT, w.head * p.G);
         }
         ++q_it[t];
       }
       for (int j = 0; j < nbmax && ok; ++j) {
         const int y = (w.u0 + j) * 128 & (p.page - 1);  // 0 unless a page holds two blocks
-        const int zn = j + 1 < nbmax ? box_page(w.u0 + j + 1) : -1;
+        const int next = j + 1 < nbmax ? box_page(w.u0 + j + 1) : -2;
+        // tensor-map page index; -1 (zeros) past the sequence or for a page
+        // outside the cache
+        const bool in_cache = page >= 0 && page < p.n_pages;
+        if (!in_cache && page != -2)
+          atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(w.b, 0xFFFF) << 16));
+        const int z = in_cache ? page * p.Hkv + w.head : -1;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
           const uint32_t slot = kv_it % L::kSlots;
@@ -277,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++kv_it;
         }
-        z = zn;
+        page = next;
       }
     }
     // Drain: every copy this warp issued must have landed before the CTA may
@@ -309,11 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         aborted = !__all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull + slot), par, wd, 71));
       return slot;
     };
-    for (; w.left > 0; w.advance(p, TT)) {
+    for (; w.left > 0; w.next(p, TT)) {
       const int nbmax = max(w.n[0], w.n[1]);
-      if (nbmax > 0 && w.u0 == 0 && !w.whole() && lane == 0) {
-        p.desc[2 * blockIdx.x] = make_int4(1 + (int)((w.nb - w.u1 + st.share - 1) / st.share),
-                                           w.head, 2 * w.qp * TT, 0);
+      if (w.x0 == 0 && !w.whole() && lane == 0) {
+        p.desc[2 * blockIdx.x] = make_int4(w.parts(), w.head, 2 * w.item * TT, 0);
         p.desc[2 * blockIdx.x + 1] = make_int4(w.sq.s0, w.sq.qlen, 0, 0);
       }
       if (nbmax == 0) continue;  // the same skip in every role
@@ -374,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_f16_ts(ocol, pcol + kk * 8, desc_plus(vd, mnmajor16_off(kk)), kIdO,
                    kk > 0 ? 1u : acc0);
     };
-    for (; w.left > 0; w.advance(p, TT)) {
+    for (; w.left > 0; w.next(p, TT)) {
       const int nb0 = w.n[0], nb1 = w.n[1];
       const int nbmax = max(nb0, nb1);
       if (nbmax == 0) continue;  // the same skip in every role
@@ -461,19 +368,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gi = r / TT, ti = r - gi * TT;  // query head of the group, token of the tile
     uint32_t s_it = 0, o_it = 0;
     bool aborted = false;
-    for (; w.left > 0; w.advance(p, TT)) {
+    for (; w.left > 0; w.next(p, TT)) {
       if (w.nothing()) continue;
       const int nb = w.n[t];
-      const int token = (2 * w.qp + t) * TT + ti;
+      const int token = (2 * w.item + t) * TT + ti;
       const bool live = gi < p.G && token < w.sq.qlen;
       const size_t grow = (size_t)(w.head * p.G + gi) * p.total + w.sq.s0 + token;
       const bool whole = w.whole();
-      const size_t slot = 2 * (size_t)blockIdx.x + (w.u0 == 0 ? 1 : 0);
+      const size_t slot = 2 * (size_t)blockIdx.x + (w.x0 == 0 ? 1 : 0);
       float2* const ml =
           reinterpret_cast<float2*>(p.part_ml) + slot * kRows + t * 128 + r;
       if (nb == 0) {
         // A tile without rows, or whose rows see no key of this share.
-        if (w.here[t]) {
+        if (t == 0 || w.two) {
           if (!whole) {
             *ml = make_float2(-INFINITY, 0.f);
           } else if (live) {
@@ -585,21 +492,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (whole) {
         const float inv_l = l > 0.f ? 1.0f / l : 0.f;
-        uint4* orow = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + grow * D);
+        // Rows go out through the warp's stage, 64 columns at a time (swizzled
+        // 16-byte pieces), so that a store covers whole 128-byte row pieces:
+        // a lane per row would write 16 bytes of 32 lines.
+        uint8_t* const stage = smem + L::kStageOff + warp * kStageBytes;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t raw[32];
-          tmem_ld32_sync(o_addr + c * 32, raw);
-          uint32_t pk[16];
+        for (int c0 = 0; c0 < D / 32; c0 += 2) {
+          constexpr int kPieces = 8;
+          const int pieces = D / 32 - c0 >= 2 ? kPieces : kPieces / 2;  // of a row
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = pack2<BF16>(__uint_as_float(raw[2 * i]) * inv_l,
-                                __uint_as_float(raw[2 * i + 1]) * inv_l);
-          if (live) {
+          for (int c = c0; c < c0 + pieces / 4; ++c) {
+            uint32_t raw[32];
+            tmem_ld32_sync(o_addr + c * 32, raw);
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              orow[c * 4 + v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+            for (int v = 0; v < 4; ++v) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                pk[i] = pack2<BF16>(__uint_as_float(raw[8 * v + 2 * i]) * inv_l,
+                                    __uint_as_float(raw[8 * v + 2 * i + 1]) * inv_l);
+              const int pc = (c - c0) * 4 + v;
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((pc ^ (lane & 7)) << 4)) =
+                  make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < pieces; ++i) {
+            const int row = i * (32 / pieces) + lane / pieces, pc = lane % pieces;
+            const uint4 x =
+                *reinterpret_cast<const uint4*>(stage + row * 128 + ((pc ^ (row & 7)) << 4));
+            const int at = __shfl_sync(0xffffffffu, live ? (int)grow : -1, row);
+            if (at >= 0)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (size_t)at * D + c0 * 32 +
+                                        pc * 8) = x;
+          }
+          __syncwarp();
         }
         if (live) p.lse[grow] = (m + log2f(l)) * 0.69314718055994530942f;
       } else {
@@ -619,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  asm volatile("griddepcontrol.launch_dependents;");
+  grid_release();
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
@@ -635,8 +563,8 @@ cudaError_t launch_db(const PagedLaunch& a) {
   static DeviceFlags configured;
   cudaError_t e = ensure_dyn_smem(kern, L::kDynSmem, configured);
   if (e != cudaSuccess) return e;
-  kern<<<a.grid, kThreads, L::kDynSmem, a.stream>>>(a.tmQ, a.tmK, a.tmV, a.params);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3((unsigned)a.grid), kThreads, L::kDynSmem, a.stream, a.tmQ,
+                          a.tmK, a.tmV, a.params);
 }
 
 template <int D>

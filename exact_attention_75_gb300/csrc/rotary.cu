@@ -33,6 +33,7 @@
 #include "attn.h"
 #include "rotary.cuh"
 #include "sm103_ptx.cuh"
+#include "smem_attr.cuh"
 
 namespace attn {
 
@@ -130,6 +131,8 @@ __device__ __forceinline__ void turn_pieces(uint4& lo, uint4& hi, const float (&
 
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
+  grid_wait();
+  grid_release();
   const int per_row = p.d / 16;
   const int group = blockIdx.x % p.head_groups;
   const int64_t idx = (int64_t)(blockIdx.x / p.head_groups) * kThreads + threadIdx.x;
@@ -193,6 +196,8 @@ __device__ __forceinline__ void report_bad(uint32_t* status, int site, int index
 
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams p) {
+  grid_wait();
+  grid_release();
   const int per_row = p.d / 16;
   const int group = blockIdx.x % p.head_groups;
   const int64_t idx = (int64_t)(blockIdx.x / p.head_groups) * kThreads + threadIdx.x;
@@ -295,13 +300,13 @@ cudaError_t launch_rope(const RopeLaunch& a, int num_sms) {
   p.head_groups = (heads + p.group_heads - 1) / p.group_heads;
   const dim3 grid((unsigned)(bx * p.head_groups), 1, (unsigned)a.B);
   if (a.bf16) {
-    if (a.interleaved) rope_kernel<true, true><<<grid, kThreads, 0, a.stream>>>(p);
-    else rope_kernel<true, false><<<grid, kThreads, 0, a.stream>>>(p);
-  } else {
-    if (a.interleaved) rope_kernel<false, true><<<grid, kThreads, 0, a.stream>>>(p);
-    else rope_kernel<false, false><<<grid, kThreads, 0, a.stream>>>(p);
+    if (a.interleaved)
+      return launch_dependent(rope_kernel<true, true>, grid, kThreads, 0, a.stream, p);
+    return launch_dependent(rope_kernel<true, false>, grid, kThreads, 0, a.stream, p);
   }
-  return cudaGetLastError();
+  if (a.interleaved)
+    return launch_dependent(rope_kernel<false, true>, grid, kThreads, 0, a.stream, p);
+  return launch_dependent(rope_kernel<false, false>, grid, kThreads, 0, a.stream, p);
 }
 
 cudaError_t launch_append(const AppendLaunch& a, int num_sms) {
@@ -312,13 +317,13 @@ cudaError_t launch_append(const AppendLaunch& a, int num_sms) {
   p.head_groups = (heads + p.group_heads - 1) / p.group_heads;
   const dim3 grid((unsigned)(bx * p.head_groups));
   if (a.bf16) {
-    if (a.interleaved) append_kernel<true, true><<<grid, kThreads, 0, a.stream>>>(p);
-    else append_kernel<true, false><<<grid, kThreads, 0, a.stream>>>(p);
-  } else {
-    if (a.interleaved) append_kernel<false, true><<<grid, kThreads, 0, a.stream>>>(p);
-    else append_kernel<false, false><<<grid, kThreads, 0, a.stream>>>(p);
+    if (a.interleaved)
+      return launch_dependent(append_kernel<true, true>, grid, kThreads, 0, a.stream, p);
+    return launch_dependent(append_kernel<true, false>, grid, kThreads, 0, a.stream, p);
   }
-  return cudaGetLastError();
+  if (a.interleaved)
+    return launch_dependent(append_kernel<false, true>, grid, kThreads, 0, a.stream, p);
+  return launch_dependent(append_kernel<false, false>, grid, kThreads, 0, a.stream, p);
 }
 
 }  // namespace attn

@@ -331,6 +331,21 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ------------------------------------------------ programmatic dependence ---
+// A kernel launched as a programmatic dependent may start before the previous
+// kernel of its stream has finished: grid_wait() returns once that one has
+// completed and its writes are visible, and comes before the first access to
+// memory that another kernel may touch.  grid_release() lets the next
+// dependent start its launch.
+
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void grid_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ math ---
 
 // Hardware base-2 exponential (MUFU), flush-to-zero.

@@ -1,4 +1,5 @@
-// Opting a kernel into more than 48 KB of dynamic shared memory.
+// Kernel launches: opting into more than 48 KB of dynamic shared memory, and
+// launching as a programmatic dependent.
 //
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) is a setting of the
 // current device's context, so a process that calls on device 0 and then on
@@ -18,6 +19,24 @@ namespace attn {
 constexpr int kMaxAttrDevices = 64;
 
 using DeviceFlags = std::atomic<bool>[kMaxAttrDevices];
+
+// Launches a kernel that calls grid_wait() as a programmatic dependent of the
+// previous kernel on the stream.
+template <typename Kern, typename... Args>
+cudaError_t launch_dependent(Kern kern, dim3 grid, int threads, int smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 template <typename Kern>
 cudaError_t ensure_dyn_smem(Kern kern, int bytes, DeviceFlags& configured) {
