@@ -467,7 +467,7 @@ struct PagedWorkspace {
   PagedWorkspace(bool decode, int d) {
     const size_t ctas = decode ? 2 * kPagedMaxSms : kPagedMaxSms;
     const size_t rows = 2 * ctas * (decode ? kPagedRows : kPagedTileRows);
-    ml = 2 * ctas * sizeof(int4);
+    ml = 4 * ctas * sizeof(int4);
     o = ml + rows * sizeof(float2);
     bytes = o + rows * d * sizeof(float);
   }
@@ -637,13 +637,13 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   p.desc = reinterpret_cast<int4*>(w);
   p.part_ml = reinterpret_cast<float*>(w + ws.ml);
   p.part_o = reinterpret_cast<float*>(w + ws.o);
-  p.min_share = decode ? 128 : 256;
+  p.min_share = decode ? 128 : 768;
   const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
   a.grid = decode ? 2 * sms : sms;
   a.rows = decode ? max_q * p.G : kPagedTileRows;
   a.stream = static_cast<cudaStream_t>(stream);
-  // the largest batch of these sizes stays in 63 bits of keys
-  const int64_t keys = (int64_t)max_pages * page + kPagedOverhead;
+  // the cost of the largest batch of these sizes stays in 63 bits
+  const int64_t keys = 3 * ((int64_t)max_pages * page + 1024);
   const int64_t items = (((int64_t)total * p.G) / 64 + n_seq) * Hkv;
   if (keys > INT64_MAX / items) return ATTN_ERR_INVALID_ARG;
   const int64_t heads = (int64_t)n_pages * Hkv;

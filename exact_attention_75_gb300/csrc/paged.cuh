@@ -3,9 +3,9 @@
 // over a persistent grid, and the partial results).
 //
 // Work.  A sequence with new tokens gives each of its key/value heads a run
-// of items; an item is a tile of query rows, and costs the keys they see plus
-// kPagedOverhead (its prologue and epilogue).  All items of the batch laid end
-// to end (sequence, key/value head, tile) form one line, and CTA c of the grid
+// of items; an item is a tile of query rows, and costs the keys they see, times
+// a weight, plus an overhead (PagedCost).  All items of the batch laid end to
+// end (sequence, key/value head, tile) form one line, and CTA c of the grid
 // takes [c w, (c + 1) w) of it: equal shares whatever the lengths are, so one
 // long sequence spreads over every SM and a ragged batch balances itself.  A
 // key block belongs to the share that its first key falls in.  The lengths
@@ -16,10 +16,11 @@
 //
 // An item that lies in one CTA's share is finished there.  One that crosses
 // shares leaves a partial result per share: an unnormalised O and the (m, l)
-// of each row, in slot 0 of the CTA that continues it and slot 1 of the CTA
-// that begins it.  The beginning CTA describes the item in desc[cta], and
-// the join kernel combines its parts in key order, so equal calls give equal
-// bits.
+// of each row, in slot 0 of a CTA that continues it and slot 1 of the CTA that
+// begins it, each described in desc.  The join kernel combines an item's parts
+// in key order, so equal calls give equal bits; a CTA of it takes a slice of
+// the item that its counterpart had a part of, so the join is shared out as
+// evenly as the parts are.
 #pragma once
 
 #include <cuda.h>
@@ -39,8 +40,6 @@ constexpr int kPagedTileRows = 256;
 constexpr int kPagedBlock = 16;
 // Query heads per key/value head at most.
 constexpr int kPagedMaxGroup = 128;
-// Keys an item's prologue and epilogue cost as much as.
-constexpr int kPagedOverhead = 128;
 
 struct PagedParams {
   const void* q;            // [Hkv * G, total, D]
@@ -50,8 +49,8 @@ struct PagedParams {
   const int* block_table;   // [n_seq, max_pages]
   const int* cu_seqlens;    // [n_seq + 1]
   const int* kv_lens;       // [n_seq], new tokens included
-  int4* desc;               // [grid][2] of the item the CTA began and others continue: parts
-                            // (0: none), key/value head, first token; s0, qlen of its sequence
+  int4* desc;               // [grid][slot][2] of the CTA's part of an item: parts in all (0: the
+                            // slot is empty), its number, key/value head, first token; s0, qlen
   float* part_ml;           // [grid][2][rows][2]
   float* part_o;            // [grid][2][rows][D], of the tile kernel [grid][2][D / 4][rows][4]
   int n_seq, total, max_q, n_pages, page, page_log2, max_pages, Hkv, G;
@@ -103,9 +102,23 @@ __device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
     atomicCAS(p.status, 0u, 1u | (63u << 8) | ((uint32_t)min(b, 0xFFFF) << 16));
 }
 
+// How a kernel's items are cut and what they cost.  UNIT: keys of a block.
+// KEY1, KEY2: cost of a key in an item whose rows fill one query tile or
+// reach into the second (the last item of a sequence may have one tile, all
+// before it have two); OVERHEAD: of an item's prologue and epilogue.
+template <int UNIT_, int KEY1_, int KEY2_, int OVERHEAD_>
+struct PagedCost {
+  static constexpr int UNIT = UNIT_, KEY1 = KEY1_, KEY2 = KEY2_, OVERHEAD = OVERHEAD_;
+};
+
 // Items of one key/value head of a sequence: W new tokens each.
 __device__ __forceinline__ int paged_items(const PagedSeq& s, int W) {
   return (s.qlen + W - 1) / W;
+}
+
+// Whether item i has rows in its second half.
+__device__ __forceinline__ bool paged_two(const PagedSeq& s, int W, int i) {
+  return i * W + W / 2 < s.qlen;
 }
 
 // Keys that item i's rows see: all klen in the last item (and without causal
@@ -115,44 +128,70 @@ __device__ __forceinline__ int paged_keys(const PagedSeq& s, int W, int causal, 
 }
 
 // Cost of a head's items 0 .. q-1, q at most their number.
+template <typename Cost>
 __device__ __forceinline__ long long paged_line(const PagedSeq& s, int W, int causal, int q) {
-  long long sum = (long long)q * kPagedOverhead;
-  if (q == 0) return sum;
-  if (!causal) return sum + (long long)q * s.klen;
-  const int koff = s.klen - s.qlen;
-  const int i0 = koff + W > 0 ? 0 : -koff / W;  // the first item that sees a key
-  const long long n = q - 1 - i0;               // items from it up to the one before the last
-  if (n > 0) sum += n * ((long long)(i0 + 1) * W + koff) + n * (n - 1) / 2 * W;
-  return sum + paged_keys(s, W, causal, q - 1);
+  if (q == 0) return 0;
+  long long keys = 0;  // of the items before the last of the q
+  if (!causal) {
+    keys = (long long)(q - 1) * s.klen;
+  } else {
+    const int koff = s.klen - s.qlen;
+    const int i0 = koff + W > 0 ? 0 : -koff / W;  // the first item that sees a key
+    const long long n = q - 1 - i0;
+    if (n > 0) keys = n * ((long long)(i0 + 1) * W + koff) + n * (n - 1) / 2 * W;
+  }
+  return (long long)q * Cost::OVERHEAD + keys * Cost::KEY2 +
+         (long long)paged_keys(s, W, causal, q - 1) *
+             (paged_two(s, W, q - 1) ? Cost::KEY2 : Cost::KEY1);
 }
 
 // A CTA's walk along its share, one piece (an item, or the part of one that
-// the share holds) at a time.  UNIT: keys of a block.
-template <int UNIT>
+// the share holds) at a time.
+template <typename Cost>
 struct PagedWalk {
   long long left;     // of the share, the current piece included
   long long share;
   int b, head, item;  // sequence, key/value head, tile of rows
   PagedSeq sq;
-  int x0, take;       // the piece: [x0, x0 + take) of the item's cost
+  long long x0, take; // the piece: [x0, x0 + take) of the item's cost
   int nb;             // the item's key blocks
   int u0, u1;         // those of the piece
+  bool two;           // rows in the item's second half
 
+  __device__ __forceinline__ int key_cost() const { return two ? Cost::KEY2 : Cost::KEY1; }
+  // Blocks that start before offset x of the item.
+  __device__ __forceinline__ int blocks(long long x) const {
+    constexpr unsigned long long c1 = Cost::UNIT * Cost::KEY1, c2 = Cost::UNIT * Cost::KEY2;
+    const unsigned long long n = two ? ((unsigned long long)x + c2 - 1) / c2
+                                     : ((unsigned long long)x + c1 - 1) / c1;
+    return (int)min(n, (unsigned long long)nb);
+  }
   __device__ __forceinline__ void piece(const PagedParams& p, int W) {
     const int keys = paged_keys(sq, W, p.causal, item);
-    nb = (keys + UNIT - 1) / UNIT;
-    take = (int)min((long long)(keys + kPagedOverhead - x0), left);
-    u0 = min((x0 + UNIT - 1) / UNIT, nb);
-    u1 = min((x0 + take + UNIT - 1) / UNIT, nb);
+    two = paged_two(sq, W, item);
+    nb = (keys + Cost::UNIT - 1) / Cost::UNIT;
+    take = min((long long)keys * key_cost() + Cost::OVERHEAD - x0, left);
+    u0 = blocks(x0);
+    u1 = blocks(x0 + take);
   }
   // The item is finished here.
   __device__ __forceinline__ bool whole() const { return x0 == 0 && u1 == nb; }
   // No block of the item starts in this share (and if it has none at all, the
   // share that begins it sees to its rows).
   __device__ __forceinline__ bool nothing() const { return u0 == u1 && (nb > 0 || x0 > 0); }
-  // Parts of an item that this share begins and others continue.
+  // Shares between the one that begins the item and this one: the number of
+  // the piece among the item's parts, and the parts in all.
+  __device__ __forceinline__ int part() const { return (int)((x0 + share - 1) / share); }
   __device__ __forceinline__ int parts() const {
-    return (int)((share - left + (long long)(nb - 1) * UNIT) / share) + 1;
+    const long long at = x0 == 0 ? share - left : part() * share - x0;  // in the share that begins it
+    return (int)((at + (long long)(nb - 1) * Cost::UNIT * key_cost()) / share) + 1;
+  }
+  // Describes the piece, a part of its item, to the join; token: the item's
+  // first row's.
+  __device__ __forceinline__ void describe(const PagedParams& p, int token) const {
+    int4* d = p.desc + 2 * (2 * blockIdx.x + (x0 == 0 ? 1 : 0));
+    d[0] = make_int4(parts(), part(), head, token);
+    d[1] = make_int4(sq.s0, sq.qlen, 0, 0);
   }
   __device__ __forceinline__ void advance(const PagedParams& p, int W) {
     left -= take;
@@ -171,13 +210,19 @@ struct PagedWalk {
   }
 };
 
+// One thread of a CTA, before its pieces are described.
+__device__ __forceinline__ void paged_clear(const PagedParams& p) {
+  p.desc[4 * blockIdx.x] = make_int4(0, 0, 0, 0);
+  p.desc[4 * blockIdx.x + 2] = make_int4(0, 0, 0, 0);
+}
+
 // Places the CTA at the start of its share (left 0: it has none).  Every
 // thread calls this.  The threads take runs of sequences, a scan over their
 // sums places the share, and the thread whose run holds its start walks there.
-template <int UNIT, int THREADS>
-__device__ __forceinline__ PagedWalk<UNIT> paged_start(const PagedParams& p, int W) {
+template <typename Cost, int THREADS>
+__device__ __forceinline__ PagedWalk<Cost> paged_start(const PagedParams& p, int W) {
   __shared__ long long warp_sum[THREADS / 32];
-  __shared__ PagedWalk<UNIT> start;
+  __shared__ PagedWalk<Cost> start;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.n_seq + THREADS - 1) / THREADS;
   const int b0 = min(tid * run, p.n_seq), b1 = min(b0 + run, p.n_seq);
@@ -185,7 +230,7 @@ __device__ __forceinline__ PagedWalk<UNIT> paged_start(const PagedParams& p, int
   PagedSeq sq = {0, 0, 0};
   for (int b = b0; b < b1; ++b) {
     sq = paged_seq(p, b);
-    line = paged_line(sq, W, p.causal, paged_items(sq, W));
+    line = paged_line<Cost>(sq, W, p.causal, paged_items(sq, W));
     sum += line * p.Hkv;
     if (blockIdx.x == 0) paged_check(p, b);
   }
@@ -212,12 +257,12 @@ __device__ __forceinline__ PagedWalk<UNIT> paged_start(const PagedParams& p, int
     if (run > 1) {  // the last sequence's line is known, the others' not
       for (b = b0; b < b1; ++b) {
         sq = paged_seq(p, b);
-        line = paged_line(sq, W, p.causal, paged_items(sq, W));
+        line = paged_line<Cost>(sq, W, p.causal, paged_items(sq, W));
         if (s < at + line * p.Hkv) break;
         at += line * p.Hkv;
       }
     }
-    PagedWalk<UNIT> w;
+    PagedWalk<Cost> w;
     w.b = b;
     w.sq = sq;
     w.share = share;
@@ -227,11 +272,11 @@ __device__ __forceinline__ PagedWalk<UNIT> paged_start(const PagedParams& p, int
     int lo = 0, hi = paged_items(sq, W) - 1;  // the last item that starts at or before off
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (paged_line(sq, W, p.causal, mid) <= off) lo = mid;
+      if (paged_line<Cost>(sq, W, p.causal, mid) <= off) lo = mid;
       else hi = mid - 1;
     }
     w.item = lo;
-    w.x0 = (int)(off - paged_line(sq, W, p.causal, lo));
+    w.x0 = off - paged_line<Cost>(sq, W, p.causal, lo);
     w.piece(p, W);
     start = w;
   }

@@ -49,7 +49,8 @@ __device__ __forceinline__ uint32_t sw_off(int row, int piece) {
 // An item is a sequence's key/value head; the warps take the 16-key blocks of
 // its kUnit-key cost blocks in turn.
 constexpr int kUnit = kWarps * kKeys;
-using Walk = PagedWalk<kUnit>;
+using Cost = PagedCost<kUnit, 1, 1, 128>;
+using Walk = PagedWalk<Cost>;
 
 __device__ __forceinline__ int warp_blocks(const Walk& w, int warp) {
   const int keys = min(w.u1 * kUnit, w.sq.klen) - w.u0 * kUnit;
@@ -86,8 +87,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tmV);
   }
   grid_wait();
-  if (threadIdx.x == 0) p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-  Walk w = paged_start<kUnit, kThreads>(p, p.max_q);
+  if (threadIdx.x == 0) paged_clear(p);
+  Walk w = paged_start<Cost, kThreads>(p, p.max_q);
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
@@ -296,10 +297,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // The warps' (O, m, l) meet in shared memory, kMeet rows at a time.
     const bool whole = w.whole();
     const size_t slot = 2 * (size_t)blockIdx.x + (w.x0 == 0 ? 1 : 0);
-    if (!whole && w.x0 == 0 && threadIdx.x == 0) {
-      p.desc[2 * blockIdx.x] = make_int4(w.parts(), w.head, 0, 0);
-      p.desc[2 * blockIdx.x + 1] = make_int4(sq.s0, sq.qlen, 0, 0);
-    }
+    if (!whole && threadIdx.x == 0) w.describe(p, 0);
     for (int pass = 0; pass * kMeet < rows; ++pass) {
       if (pass > 0) __syncthreads();
       if ((r0 >> 2) == (pass & 1)) {

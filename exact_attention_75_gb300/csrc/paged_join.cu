@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kFlight = 4;  // parts read together
+constexpr int kWays = 4;  // warps that share a segment's parts (decoding)
 
 struct Sum {
   float m, l;
@@ -41,97 +41,123 @@ __device__ __forceinline__ void add(Sum& s, float m, float l, const float4& o) {
   s.o.w = s.o.w * f + o.w * g;
 }
 
-// ROWS: rows of an item's partial result (kPagedRows: the decoding kernel;
-// kPagedTileRows: a pair of query tiles).
-template <int D, bool BF16, int ROWS>
-__global__ void __launch_bounds__(kThreads, 4) paged_join_kernel(const PagedParams p) {
-  constexpr bool kDecode = ROWS == kPagedRows;
-  constexpr int kWays = kDecode ? 4 : 1;  // warps that share a segment's parts
-  constexpr int kSegs = ROWS * (D / 4) / 32;
-  __shared__ Sum meet[kDecode ? kThreads : 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int way = warp % kWays;
-  grid_wait();
-  grid_release();
-  const int4 item = p.desc[2 * blockIdx.x], seq = p.desc[2 * blockIdx.x + 1];
-  const int parts = item.x;
-  if (parts == 0) return;
-  // decoding: the grid covers the live segments in one round
-  const int segs = kDecode ? (int)gridDim.y * (kWarps / kWays) : kSegs;
-  for (int s0 = blockIdx.y * (kWarps / kWays); s0 < segs; s0 += gridDim.y * (kWarps / kWays)) {
-    const int seg = s0 + warp / kWays;
-    const int e = min(seg, kSegs - 1) * 32 + lane;
-    int r, c4, token, head;  // row of the item, columns; token of the sequence, head of the group
-    if constexpr (kDecode) {
-      r = e / (D / 4);
-      c4 = e % (D / 4);
-      token = r / p.G;
-      head = r - token * p.G;
-    } else {
-      r = e % ROWS;
-      c4 = e / ROWS;
-      const int TT = 128 / p.G;
-      head = (r & 127) / TT;
-      token = item.z + (r >> 7) * TT + (r & 127) - head * TT;
-    }
-    const bool live = seg < kSegs && head < p.G && token < seq.y;
-    Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int k0 = way * kFlight; live && k0 < parts; k0 += kWays * kFlight) {
-      float2 ml[kFlight];
-      float4 o[kFlight];
+template <int D, bool BF16>
+__device__ __forceinline__ void store(const PagedParams& p, size_t row, int c4, const Sum& s) {
+  const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + 4 * c4) = make_uint2(
+      pack2<BF16>(s.o.x * inv, s.o.y * inv), pack2<BF16>(s.o.z * inv, s.o.w * inv));
+  if (c4 == 0) p.lse[row] = s.l > 0.f ? (s.m + log2f(s.l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Adds parts k0, k0 + 1, .. (at most FLIGHT of them) of element e (row r) of
+// the item that CTA first began.
+template <int D, int ROWS, int FLIGHT>
+__device__ __forceinline__ void add_parts(const PagedParams& p, Sum& s, int first, int e, int r,
+                                          int k0, int parts) {
+  float2 ml[FLIGHT];
+  float4 o[FLIGHT];
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        if (k0 + i >= parts) break;
-        const int k = k0 + i;
-        const size_t slot = 2 * ((size_t)blockIdx.x + k) + (k == 0 ? 1 : 0);
-        ml[i] = *reinterpret_cast<const float2*>(p.part_ml + (slot * ROWS + r) * 2);
-        o[i] = *reinterpret_cast<const float4*>(p.part_o + slot * ROWS * D + (size_t)e * 4);
-      }
+  for (int i = 0; i < FLIGHT; ++i) {
+    if (k0 + i >= parts) break;
+    const size_t slot = 2 * (size_t)(first + k0 + i) + (k0 + i == 0 ? 1 : 0);
+    ml[i] = *reinterpret_cast<const float2*>(p.part_ml + (slot * ROWS + r) * 2);
+    o[i] = *reinterpret_cast<const float4*>(p.part_o + slot * ROWS * D + (size_t)e * 4);
+  }
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        if (k0 + i >= parts) break;
-        // a part with no key for the row holds no O
-        if (ml[i].x != -INFINITY) add(s, ml[i].x, ml[i].y, o[i]);
-      }
-    }
-    if constexpr (kDecode) {
-      if (parts > kFlight) {  // the other warps have some
-        meet[threadIdx.x] = s;
-        __syncthreads();
-        if (way == 0) {
-#pragma unroll
-          for (int w = 1; w < kWays; ++w) {
-            const Sum& x = meet[threadIdx.x + 32 * w];
-            add(s, x.m, x.l, x.o);
-          }
-        }
-        __syncthreads();
-      }
-      if (way != 0) continue;
-    }
-    if (!live) continue;
-    const size_t gr = (size_t)(item.y * p.G + head) * p.total + seq.x + token;
-    const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + 4 * c4) = make_uint2(
-        pack2<BF16>(s.o.x * inv, s.o.y * inv), pack2<BF16>(s.o.z * inv, s.o.w * inv));
-    if (c4 == 0) p.lse[gr] = s.l > 0.f ? (s.m + log2f(s.l)) * 0.69314718055994531f : -INFINITY;
+  for (int i = 0; i < FLIGHT; ++i) {
+    if (k0 + i >= parts) break;
+    // a part with no key for the row holds no O
+    if (ml[i].x != -INFINITY) add(s, ml[i].x, ml[i].y, o[i]);
   }
 }
 
-template <int D, bool BF16, int ROWS>
-cudaError_t launch_dbr(const PagedLaunch& a) {
-  // decoding: every live segment at once, kWarps / 4 in a CTA; tiles: two
-  // rounds of kWarps segments per CTA
-  const unsigned y = ROWS == kPagedRows ? (unsigned)(a.rows * (D / 4) + 63) / 64 : D / 8;
-  return launch_dependent(paged_join_kernel<D, BF16, ROWS>, dim3((unsigned)a.grid, y), kThreads, 0,
-                          a.stream, a.params);
+// The decoding kernel's items: rows of D columns, kWays warps per segment of
+// 32 (row, four columns) elements.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) paged_join_rows_kernel(const PagedParams p) {
+  constexpr int kSegs = kWarps / kWays;  // at once
+  __shared__ Sum meet[kThreads];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp % kWays;
+  grid_wait();
+  grid_release();
+  const int4* d = p.desc + 2 * (2 * blockIdx.x + (blockIdx.y & 1));
+  const int4 item = d[0], seq = d[1];
+  const int parts = item.x;
+  if (parts == 0) return;
+  const int elements = seq.y * p.G * (D / 4);
+  const int slices = parts * (gridDim.y / 2), slice = item.y * (gridDim.y / 2) + (blockIdx.y >> 1);
+  for (int s0 = slice * kSegs; s0 * 32 < elements; s0 += slices * kSegs) {
+    const int e = (s0 + warp / kWays) * 32 + lane;
+    const int r = e / (D / 4), c4 = e % (D / 4);
+    const bool live = e < elements;
+    Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (live)
+      for (int k0 = way * 4; k0 < parts; k0 += kWays * 4)
+        add_parts<D, kPagedRows, 4>(p, s, blockIdx.x - item.y, e, r, k0, parts);
+    if (parts > 4) {  // the other warps have some
+      meet[threadIdx.x] = s;
+      __syncthreads();
+      if (way == 0) {
+#pragma unroll
+        for (int w = 1; w < kWays; ++w) {
+          const Sum& x = meet[threadIdx.x + 32 * w];
+          add(s, x.m, x.l, x.o);
+        }
+      }
+      __syncthreads();
+    }
+    const int token = r / p.G, head = r - token * p.G;  // of the sequence, of the group
+    if (live && way == 0)
+      store<D, BF16>(p, (size_t)(item.z * p.G + head) * p.total + seq.x + token, c4, s);
+  }
+}
+
+// The tile kernel's items: four columns of 256 rows at a time.  A warp takes
+// the same 32 rows throughout and walks two column groups at once.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) paged_join_tiles_kernel(const PagedParams p) {
+  const int r = threadIdx.x;
+  const int TT = 128 / p.G, head = (r & 127) / TT;
+  const int token_of = (r >> 7) * TT + (r & 127) - head * TT;
+  grid_wait();
+  grid_release();
+  const int4* d = p.desc + 2 * (2 * blockIdx.x + (blockIdx.y & 1));
+  const int4 item = d[0], seq = d[1];
+  const int parts = item.x;
+  const int token = item.w + token_of;
+  if (parts == 0 || head >= p.G || token >= seq.y) return;
+  const int slices = parts * (gridDim.y / 2), slice = item.y * (gridDim.y / 2) + (blockIdx.y >> 1);
+  const size_t row = (size_t)(item.z * p.G + head) * p.total + seq.x + token;
+  for (int c4 = 2 * slice; c4 < D / 4; c4 += 2 * slices) {
+    Sum s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k0 = 0; k0 < parts; k0 += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        add_parts<D, kPagedTileRows, 2>(p, s[h], blockIdx.x - item.y,
+                                        (c4 + h) * kPagedTileRows + r, r, k0, parts);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) store<D, BF16>(p, row, c4 + h, s[h]);
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_db(const PagedLaunch& a, bool decode) {
+  // per slot of a CTA (its item has two parts at least); rows: every live
+  // segment at once; tiles: 4
+  const unsigned y = decode ? (unsigned)(a.rows * (D / 4) + 127) / 128 : 4;
+  const dim3 grid((unsigned)a.grid, 2 * y);
+  return decode ? launch_dependent(paged_join_rows_kernel<D, BF16>, grid, kThreads, 0, a.stream,
+                                   a.params)
+                : launch_dependent(paged_join_tiles_kernel<D, BF16>, grid, kThreads, 0, a.stream,
+                                   a.params);
 }
 
 template <int D>
 cudaError_t launch_d(const PagedLaunch& a, bool bf16, bool decode) {
-  if (decode)
-    return bf16 ? launch_dbr<D, true, kPagedRows>(a) : launch_dbr<D, false, kPagedRows>(a);
-  return bf16 ? launch_dbr<D, true, kPagedTileRows>(a) : launch_dbr<D, false, kPagedTileRows>(a);
+  return bf16 ? launch_db<D, true>(a, decode) : launch_db<D, false>(a, decode);
 }
 
 }  // namespace
