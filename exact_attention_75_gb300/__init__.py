@@ -68,7 +68,7 @@ def lib() -> ctypes.CDLL:
         "attn_bwd": ([vp] * 10 + [sz, i, i, i, i, i, f, i, vp], i),
         "attn_rope": ([vp] * 6 + [i, i, vp] + [i] * 9 + [vp], i),
         "attn_append_kv": ([vp] * 11 + [i, vp] + [i] * 11 + [vp], i),
-        "attn_fwd_paged_workspace_bytes": ([i, i, i, i], sz),
+        "attn_fwd_paged_workspace_bytes": ([i, i, ctypes.c_int64, i, i, i], sz),
         "attn_fwd_paged": ([vp] * 9 + [sz] + [i] * 10 + [f, i, vp], i),
         "attn_quantize_fp8": ([vp, vp, vp, i, i, i, i, i, vp, i, vp], i),
         "attn_fwd_fp8": ([vp] * 8 + [i, i, i, i, i, f, vp], i),
@@ -566,10 +566,10 @@ def _rope(q, k, positions, table, interleaved, out_q, out_k, inverse):
     if k is not None:
         st += _turn_strides(k, "k") + _out_strides(out_k, k, dev, "out_k")
         if out_k is None:
-            out_k = k.new_empty(kshape)
+            out_k = torch.empty(kshape, dtype=q.dtype, device=q.device)
         okp = out_k.data_ptr()
     if out_q is None:
-        out_q = q.new_empty(shape)
+        out_q = torch.empty(shape, dtype=q.dtype, device=q.device)
     _call(lib().attn_rope, "attn_rope_bwd" if inverse else "attn_rope", dev, q.data_ptr(), kp,
           out_q.data_ptr(), okp, _I64[len(st)](*st), positions.data_ptr(), pos_batches, n_axes,
           table.data_ptr(), rot, 1 if interleaved else 0, inverse, B, H, Hkv, N, d, code)
@@ -673,7 +673,7 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
         st += _row_strides(q, "q")[:-1]
         qp = q.data_ptr()
         if out_q is None:
-            out_q = q.new_empty(qshape)
+            out_q = torch.empty(qshape, dtype=dt, device=q.device)
         elif out_q.shape != qshape or out_q.dtype != dt or out_q.get_device() != dev \
                 or not out_q.is_contiguous():
             raise ValueError("out_q must be contiguous with q's shape, dtype and device")
@@ -687,8 +687,11 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
     return out_q
 
 
-def fwd_paged_workspace_bytes(max_q: int, Hq: int, Hkv: int, d: int) -> int:
-    return int(lib().attn_fwd_paged_workspace_bytes(max_q, Hq, Hkv, d))
+def fwd_paged_workspace_bytes(n_seq: int, max_q: int, max_keys: int, Hq: int, Hkv: int,
+                              d: int) -> int:
+    """Workspace of fwd_paged for n_seq sequences, max_q new tokens and
+    max_keys = max_pages * page cached positions of each at most."""
+    return int(lib().attn_fwd_paged_workspace_bytes(n_seq, max_q, max_keys, Hq, Hkv, d))
 
 
 def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -727,16 +730,20 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                                   or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
     L = lib()
-    need = L.attn_fwd_paged_workspace_bytes(max_q, H, Hkv, d) if workspace is None else 0
-    if out is None:
-        out = q.new_empty(shape)
-    if lse is None:
-        lse = q.new_empty((H, total), dtype=torch.float32)
+    wp = ws = 0
     if workspace is None:
-        workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
+        ws = L.attn_fwd_paged_workspace_bytes(n_seq, max_q, max_pages * page, H, Hkv, d)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
+    if ws:
+        workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        wp, ws = workspace.data_ptr(), workspace.numel()
     _call(L.attn_fwd_paged, "attn_fwd_paged", dev, q.data_ptr(), k_pages.data_ptr(),
           v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
-          cu_seqlens.data_ptr(), kv_lens.data_ptr(), workspace.data_ptr(), workspace.numel(),
+          cu_seqlens.data_ptr(), kv_lens.data_ptr(), wp, ws,
           n_seq, max_q, total, n_pages, page, max_pages, H, Hkv, d, 1 if causal else 0,
           1.0 / math.sqrt(d) if scale is None else float(scale), _CODES[dt])
     return out, lse

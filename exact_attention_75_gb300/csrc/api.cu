@@ -433,6 +433,17 @@ bool strides_ok(const int64_t* s, int n) {
   return true;
 }
 
+// A decoding batch runs in clusters up to this many items (sequences x
+// key/value heads: the clusters are resident at once) and this reach of the
+// block table.  Measured per call in a graph, clusters against equal shares
+// (bf16, d = 128, 16 query heads on 4): 4 items of 64 keys 5.0 / 6.0 us, 1024
+// keys 5.9 / 8.6, 4096 keys 10.5 / 9.6, 8192 keys 16.5 / 11.5; 16 items of 2048
+// keys 8.6 / 9.1; 32 of up to 4096 13.8 / 15.1; 64 items of 256 keys 11.1 / 8.7,
+// 256 of 512 43 / 19.  Called without a graph, the one launch without a
+// workspace takes 18 to 19 us of the host against 24.
+constexpr int64_t kPagedClusterItems = 36;
+constexpr int64_t kPagedClusterKeys = 4096;
+
 int log2_of(int pow2) {
   int n = 0;
   while ((1 << n) < pow2) ++n;
@@ -456,16 +467,18 @@ attn_status paged_args(const void* k_pages, const void* v_pages, const int32_t* 
   return ATTN_OK;
 }
 
-// At most 16 query rows per sequence and key/value head run on the decoding
-// kernel (16 rows of the warp-level product, two CTAs per SM), more on the
-// tile kernel.
-bool paged_decode(int max_q, int group) { return (int64_t)max_q * group <= kPagedRows; }
-
-// The partial results of a grid in the workspace: desc, (m, l), O.
-struct PagedWorkspace {
-  size_t ml, o, bytes;
-  PagedWorkspace(bool decode, int d) {
-    const size_t ctas = decode ? 2 * kPagedMaxSms : kPagedMaxSms;
+// How a call runs: at most 16 query rows per sequence and key/value head on
+// the decoding kernel (16 rows of the warp-level product, two CTAs per SM),
+// more on the tile kernel, both in equal shares with the join behind them,
+// and small decoding batches in clusters, one launch without a workspace.
+struct PagedPlan {
+  bool decode, cluster;
+  size_t ml, o, bytes;  // partial results in the workspace: desc, (m, l), O
+  PagedPlan(int n_seq, int max_q, int64_t max_keys, int Hkv, int group, int d) {
+    decode = (int64_t)max_q * group <= kPagedRows;
+    cluster = decode && (int64_t)n_seq * Hkv <= kPagedClusterItems &&
+              max_keys <= kPagedClusterKeys;
+    const size_t ctas = cluster ? 0 : (decode ? 2 * kPagedMaxSms : kPagedMaxSms);
     const size_t rows = 2 * ctas * (decode ? kPagedRows : kPagedTileRows);
     ml = 4 * ctas * sizeof(int4);
     o = ml + rows * sizeof(float2);
@@ -580,10 +593,12 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
   return launch_result(launch_append(a, di->num_sms));
 }
 
-size_t attn_fwd_paged_workspace_bytes(int max_q, int Hq, int Hkv, int d) {
-  if (max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
+size_t attn_fwd_paged_workspace_bytes(int n_seq, int max_q, int64_t max_keys, int Hq, int Hkv,
+                                      int d) {
+  if (n_seq < 1 || max_q < 1 || max_keys < 1 || max_keys > 0x7FFF0000) return 0;
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (int64_t)n_seq * Hkv > 0x7FFFFFFF) return 0;
   if (d != 64 && d != 96 && d != 128) return 0;
-  return PagedWorkspace(paged_decode(max_q, Hq / Hkv), d).bytes;
+  return PagedPlan(n_seq, max_q, max_keys, Hkv, Hq / Hkv, d).bytes;
 }
 
 attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o,
@@ -592,8 +607,7 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
                            int n_seq, int max_q, int total, int n_pages, int page, int max_pages,
                            int Hq, int Hkv, int d, int causal, float scale, attn_dtype dtype,
                            void* stream) {
-  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned(workspace, 256))
-    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
   if (!dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
@@ -603,7 +617,8 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   if (max_q < 1 || max_q > total) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 96 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (Hq / Hkv > kPagedMaxGroup) return ATTN_ERR_UNSUPPORTED;
-  if (workspace_bytes < attn_fwd_paged_workspace_bytes(max_q, Hq, Hkv, d))
+  const PagedPlan plan(n_seq, max_q, (int64_t)max_pages * page, Hkv, Hq / Hkv, d);
+  if (plan.bytes > 0 && (workspace_bytes < plan.bytes || !aligned(workspace, 256)))
     return ATTN_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
@@ -631,15 +646,14 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   p.causal = causal;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = g_wait_limit_ns.load();
-  const bool decode = paged_decode(max_q, p.G);
-  const PagedWorkspace ws(decode, d);
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.desc = reinterpret_cast<int4*>(w);
-  p.part_ml = reinterpret_cast<float*>(w + ws.ml);
-  p.part_o = reinterpret_cast<float*>(w + ws.o);
+  p.part_ml = reinterpret_cast<float*>(w + plan.ml);
+  p.part_o = reinterpret_cast<float*>(w + plan.o);
+  const bool decode = plan.decode;
   p.min_share = decode ? 128 : 768;
   const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
-  a.grid = decode ? 2 * sms : sms;
+  a.grid = plan.cluster ? n_seq * Hkv * kPagedCluster : (decode ? 2 * sms : sms);
   a.rows = decode ? max_q * p.G : kPagedTileRows;
   a.stream = static_cast<cudaStream_t>(stream);
   // the cost of the largest batch of these sizes stays in 63 bits
@@ -655,8 +669,9 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
                             CU_TENSOR_MAP_SWIZZLE_128B, p.G))
     return ATTN_ERR_CUDA;
   const bool bf16 = dtype == ATTN_BF16;
-  cudaError_t e = decode ? launch_paged_decode(a, d, bf16) : launch_paged_tile(a, d, bf16);
-  if (e == cudaSuccess) e = launch_paged_join(a, d, bf16, decode);
+  cudaError_t e =
+      decode ? launch_paged_decode(a, d, bf16, plan.cluster) : launch_paged_tile(a, d, bf16);
+  if (e == cudaSuccess && !plan.cluster) e = launch_paged_join(a, d, bf16, decode);
   return launch_result(e);
 }
 

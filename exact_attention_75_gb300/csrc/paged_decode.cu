@@ -62,7 +62,10 @@ __device__ __forceinline__ int first_key(const Walk& w, int warp, int j) {
   return w.u0 * kUnit + (warp + j * kWarps) * kKeys;
 }
 
-template <int D, bool BF16>
+// CLUSTER: an item is shared by the kPagedCluster CTAs of a cluster, which
+// join their parts through each other's shared memory; otherwise the grid
+// takes equal shares of the whole batch and leaves parts to the join kernel.
+template <int D, bool BF16, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
@@ -87,8 +90,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tmV);
   }
   grid_wait();
-  if (threadIdx.x == 0) paged_clear(p);
-  Walk w = paged_start<Cost, kThreads>(p, p.max_q);
+  Walk w;
+  if constexpr (CLUSTER) {
+    const int item = blockIdx.x / kPagedCluster, rank = blockIdx.x % kPagedCluster;
+    w.b = item / p.Hkv;
+    w.head = item - w.b * p.Hkv;
+    w.sq = paged_seq(p, w.b);
+    w.nb = (w.sq.klen + kUnit - 1) / kUnit;
+    w.u0 = (int)((long long)rank * w.nb / kPagedCluster);
+    w.u1 = (int)((long long)(rank + 1) * w.nb / kPagedCluster);
+    w.x0 = 0;
+    w.take = 1;
+    w.left = w.sq.qlen > 0 ? 1 : 0;
+    if (threadIdx.x == 0 && rank == 0 && w.head == 0) paged_check(p, w.b);
+    __syncthreads();
+  } else {
+    if (threadIdx.x == 0) paged_clear(p);
+    w = paged_start<Cost, kThreads>(p, p.max_q);
+  }
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
@@ -135,9 +154,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   float* meet = reinterpret_cast<float*>(smem + L::kMeetOff);
   float2* meet_ml = reinterpret_cast<float2*>(smem + L::kMlOff);  // [kWarps][kMeet]
+  // The CTA's part of a cluster's item, over the idle ring: O, (m, l) by row.
+  float* part = reinterpret_cast<float*>(smem);
+  float2* part_ml = reinterpret_cast<float2*>(smem + kPagedRows * D * 4);
+  bool given_up = false;
 
   for (; w.left > 0; w.advance(p, p.max_q)) {
-    if (w.nothing()) continue;
+    if (!CLUSTER && w.nothing()) continue;
     const int nbw = warp_blocks(w, warp);
     const PagedSeq sq = w.sq;
     const int rows = min(kPagedRows, sq.qlen * p.G);
@@ -287,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // The warps leave together when one has given up; the barrier also frees
     // the meeting place from the piece before.
-    if (__syncthreads_or(aborted)) break;
+    given_up = __syncthreads_or(aborted);
+    if (given_up) break;
 
     lA += __shfl_xor_sync(0xffffffffu, lA, 1);
     lA += __shfl_xor_sync(0xffffffffu, lA, 2);
@@ -295,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     lB += __shfl_xor_sync(0xffffffffu, lB, 2);
 
     // The warps' (O, m, l) meet in shared memory, kMeet rows at a time.
-    const bool whole = w.whole();
+    const bool whole = !CLUSTER && w.whole();
     const size_t slot = 2 * (size_t)blockIdx.x + (w.x0 == 0 ? 1 : 0);
-    if (!whole && threadIdx.x == 0) w.describe(p, 0);
+    if (!CLUSTER && !whole && threadIdx.x == 0) w.describe(p, 0);
     for (int pass = 0; pass * kMeet < rows; ++pass) {
       if (pass > 0) __syncthreads();
       if ((r0 >> 2) == (pass & 1)) {
@@ -331,7 +355,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           acc.z += f * x.z;
           acc.w += f * x.w;
         }
-        if (whole) {
+        if constexpr (CLUSTER) {
+          *reinterpret_cast<float4*>(part + r * D + c) = acc;
+          if (c == 0) part_ml[r] = make_float2(M, lsum);
+        } else if (whole) {
           const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
           const size_t gr = grow(r);
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + c) = make_uint2(
@@ -346,6 +373,45 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
+  if constexpr (CLUSTER) {
+    if (w.sq.qlen > 0) {  // the same in every CTA of the cluster
+      cluster_sync();
+      const int rows = min(kPagedRows, w.sq.qlen * p.G);
+      const int rank = blockIdx.x % kPagedCluster;
+      for (int e = rank * kThreads + threadIdx.x; !given_up && e < rows * (D / 4);
+           e += kPagedCluster * kThreads) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4;
+        float2 ml[kPagedCluster];
+        float4 x[kPagedCluster];
+#pragma unroll
+        for (int k = 0; k < kPagedCluster; ++k) {
+          ml[k] = cluster_load2(smem_u32(part_ml + r), k);
+          x[k] = cluster_load4(smem_u32(part + r * D + c), k);
+        }
+        float M = ml[0].x;
+#pragma unroll
+        for (int k = 1; k < kPagedCluster; ++k) M = fmaxf(M, ml[k].x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lsum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPagedCluster; ++k) {
+          const float f = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
+          lsum += f * ml[k].y;
+          acc.x += f * x[k].x;
+          acc.y += f * x[k].y;
+          acc.z += f * x[k].z;
+          acc.w += f * x[k].w;
+        }
+        const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+        const int i = r / p.G, h = r - i * p.G;
+        const size_t gr = (size_t)(w.head * p.G + h) * p.total + w.sq.s0 + i;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + c) = make_uint2(
+            pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+        if (c == 0) p.lse[gr] = lsum > 0.f ? (M + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+      }
+      cluster_sync();  // the others have read this CTA's part
+    }
+  }
   // After an abort, copies still on their way must land before the CTA exits.
   Watchdog dw = wd;
   volatile int never = 0;
@@ -355,28 +421,35 @@ __global__ void __launch_bounds__(kThreads, 2)
   grid_release();
 }
 
-template <int D, bool BF16>
-cudaError_t launch_db(const PagedLaunch& a) {
+template <int D, bool BF16, bool CLUSTER>
+cudaError_t launch_dbc(const PagedLaunch& a) {
   using L = PagedDecodeLayout<D>;
   static DeviceFlags configured;
-  cudaError_t e = ensure_dyn_smem(paged_decode_kernel<D, BF16>, L::kBytes, configured);
+  auto kern = paged_decode_kernel<D, BF16, CLUSTER>;
+  cudaError_t e = ensure_dyn_smem(kern, L::kBytes, configured);
   if (e != cudaSuccess) return e;
-  return launch_dependent(paged_decode_kernel<D, BF16>, dim3((unsigned)a.grid), kThreads,
-                          L::kBytes, a.stream, a.tmK, a.tmV, a.params);
+  return launch_dependent<CLUSTER ? kPagedCluster : 1>(kern, dim3((unsigned)a.grid), kThreads,
+                                                       L::kBytes, a.stream, a.tmK, a.tmV,
+                                                       a.params);
+}
+
+template <int D, bool BF16>
+cudaError_t launch_db(const PagedLaunch& a, bool cluster) {
+  return cluster ? launch_dbc<D, BF16, true>(a) : launch_dbc<D, BF16, false>(a);
 }
 
 template <int D>
-cudaError_t launch_d(const PagedLaunch& a, bool bf16) {
-  return bf16 ? launch_db<D, true>(a) : launch_db<D, false>(a);
+cudaError_t launch_d(const PagedLaunch& a, bool bf16, bool cluster) {
+  return bf16 ? launch_db<D, true>(a, cluster) : launch_db<D, false>(a, cluster);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16) {
+cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16, bool cluster) {
   switch (d) {
-    case 64: return launch_d<64>(a, bf16);
-    case 96: return launch_d<96>(a, bf16);
-    default: return launch_d<128>(a, bf16);
+    case 64: return launch_d<64>(a, bf16, cluster);
+    case 96: return launch_d<96>(a, bf16, cluster);
+    default: return launch_d<128>(a, bf16, cluster);
   }
 }
 

@@ -21,8 +21,8 @@ constexpr int kMaxAttrDevices = 64;
 using DeviceFlags = std::atomic<bool>[kMaxAttrDevices];
 
 // Launches a kernel that calls grid_wait() as a programmatic dependent of the
-// previous kernel on the stream.
-template <typename Kern, typename... Args>
+// previous kernel on the stream, in clusters of CLUSTER CTAs.
+template <int CLUSTER = 1, typename Kern, typename... Args>
 cudaError_t launch_dependent(Kern kern, dim3 grid, int threads, int smem, cudaStream_t stream,
                              const Args&... args) {
   cudaLaunchConfig_t cfg = {};
@@ -30,11 +30,13 @@ cudaError_t launch_dependent(Kern kern, dim3 grid, int threads, int smem, cudaSt
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {CLUSTER, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 

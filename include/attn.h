@@ -319,11 +319,14 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
                            attn_dtype dtype, void* stream);
 
 /*
- * Bytes of device workspace attn_fwd_paged needs for at most max_q new tokens
- * per sequence (partial results of tiles whose keys are shared out over
- * several CTAs).  Returns 0 for sizes it does not take.
+ * Bytes of device workspace attn_fwd_paged needs for n_seq sequences of at
+ * most max_q new tokens and max_keys (= max_pages * page) cached positions:
+ * partial results of tiles whose keys are shared out over several CTAs.  0 if
+ * the call needs none (small decoding batches), and for sizes it does not
+ * take.
  */
-size_t attn_fwd_paged_workspace_bytes(int max_q, int Hq, int Hkv, int d);
+size_t attn_fwd_paged_workspace_bytes(int n_seq, int max_q, int64_t max_keys, int Hq, int Hkv,
+                                      int d);
 
 /*
  * Forward pass of new tokens against a paged cache (see attn_append_kv):
@@ -334,8 +337,8 @@ size_t attn_fwd_paged_workspace_bytes(int max_q, int Hq, int Hkv, int d);
  *   causal = 1: row i of a sequence's n rows sees keys j <= i + kv_lens[b] - n
  *               (the rows are the last positions); causal = 0: all kv_lens[b].
  *               A row that sees no key gets O = 0, LSE = -inf.
- *   workspace : >= attn_fwd_paged_workspace_bytes bytes, 256-byte aligned,
- *               caller-owned; contents on entry are ignored.  Calls in flight
+ *   workspace : >= attn_fwd_paged_workspace_bytes bytes, 256-byte aligned
+ *               (NULL if that is 0), caller-owned; contents on entry are ignored.  Calls in flight
  *               at once need one each; calls in stream order may share one.
  * Cache rows that no row of the batch sees may hold anything (NaN included).
  * A value row that is infinite or NaN may reach every row of its sequence.

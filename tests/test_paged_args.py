@@ -68,8 +68,8 @@ PAGED = dict(q=P, kp=P, vp=P, o=P, lse=P, table=P, cu=P, kv=P, ws=P, ws_bytes=1 
 
 @pytest.mark.parametrize("change,want", [
     (dict(q=BAD), INVALID), (dict(o=None), INVALID), (dict(lse=None), INVALID),
-    (dict(kp=BAD), INVALID), (dict(ws=BAD), INVALID), (dict(ws=None), INVALID),
-    (dict(ws_bytes=256), INVALID), (dict(max_q=0), INVALID), (dict(max_q=10), INVALID),
+    (dict(kp=BAD), INVALID), (dict(ws=BAD, max_q=9), INVALID), (dict(ws=None, max_q=9), INVALID),
+    (dict(ws_bytes=256, max_q=9), INVALID), (dict(max_q=0), INVALID), (dict(max_q=10), INVALID),
     (dict(Hq=5), INVALID), (dict(Hq=258), UNSUPPORTED), (dict(d=192), UNSUPPORTED),
     (dict(d=80), UNSUPPORTED), (dict(page=512), UNSUPPORTED), (dict(causal=2), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID),
@@ -79,8 +79,12 @@ def test_paged_refusals(L, change, want):
 
 
 def test_workspace_sizes(L):
-    assert attn.fwd_paged_workspace_bytes(1, 16, 4, 128) > 0
-    for bad in ((0, 16, 4, 128), (1, 16, 5, 128), (1, 16, 4, 192), (1, 0, 1, 64)):
+    assert attn.fwd_paged_workspace_bytes(64, 1, 65536, 16, 4, 128) > 0
+    assert attn.fwd_paged_workspace_bytes(1, 40, 64, 16, 4, 128) > 0
+    assert attn.fwd_paged_workspace_bytes(1, 1, 64, 16, 4, 128) == 0  # small: none needed
+    for bad in ((0, 40, 64, 16, 4, 128), (1, 0, 64, 16, 4, 128), (1, 40, 0, 16, 4, 128),
+                (1, 40, 1 << 40, 16, 4, 128), (1, 40, 64, 16, 5, 128), (1, 40, 64, 16, 4, 192),
+                (1, 40, 64, 0, 1, 64)):
         assert attn.fwd_paged_workspace_bytes(*bad) == 0
 
 

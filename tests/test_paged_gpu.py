@@ -58,6 +58,12 @@ def run(attn, x, causal, **kw):
                           causal=causal, **kw)
 
 
+def workspace_bytes(attn, x):
+    return attn.fwd_paged_workspace_bytes(len(x["kv"]), x["max_q"],
+                                          x["table"].shape[1] * x["k"].shape[2], x["q"].shape[0],
+                                          x["k"].shape[1], x["q"].shape[2])
+
+
 def check(x, o, lse, causal, scale=None):
     d = x["q"].shape[2]
     scale = d ** -0.5 if scale is None else scale
@@ -125,7 +131,7 @@ def test_padding_rows_are_left_alone_and_runs_repeat(attn_lib, lens, Hq):
     x = make(lens, Hq, 2, 128, 16, "bf16", seed=8, pad=5)
     live = int(x["cu"][-1])
     outs = []
-    ws = torch.full((attn_lib.fwd_paged_workspace_bytes(x["max_q"], Hq, 2, 128),), 0xFF,
+    ws = torch.full((workspace_bytes(attn_lib, x),), 0xFF,
                     dtype=torch.uint8, device="cuda")
     for fill in (3.0, -2.0):
         o = torch.full_like(x["q"], fill)
@@ -206,7 +212,7 @@ def test_captured_call_replays_with_new_lengths(attn_lib, chunk):
         s["table"] = torch.cat([s["table"], s["table"].new_zeros(2, wide - s["table"].shape[1])], 1)
         s["new"] = torch.randn(2, Hkv, s["q"].shape[1], d, device="cuda").to(dt)
     hold = {k: v.clone() if torch.is_tensor(v) else v for k, v in x.items()}
-    ws = torch.empty(attn_lib.fwd_paged_workspace_bytes(chunk, Hq, Hkv, d), dtype=torch.uint8,
+    ws = torch.empty(attn_lib.fwd_paged_workspace_bytes(2, chunk, 4096, Hq, Hkv, d), dtype=torch.uint8,
                      device="cuda")
 
     def step(s):
