@@ -487,8 +487,15 @@ def _row_strides(t: torch.Tensor, what: str, written: bool = False) -> Tuple[int
 
 def _turn_strides(t: torch.Tensor, what: str, written: bool = False) -> Tuple[int, ...]:
     """Batch, head and token strides of a [B, H, N, d] or packed [H, N, d] tensor."""
-    st = _row_strides(t, what, written)
-    return st[:3] if len(st) == 4 else (0, st[0], st[1])
+    st = t.stride()
+    if len(st) == 4:
+        b, h, n, one = st
+    else:
+        (h, n, one), b = st, 0
+    if one != 1 or (b | h | n) & 7 or written:
+        st = _row_strides(t, what, written)
+        return st[:3] if len(st) == 4 else (0, st[0], st[1])
+    return b, h, n
 
 
 def _out_strides(out: Optional[torch.Tensor], x: torch.Tensor, device: int,

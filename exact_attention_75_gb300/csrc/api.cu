@@ -654,7 +654,6 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   p.min_share = decode ? 128 : 768;
   const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
   a.grid = plan.cluster ? n_seq * Hkv * kPagedCluster : (decode ? 2 * sms : sms);
-  a.rows = decode ? max_q * p.G : kPagedTileRows;
   a.stream = static_cast<cudaStream_t>(stream);
   // the cost of the largest batch of these sizes stays in 63 bits
   const int64_t keys = 3 * ((int64_t)max_pages * page + 1024);

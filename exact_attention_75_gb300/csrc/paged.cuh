@@ -67,7 +67,6 @@ struct PagedLaunch {
   CUtensorMap tmK, tmV;     // [n_pages * Hkv, page, D]
   PagedParams params;
   int grid;                 // CTAs of the main kernel
-  int rows;                 // rows of an item at most
   cudaStream_t stream;
 };
 

@@ -112,10 +112,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
   // The warp's stream of blocks runs over the pieces without a break: ahead
-  // walks it as far as the ring reaches, the page of its next block already
-  // read.  issued, it: blocks issued to and taken from the ring.
+  // walks it as far as the ring reaches.  Lane i holds the page of the piece's
+  // block 32 n + i, so that a table read's latency is paid once in 32 blocks.
+  // issued, it: blocks issued to and taken from the ring.
   Walk ahead = w;
-  int aj = 0, an = w.left > 0 ? warp_blocks(w, warp) : 0, apage = -1;
+  int aj = 0, an = w.left > 0 ? warp_blocks(w, warp) : 0, pages = -1;
   uint32_t issued = 0, it = 0;
   auto find_next = [&]() {  // settles ahead on its next block, or on left <= 0
     while (ahead.left > 0 && aj >= an) {
@@ -123,20 +124,24 @@ __global__ void __launch_bounds__(kThreads, 2)
       an = warp_blocks(ahead, warp);
       aj = 0;
     }
-    if (ahead.left > 0)
-      apage = __ldg(p.block_table + (size_t)ahead.b * p.max_pages +
-                    (first_key(ahead, warp, aj) >> p.page_log2));
+    if (ahead.left > 0 && (aj & 31) == 0) {
+      const int j = aj + lane;
+      pages = j < an ? __ldg(p.block_table + (size_t)ahead.b * p.max_pages +
+                             (first_key(ahead, warp, j) >> p.page_log2))
+                     : -1;
+    }
   };
   auto issue = [&]() {
     if (ahead.left <= 0) return;
+    const int page = __shfl_sync(0xffffffffu, pages, aj & 31);
     if (lane == 0) {
       const int s = (int)(issued % NS);
       const uint32_t dk = ring + (uint32_t)(s * L::kSlotBytes);
       const uint32_t dv = dk + L::kChunks * kBoxBytes;
-      const bool ok = apage >= 0 && apage < p.n_pages;
+      const bool ok = page >= 0 && page < p.n_pages;
       if (!ok)
         atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(ahead.b, 0xFFFF) << 16));
-      const int z = ok ? apage * p.Hkv + ahead.head : -1;  // -1: the box reads zeros
+      const int z = ok ? page * p.Hkv + ahead.head : -1;  // -1: the box reads zeros
       const int y = first_key(ahead, warp, aj) & (p.page - 1);
       mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
 #pragma unroll

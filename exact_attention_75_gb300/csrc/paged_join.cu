@@ -22,7 +22,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kWays = 4;  // warps that share a segment's parts (decoding)
 
 struct Sum {
   float m, l;
@@ -71,35 +70,37 @@ __device__ __forceinline__ void add_parts(const PagedParams& p, Sum& s, int firs
   }
 }
 
-// The decoding kernel's items: rows of D columns, kWays warps per segment of
-// 32 (row, four columns) elements.
+// The decoding kernel's items: rows of D columns.  Up to 4 parts a warp takes
+// a segment of 32 (row, four columns) elements alone, beyond that 4 warps
+// share a segment's parts, beyond 16 parts 8 warps (one item of 65536 keys,
+// some 76 parts: 30.8 us of kernel and join against 32.8 with 4 warps; 64 items
+// of 1024 keys: 16.4 with 4, 19.4 with 8).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) paged_join_rows_kernel(const PagedParams p) {
-  constexpr int kSegs = kWarps / kWays;  // at once
   __shared__ Sum meet[kThreads];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp % kWays;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_wait();
   grid_release();
-  const int4* d = p.desc + 2 * (2 * blockIdx.x + (blockIdx.y & 1));
+  const int4* d = p.desc + 2 * (2 * blockIdx.x + blockIdx.y);
   const int4 item = d[0], seq = d[1];
   const int parts = item.x;
   if (parts == 0) return;
+  const int ways = parts > 16 ? 8 : (parts > 4 ? 4 : 1), segs = kWarps / ways;
+  const int way = warp % ways;
   const int elements = seq.y * p.G * (D / 4);
-  const int slices = parts * (gridDim.y / 2), slice = item.y * (gridDim.y / 2) + (blockIdx.y >> 1);
-  for (int s0 = slice * kSegs; s0 * 32 < elements; s0 += slices * kSegs) {
-    const int e = (s0 + warp / kWays) * 32 + lane;
+  for (int s0 = item.y * segs; s0 * 32 < elements; s0 += parts * segs) {
+    const int e = (s0 + warp / ways) * 32 + lane;
     const int r = e / (D / 4), c4 = e % (D / 4);
     const bool live = e < elements;
     Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (live)
-      for (int k0 = way * 4; k0 < parts; k0 += kWays * 4)
+      for (int k0 = way * 4; k0 < parts; k0 += ways * 4)
         add_parts<D, kPagedRows, 4>(p, s, blockIdx.x - item.y, e, r, k0, parts);
-    if (parts > 4) {  // the other warps have some
+    if (ways > 1) {
       meet[threadIdx.x] = s;
       __syncthreads();
       if (way == 0) {
-#pragma unroll
-        for (int w = 1; w < kWays; ++w) {
+        for (int w = 1; w < ways; ++w) {
           const Sum& x = meet[threadIdx.x + 32 * w];
           add(s, x.m, x.l, x.o);
         }
@@ -145,10 +146,8 @@ __global__ void __launch_bounds__(kThreads, 4) paged_join_tiles_kernel(const Pag
 
 template <int D, bool BF16>
 cudaError_t launch_db(const PagedLaunch& a, bool decode) {
-  // per slot of a CTA (its item has two parts at least); rows: every live
-  // segment at once; tiles: 4
-  const unsigned y = decode ? (unsigned)(a.rows * (D / 4) + 127) / 128 : 4;
-  const dim3 grid((unsigned)a.grid, 2 * y);
+  // a CTA per slot of the main kernel's, four for tiles
+  const dim3 grid((unsigned)a.grid, decode ? 2 : 8);
   return decode ? launch_dependent(paged_join_rows_kernel<D, BF16>, grid, kThreads, 0, a.stream,
                                    a.params)
                 : launch_dependent(paged_join_tiles_kernel<D, BF16>, grid, kThreads, 0, a.stream,
