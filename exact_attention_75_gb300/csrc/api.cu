@@ -461,7 +461,7 @@ attn_status paged_args(const void* k_pages, const void* v_pages, const int32_t* 
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256)
     return ATTN_ERR_UNSUPPORTED;
-  if ((int64_t)max_pages * page > 0x7FFF0000 || (int64_t)n_pages * Hkv > 0x7FFFFFFF ||
+  if ((int64_t)max_pages * page > (1 << 30) || (int64_t)n_pages * Hkv > 0x7FFFFFFF ||
       (int64_t)n_seq * Hkv > 0x7FFFFFFF || (int64_t)Hq * total > 0x7FFFFFFF)
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
@@ -595,7 +595,7 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
 
 size_t attn_fwd_paged_workspace_bytes(int n_seq, int max_q, int64_t max_keys, int Hq, int Hkv,
                                       int d) {
-  if (n_seq < 1 || max_q < 1 || max_keys < 1 || max_keys > 0x7FFF0000) return 0;
+  if (n_seq < 1 || max_q < 1 || max_keys < 1 || max_keys > (1 << 30)) return 0;
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (int64_t)n_seq * Hkv > 0x7FFFFFFF) return 0;
   if (d != 64 && d != 96 && d != 128) return 0;
   return PagedPlan(n_seq, max_q, max_keys, Hkv, Hq / Hkv, d).bytes;

@@ -154,24 +154,24 @@ struct PagedWalk {
   long long share;
   int b, head, item;  // sequence, key/value head, tile of rows
   PagedSeq sq;
-  long long x0, take; // the piece: [x0, x0 + take) of the item's cost
+  uint32_t x0, take;  // the piece: [x0, x0 + take) of the item's cost (keys <= 2^30, times 3)
   int nb;             // the item's key blocks
   int u0, u1;         // those of the piece
   bool two;           // rows in the item's second half
 
   __device__ __forceinline__ int key_cost() const { return two ? Cost::KEY2 : Cost::KEY1; }
   // Blocks that start before offset x of the item.
-  __device__ __forceinline__ int blocks(long long x) const {
-    constexpr unsigned long long c1 = Cost::UNIT * Cost::KEY1, c2 = Cost::UNIT * Cost::KEY2;
-    const unsigned long long n = two ? ((unsigned long long)x + c2 - 1) / c2
-                                     : ((unsigned long long)x + c1 - 1) / c1;
-    return (int)min(n, (unsigned long long)nb);
+  __device__ __forceinline__ int blocks(uint32_t x) const {
+    constexpr uint32_t c1 = Cost::UNIT * Cost::KEY1, c2 = Cost::UNIT * Cost::KEY2;
+    const uint32_t n = two ? x / c2 + (x % c2 != 0) : x / c1 + (x % c1 != 0);
+    return min((int)n, nb);
   }
   __device__ __forceinline__ void piece(const PagedParams& p, int W) {
     const int keys = paged_keys(sq, W, p.causal, item);
     two = paged_two(sq, W, item);
     nb = (keys + Cost::UNIT - 1) / Cost::UNIT;
-    take = min((long long)keys * key_cost() + Cost::OVERHEAD - x0, left);
+    const uint32_t rest = (uint32_t)keys * key_cost() + Cost::OVERHEAD - x0;
+    take = left < (long long)rest ? (uint32_t)left : rest;
     u0 = blocks(x0);
     u1 = blocks(x0 + take);
   }
@@ -250,7 +250,11 @@ __device__ __forceinline__ PagedWalk<Cost> paged_start(const PagedParams& p, int
     if (w < warp) before += warp_sum[w];
     all += warp_sum[w];
   }
-  const long long share = max((all + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
+  // (a 32-bit division where it does; the 64-bit one costs three times as much)
+  const long long share =
+      max(all >> 31 ? (all - 1) / gridDim.x + 1
+                    : (long long)(((uint32_t)all + gridDim.x - 1) / gridDim.x),
+          (long long)p.min_share);
   const long long s = share * blockIdx.x;
   long long at = before + incl - sum;
   if (s < all && s >= at && s < at + sum) {
@@ -268,7 +272,10 @@ __device__ __forceinline__ PagedWalk<Cost> paged_start(const PagedParams& p, int
     w.sq = sq;
     w.share = share;
     w.left = min(share, all - s);
-    w.head = (int)((s - at) / line);
+    // the head by a rounded quotient, put right by at most a few steps
+    w.head = min((int)__fdividef((float)(s - at), (float)line), p.Hkv - 1);
+    while (w.head * line > s - at) --w.head;
+    while ((w.head + 1) * line <= s - at) ++w.head;
     const long long off = s - at - w.head * line;
     int lo = 0, hi = paged_items(sq, W) - 1;  // the last item that starts at or before off
     while (lo < hi) {
@@ -277,7 +284,7 @@ __device__ __forceinline__ PagedWalk<Cost> paged_start(const PagedParams& p, int
       else hi = mid - 1;
     }
     w.item = lo;
-    w.x0 = off - paged_line<Cost>(sq, W, p.causal, lo);
+    w.x0 = (uint32_t)(off - paged_line<Cost>(sq, W, p.causal, lo));
     w.piece(p, W);
     start = w;
   }

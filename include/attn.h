@@ -279,6 +279,7 @@ attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
  *                 128, 256} rows (ATTN_ERR_UNSUPPORTED otherwise).
  *   block_table : DEVICE int32 [n_seq, max_pages]: position p of sequence b
  *                 lies in row p % page of page block_table[b, p / page].
+ *                 max_pages * page <= 2^30.
  *                 Entries past a sequence's length are not read.
  *   cu_seqlens  : DEVICE int32 [n_seq + 1], cu_seqlens[0] = 0, non-decreasing,
  *                 the last at most total: sequence b's new tokens are rows
