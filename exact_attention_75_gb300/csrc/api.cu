@@ -422,7 +422,7 @@ bool aligned(const void* p, uintptr_t n) {
 
 // A rotary table of rot turning channels, positions on n_axes axes.
 bool rotary_ok(const int64_t* table, int rot, int n_axes, int d) {
-  return aligned(table, 8) && rot >= 16 && rot <= d && rot % 16 == 0 && n_axes >= 1 &&
+  return aligned16(table) && rot >= 16 && rot <= d && rot % 16 == 0 && n_axes >= 1 &&
          n_axes <= kMaxAxes;
 }
 
@@ -461,7 +461,7 @@ attn_status paged_args(const void* k_pages, const void* v_pages, const int32_t* 
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256)
     return ATTN_ERR_UNSUPPORTED;
-  if ((int64_t)max_pages * page > (1 << 30) || (int64_t)n_pages * Hkv > 0x7FFFFFFF ||
+  if ((int64_t)max_pages * page > (1 << 29) || (int64_t)n_pages * Hkv > 0x7FFFFFFF ||
       (int64_t)n_seq * Hkv > 0x7FFFFFFF || (int64_t)Hq * total > 0x7FFFFFFF)
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
@@ -595,7 +595,7 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
 
 size_t attn_fwd_paged_workspace_bytes(int n_seq, int max_q, int64_t max_keys, int Hq, int Hkv,
                                       int d) {
-  if (n_seq < 1 || max_q < 1 || max_keys < 1 || max_keys > (1 << 30)) return 0;
+  if (n_seq < 1 || max_q < 1 || max_keys < 1 || max_keys > (1 << 29)) return 0;
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (int64_t)n_seq * Hkv > 0x7FFFFFFF) return 0;
   if (d != 64 && d != 96 && d != 128) return 0;
   return PagedPlan(n_seq, max_q, max_keys, Hkv, Hq / Hkv, d).bytes;
@@ -651,12 +651,12 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   p.part_ml = reinterpret_cast<float*>(w + plan.ml);
   p.part_o = reinterpret_cast<float*>(w + plan.o);
   const bool decode = plan.decode;
-  p.min_share = decode ? 128 : 768;
+  p.min_share = decode ? 128 : 1024;
   const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
   a.grid = plan.cluster ? n_seq * Hkv * kPagedCluster : (decode ? 2 * sms : sms);
   a.stream = static_cast<cudaStream_t>(stream);
   // the cost of the largest batch of these sizes stays in 63 bits
-  const int64_t keys = 3 * ((int64_t)max_pages * page + 1024);
+  const int64_t keys = 4 * ((int64_t)max_pages * page + 1024);
   const int64_t items = (((int64_t)total * p.G) / 64 + n_seq) * Hkv;
   if (keys > INT64_MAX / items) return ATTN_ERR_INVALID_ARG;
   const int64_t heads = (int64_t)n_pages * Hkv;

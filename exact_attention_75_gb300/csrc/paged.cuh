@@ -154,7 +154,7 @@ struct PagedWalk {
   long long share;
   int b, head, item;  // sequence, key/value head, tile of rows
   PagedSeq sq;
-  uint32_t x0, take;  // the piece: [x0, x0 + take) of the item's cost (keys <= 2^30, times 3)
+  uint32_t x0, take;  // the piece: [x0, x0 + take) of the item's cost (keys <= 2^29, times 4)
   int nb;             // the item's key blocks
   int u0, u1;         // those of the piece
   bool two;           // rows in the item's second half

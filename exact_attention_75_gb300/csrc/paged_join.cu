@@ -3,11 +3,10 @@
 //   M = max m_k,  l = sum l_k 2^(m_k - M),  O = sum O_k 2^(m_k - M) / l.
 //
 // A warp takes a segment of 32 (row, four columns) elements, contiguous in
-// every part (512 bytes a read), four parts in flight at a time.  The
-// decoding kernel's items are small and may be spread over every CTA (one
-// sequence with a long cache), so four warps share the parts of a segment and
-// meet in shared memory; a pair of query tiles has enough segments.  Launched
-// as a programmatic dependent of the kernel that wrote the parts.
+// every part (512 bytes a read), up to four parts in flight at a time; where
+// an item has many parts (one sequence with a long cache is spread over every
+// CTA), several warps share them and meet in shared memory.  Launched as a
+// programmatic dependent of the kernel that wrote the parts.
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -113,34 +112,69 @@ __global__ void __launch_bounds__(kThreads, 4) paged_join_rows_kernel(const Page
   }
 }
 
-// The tile kernel's items: four columns of 256 rows at a time.  A warp takes
-// the same 32 rows throughout and walks two column groups at once.
+// The tile kernel's items, four columns of 256 rows at a time.  Up to 4 parts a
+// thread takes a row and walks two column groups at once; beyond that one, and
+// beyond 16 parts four threads share a row's parts (a 64-token chunk of 4
+// key/value heads over 32768 keys, 38 parts an item: 44 us of kernel and join
+// with the first form alone).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) paged_join_tiles_kernel(const PagedParams p) {
-  const int r = threadIdx.x;
-  const int TT = 128 / p.G, head = (r & 127) / TT;
-  const int token_of = (r >> 7) * TT + (r & 127) - head * TT;
+  __shared__ Sum meet[kThreads];
   grid_wait();
   grid_release();
   const int4* d = p.desc + 2 * (2 * blockIdx.x + (blockIdx.y & 1));
   const int4 item = d[0], seq = d[1];
   const int parts = item.x;
-  const int token = item.w + token_of;
-  if (parts == 0 || head >= p.G || token >= seq.y) return;
+  if (parts == 0) return;
+  const int TT = 128 / p.G;
+  // row r of the item: whether it is one, and its row of O
+  auto place = [&](int r, size_t& row) {
+    const int head = (r & 127) / TT;
+    const int token = item.w + (r >> 7) * TT + (r & 127) - head * TT;
+    row = (size_t)(item.z * p.G + head) * p.total + seq.x + token;
+    return head < p.G && token < seq.y;
+  };
+  const int first = blockIdx.x - item.y;
   const int slices = parts * (gridDim.y / 2), slice = item.y * (gridDim.y / 2) + (blockIdx.y >> 1);
-  const size_t row = (size_t)(item.z * p.G + head) * p.total + seq.x + token;
-  for (int c4 = 2 * slice; c4 < D / 4; c4 += 2 * slices) {
-    Sum s[2];
+  size_t row;
+  if (parts <= 4) {
+    const int r = threadIdx.x;
+    if (!place(r, row)) return;
+    for (int c4 = 2 * slice; c4 < D / 4; c4 += 2 * slices) {
+      Sum s[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) s[h] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int k0 = 0; k0 < parts; k0 += 2) {
+      for (int h = 0; h < 2; ++h) s[h] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int k0 = 0; k0 < parts; k0 += 2) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        add_parts<D, kPagedTileRows, 2>(p, s[h], blockIdx.x - item.y,
-                                        (c4 + h) * kPagedTileRows + r, r, k0, parts);
+        for (int h = 0; h < 2; ++h)
+          add_parts<D, kPagedTileRows, 2>(p, s[h], first, (c4 + h) * kPagedTileRows + r, r, k0,
+                                          parts);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) store<D, BF16>(p, row, c4 + h, s[h]);
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) store<D, BF16>(p, row, c4 + h, s[h]);
+    return;
+  }
+  const int ways = parts > 16 ? 4 : 1, rows = kThreads / ways;  // rows at once
+  const int way = threadIdx.x / rows;
+  for (int u = slice; u < D / 4 * ways; u += slices) {
+    const int c4 = u / ways, r = u % ways * rows + threadIdx.x % rows;
+    const bool live = place(r, row);
+    Sum s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k0 = way * 4; live && k0 < parts; k0 += ways * 4)
+      add_parts<D, kPagedTileRows, 4>(p, s, first, c4 * kPagedTileRows + r, r, k0, parts);
+    if (ways > 1) {
+      meet[threadIdx.x] = s;
+      __syncthreads();
+      if (way == 0) {
+        for (int w = 1; w < ways; ++w) {
+          const Sum& x = meet[threadIdx.x + rows * w];
+          add(s, x.m, x.l, x.o);
+        }
+      }
+      __syncthreads();
+    }
+    if (live && way == 0) store<D, BF16>(p, row, c4, s);
   }
 }
 

@@ -54,9 +54,10 @@ struct PagedTileLayout {
 };
 
 // A walk along the CTA's share; an item is a pair of tiles of TT tokens each.
-// A key block of one tile takes two thirds of the time of a pair's (measured
-// 1.06 against 1.55 us, the items' borders 3 to 4 us).
-using Cost = PagedCost<128, 2, 3, 768>;
+// Weights: a key block of one tile was measured at 1.06 us, of a pair at 1.55,
+// an item's borders at 3 to 4 us; 3 : 4 and two blocks an item balance best (a
+// mixed batch 58.5 us, with 2 : 3 59.8, with equal weights 60.4).
+using Cost = PagedCost<128, 3, 4, 1024>;
 struct Walk : PagedWalk<Cost> {
   int n[2];  // key blocks of the piece that tile 0 / 1 sees (two: tile 1 has rows)
 
@@ -109,12 +110,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_fence_init();
   }
+  grid_wait();
+  // Tensor memory only now: held earlier, it could be what a block of the
+  // previous kernel still waits for.
   if (warp == kWarpMma) {
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  grid_wait();
   if (threadIdx.x == 0) paged_clear(p);
   Walk w;
   static_cast<PagedWalk<Cost>&>(w) = paged_start<Cost, kThreads>(p, 2 * TT);  // a CTA barrier

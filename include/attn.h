@@ -259,8 +259,9 @@ attn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const v
  *               non-negative multiple of 8.
  *   positions : DEVICE int32 [n_axes, pos_batches, N]; pos_batches = B, or 1
  *               for one set of positions shared by the batch.  Any value.
- *   table     : DEVICE int64 [2, rot/2]: f_p in units of 2^-64 turns (radians
- *               / 2 pi, modulo 1 turn), then axis_p (clamped to [0, n_axes)).
+ *   table     : DEVICE int64 [2, rot/2], 16-byte aligned: f_p in units of 2^-64
+ *               turns (radians / 2 pi, modulo 1 turn), then axis_p (clamped to
+ *               [0, n_axes)).
  *   rot       : a multiple of 16, 16 <= rot <= d;  1 <= n_axes <= 8.
  * d in {64, 96, 128, 192, 256}; B <= 65535, (Hq + Hkv) * N < 2^31.  Angles are formed
  * modulo a turn in 64-bit integers, so they hold at any position; values are
@@ -279,7 +280,7 @@ attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
  *                 128, 256} rows (ATTN_ERR_UNSUPPORTED otherwise).
  *   block_table : DEVICE int32 [n_seq, max_pages]: position p of sequence b
  *                 lies in row p % page of page block_table[b, p / page].
- *                 max_pages * page <= 2^30.
+ *                 max_pages * page <= 2^29.
  *                 Entries past a sequence's length are not read.
  *   cu_seqlens  : DEVICE int32 [n_seq + 1], cu_seqlens[0] = 0, non-decreasing,
  *                 the last at most total: sequence b's new tokens are rows

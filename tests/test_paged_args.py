@@ -31,7 +31,7 @@ ROPE = dict(q=P, k=P, oq=P, ok=P, strides=_strides(12), pos=P, pos_batches=1, ax
 @pytest.mark.parametrize("change,want", [
     (dict(q=BAD), INVALID), (dict(oq=None), INVALID), (dict(k=None), INVALID),
     (dict(ok=None), INVALID), (dict(k=None, ok=None), INVALID), (dict(Hkv=0), INVALID),
-    (dict(table=None), INVALID), (dict(pos=None), INVALID), (dict(pos_batches=3), INVALID),
+    (dict(table=None), INVALID), (dict(table=BAD), INVALID), (dict(pos=None), INVALID), (dict(pos_batches=3), INVALID),
     (dict(rot=0), INVALID), (dict(rot=24), INVALID), (dict(rot=80), INVALID),
     (dict(axes=0), INVALID), (dict(axes=9), INVALID), (dict(strides=_strides(12, 63)), INVALID),
     (dict(strides=_strides(12, -64)), INVALID), (dict(strides=None), INVALID),
@@ -55,7 +55,7 @@ APPEND = dict(k=P, v=P, q=P, oq=P, strides=_strides(6), kp=P, vp=P, table=P, cu=
     (dict(page=8), UNSUPPORTED), (dict(d=72), UNSUPPORTED), (dict(rot=128), INVALID),
     (dict(rtable=None, pos=P), INVALID), (dict(n_seq=0), INVALID), (dict(total=0), INVALID),
     (dict(n_pages=0), INVALID), (dict(max_pages=0), INVALID), (dict(Hkv=0), INVALID),
-    (dict(max_pages=1 << 28), INVALID), (dict(n_pages=1 << 30), INVALID),
+    (dict(max_pages=1 << 26), INVALID), (dict(rtable=BAD), INVALID), (dict(n_pages=1 << 30), INVALID),
     (dict(strides=_strides(6, 12)), INVALID), (dict(inter=3), INVALID)])
 def test_append_refusals(L, change, want):
     assert L.attn_append_kv(*dict(APPEND, **change).values()) == want

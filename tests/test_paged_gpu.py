@@ -104,6 +104,22 @@ def test_few_rows(attn_lib, causal, dtype, d, lens, Hq, Hkv, page):
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
 @pytest.mark.parametrize("lens,Hq,Hkv,page", [
+    (DECODE * 5, 4, 1, 16), (DECODE * 3, 8, 4, 64), (DRAFTS * 4, 10, 2, 32), ([(1, 5000)], 16, 1, 256),
+    ([(2, 4700), (1, 4097)], 4, 2, 16), ([(1, 1)] * 400, 1, 1, 16), ([(1, 64)] * 37, 2, 1, 64),
+    ([(16, 900)] * 38, 1, 1, 32)])
+def test_few_rows_in_equal_shares(attn_lib, causal, dtype, d, lens, Hq, Hkv, page):
+    """Batches past the sizes that run in clusters: pieces of items, items of
+    one CTA, items spread over many, CTAs without work."""
+    x = make(lens, Hq, Hkv, d, page, dtype, seed=d + page + len(lens), pad=1)
+    assert workspace_bytes(attn_lib, x) > 0
+    o, lse = run(attn_lib, x, causal)
+    assert attn_lib.poll_status() == (0, 0)
+    check(x, o, lse, causal)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("lens,Hq,Hkv,page", [
     (CHUNKS, 4, 2, 16), (CHUNKS, 2, 2, 64), (CHUNKS, 3, 1, 32), (CHUNKS, 7, 1, 128),
     ([(33, 1000)], 8, 1, 256), ([(1, 100), (1, 900)], 34, 1, 64), ([(9, 50), (2, 600)], 128, 1, 16),
     ([(700, 700)], 1, 1, 64), ([(257, 1500)], 2, 1, 16), ([(18, 20)] * 40, 1, 1, 16)])
@@ -126,12 +142,22 @@ def test_rows_without_a_key(attn_lib, causal, lens, Hq, Hkv):
     check(x, o, lse, causal)
 
 
-@pytest.mark.parametrize("lens,Hq", [(DECODE, 4), (CHUNKS, 4)])
+@pytest.mark.parametrize("max_q,n_seq", [(1, 2), (1, 50), (30, 2)])
+def test_no_new_tokens_at_all(attn_lib, max_q, n_seq):
+    x = make([(0, 5), (0, 0)] * (n_seq // 2), 4, 2, 64, 16, "bf16", seed=6, pad=30)
+    o = torch.full_like(x["q"], 5.0)
+    lse = torch.full(x["q"].shape[:2], 5.0, device="cuda")
+    run(attn_lib, dict(x, max_q=max_q), True, out=o, lse=lse)
+    assert attn_lib.poll_status() == (0, 0)
+    assert (o == 5.0).all() and (lse == 5.0).all()
+
+
+@pytest.mark.parametrize("lens,Hq", [(DECODE, 4), (DECODE * 5, 4), (CHUNKS, 4)])
 def test_padding_rows_are_left_alone_and_runs_repeat(attn_lib, lens, Hq):
     x = make(lens, Hq, 2, 128, 16, "bf16", seed=8, pad=5)
     live = int(x["cu"][-1])
     outs = []
-    ws = torch.full((workspace_bytes(attn_lib, x),), 0xFF,
+    ws = torch.full((max(workspace_bytes(attn_lib, x), 256),), 0xFF,
                     dtype=torch.uint8, device="cuda")
     for fill in (3.0, -2.0):
         o = torch.full_like(x["q"], fill)
@@ -143,7 +169,8 @@ def test_padding_rows_are_left_alone_and_runs_repeat(attn_lib, lens, Hq):
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
 
 
-@pytest.mark.parametrize("lens", [[(1, 700), (1, 64)], [(40, 700), (1, 64)]])
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 64)], [(1, 700), (1, 64)] * 12,
+                                  [(40, 700), (1, 64)]])
 @pytest.mark.parametrize("amp,scale", [(30.0, None), (1.0, 1e-4)])
 def test_large_and_small_logits(attn_lib, lens, amp, scale):
     x = make(lens, 4, 2, 128, 32, "fp16", seed=11, amp=amp)
@@ -152,7 +179,8 @@ def test_large_and_small_logits(attn_lib, lens, amp, scale):
     check(x, o, lse, True, scale)
 
 
-@pytest.mark.parametrize("lens", [[(1, 50), (1, 40), (1, 30)], [(50, 50), (1, 40), (20, 30)]])
+@pytest.mark.parametrize("lens", [[(1, 50), (1, 40), (1, 30)], [(1, 50), (1, 40), (1, 30)] * 8,
+                                  [(50, 50), (1, 40), (20, 30)]])
 def test_bad_pages_lengths_and_offsets_are_reported(attn_lib, lens):
     """Out-of-range page numbers, lengths past the table and offsets past the
     tensors: the call reports them and the other sequences keep their values."""
@@ -175,11 +203,11 @@ def test_bad_pages_lengths_and_offsets_are_reported(attn_lib, lens):
         o, _ = run(attn_lib, c, True)
         st, detail = attn_lib.poll_status()
         assert st == 1 and detail >> 16 == 1, (i, st, hex(detail))
-        for b in (0, 2):
+        for b in [j for j in range(len(lens)) if j != 1]:
             assert torch.isfinite(o[:, cu[b]:cu[b + 1]]).all()
             err = (o - good)[:, cu[b]:cu[b + 1]].float().abs().max()
             assert err <= 2 ** -5 * good.float().abs().max(), (i, b)
-    for bad in ([0, cu[1], cu[1] - 1, cu[3]], [0, cu[1], cu[2], cu[3] + 9], [1] + cu[1:]):
+    for bad in (cu[:2] + [cu[1] - 1] + cu[3:], cu[:-1] + [cu[-1] + 9], [1] + cu[1:]):
         run(attn_lib, dict(x, cu=cuda_i32(bad)), True)
         assert attn_lib.poll_status()[0] == 1
     o, _ = run(attn_lib, x, True)
@@ -281,11 +309,98 @@ def test_serving_run(attn_lib, axes):
         check(x, o, lse, True)
 
 
+def test_max_q_below_a_length_is_reported(attn_lib):
+    for lens, max_q in (([(1, 9), (3, 50), (2, 60)], 2), ([(40, 90), (60, 60), (3, 5)], 50)):
+        x = make(lens, 4, 2, 64, 16, "bf16", seed=14)
+        good, _ = run(attn_lib, x, True)
+        assert attn_lib.poll_status() == (0, 0)
+        o = torch.full_like(good, 9.0)
+        run(attn_lib, dict(x, max_q=max_q), True, out=o)
+        st, detail = attn_lib.poll_status()
+        assert st == 1 and detail >> 16 == 1
+        cu = x["cu"].tolist()
+        assert (o[:, cu[1] + max_q:cu[2]] == 9.0).all()
+        for b in (0, 2):
+            err = (o - good)[:, cu[b]:cu[b + 1]].float().abs().max()
+            assert err <= 2 ** -5 * good.float().abs().max()
+
+
+@pytest.mark.parametrize("chunk", [1, 3, 40])
+def test_pages_past_two_to_the_31_elements(attn_lib, chunk):
+    """A cache of 2.4e9 elements: pages at both ends, two sequences that share
+    their first pages; the append writes there and the attention reads it."""
+    Hq, Hkv, d, page, dt = 4, 2, 128, 64, torch.float16
+    n_pages = 147_000
+    kp = torch.empty(n_pages, Hkv, page, d, dtype=dt, device="cuda")
+    vp = torch.empty_like(kp)
+    assert kp.numel() > 2 ** 31
+    table = cuda_i32([[n_pages - 1, 3, n_pages - 2], [n_pages - 1, 3, n_pages - 7]])
+    kv = [150 + chunk, 170]
+    g = torch.Generator("cuda").manual_seed(41)
+    for t in (kp, vp):
+        for i in set(table.flatten().tolist()):
+            t[i].normal_(generator=g)
+    n = chunk + 1
+    q, k, v = (torch.randn(h, n, d, generator=g, device="cuda").to(dt) for h in (Hq, Hkv, Hkv))
+    cu = cuda_i32([0, chunk, n])
+    small = lambda t: t[table.flatten().long()].clone()  # noqa: E731
+    kref, vref = small(kp), small(vp)
+    tref = np.arange(6).reshape(2, 3)
+    attn_lib.append_kv(k, v, kp, vp, table, cu, cuda_i32(kv))
+    kref = oracle.append_paged(to64(k), to64(kref), tref, cu.tolist(), kv)
+    vref = oracle.append_paged(to64(v), to64(vref), tref, cu.tolist(), kv)
+    o, lse = attn_lib.fwd_paged(q, kp, vp, table, cu, cuda_i32(kv), chunk, causal=True)
+    assert attn_lib.poll_status() == (0, 0)
+    assert np.array_equal(to64(small(kp)), kref) and np.array_equal(to64(small(vp)), vref)
+    y = dict(q=q, k=torch.tensor(kref), v=torch.tensor(vref), table=torch.tensor(tref), cu=cu,
+             kv=cuda_i32(kv))
+    check(y, o, lse, True)
+
+
+def test_two_graphs_share_a_workspace(attn_lib):
+    """Captured calls of different shapes (decoding, chunks) over one workspace,
+    replayed in turn, give what they give with workspaces of their own."""
+    xs = [make(DECODE * 5, 4, 2, 64, 16, "bf16", seed=43), make(CHUNKS, 4, 2, 64, 16, "bf16", seed=47),
+          make([(1, 6000), (2, 900)], 8, 1, 64, 16, "bf16", seed=53)]
+    ws = torch.empty(max(workspace_bytes(attn_lib, x) for x in xs), dtype=torch.uint8, device="cuda")
+    want = [run(attn_lib, x, True) for x in xs]
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for x in xs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            outs.append(run(attn_lib, x, True, workspace=ws))
+    for i in (0, 1, 2, 1, 0, 2, 2, 0):
+        outs[i][0].fill_(7.0)
+        graphs[i].replay()
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+    assert attn_lib.poll_status() == (0, 0)
+
+
+def test_calls_on_two_streams(attn_lib):
+    """Calls that overlap on two streams, each with its own workspace."""
+    xs = [make(DECODE * 20, 4, 2, 128, 16, "bf16", seed=59),
+          make([(200, 900), (128, 2000)], 4, 2, 128, 16, "bf16", seed=61)]
+    want = [run(attn_lib, x, True) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(10):
+        for x, st, g in zip(xs, streams, got):
+            with torch.cuda.stream(st):
+                g.append(run(attn_lib, x, True))
+    torch.cuda.synchronize()
+    assert attn_lib.poll_status() == (0, 0)
+    for g, w in zip(got, want):
+        assert all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for o, l in g)
+
+
 def test_timeouts_wind_down(attn_lib):
     """Waits that run out report ATTN_ERR_TIMEOUT and the next call is right."""
     x = make([(1, 3000)] * 40, 16, 8, 128, 64, "bf16", seed=31)
     y = make([(300, 3000)] * 3, 16, 8, 128, 64, "bf16", seed=37)
-    for s in (x, y):
+    z = make([(1, 3000)] * 4, 16, 8, 128, 64, "bf16", seed=67)
+    for s in (x, y, z):
         run(attn_lib, s, True)
         assert attn_lib.poll_status() == (0, 0)
         want, _ = run(attn_lib, s, True)
