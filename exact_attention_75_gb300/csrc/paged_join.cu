@@ -112,11 +112,59 @@ __global__ void __launch_bounds__(kThreads, 4) paged_join_rows_kernel(const Page
   }
 }
 
-// The tile kernel's items, four columns of 256 rows at a time.  Up to 4 parts a
-// thread takes a row and walks two column groups at once; beyond that one, and
-// beyond 16 parts four threads share a row's parts (a 64-token chunk of 4
-// key/value heads over 32768 keys, 38 parts an item: 44 us of kernel and join
-// with the first form alone).
+// The few parts (at most PARTS) of a tile's row: the weights 2^(m_k - M) once,
+// then COLS groups of four columns at a time, all their reads in flight
+// together.
+template <int D, bool BF16, int PARTS, int COLS>
+__device__ __forceinline__ void join_few(const PagedParams& p, int first, int parts, int r,
+                                         size_t row, int c, int step) {
+  auto slot = [&](int k) { return 2 * (size_t)(first + k) + (k == 0 ? 1 : 0); };
+  float2 ml[PARTS];
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k)
+    ml[k] = k < parts ? *reinterpret_cast<const float2*>(p.part_ml +
+                                                         (slot(k) * kPagedTileRows + r) * 2)
+                      : make_float2(-INFINITY, 0.f);
+  float M = ml[0].x, l = 0.f, f[PARTS];
+#pragma unroll
+  for (int k = 1; k < PARTS; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    f[k] = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
+    l += f[k] * ml[k].y;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (c == 0) p.lse[row] = l > 0.f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  for (; c < D / 4; c += step) {
+    float4 x[COLS][PARTS];
+#pragma unroll
+    for (int h = 0; h < COLS; ++h)
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k)
+        // a part with no key for the row holds no O
+        x[h][k] = f[k] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : *reinterpret_cast<const float4*>(
+                                    p.part_o + slot(k) * kPagedTileRows * D +
+                                    ((size_t)(c + h) * kPagedTileRows + r) * 4);
+#pragma unroll
+    for (int h = 0; h < COLS; ++h) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k) {
+        o.x += f[k] * x[h][k].x;
+        o.y += f[k] * x[h][k].y;
+        o.z += f[k] * x[h][k].z;
+        o.w += f[k] * x[h][k].w;
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + 4 * (c + h)) = make_uint2(
+          pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+    }
+  }
+}
+
+// The tile kernel's items, a thread a row: up to 8 parts in one go, beyond that
+// four at a time, and beyond 16 parts four threads share a row's parts (a 64-token chunk of 4 key/value heads over 32768 keys,
+// 38 parts an item: 29 us of kernel and join, 44 with a thread a row).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 4) paged_join_tiles_kernel(const PagedParams p) {
   __shared__ Sum meet[kThreads];
@@ -137,22 +185,15 @@ __global__ void __launch_bounds__(kThreads, 4) paged_join_tiles_kernel(const Pag
   const int first = blockIdx.x - item.y;
   const int slices = parts * (gridDim.y / 2), slice = item.y * (gridDim.y / 2) + (blockIdx.y >> 1);
   size_t row;
-  if (parts <= 4) {
+  if (parts <= 8) {
     const int r = threadIdx.x;
     if (!place(r, row)) return;
-    for (int c4 = 2 * slice; c4 < D / 4; c4 += 2 * slices) {
-      Sum s[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) s[h] = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      for (int k0 = 0; k0 < parts; k0 += 2) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          add_parts<D, kPagedTileRows, 2>(p, s[h], first, (c4 + h) * kPagedTileRows + r, r, k0,
-                                          parts);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) store<D, BF16>(p, row, c4 + h, s[h]);
-    }
+    if (parts == 2)
+      join_few<D, BF16, 2, 4>(p, first, parts, r, row, 4 * slice, 4 * slices);
+    else if (parts <= 4)
+      join_few<D, BF16, 4, 2>(p, first, parts, r, row, 2 * slice, 2 * slices);
+    else
+      join_few<D, BF16, 8, 1>(p, first, parts, r, row, slice, slices);
     return;
   }
   const int ways = parts > 16 ? 4 : 1, rows = kThreads / ways;  // rows at once
