@@ -381,10 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           reinterpret_cast<float2*>(p.part_ml) + slot * kRows + t * 128 + r;
       if (nb == 0) {
         // A tile without rows, or whose rows see no key of this share.
-        if (t == 0 || w.two) {
+        if (live) {
           if (!whole) {
             *ml = make_float2(-INFINITY, 0.f);
-          } else if (live) {
+          } else {
             uint4* orow = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + grow * D);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -537,12 +537,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < D / 32; ++c) {
           uint32_t raw[32];
           tmem_ld32_sync(o_addr + c * 32, raw);
+          if (live) {  // the join reads no other rows
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            part[(size_t)(c * 8 + v) * kRows + t * 128 + r] =
-                make_uint4(raw[4 * v], raw[4 * v + 1], raw[4 * v + 2], raw[4 * v + 3]);
+            for (int v = 0; v < 8; ++v)
+              part[(size_t)(c * 8 + v) * kRows + t * 128 + r] =
+                  make_uint4(raw[4 * v], raw[4 * v + 1], raw[4 * v + 2], raw[4 * v + 3]);
+          }
         }
-        *ml = make_float2(m, l);
+        if (live) *ml = make_float2(m, l);
       }
       tc_fence_before();
     }
