@@ -18,14 +18,19 @@
 // 16-byte writes.  The kernels are bound by those HBM bytes, so the rows of
 // the next four heads are always on their way while four are turned, and the
 // first are asked for before the angles and the token's place in the cache
-// are worked out.  q and k of a fused projection, 2 x 8192 tokens x 32 heads,
-// d = 128 (268 MB): 44.5 us, 6.0 TB/s, 0.89 of the measured copy rate.  The
-// append of ragged prompts (225 MB in 16-token pages, d = 64, three axes):
-// 39.5 us, 5.7 TB/s; one batch of 8 heads per thread without the overlap took
-// 45.9 us there, two heads at a time 39.8, 32 heads per thread 41.3.  Blocks
-// of 128 threads, head groups fastest (a projection's row is then read by
-// neighbouring blocks): 256 threads with tokens fastest took 4.3 us against
-// 3.3 for a 577-token image and were equal at the large sizes.
+// are worked out.  Measured (bf16, in a graph): q and k of a fused projection,
+// 2 x 8192 tokens x 32 heads, d = 128 (268 MB) 43.6 us, 6.2 TB/s, 0.91 of the
+// measured copy rate; the backward of 20 heads with three axes (168 MB) 28.2 us,
+// 6.0 TB/s; the append of ragged prompts (225 MB in 16-token pages, d = 64,
+// three axes) 38.7 us, 5.8 TB/s, of one prompt of 16384 tokens (268 MB) 44.4 us.
+// What else was tried: one batch of 8 heads per thread without the overlap
+// took 45.9 us for the ragged prompts, two heads at a time 39.8, 32 heads per
+// thread 41.3.  Blocks of 128 threads, head groups fastest (a projection's row
+// is then read by neighbouring blocks): 256 threads with tokens fastest took
+// 4.3 us against 3.3 for a 577-token image and were equal at the large sizes.
+// Five blocks an SM (96 registers) against four: 28.2 / 29.6 us for that
+// backward, but 27.9 / 24.9 for 32 interleaved heads of 8192 tokens and 40.6 /
+// 38.7 for the ragged prompts, so the half-split rotation alone takes five.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -130,7 +135,7 @@ __device__ __forceinline__ void turn_pieces(uint4& lo, uint4& hi, const float (&
 }
 
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, INTER ? 4 : 5) rope_kernel(const RopeParams p) {
   grid_wait();
   grid_release();
   const int per_row = p.d / 16;
@@ -283,11 +288,12 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
 }
 
 // Heads per thread: as many as leave every SM its blocks (the angles are
-// computed once per thread).
+// computed once per thread), the same for every group.
 int heads_per_block(int64_t blocks_x, int heads, int num_sms) {
   int g = kHeads;
   while (g > 1 && blocks_x * ((heads + g - 1) / g) < 4LL * num_sms) g >>= 1;
-  return g;
+  const int groups = (heads + g - 1) / g;
+  return (heads + groups - 1) / groups;
 }
 
 }  // namespace
