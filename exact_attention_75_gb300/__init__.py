@@ -2,7 +2,8 @@
 
 Every function here only marshals arguments: it checks tensors, takes their
 device pointers and the current CUDA stream, and calls the C ABI declared in
-``include/attn.h``.  All computation runs in the library's CUDA kernels.  If
+``include/attn.h`` (through ctypes, or, for the calls of a decoding step,
+through the compiled ``csrc/binding.cpp``).  All computation runs in the library's CUDA kernels.  If
 the library has not been built, or no sm_103a GPU is present, calls raise —
 there is no fallback path.
 
@@ -13,6 +14,8 @@ Build the library first::
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 from typing import Optional, Sequence, Tuple
@@ -30,6 +33,7 @@ STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED",
 _F16, _BF16 = 0, 1
 _MAX_AXES = 8  # position axes of a rotary table
 _lib = None
+_bind = None
 
 
 class AttnError(RuntimeError):
@@ -84,6 +88,30 @@ def lib() -> ctypes.CDLL:
         fn.restype = res
     _lib = L
     return L
+
+
+def binding_path() -> str:
+    return os.path.join(_HERE, "_build", "_binding.so")
+
+
+def _binding():
+    """The compiled Python entry (csrc/binding.cpp) of the calls of a decoding
+    step, over the same loaded libattn.so."""
+    global _bind
+    if _bind is None:
+        path = binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m exact_attention_75_gb300.build` (needs nvcc)")
+        loader = importlib.machinery.ExtensionFileLoader(__name__ + "._binding", path)
+        spec = importlib.util.spec_from_file_location(loader.name, path, loader=loader)
+        mod = importlib.util.module_from_spec(spec)
+        loader.exec_module(mod)
+        L = lib()
+        mod.init(AttnError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "attn_rope", "attn_append_kv", "attn_fwd_paged", "attn_fwd_paged_workspace_bytes")))
+        _bind = mod
+    return _bind
 
 
 def _check(status: int, what: str) -> None:
@@ -458,131 +486,6 @@ def rope_table(rot: int, theta: float = 10000.0, axes: Optional[Sequence[int]] =
     return torch.tensor([step, axis], dtype=torch.int64).to(device)
 
 
-# The checks below run on every call of a decoding step, so they are written
-# for few attribute reads and no temporaries, and outputs are allocated after
-# them: the allocator's locks wait for the previous launch's doorbell to reach
-# the GPU, which the checks' plain Python overlaps (measured on the Grace host,
-# rope of q and k: 26 us a call with the allocations first, 15 us without any).
-
-_I64 = {n: ctypes.c_int64 * n for n in (4, 6, 12)}
-_CODES = {torch.float16: _F16, torch.bfloat16: _BF16}
-
-
-def _row_strides(t: torch.Tensor, what: str, written: bool = False) -> Tuple[int, ...]:
-    """Strides of a tensor whose rows are read or written 16 bytes at a time
-    (0 for a dimension of size 1)."""
-    st = t.stride()
-    low = 0
-    for x in st[:-1]:
-        low |= x
-    if st[-1] != 1 or low & 7 or written:
-        st = tuple(x if n > 1 else 0 for x, n in zip(st[:-1], t.shape)) + (st[-1],)
-        if st[-1] != 1 or any(x & 7 for x in st[:-1]):
-            raise ValueError(f"{what}: the last dimension must be contiguous and the other "
-                             "strides multiples of 8 elements")
-        if written and any(x == 0 and n > 1 for x, n in zip(st, t.shape)):
-            raise ValueError(f"{what} must not be an expanded tensor")
-    return st
-
-
-def _turn_strides(t: torch.Tensor, what: str, written: bool = False) -> Tuple[int, ...]:
-    """Batch, head and token strides of a [B, H, N, d] or packed [H, N, d] tensor."""
-    st = t.stride()
-    if len(st) == 4:
-        b, h, n, one = st
-    else:
-        (h, n, one), b = st, 0
-    if one != 1 or (b | h | n) & 7 or written:
-        st = _row_strides(t, what, written)
-        return st[:3] if len(st) == 4 else (0, st[0], st[1])
-    return b, h, n
-
-
-def _out_strides(out: Optional[torch.Tensor], x: torch.Tensor, device: int,
-                 what: str) -> Tuple[int, ...]:
-    """The same of an output like x, contiguous where it is still to be allocated."""
-    shape = x.shape
-    if out is None:
-        H, N, d = shape[-3:]
-        return H * N * d, N * d, d
-    if out.shape != shape or out.dtype != x.dtype or out.get_device() != device:
-        raise ValueError(f"{what} must have the shape, dtype and device of {what[-1]}")
-    return _turn_strides(out, what, True)
-
-
-def _call(fn, what: str, device: int, *args) -> None:
-    """fn(*args, stream) on the current stream of the tensors' device."""
-    if torch.cuda.current_device() == device:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
-    if st != 0:
-        raise AttnError(what, st)
-
-
-def _check_table(table: torch.Tensor, d: int, device: int) -> int:
-    shape = table.shape
-    if (table.dtype != torch.int64 or len(shape) != 2 or shape[0] != 2
-            or not table.is_contiguous() or table.get_device() != device):
-        raise ValueError("table must be a contiguous int64 [2, rot/2] tensor (rope_table) on the "
-                         "tensors' device")
-    rot = 2 * shape[1]
-    if rot < 16 or rot & 15 or rot > d:
-        raise ValueError("the table must turn a multiple of 16 channels, at most the head dim")
-    return rot
-
-
-def _rope(q, k, positions, table, interleaved, out_q, out_k, inverse):
-    shape, code = q.shape, _CODES.get(q.dtype)
-    if len(shape) == 4:
-        B, H, N, d = shape
-    elif len(shape) == 3:  # packed: one batch
-        (H, N, d), B = shape, 1
-    else:
-        raise ValueError("tensors must be [B, H, N, d] or packed [H, total, d]")
-    if code is None:
-        raise TypeError(f"q and k must be float16 or bfloat16, got {q.dtype}")
-    if not q.is_cuda:
-        raise ValueError("all tensors must be on the same CUDA device")
-    if q.numel() == 0:
-        raise ValueError("tensors must not be empty")
-    dev = q.get_device()
-    rot = _check_table(table, d, dev)
-    pshape = positions.shape
-    if positions.dtype != torch.int32 or positions.get_device() != dev \
-            or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous int32 tensor on the tensors' device")
-    n_axes = pshape[0] if len(pshape) in (2, 3) else 0
-    pos_batches = pshape[1] if len(pshape) == 3 else 1
-    if not 1 <= n_axes <= _MAX_AXES or pshape[-1] != N or (pos_batches != 1 and pos_batches != B):
-        raise ValueError(f"positions must be [axes, N] or [axes, B, N], at most {_MAX_AXES} axes")
-    kp = okp = Hkv = 0
-    kshape = None
-    if k is not None:
-        kshape = k.shape
-        if len(kshape) != len(shape) or kshape[-2:] != shape[-2:] or k.dtype != q.dtype \
-                or k.get_device() != dev or (len(shape) == 4 and kshape[0] != B) \
-                or k.numel() == 0:
-            raise ValueError("q and k must share batch, length, head dim, dtype and device")
-        Hkv = kshape[-3]
-        kp = k.data_ptr()
-    elif out_k is not None:
-        raise ValueError("out_k without k")
-    st = _turn_strides(q, "q") + _out_strides(out_q, q, dev, "out_q")
-    if k is not None:
-        st += _turn_strides(k, "k") + _out_strides(out_k, k, dev, "out_k")
-        if out_k is None:
-            out_k = torch.empty(kshape, dtype=q.dtype, device=q.device)
-        okp = out_k.data_ptr()
-    if out_q is None:
-        out_q = torch.empty(shape, dtype=q.dtype, device=q.device)
-    _call(lib().attn_rope, "attn_rope_bwd" if inverse else "attn_rope", dev, q.data_ptr(), kp,
-          out_q.data_ptr(), okp, _I64[len(st)](*st), positions.data_ptr(), pos_batches, n_axes,
-          table.data_ptr(), rot, 1 if interleaved else 0, inverse, B, H, Hkv, N, d, code)
-    return out_q, out_k
-
-
 def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, table: torch.Tensor,
          interleaved: bool = False, out_q: Optional[torch.Tensor] = None,
          out_k: Optional[torch.Tensor] = None):
@@ -593,7 +496,7 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, ta
     strided views with contiguous rows (a slice of a fused projection); new
     outputs are contiguous, and out_q / out_k may be q / k themselves.
     positions: int32 [axes, N] or [axes, B, N].  Returns (q', k')."""
-    return _rope(q, k, positions, table, interleaved, out_q, out_k, 0)
+    return _binding().rope(q, k, positions, table, interleaved, out_q, out_k, False)
 
 
 def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor,
@@ -601,35 +504,7 @@ def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tens
              out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None):
     """Backward pass of rope: gradients with respect to q', k' in, with respect
     to q, k out (the opposite turn); arguments as in rope."""
-    return _rope(dq, dk, positions, table, interleaved, out_q, out_k, 1)
-
-
-def _check_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens) -> int:
-    """Shapes of a paged cache [n_pages, Hkv, page, d] and its batch; q is a
-    packed [H, total, d] tensor of new tokens.  Returns the device."""
-    qshape, kshape, bshape = q.shape, k_pages.shape, block_table.shape
-    if len(qshape) != 3:
-        raise ValueError("packed tensors must be [H, total, d]")
-    if len(kshape) != 4 or kshape != v_pages.shape or kshape[3] != qshape[2]:
-        raise ValueError("k_pages, v_pages must be [n_pages, Hkv, page, d] with the tokens' d")
-    dev, dt = q.get_device(), q.dtype
-    if dt not in _CODES:
-        raise TypeError(f"tokens must be float16 or bfloat16, got {dt}")
-    if not q.is_cuda or k_pages.get_device() != dev or v_pages.get_device() != dev \
-            or k_pages.dtype != dt or v_pages.dtype != dt:
-        raise ValueError("tokens and pages must be CUDA tensors of one dtype on one device")
-    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
-        raise ValueError("k_pages, v_pages must be contiguous")
-    n = kv_lens.shape
-    if len(bshape) != 2 or len(n) != 1 or bshape[0] != n[0] or n[0] < 1 \
-            or cu_seqlens.shape != (n[0] + 1,):
-        raise ValueError("block_table must be [n_seq, max_pages], cu_seqlens [n_seq + 1], "
-                         "kv_lens [n_seq]")
-    for t in (block_table, cu_seqlens, kv_lens):
-        if t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("block_table, cu_seqlens and kv_lens must be contiguous int32 "
-                             "tensors on the tokens' device")
-    return dev
+    return _binding().rope(dq, dk, positions, table, interleaved, out_q, out_k, True)
 
 
 def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -649,49 +524,8 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
     int32 [axes, total] (None: the position in the cache on every axis).
     Returns the turned queries (None without q); rows behind the last sequence
     are left as they were."""
-    dev = _check_paged(k, k_pages, v_pages, block_table, cu_seqlens, kv_lens)
-    shape, dt = k.shape, k.dtype
-    Hkv, total, d = shape
-    n_pages, cache_heads, page, _ = k_pages.shape
-    n_seq, max_pages = block_table.shape
-    if Hkv != cache_heads or v.shape != shape or v.dtype != dt or v.get_device() != dev:
-        raise ValueError("k and v must be [Hkv, total, d] with the cache's heads")
-    rot, tp = (0, 0) if table is None else (_check_table(table, d, dev), table.data_ptr())
-    pp, n_axes = 0, 1
-    if positions is not None:
-        pshape = positions.shape
-        if table is None:
-            raise ValueError("positions without a table")
-        if positions.dtype != torch.int32 or positions.get_device() != dev or len(pshape) != 2 \
-                or pshape[1] != total or not 1 <= pshape[0] <= _MAX_AXES \
-                or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous int32 [axes, total] tensor, at most "
-                             f"{_MAX_AXES} axes")
-        pp, n_axes = positions.data_ptr(), pshape[0]
-    st = _row_strides(k, "k")[:-1] + _row_strides(v, "v")[:-1]
-    Hq = qp = op = 0
-    if q is not None:
-        qshape = q.shape
-        Hq = qshape[0]
-        if len(qshape) != 3 or qshape[1:] != shape[1:] or q.dtype != dt \
-                or q.get_device() != dev or Hq < 1 or Hq % Hkv != 0:
-            raise ValueError("q must be [Hq, total, d] with k's total, d, dtype and device, "
-                             "Hq a multiple of Hkv")
-        st += _row_strides(q, "q")[:-1]
-        qp = q.data_ptr()
-        if out_q is None:
-            out_q = torch.empty(qshape, dtype=dt, device=q.device)
-        elif out_q.shape != qshape or out_q.dtype != dt or out_q.get_device() != dev \
-                or not out_q.is_contiguous():
-            raise ValueError("out_q must be contiguous with q's shape, dtype and device")
-        op = out_q.data_ptr()
-    elif out_q is not None:
-        raise ValueError("out_q without q")
-    _call(lib().attn_append_kv, "attn_append_kv", dev, k.data_ptr(), v.data_ptr(), qp, op,
-          _I64[len(st)](*st), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-          cu_seqlens.data_ptr(), kv_lens.data_ptr(), pp, n_axes, tp, rot,
-          1 if interleaved else 0, n_seq, total, n_pages, page, max_pages, Hq, Hkv, d, _CODES[dt])
-    return out_q
+    return _binding().append_kv(k, v, k_pages, v_pages, block_table, cu_seqlens, kv_lens, table,
+                                positions, interleaved, q, out_q)
 
 
 def fwd_paged_workspace_bytes(n_seq: int, max_q: int, max_keys: int, Hq: int, Hkv: int,
@@ -715,45 +549,8 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     j <= i + kv_lens[b] - n.  A row that sees no key gets O = 0, LSE = -inf;
     rows behind the last sequence are left as they were.  workspace: uint8,
     fwd_paged_workspace_bytes long; calls that may overlap need their own."""
-    dev = _check_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens)
-    shape, dt = q.shape, q.dtype
-    H, total, d = shape
-    n_pages, Hkv, page, _ = k_pages.shape
-    n_seq, max_pages = block_table.shape
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous [Hq, total, d]")
-    if Hkv < 1 or H % Hkv != 0:
-        raise ValueError("the number of key/value heads must divide the query heads")
-    max_q = int(max_q)
-    if not 1 <= max_q <= total:
-        raise ValueError("max_q must lie in [1, total]")
-    if out is not None and (out.shape != shape or out.dtype != dt or out.get_device() != dev
-                            or not out.is_contiguous()):
-        raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
-    if lse is not None and (lse.shape != (H, total) or lse.dtype != torch.float32
-                            or lse.get_device() != dev or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 [Hq, total] tensor on q's device")
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.get_device() != dev
-                                  or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on q's device")
-    L = lib()
-    wp = ws = 0
-    if workspace is None:
-        ws = L.attn_fwd_paged_workspace_bytes(n_seq, max_q, max_pages * page, H, Hkv, d)
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((H, total), dtype=torch.float32, device=q.device)
-    if ws:
-        workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
-    if workspace is not None:
-        wp, ws = workspace.data_ptr(), workspace.numel()
-    _call(L.attn_fwd_paged, "attn_fwd_paged", dev, q.data_ptr(), k_pages.data_ptr(),
-          v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
-          cu_seqlens.data_ptr(), kv_lens.data_ptr(), wp, ws,
-          n_seq, max_q, total, n_pages, page, max_pages, H, Hkv, d, 1 if causal else 0,
-          1.0 / math.sqrt(d) if scale is None else float(scale), _CODES[dt])
-    return out, lse
+    return _binding().fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, max_q,
+                                causal, scale, out, lse, workspace)
 
 
 def num_sms() -> int:

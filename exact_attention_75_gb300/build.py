@@ -1,11 +1,13 @@
-"""Build libattn.so in-tree with nvcc for sm_103a.
+"""Build libattn.so in-tree with nvcc for sm_103a, and the Python entry of the
+decoding-step calls (_binding.so) with the host compiler.
 
     python -m exact_attention_75_gb300.build [--force]
 
 Each .cu file under csrc/ is compiled in parallel to an object file in
 ``_build/``, then linked into ``_build/libattn.so`` (CUDA runtime linked
 statically; the driver API is reached through cudaGetDriverEntryPointByVersion,
-so the library loads on machines without a GPU driver).  A file is recompiled
+so the library loads on machines without a GPU driver).  csrc/binding.cpp is
+compiled against the installed torch and Python headers.  A file is recompiled
 only when it, or a header under csrc/ or include/, is newer than its object.
 """
 from __future__ import annotations
@@ -24,6 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libattn.so")
+BINDING = os.path.join(BUILD, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
                   "-I", CSRC, "-I", INCLUDE, "--expt-relaxed-constexpr"]
@@ -51,6 +54,28 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
     return r.stderr
 
 
+def _compile_binding(src: str, out: str) -> str:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = out + ".tmp"
+    cmd = [os.environ.get("CXX", "c++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-Wl,-rpath," + os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {os.path.basename(src)} failed:\n{r.stderr[-6000:]}")
+    os.replace(tmp, out)
+    return r.stderr
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if needed) and return the path of libattn.so."""
     os.makedirs(BUILD, exist_ok=True)
@@ -63,9 +88,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(o)
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), hdr):
             jobs[s] = o
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
-            futs = {ex.submit(_compile, s, o, verbose): s for s, o in jobs.items()}
+    src = os.path.join(CSRC, "binding.cpp")
+    header = os.path.getmtime(os.path.join(INCLUDE, "attn.h"))
+    bind = force or not os.path.exists(BINDING) or \
+        os.path.getmtime(BINDING) < max(os.path.getmtime(src), header)
+    if jobs or bind:
+        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + bind)) as ex:
+            futs = {ex.submit(_compile_binding, src, BINDING): src} if bind else {}
+            futs.update({ex.submit(_compile, s, o, verbose): s for s, o in jobs.items()})
             for f in cf.as_completed(futs):
                 log = f.result()
                 if verbose and log:

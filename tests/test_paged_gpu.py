@@ -414,3 +414,62 @@ def test_timeouts_wind_down(attn_lib):
         assert st in (0, 4)
         got, _ = run(attn_lib, s, True)
         assert attn_lib.poll_status() == (0, 0) and torch.equal(got, want)
+
+
+def test_binding_refuses_wrong_tensors(attn_lib):
+    """What the Python entry checks before the C ABI: types, shapes, devices,
+    strides.  Nothing is launched; the same arguments put right then work."""
+    x = make([(1, 5), (2, 40)], 4, 2, 64, 16, "bf16", seed=71)
+    good = [x["q"], x["k"], x["v"], x["table"], x["cu"], x["kv"], 2]
+    half, cpu = x["q"].half(), x["q"].cpu()
+    wide = torch.zeros(4, 3, 128, dtype=torch.bfloat16, device="cuda")
+    bad = [(0, half, ValueError), (0, x["q"].float(), TypeError), (0, cpu, ValueError),
+           (0, wide, ValueError), (0, x["q"][:3], ValueError), (0, x["q"][0], ValueError),
+           (0, wide[..., ::2], ValueError), (0, None, TypeError), (0, 3, TypeError),
+           (1, x["k"][1:], ValueError), (1, x["k"].transpose(1, 2), ValueError),
+           (3, x["table"].long(), ValueError), (3, x["table"][:1], ValueError),
+           (3, x["table"].cpu(), ValueError), (4, x["cu"][:2], ValueError),
+           (5, x["kv"].long(), ValueError), (5, x["kv"][None], ValueError),
+           (6, 0, ValueError), (6, 4, ValueError), (6, 1 << 40, ValueError), (6, "two", ValueError)]
+    for i, value, error in bad:
+        with pytest.raises(error):
+            attn_lib.fwd_paged(*(good[:i] + [value] + good[i + 1:]))
+    o, lse = torch.empty_like(x["q"]), torch.empty(4, 3, device="cuda")
+    for kw, error in ((dict(out=half), ValueError), (dict(out=o.cpu()), ValueError),
+                      (dict(out=wide[..., :64]), ValueError), (dict(lse=lse.half()), ValueError),
+                      (dict(lse=lse.t()), ValueError), (dict(workspace=lse), ValueError),
+                      (dict(scale="x"), TypeError), (dict(out=1), TypeError)):
+        with pytest.raises(error):
+            attn_lib.fwd_paged(*good, **kw)
+    with pytest.raises(attn_lib.AttnError) as e:
+        attn_lib.fwd_paged(*good, scale=-1.0)
+    assert e.value.status == 1
+
+    table = attn_lib.rope_table(64)
+    k = torch.zeros(2, 3, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    cache = [x["k"], x["v"], x["table"], x["cu"], x["kv"]]
+    for args, kw in (((k, k.half()), {}), ((k[:1], k[:1]), {}), ((k, k[:, :2]), {}),
+                     ((k.float(), k.float()), {}), ((wide[:2, :, ::2], k), {}),
+                     ((k, k), dict(positions=pos)), ((k, k), dict(table=table.int())),
+                     ((k, k), dict(table=table[:1])), ((k, k), dict(table=attn_lib.rope_table(128))),
+                     ((k, k), dict(table=table, positions=pos.long())),
+                     ((k, k), dict(table=table, positions=pos[:, :2])),
+                     ((k, k), dict(q=x["q"][:3])), ((k, k), dict(q=half)), ((k, k), dict(out_q=x["q"])),
+                     ((k, k), dict(q=x["q"], out_q=x["q"].transpose(0, 1).contiguous().transpose(0, 1)))):
+        with pytest.raises((ValueError, TypeError)):
+            attn_lib.append_kv(*args, *cache, **kw)
+    q4 = torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device="cuda")
+    for args, kw in (((q4, q4[:1], pos), {}), ((q4, q4.half(), pos), {}), ((q4[0, 0], None, pos), {}),
+                     ((q4, None, pos[:, :2]), {}), ((q4, None, pos[0]), {}),
+                     ((q4, None, pos[:, None].expand(1, 3, 3)), {}), ((q4, None, pos.long()), {}),
+                     ((q4[..., ::2], None, pos), {}), ((q4[:, :0], None, pos), {}),
+                     ((q4, None, pos), dict(out_k=q4)), ((q4, None, pos), dict(out_q=q4[:1])),
+                     ((q4, None, pos), dict(out_q=q4[:, :1].expand(2, 4, 3, 64)))):
+        with pytest.raises((ValueError, TypeError)):
+            attn_lib.rope(*args, table, **kw)
+    assert attn_lib.poll_status() == (0, 0)
+    attn_lib.fwd_paged(*good)
+    attn_lib.append_kv(k, k, *cache, table=table, positions=pos, q=x["q"])
+    attn_lib.rope(q4, q4[:, :2], pos, table)
+    assert attn_lib.poll_status() == (0, 0)
