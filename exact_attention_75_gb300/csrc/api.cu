@@ -436,11 +436,10 @@ bool strides_ok(const int64_t* s, int n) {
 // A decoding batch runs in clusters up to this many items (sequences x
 // key/value heads: the clusters are resident at once) and this reach of the
 // block table.  Measured per call in a graph, clusters against equal shares
-// (bf16, d = 128, 16 query heads on 4): 4 items of 64 keys 5.0 / 6.0 us, 1024
-// keys 5.9 / 8.6, 4096 keys 10.5 / 9.6, 8192 keys 16.5 / 11.5; 16 items of 2048
-// keys 8.6 / 9.1; 32 of up to 4096 13.8 / 15.1; 64 items of 256 keys 11.1 / 8.7,
-// 256 of 512 43 / 19.  Called without a graph, the one launch without a
-// workspace takes 18 to 19 us of the host against 24.
+// (bf16, d = 128, 16 query heads on 4): 4 items of 64 keys 5.1 / 6.0 us, 1024
+// keys 5.8 / 8.3, 4096 keys 10.1 / 8.9, 8192 keys 16.0 / 10.0; 16 items of 2048
+// keys 8.3 / 9.1; 36 items of 256 keys 6.0 / 8.4, of 4096 17.3 / 19.6; 64 items
+// of 256 keys 11.1 / 8.5, 128 of 256 20.6 / 9.6.
 constexpr int64_t kPagedClusterItems = 36;
 constexpr int64_t kPagedClusterKeys = 4096;
 
