@@ -433,15 +433,25 @@ bool strides_ok(const int64_t* s, int n) {
   return true;
 }
 
-// A decoding batch runs in clusters up to this many items (sequences x
-// key/value heads: the clusters are resident at once) and this reach of the
-// block table.  Measured per call in a graph, clusters against equal shares
-// (bf16, d = 128, 16 query heads on 4): 4 items of 64 keys 5.1 / 6.0 us, 1024
-// keys 5.8 / 8.3, 4096 keys 10.1 / 8.9, 8192 keys 16.0 / 10.0; 16 items of 2048
-// keys 8.3 / 9.1; 36 items of 256 keys 6.0 / 8.4, of 4096 17.3 / 19.6; 64 items
-// of 256 keys 11.1 / 8.5, 128 of 256 20.6 / 9.6.
-constexpr int64_t kPagedClusterItems = 36;
-constexpr int64_t kPagedClusterKeys = 4096;
+// A decoding batch runs in clusters of 8, 4, 2 or 1 CTAs an item (sequence and
+// key/value head), as many as are resident at once, while the block table
+// reaches no further than kPagedClusterKeys a CTA (a long sequence among short
+// ones keeps its cluster's CTAs to itself).  Measured per call in a graph,
+// clusters against equal shares (bf16, d = 128):
+//   4 items (8 CTAs each)   64 keys 5.1 / 6.0 us, 1024 5.8 / 8.3, 4096 10.1 / 8.9,
+//                           8192 16.0 / 10.0
+//   36 items (8)            256 keys 6.0 / 8.4, 4096 17.3 / 19.6
+//   38 items (8: the last clusters wait)  256 keys 10.7 / 8.4
+//   40 items (4)            256 keys 5.9 / 8.4, 2048 13.6 / 14.9
+//   80 items (2)            256 keys 6.4 / 8.6, 1024 13.4 / 15.0
+//   300 items (1)           256 keys 11.3 / 16.0, 1024 29.0 / 33.3, 256 to 1024
+//                           keys 23.2 / 25.5
+// Without a graph a call in shares takes the host 9 to 10 us at least (two
+// launches and a workspace), in clusters 6.
+constexpr int kPagedClusterWide = 288;  // resident CTAs in clusters of 8 or 4
+constexpr int kPagedClusterCtas = 300;
+constexpr int64_t kPagedClusterKeys = 512;      // times the CTAs of an item,
+constexpr int64_t kPagedClusterKeysMin = 1024;  // at least
 
 int log2_of(int pow2) {
   int n = 0;
@@ -471,12 +481,17 @@ attn_status paged_args(const void* k_pages, const void* v_pages, const int32_t* 
 // more on the tile kernel, both in equal shares with the join behind them,
 // and small decoding batches in clusters, one launch without a workspace.
 struct PagedPlan {
-  bool decode, cluster;
+  bool decode;
+  int cluster;          // CTAs of an item's cluster, 0: equal shares
   size_t ml, o, bytes;  // partial results in the workspace: desc, (m, l), O
   PagedPlan(int n_seq, int max_q, int64_t max_keys, int Hkv, int group, int d) {
     decode = (int64_t)max_q * group <= kPagedRows;
-    cluster = decode && (int64_t)n_seq * Hkv <= kPagedClusterItems &&
-              max_keys <= kPagedClusterKeys;
+    const int64_t items = (int64_t)n_seq * Hkv;
+    cluster = decode ? kPagedCluster : 0;
+    while (cluster > 0 && items * cluster > (cluster > 2 ? kPagedClusterWide : kPagedClusterCtas))
+      cluster >>= 1;
+    const int64_t keys = kPagedClusterKeys * cluster;
+    if (max_keys > (keys > kPagedClusterKeysMin ? keys : kPagedClusterKeysMin)) cluster = 0;
     const size_t ctas = cluster ? 0 : (decode ? 2 * kPagedMaxSms : kPagedMaxSms);
     const size_t rows = 2 * ctas * (decode ? kPagedRows : kPagedTileRows);
     ml = 4 * ctas * sizeof(int4);
@@ -652,7 +667,8 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
   const bool decode = plan.decode;
   p.min_share = decode ? 128 : 1024;
   const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
-  a.grid = plan.cluster ? n_seq * Hkv * kPagedCluster : (decode ? 2 * sms : sms);
+  p.cluster = plan.cluster;
+  a.grid = plan.cluster ? n_seq * Hkv * plan.cluster : (decode ? 2 * sms : sms);
   a.stream = static_cast<cudaStream_t>(stream);
   // the cost of the largest batch of these sizes stays in 63 bits
   const int64_t keys = 4 * ((int64_t)max_pages * page + 1024);
@@ -667,9 +683,8 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
                             CU_TENSOR_MAP_SWIZZLE_128B, p.G))
     return ATTN_ERR_CUDA;
   const bool bf16 = dtype == ATTN_BF16;
-  cudaError_t e =
-      decode ? launch_paged_decode(a, d, bf16, plan.cluster) : launch_paged_tile(a, d, bf16);
-  if (e == cudaSuccess && !plan.cluster) e = launch_paged_join(a, d, bf16, decode);
+  cudaError_t e = decode ? launch_paged_decode(a, d, bf16) : launch_paged_tile(a, d, bf16);
+  if (e == cudaSuccess && plan.cluster == 0) e = launch_paged_join(a, d, bf16, decode);
   return launch_result(e);
 }
 

@@ -38,7 +38,7 @@ constexpr int kPagedRows = 16;
 constexpr int kPagedTileRows = 256;
 // Keys of a block there (rows of the tensor-map box).
 constexpr int kPagedBlock = 16;
-// CTAs that share an item of a small batch there.
+// CTAs at most that share an item of a small batch there.
 constexpr int kPagedCluster = 8;
 // Query heads per key/value head at most.
 constexpr int kPagedMaxGroup = 128;
@@ -58,6 +58,7 @@ struct PagedParams {
   int n_seq, total, max_q, n_pages, page, page_log2, max_pages, Hkv, G;
   int causal;               // query i of n sees keys j <= i + kv_len - n
   int min_share;            // least share, at least one key block
+  int cluster;              // CTAs of an item's cluster (decoding kernel; 0: equal shares)
   float scale_log2;         // scale * log2(e)
   unsigned long long wait_limit_ns;
 };
@@ -73,7 +74,7 @@ struct PagedLaunch {
 // d in {64, 96, 128}.  The decoding kernel takes at most kPagedRows query
 // rows per sequence and key/value head, the tile kernel any number; the join
 // follows either with the same grid.
-cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16, bool cluster);
+cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16);
 cudaError_t launch_paged_tile(const PagedLaunch& a, int d, bool bf16);
 cudaError_t launch_paged_join(const PagedLaunch& a, int d, bool bf16, bool decode);
 

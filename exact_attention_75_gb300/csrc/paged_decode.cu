@@ -62,8 +62,8 @@ __device__ __forceinline__ int first_key(const Walk& w, int warp, int j) {
   return w.u0 * kUnit + (warp + j * kWarps) * kKeys;
 }
 
-// CLUSTER: an item is shared by the kPagedCluster CTAs of a cluster, which
-// join their parts through each other's shared memory; otherwise the grid
+// CLUSTER: an item is shared by the p.cluster CTAs of a cluster, which join
+// their parts through each other's shared memory; otherwise the grid
 // takes equal shares of the whole batch and leaves parts to the join kernel.
 template <int D, bool BF16, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -92,13 +92,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   grid_wait();
   Walk w;
   if constexpr (CLUSTER) {
-    const int item = blockIdx.x / kPagedCluster, rank = blockIdx.x % kPagedCluster;
+    const int item = blockIdx.x / p.cluster, rank = blockIdx.x - item * p.cluster;
     w.b = item / p.Hkv;
     w.head = item - w.b * p.Hkv;
     w.sq = paged_seq(p, w.b);
     w.nb = (w.sq.klen + kUnit - 1) / kUnit;
-    w.u0 = (int)((long long)rank * w.nb / kPagedCluster);
-    w.u1 = (int)((long long)(rank + 1) * w.nb / kPagedCluster);
+    w.u0 = (int)((long long)rank * w.nb / p.cluster);
+    w.u1 = (int)((long long)(rank + 1) * w.nb / p.cluster);
     w.x0 = 0;
     w.take = 1;
     w.left = w.sq.qlen > 0 ? 1 : 0;
@@ -382,14 +382,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (w.sq.qlen > 0) {  // the same in every CTA of the cluster
       cluster_sync();
       const int rows = min(kPagedRows, w.sq.qlen * p.G);
-      const int rank = blockIdx.x % kPagedCluster;
+      const int rank = blockIdx.x % p.cluster;
       for (int e = rank * kThreads + threadIdx.x; !given_up && e < rows * (D / 4);
-           e += kPagedCluster * kThreads) {
+           e += p.cluster * kThreads) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
         float2 ml[kPagedCluster];
         float4 x[kPagedCluster];
 #pragma unroll
         for (int k = 0; k < kPagedCluster; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.f);
+          if (k >= p.cluster) continue;
           ml[k] = cluster_load2(smem_u32(part_ml + r), k);
           x[k] = cluster_load4(smem_u32(part + r * D + c), k);
         }
@@ -400,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float lsum = 0.f;
 #pragma unroll
         for (int k = 0; k < kPagedCluster; ++k) {
+          if (k >= p.cluster) continue;
           const float f = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
           lsum += f * ml[k].y;
           acc.x += f * x[k].x;
@@ -433,28 +436,27 @@ cudaError_t launch_dbc(const PagedLaunch& a) {
   auto kern = paged_decode_kernel<D, BF16, CLUSTER>;
   cudaError_t e = ensure_dyn_smem(kern, L::kBytes, configured);
   if (e != cudaSuccess) return e;
-  return launch_dependent<CLUSTER ? kPagedCluster : 1>(kern, dim3((unsigned)a.grid), kThreads,
-                                                       L::kBytes, a.stream, a.tmK, a.tmV,
-                                                       a.params);
+  return launch_clusters(kern, CLUSTER ? a.params.cluster : 1, dim3((unsigned)a.grid), kThreads,
+                         L::kBytes, a.stream, a.tmK, a.tmV, a.params);
 }
 
 template <int D, bool BF16>
-cudaError_t launch_db(const PagedLaunch& a, bool cluster) {
-  return cluster ? launch_dbc<D, BF16, true>(a) : launch_dbc<D, BF16, false>(a);
+cudaError_t launch_db(const PagedLaunch& a) {
+  return a.params.cluster > 0 ? launch_dbc<D, BF16, true>(a) : launch_dbc<D, BF16, false>(a);
 }
 
 template <int D>
-cudaError_t launch_d(const PagedLaunch& a, bool bf16, bool cluster) {
-  return bf16 ? launch_db<D, true>(a, cluster) : launch_db<D, false>(a, cluster);
+cudaError_t launch_d(const PagedLaunch& a, bool bf16) {
+  return bf16 ? launch_db<D, true>(a) : launch_db<D, false>(a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16, bool cluster) {
+cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16) {
   switch (d) {
-    case 64: return launch_d<64>(a, bf16, cluster);
-    case 96: return launch_d<96>(a, bf16, cluster);
-    default: return launch_d<128>(a, bf16, cluster);
+    case 64: return launch_d<64>(a, bf16);
+    case 96: return launch_d<96>(a, bf16);
+    default: return launch_d<128>(a, bf16);
   }
 }
 

@@ -21,10 +21,10 @@ constexpr int kMaxAttrDevices = 64;
 using DeviceFlags = std::atomic<bool>[kMaxAttrDevices];
 
 // Launches a kernel that calls grid_wait() as a programmatic dependent of the
-// previous kernel on the stream, in clusters of CLUSTER CTAs.
-template <int CLUSTER = 1, typename Kern, typename... Args>
-cudaError_t launch_dependent(Kern kern, dim3 grid, int threads, int smem, cudaStream_t stream,
-                             const Args&... args) {
+// previous kernel on the stream, in clusters of `cluster` CTAs.
+template <typename Kern, typename... Args>
+cudaError_t launch_clusters(Kern kern, int cluster, dim3 grid, int threads, int smem,
+                            cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
@@ -34,10 +34,16 @@ cudaError_t launch_dependent(Kern kern, dim3 grid, int threads, int smem, cudaSt
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {CLUSTER, 1, 1};
+  attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = CLUSTER > 1 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename Kern, typename... Args>
+cudaError_t launch_dependent(Kern kern, dim3 grid, int threads, int smem, cudaStream_t stream,
+                             const Args&... args) {
+  return launch_clusters(kern, 1, grid, threads, smem, stream, args...);
 }
 
 template <typename Kern>

@@ -53,6 +53,16 @@ def make(lens, Hq, Hkv, d, page, dtype, seed=0, pad=0, amp=1.0):
                 kv=cuda_i32(keys), max_q=max(max(new), 1))
 
 
+def widen(x, keys=5000):
+    """The same batch with a block table that reaches further (poison past the
+    lengths): decoding then runs in equal shares, not in clusters."""
+    t = x["table"]
+    more = -(-keys // x["k"].shape[2]) - t.shape[1]
+    if more <= 0:
+        return x
+    return dict(x, table=torch.cat([t, t.new_full((t.shape[0], more), 0x7FFFFFFF)], 1))
+
+
 def run(attn, x, causal, **kw):
     return attn.fwd_paged(x["q"], x["k"], x["v"], x["table"], x["cu"], x["kv"], x["max_q"],
                           causal=causal, **kw)
@@ -101,6 +111,17 @@ def test_few_rows(attn_lib, causal, dtype, d, lens, Hq, Hkv, page):
     check(x, o, lse, causal)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("copies,Hq,Hkv", [(1, 16, 4), (4, 8, 2), (8, 4, 2), (16, 2, 2), (30, 1, 1)])
+def test_clusters_of_every_size(attn_lib, dtype, d, copies, Hq, Hkv):
+    """Small batches with 8, 4, 2 and 1 CTAs an item, and one past them."""
+    x = make(DECODE * copies, Hq, Hkv, d, 32, dtype, seed=copies, pad=1)
+    assert workspace_bytes(attn_lib, x) == 0
+    o, lse = run(attn_lib, x, True)
+    assert attn_lib.poll_status() == (0, 0)
+    check(x, o, lse, True)
+
+
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
 @pytest.mark.parametrize("lens,Hq,Hkv,page", [
@@ -110,7 +131,7 @@ def test_few_rows(attn_lib, causal, dtype, d, lens, Hq, Hkv, page):
 def test_few_rows_in_equal_shares(attn_lib, causal, dtype, d, lens, Hq, Hkv, page):
     """Batches past the sizes that run in clusters: pieces of items, items of
     one CTA, items spread over many, CTAs without work."""
-    x = make(lens, Hq, Hkv, d, page, dtype, seed=d + page + len(lens), pad=1)
+    x = widen(make(lens, Hq, Hkv, d, page, dtype, seed=d + page + len(lens), pad=1))
     assert workspace_bytes(attn_lib, x) > 0
     o, lse = run(attn_lib, x, causal)
     assert attn_lib.poll_status() == (0, 0)
@@ -142,9 +163,9 @@ def test_rows_without_a_key(attn_lib, causal, lens, Hq, Hkv):
     check(x, o, lse, causal)
 
 
-@pytest.mark.parametrize("max_q,n_seq", [(1, 2), (1, 50), (30, 2)])
-def test_no_new_tokens_at_all(attn_lib, max_q, n_seq):
-    x = make([(0, 5), (0, 0)] * (n_seq // 2), 4, 2, 64, 16, "bf16", seed=6, pad=30)
+@pytest.mark.parametrize("max_q,n_seq,reach", [(1, 2, 16), (1, 50, 5000), (30, 2, 16)])
+def test_no_new_tokens_at_all(attn_lib, max_q, n_seq, reach):
+    x = widen(make([(0, 5), (0, 0)] * (n_seq // 2), 4, 2, 64, 16, "bf16", seed=6, pad=30), reach)
     o = torch.full_like(x["q"], 5.0)
     lse = torch.full(x["q"].shape[:2], 5.0, device="cuda")
     run(attn_lib, dict(x, max_q=max_q), True, out=o, lse=lse)
@@ -152,9 +173,9 @@ def test_no_new_tokens_at_all(attn_lib, max_q, n_seq):
     assert (o == 5.0).all() and (lse == 5.0).all()
 
 
-@pytest.mark.parametrize("lens,Hq", [(DECODE, 4), (DECODE * 5, 4), (CHUNKS, 4)])
-def test_padding_rows_are_left_alone_and_runs_repeat(attn_lib, lens, Hq):
-    x = make(lens, Hq, 2, 128, 16, "bf16", seed=8, pad=5)
+@pytest.mark.parametrize("lens,reach", [(DECODE, 16), (DECODE * 5, 5000), (CHUNKS, 16)])
+def test_padding_rows_are_left_alone_and_runs_repeat(attn_lib, lens, reach):
+    x = widen(make(lens, 4, 2, 128, 16, "bf16", seed=8, pad=5), reach)
     live = int(x["cu"][-1])
     outs = []
     ws = torch.full((max(workspace_bytes(attn_lib, x), 256),), 0xFF,
@@ -172,8 +193,9 @@ def test_padding_rows_are_left_alone_and_runs_repeat(attn_lib, lens, Hq):
 @pytest.mark.parametrize("lens", [[(1, 700), (1, 64)], [(1, 700), (1, 64)] * 12,
                                   [(40, 700), (1, 64)]])
 @pytest.mark.parametrize("amp,scale", [(30.0, None), (1.0, 1e-4)])
-def test_large_and_small_logits(attn_lib, lens, amp, scale):
-    x = make(lens, 4, 2, 128, 32, "fp16", seed=11, amp=amp)
+@pytest.mark.parametrize("reach", [16, 5000])
+def test_large_and_small_logits(attn_lib, lens, amp, scale, reach):
+    x = widen(make(lens, 4, 2, 128, 32, "fp16", seed=11, amp=amp), reach)
     o, lse = run(attn_lib, x, True, scale=scale)
     assert attn_lib.poll_status() == (0, 0)
     check(x, o, lse, True, scale)
@@ -181,10 +203,11 @@ def test_large_and_small_logits(attn_lib, lens, amp, scale):
 
 @pytest.mark.parametrize("lens", [[(1, 50), (1, 40), (1, 30)], [(1, 50), (1, 40), (1, 30)] * 8,
                                   [(50, 50), (1, 40), (20, 30)]])
-def test_bad_pages_lengths_and_offsets_are_reported(attn_lib, lens):
+@pytest.mark.parametrize("reach", [16, 5000])
+def test_bad_pages_lengths_and_offsets_are_reported(attn_lib, lens, reach):
     """Out-of-range page numbers, lengths past the table and offsets past the
     tensors: the call reports them and the other sequences keep their values."""
-    x = make(lens, 4, 2, 64, 16, "bf16", seed=13)
+    x = widen(make(lens, 4, 2, 64, 16, "bf16", seed=13), reach)
     good, _ = run(attn_lib, x, True)
     assert attn_lib.poll_status() == (0, 0)
     cu = x["cu"].tolist()
@@ -360,7 +383,7 @@ def test_pages_past_two_to_the_31_elements(attn_lib, chunk):
 def test_two_graphs_share_a_workspace(attn_lib):
     """Captured calls of different shapes (decoding, chunks) over one workspace,
     replayed in turn, give what they give with workspaces of their own."""
-    xs = [make(DECODE * 5, 4, 2, 64, 16, "bf16", seed=43), make(CHUNKS, 4, 2, 64, 16, "bf16", seed=47),
+    xs = [widen(make(DECODE * 5, 4, 2, 64, 16, "bf16", seed=43)), make(CHUNKS, 4, 2, 64, 16, "bf16", seed=47),
           make([(1, 6000), (2, 900)], 8, 1, 64, 16, "bf16", seed=53)]
     ws = torch.empty(max(workspace_bytes(attn_lib, x) for x in xs), dtype=torch.uint8, device="cuda")
     want = [run(attn_lib, x, True) for x in xs]
@@ -379,7 +402,7 @@ def test_two_graphs_share_a_workspace(attn_lib):
 
 def test_calls_on_two_streams(attn_lib):
     """Calls that overlap on two streams, each with its own workspace."""
-    xs = [make(DECODE * 20, 4, 2, 128, 16, "bf16", seed=59),
+    xs = [widen(make(DECODE * 20, 4, 2, 128, 16, "bf16", seed=59)),
           make([(200, 900), (128, 2000)], 4, 2, 128, 16, "bf16", seed=61)]
     want = [run(attn_lib, x, True) for x in xs]
     torch.cuda.synchronize()
@@ -400,6 +423,7 @@ def test_timeouts_wind_down(attn_lib):
     x = make([(1, 3000)] * 40, 16, 8, 128, 64, "bf16", seed=31)
     y = make([(300, 3000)] * 3, 16, 8, 128, 64, "bf16", seed=37)
     z = make([(1, 3000)] * 4, 16, 8, 128, 64, "bf16", seed=67)
+    assert workspace_bytes(attn_lib, x) > 0 and workspace_bytes(attn_lib, z) == 0
     for s in (x, y, z):
         run(attn_lib, s, True)
         assert attn_lib.poll_status() == (0, 0)
