@@ -418,6 +418,49 @@ def test_calls_on_two_streams(attn_lib):
         assert all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for o, l in g)
 
 
+@pytest.mark.parametrize("lens,reach", [([(1, 60), (1, 300)], 16), ([(1, 60), (1, 300)] * 6, 5000),
+                                        ([(40, 60), (1, 300)], 16)])
+def test_inputs_written_just_before_the_call(attn_lib, lens, reach):
+    """The kernels may start before the work ahead of them in the stream has
+    finished; what that work writes (copies from the host, a kernel's output)
+    is what they read, and what they overwrite has been read."""
+    Hq, Hkv, d, page = 4, 2, 64, 16
+    xs = [widen(make(lens, Hq, Hkv, d, page, "bf16", seed=s), reach) for s in (73, 79)]
+    table = attn_lib.rope_table(d)
+    hold = {k: v.clone() if torch.is_tensor(v) else v for k, v in xs[0].items()}
+    pinned = [{k: x[k].cpu().pin_memory() for k in ("cu", "kv", "table")} for x in xs]
+    new = [torch.randn(2, Hkv, x["q"].shape[1], d, device="cuda").bfloat16() for x in xs]
+    big = torch.randn(64 << 20, device="cuda")
+
+    def step(x, q, kv):
+        q = attn_lib.append_kv(kv[0], kv[1], x["k"], x["v"], x["table"], x["cu"], x["kv"],
+                               table=table, q=q)
+        return attn_lib.fwd_paged(q, x["k"], x["v"], x["table"], x["cu"], x["kv"], x["max_q"],
+                                  causal=True)
+
+    want = [step({k: v.clone() if torch.is_tensor(v) else v for k, v in x.items()}, x["q"], n)
+            for x, n in zip(xs, new)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    with torch.cuda.stream(side):
+        for i in (0, 1) * 8:
+            big.mul_(1.0)  # keeps the stream busy
+            for key in ("cu", "kv", "table"):
+                hold[key].copy_(pinned[i][key], non_blocking=True)
+            hold["k"].copy_(xs[i]["k"])
+            hold["v"].copy_(xs[i]["v"])
+            q = xs[i]["q"] * 2.0 * 0.5  # a kernel's output
+            o, lse = step(hold, q, new[i])
+            got.append((i, o * 1.0, lse * 1.0))
+            o.fill_(float("nan"))  # the memory goes back for the next step's outputs
+            del o, lse, q
+    torch.cuda.synchronize()
+    assert attn_lib.poll_status() == (0, 0)
+    for i, o, lse in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 def test_timeouts_wind_down(attn_lib):
     """Waits that run out report ATTN_ERR_TIMEOUT and the next call is right."""
     x = make([(1, 3000)] * 40, 16, 8, 128, 64, "bf16", seed=31)
