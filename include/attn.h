@@ -286,7 +286,7 @@ attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
  *                 the last at most total: sequence b's new tokens are rows
  *                 [cu_seqlens[b], cu_seqlens[b+1]) of the packed [H, total, d]
  *                 tensors (none: the sequence is skipped).  Rows behind the
- *                 last sequence (padding) are neither read nor written.
+ *                 last sequence (padding) are not written, and hold what they will.
  *   kv_lens     : DEVICE int32 [n_seq]: positions of sequence b in the cache,
  *                 its new tokens, the last ones, included.
  * These arrays are read on the device, so a captured graph replays with new
