@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t sw_off(int row, int piece) {
 // An item is a sequence's key/value head; the warps take the 16-key blocks of
 // its kUnit-key cost blocks in turn.
 constexpr int kUnit = kWarps * kKeys;
-using Cost = PagedCost<kUnit, 1, 1, 128>;
+using Cost = PagedCost<kUnit, 1, 1, 128, true>;
 using Walk = PagedWalk<Cost>;
 
 __device__ __forceinline__ int warp_blocks(const Walk& w, int warp) {

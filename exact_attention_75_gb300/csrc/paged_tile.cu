@@ -67,7 +67,7 @@ struct PagedTileLayout {
 // Weights: a key block of one tile was measured at 1.06 us, of a pair at 1.55,
 // an item's borders at 3 to 4 us; 3 : 4 and two blocks an item balance best (a
 // mixed batch 58.5 us, with 2 : 3 59.8, with equal weights 60.4).
-using Cost = PagedCost<128, 3, 4, 1024>;
+using Cost = PagedCost<128, 3, 4, 1024, false>;
 struct Walk : PagedWalk<Cost> {
   int n[2];  // key blocks of the piece that tile 0 / 1 sees (two: tile 1 has rows)
 
