@@ -540,3 +540,33 @@ def test_binding_refuses_wrong_tensors(attn_lib):
     attn_lib.append_kv(k, k, *cache, table=table, positions=pos, q=x["q"])
     attn_lib.rope(q4, q4[:, :2], pos, table)
     assert attn_lib.poll_status() == (0, 0)
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_random_paged_case(attn_lib, seed):
+    """Seeded draws of everything at once: head layout, head dim, dtype, page
+    size, masking, lengths (empty sequences, fewer keys than tokens), a table
+    that reaches further, padding rows, a scale of its own."""
+    g = np.random.default_rng(1000 + seed)
+    Hkv = int(g.choice([1, 2, 3, 5]))
+    G = int(g.choice([1, 2, 3, 4, 7, 8, 16, 40]))
+    d, page = int(g.choice([64, 96, 128])), int(g.choice([16, 32, 64, 128, 256]))
+    n = int(g.choice([1, 2, 5, 30, 140]))
+    kind = g.choice(["single", "few", "chunks"])
+    lens = []
+    for _ in range(n):
+        new = {"single": 1, "few": int(g.integers(0, 4)),
+               "chunks": int(g.integers(0, 300 if n < 10 else 12))}[kind]
+        if g.random() < 0.1:
+            new = 0
+        lens.append((new, int(g.integers(0, 900 if n < 50 else 90))))
+    if all(m == 0 for m, _ in lens):
+        lens[0] = (1, lens[0][1])
+    x = make(lens, Hkv * G, Hkv, d, page, str(g.choice(["bf16", "fp16"])), seed=seed,
+             pad=int(g.integers(0, 4)))
+    if g.random() < 0.5:
+        x = widen(x)
+    causal, scale = bool(g.random() < 0.7), float(g.choice([d ** -0.5, 0.02, 0.3]))
+    o, lse = run(attn_lib, x, causal, scale=scale)
+    assert attn_lib.poll_status() == (0, 0)
+    check(x, o, lse, causal, scale)
