@@ -80,6 +80,19 @@ cudaError_t launch_paged_join(const PagedLaunch& a, int d, bool bf16, bool decod
 
 #ifdef __CUDACC__
 
+// A row's statistics: the maximum m and the sum l of its exponentials.  A row
+// without a key has l = 0 (one with a key has a term of about 1); m tells
+// nothing, since the maximum passes over NaN scores and stays -inf where every
+// score is one, while l is NaN then.
+__device__ __forceinline__ float paged_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float paged_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+// Weight of partial sums at maximum M.
+__device__ __forceinline__ float paged_weight(float m, float l, float M) {
+  return l == 0.f ? 0.f : exp2f(m - M);
+}
+
 // One sequence of the batch, clamped so that no access leaves the tensors.
 struct PagedSeq {
   int s0, qlen, klen;

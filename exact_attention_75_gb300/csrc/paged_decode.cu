@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
           const float2 ml = meet_ml[k * kMeet + mr];
-          const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+          const float f = paged_weight(ml.x, ml.y, M);
           lsum += f * ml.y;
           const float4 x =
               *reinterpret_cast<const float4*>(meet + (k * kMeet + mr) * L::kRowStride + c);
@@ -376,11 +376,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           *reinterpret_cast<float4*>(part + r * D + c) = acc;
           if (c == 0) part_ml[r] = make_float2(M, lsum);
         } else if (whole) {
-          const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+          const float inv = paged_inverse(lsum);
           const size_t gr = grow(r);
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + c) = make_uint2(
               pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-          if (c == 0) p.lse[gr] = lsum > 0.f ? (M + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+          if (c == 0) p.lse[gr] = paged_lse(M, lsum);
         } else {
           *reinterpret_cast<float4*>(p.part_o + (slot * kPagedRows + r) * D + c) = acc;
           if (c == 0)
@@ -415,19 +415,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int k = 0; k < kPagedCluster; ++k) {
           if (k >= p.cluster) continue;
-          const float f = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
+          const float f = paged_weight(ml[k].x, ml[k].y, M);
           lsum += f * ml[k].y;
           acc.x += f * x[k].x;
           acc.y += f * x[k].y;
           acc.z += f * x[k].z;
           acc.w += f * x[k].w;
         }
-        const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+        const float inv = paged_inverse(lsum);
         const int i = r / p.G, h = r - i * p.G;
         const size_t gr = (size_t)(w.head * p.G + h) * p.total + w.sq.s0 + i;
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + c) = make_uint2(
             pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-        if (c == 0) p.lse[gr] = lsum > 0.f ? (M + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+        if (c == 0) p.lse[gr] = paged_lse(M, lsum);
       }
       cluster_sync();  // the others have read this CTA's part
     }

@@ -41,10 +41,10 @@ __device__ __forceinline__ void add(Sum& s, float m, float l, const float4& o) {
 
 template <int D, bool BF16>
 __device__ __forceinline__ void store(const PagedParams& p, size_t row, int c4, const Sum& s) {
-  const float inv = s.l > 0.f ? 1.f / s.l : 0.f;
+  const float inv = paged_inverse(s.l);
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + 4 * c4) = make_uint2(
       pack2<BF16>(s.o.x * inv, s.o.y * inv), pack2<BF16>(s.o.z * inv, s.o.w * inv));
-  if (c4 == 0) p.lse[row] = s.l > 0.f ? (s.m + log2f(s.l)) * 0.69314718055994531f : -INFINITY;
+  if (c4 == 0) p.lse[row] = paged_lse(s.m, s.l);
 }
 
 // Adds parts k0, k0 + 1, .. (at most FLIGHT of them) of element e (row r) of
@@ -65,7 +65,7 @@ __device__ __forceinline__ void add_parts(const PagedParams& p, Sum& s, int firs
   for (int i = 0; i < FLIGHT; ++i) {
     if (k0 + i >= parts) break;
     // a part with no key for the row holds no O
-    if (ml[i].x != -INFINITY) add(s, ml[i].x, ml[i].y, o[i]);
+    if (ml[i].y != 0.f) add(s, ml[i].x, ml[i].y, o[i]);
   }
 }
 
@@ -130,11 +130,11 @@ __device__ __forceinline__ void join_few(const PagedParams& p, int first, int pa
   for (int k = 1; k < PARTS; ++k) M = fmaxf(M, ml[k].x);
 #pragma unroll
   for (int k = 0; k < PARTS; ++k) {
-    f[k] = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
+    f[k] = paged_weight(ml[k].x, ml[k].y, M);
     l += f[k] * ml[k].y;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  if (c == 0) p.lse[row] = l > 0.f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  const float inv = paged_inverse(l);
+  if (c == 0) p.lse[row] = paged_lse(M, l);
   for (; c < D / 4; c += step) {
     float4 x[COLS][PARTS];
 #pragma unroll

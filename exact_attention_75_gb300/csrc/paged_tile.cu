@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (aborted) continue;
       tc_fence_after();
       if (whole) {
-        const float inv_l = l > 0.f ? 1.0f / l : 0.f;
+        const float inv_l = paged_inverse(l);
         // Rows go out through the warp's stage, 64 columns at a time (swizzled
         // 16-byte pieces), so that a store covers whole 128-byte row pieces:
         // a lane per row would write 16 bytes of 32 lines.
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (live) p.lse[grow] = (m + log2f(l)) * 0.69314718055994530942f;
+        if (live) p.lse[grow] = paged_lse(m, l);
       } else {
         uint4* part = reinterpret_cast<uint4*>(p.part_o + slot * kRows * D);
 #pragma unroll

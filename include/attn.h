@@ -344,6 +344,8 @@ size_t attn_fwd_paged_workspace_bytes(int n_seq, int max_q, int64_t max_keys, in
  *               at once need one each; calls in stream order may share one.
  * Cache rows that no row of the batch sees may hold anything (NaN included).
  * A value row that is infinite or NaN may reach every row of its sequence.
+ * A row with a score of NaN at a key it sees (a NaN or infinite query or key)
+ * has O and LSE NaN.
  * Partial results are joined in key order: equal calls give equal bits (the
  * split depends on all lengths of the batch).  d in {64, 96, 128}.
  * Cite: the FlashAttention-2 review, "Insights" and "Discussion Points"

@@ -570,3 +570,71 @@ def test_random_paged_case(attn_lib, seed):
     o, lse = run(attn_lib, x, causal, scale=scale)
     assert attn_lib.poll_status() == (0, 0)
     check(x, o, lse, causal, scale)
+
+
+# (batch, reach of the table): decoding in clusters; in equal shares, items whole
+# and split; one item over many CTAs; chunks whole and in 2 to 7 parts; chunks
+# in more than 8 and more than 16 parts
+NAN_BATCHES = [(DECODE, 16, 4, 1), (DECODE * 5, 5000, 4, 1), ([(1, 5000), (4, 70)], 16, 4, 1),
+               ([(16, 900)] * 38, 5000, 1, 1), (CHUNKS, 16, 4, 2), ([(700, 3000), (1, 50)], 16, 2, 1),
+               ([(20, 3500)], 16, 2, 1), ([(40, 16000)], 16, 2, 1)]
+
+
+def _live_rows(lens, causal):
+    """Packed rows that see a key, by sequence."""
+    at, rows = 0, []
+    for n, k in lens:
+        rows.append([at + i for i in range(n) if (i + k - n >= 0 if causal else k > 0)])
+        at += n
+    return rows
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("lens,reach,Hq,Hkv", NAN_BATCHES)
+def test_nan_and_infinite_queries_give_nan(attn_lib, causal, dtype, d, lens, reach, Hq, Hkv):
+    """A query with a NaN or an infinity has a NaN score at every key it sees
+    (inf x +-k sums to NaN): its row is NaN in O and LSE however the batch is
+    cut, and every other row keeps its bits."""
+    x = widen(make(lens, Hq, Hkv, d, 16, dtype, seed=83, pad=2), reach)
+    clean_o, clean_lse = run(attn_lib, x, causal)
+    check(x, clean_o, clean_lse, causal)
+    rows = [r[len(r) // 2] for r in _live_rows(lens, causal) if r]
+    hit = torch.zeros(x["q"].shape[:2], dtype=torch.bool, device="cuda")
+    q = x["q"].clone()
+    for i, r in enumerate(rows):
+        h = i % Hq
+        hit[h, r] = True
+        if i % 2:
+            q[h, r] = float("nan")
+        else:  # both infinities: some product of each sign, inf - inf
+            q[h, r, 0], q[h, r, 1] = float("inf"), float("inf")
+            q[h, r, 2:] = float("-inf")
+    o, lse = run(attn_lib, dict(x, q=q), causal)
+    assert attn_lib.poll_status() == (0, 0)
+    live = int(x["cu"][-1])
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    keep = ~hit[:, :live]
+    assert torch.equal(o[:, :live][keep], clean_o[:, :live][keep])
+    assert torch.equal(lse[:, :live][keep], clean_lse[:, :live][keep])
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("lens,reach,Hq,Hkv", NAN_BATCHES)
+def test_nan_key_reaches_the_rows_that_see_it(attn_lib, dtype, d, lens, reach, Hq, Hkv):
+    """A NaN in the last key of each sequence: its last row (causal) is NaN,
+    every row before keeps its bits."""
+    x = widen(make(lens, Hq, Hkv, d, 16, dtype, seed=89), reach)
+    clean_o, clean_lse = run(attn_lib, x, True)
+    k, table = x["k"].clone(), x["table"].tolist()
+    hit = torch.zeros(x["q"].shape[1], dtype=torch.bool, device="cuda")
+    at = 0
+    for b, (n, keys) in enumerate(lens):
+        if n and keys:
+            k[table[b][(keys - 1) // 16], :, (keys - 1) % 16, 5] = float("nan")
+            hit[at + n - 1] = True
+        at += n
+    o, lse = run(attn_lib, dict(x, k=k), True)
+    assert attn_lib.poll_status() == (0, 0)
+    assert torch.isnan(o[:, hit]).all() and torch.isnan(lse[:, hit]).all()
+    assert torch.equal(o[:, ~hit], clean_o[:, ~hit]) and torch.equal(lse[:, ~hit], clean_lse[:, ~hit])
