@@ -366,11 +366,12 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
       acc[6] += f * x1.z;
       acc[7] += f * x1.w;
     }
-    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    // lsum = 0: the row sees no key; NaN: a score was NaN (which the maximum passes over)
+    const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
     *reinterpret_cast<uint4*>(ou + (size_t)r * D + c) =
         make_uint4(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv),
                    pack2<BF16>(acc[4] * inv, acc[5] * inv), pack2<BF16>(acc[6] * inv, acc[7] * inv));
-    if (c == 0) lu[r] = lsum > 0.f ? (M + log2f(lsum)) * 0.69314718055994531f : -INFINITY;
+    if (c == 0) lu[r] = lsum == 0.f ? -INFINITY : (M + log2f(lsum)) * 0.69314718055994531f;
   }
 }
 

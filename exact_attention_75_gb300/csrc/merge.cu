@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const uint16_t* __restrict__
         for (int e = 0; e < 8; ++e) acc[e] = use ? fmaf(wt, x[e], acc[e]) : acc[e];
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // l = NaN: an LSE_s is NaN
     uint32_t packed[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const uint16_t* __restrict__
     if (live) {
       *reinterpret_cast<uint4*>(o + (size_t)row * D + col) =
           make_uint4(packed[0], packed[1], packed[2], packed[3]);
-      if (col == 0) lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+      if (col == 0) lse[row] = l == 0.f ? -INFINITY : m + logf(l);
     }
   }
 }

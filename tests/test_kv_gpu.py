@@ -210,3 +210,29 @@ def test_more_queries_than_keys_is_rejected(attn_lib):
     # Nq = 200 > Nk = 100: ATTN_ERR_INVALID_ARG before any launch
     assert L.attn_fwd_kv(p, p, p, p, pl, 1, 1, 1, 1, 200, 100, 64, 1, 0.125, 1, s) == 1
     assert attn_lib.poll_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96), ("bf16", 192),
+                                     ("fp16", 256)])
+@pytest.mark.parametrize("n_split", [1, 4, 40])
+def test_nan_query_is_nan_after_the_merge(attn_lib, dtype, d, n_split):
+    """A NaN query gives NaN partials in every split that it sees keys of, and
+    NaN in the merged O and LSE (not the zeros of a row without a key); the
+    other rows keep their bits."""
+    g = torch.Generator().manual_seed(97)
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    q, k, v = (torch.randn(2, h, n, d, generator=g).to(dt).cuda()
+               for h, n in ((4, 2), (2, 3000), (2, 3000)))
+    def merged(q):
+        return attn_lib.merge(*attn_lib.fwd_kv(q, k, v, n_split, causal=True))
+    clean_o, clean_lse = merged(q)
+    bad = q.clone()
+    bad[0, 1, 1, 3], bad[1, 3, 0] = float("nan"), float("nan")
+    hit = torch.isnan(bad.float()).any(-1)
+    part_o, part_lse = attn_lib.fwd_kv(bad, k, v, n_split, causal=True)
+    seen = torch.isfinite(attn_lib.fwd_kv(q, k, v, n_split, causal=True)[1])
+    assert torch.isnan(part_lse[seen & hit]).all() and torch.isnan(part_o[seen & hit]).all()
+    o, lse = merged(bad)
+    assert attn_lib.poll_status() == (0, 0)
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(o[~hit], clean_o[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
