@@ -199,10 +199,29 @@ __device__ __forceinline__ void report_bad(uint32_t* status, int site, int index
                             ((uint32_t)min(index, 0xFFFF) << 16));
 }
 
+// Records sequence b as invalid if its offsets or its length are out of range.
+__device__ __forceinline__ void append_check(const AppendParams& p, int64_t b) {
+  const int a = __ldg(p.cu_seqlens + b), e = __ldg(p.cu_seqlens + b + 1);
+  const int k = __ldg(p.kv_lens + b);
+  if ((b == 0 && a != 0) || a < 0 || e < a || e > p.total || k < 0 ||
+      k > (p.max_pages << p.page_log2))
+    report_bad(p.status, kBadBatch, (int)b);
+}
+
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams p) {
   grid_wait();
   grid_release();
+  // The blocks behind the tokens' check the batch, a sequence a thread: what
+  // the tokens' own places do not show (a last offset past the tokens,
+  // sequences without any).  Without the check, with blocks of its own, and
+  // behind the stores of a token's first thread: 64 single tokens 3.18, 3.28
+  // and 3.30 us, a prompt of 16384 tokens 43.6, 43.6 and 43.9.
+  if (blockIdx.x >= p.token_blocks) {
+    const int64_t b = (int64_t)(blockIdx.x - p.token_blocks) * kThreads + threadIdx.x;
+    if (b < p.n_seq) append_check(p, b);
+    return;
+  }
   const int per_row = p.d / 16;
   const int group = blockIdx.x % p.head_groups;
   const int64_t idx = (int64_t)(blockIdx.x / p.head_groups) * kThreads + threadIdx.x;
@@ -321,7 +340,8 @@ cudaError_t launch_append(const AppendLaunch& a, int num_sms) {
   const int64_t bx = ((int64_t)p.total * (p.d / 16) + kThreads - 1) / kThreads;
   p.group_heads = heads_per_block(bx, heads, num_sms);
   p.head_groups = (heads + p.group_heads - 1) / p.group_heads;
-  const dim3 grid((unsigned)(bx * p.head_groups));
+  p.token_blocks = (unsigned)(bx * p.head_groups);
+  const dim3 grid(p.token_blocks + ((unsigned)p.n_seq + kThreads - 1) / kThreads);
   if (a.bf16) {
     if (a.interleaved)
       return launch_dependent(append_kernel<true, true>, grid, kThreads, 0, a.stream, p);

@@ -51,6 +51,7 @@ struct AppendParams {
   uint32_t* status;
   int n_axes, n_seq, max_pages, n_pages, page_log2, total, Hq, Hkv, d, rot;
   int group_heads, head_groups;
+  unsigned token_blocks;   // the blocks behind them check the batch
 };
 
 struct AppendLaunch {

@@ -218,3 +218,33 @@ def test_append_reports_bad_pages_and_lengths(attn_lib):
                 want_k[table[b][at // page], :, at % page] = k[:, b]
                 want_v[table[b][at // page], :, at % page] = v[:, b]
         assert torch.equal(k1, want_k) and torch.equal(v1, want_v)
+
+
+def test_append_reports_lengths_and_offsets_out_of_range(attn_lib):
+    """Offsets that run past the tokens, fall, or do not begin at 0, and a
+    length past the table of a sequence without new tokens: reported."""
+    dt, Hkv, page, d = torch.bfloat16, 1, 16, 64
+    kp, vp = _cache(6, Hkv, page, d, dt, 1)
+    k, v = _normal((Hkv, 3, d), dt, 3), _normal((Hkv, 3, d), dt, 4)
+    cuda = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = cuda([[0, 1], [2, 3], [4, 5]])
+    good = ([0, 1, 2, 3], [30, 30, 30])
+    for cu, lens, bad in [([0, 1, 2, 9], [30, 30, 30], 2), ([0, 2, 1, 3], [30, 30, 30], 1),
+                          ([0, 1, 1, 3], [30, 33, 30], 1), ([0, 1, 1, 3], [30, -1, 30], 1),
+                          ([0, 3, 3, 3], [30, 30, 40], 2), ([0, 5, 3, 3], [30, 30, 30], None),
+                          ([-1, 1, 2, 3], [30, 30, 30], 0)]:
+        for c, n, want in ((cu, lens, 1), (good[0], good[1], 0)):
+            attn_lib.append_kv(k, v, kp.clone(), vp.clone(), table, cuda(c), cuda(n))
+            st, detail = attn_lib.poll_status()
+            assert st == want, (c, n, st, hex(detail))
+            assert not want or bad is None or detail >> 16 == bad, (c, n, hex(detail))
+    # more sequences than tokens
+    many = 4000
+    cu, lens = [0] + [3] * many, [30] * many
+    table = cuda([[0, 1]] * many)
+    attn_lib.append_kv(k, v, kp.clone(), vp.clone(), table, cuda(cu), cuda(lens))
+    assert attn_lib.poll_status() == (0, 0)
+    lens[3777] = 33
+    attn_lib.append_kv(k, v, kp.clone(), vp.clone(), table, cuda(cu), cuda(lens))
+    st, detail = attn_lib.poll_status()
+    assert st == 1 and detail >> 16 == 3777
