@@ -494,7 +494,8 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, ta
     pairs are (p, p + rot/2), or (2p, 2p + 1) if interleaved; channels past rot
     pass through.  q [B,H,N,d], k [B,Hkv,N,d] (or packed [H,total,d]) may be
     strided views with contiguous rows (a slice of a fused projection); new
-    outputs are contiguous, and out_q / out_k may be q / k themselves.
+    outputs are contiguous, and out_q / out_k may be q / k themselves (the
+    same views), but must not overlap the inputs otherwise.
     positions: int32 [axes, N] or [axes, B, N].  Returns (q', k')."""
     return _binding().rope(q, k, positions, table, interleaved, out_q, out_k, False)
 
@@ -523,7 +524,8 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
     [n_pages,Hkv,page,d].  table: see rope_table (None: no turn); positions:
     int32 [axes, total] (None: the position in the cache on every axis).
     Returns the turned queries (None without q); rows behind the last sequence
-    are left as they were."""
+    are left as they were.  out_q: contiguous; it may be q if q is, and must not
+    overlap the inputs otherwise."""
     return _binding().append_kv(k, v, k_pages, v_pages, block_table, cu_seqlens, kv_lens, table,
                                 positions, interleaved, q, out_q)
 

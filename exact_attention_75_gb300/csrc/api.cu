@@ -433,6 +433,15 @@ bool strides_ok(const int64_t* s, int n) {
   return true;
 }
 
+// Whether an output at the address of its input has the input's layout (rows
+// are then read and written by the same thread): element strides s, t of
+// dimensions of size n, the ones of size 1 free.
+bool same_layout(const int64_t* s, const int64_t* t, const int64_t* n, int dims) {
+  for (int i = 0; i < dims; ++i)
+    if (n[i] > 1 && s[i] != t[i]) return false;
+  return true;
+}
+
 // A decoding batch runs in clusters of 8, 4, 2 or 1 CTAs an item (sequence and
 // key/value head), as many as are resident at once, while the block table
 // reaches no further than kPagedClusterKeys a CTA (a long sequence among short
@@ -520,6 +529,12 @@ attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
   if (pos_batches != 1 && pos_batches != B) return ATTN_ERR_INVALID_ARG;
   if (!strides_ok(strides, k != nullptr ? 12 : 6)) return ATTN_ERR_INVALID_ARG;
   if (B > 65535 || ((int64_t)Hq + Hkv) * N > 0x7FFFFFFF) return ATTN_ERR_INVALID_ARG;
+  const int64_t nq[3] = {B, Hq, N}, nk[3] = {B, Hkv, N};
+  if (q_out == q && !same_layout(strides, strides + 3, nq, 3)) return ATTN_ERR_INVALID_ARG;
+  if (k != nullptr) {
+    if (k_out == k && !same_layout(strides + 6, strides + 9, nk, 3)) return ATTN_ERR_INVALID_ARG;
+    if (q_out == k || k_out == q || q_out == k_out) return ATTN_ERR_INVALID_ARG;
+  }
   DeviceInfo* di = nullptr;
   attn_status st = device_info(&di);
   if (st != ATTN_OK) return st;
@@ -570,6 +585,12 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
                               n_pages, page, max_pages, q != nullptr ? Hq : Hkv, Hkv);
   if (st != ATTN_OK) return st;
   if ((2 * (int64_t)Hkv + Hq) * total > 0x7FFFFFFF) return ATTN_ERR_INVALID_ARG;
+  if (q != nullptr) {
+    const int64_t n[2] = {Hq, total}, contiguous[2] = {(int64_t)total * d, d};
+    if (q_out == q && !same_layout(strides + 4, contiguous, n, 2)) return ATTN_ERR_INVALID_ARG;
+    if (q_out == k || q_out == v || q_out == k_pages || q_out == v_pages)
+      return ATTN_ERR_INVALID_ARG;
+  }
   DeviceInfo* di = nullptr;
   st = device_info(&di);
   if (st != ATTN_OK) return st;

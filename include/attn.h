@@ -253,7 +253,7 @@ attn_status attn_bwd_varlen(const void* q, const void* k, const void* v, const v
  * (gradients of the outputs in, of the inputs out).
  *   q, q_out  : [B,Hq,N,d];  k, k_out : [B,Hkv,N,d], or both NULL with Hkv = 0.
  *               fp16/bf16, rows contiguous; in place (the same pointer and
- *               strides) or without overlap.
+ *               strides, ATTN_ERR_INVALID_ARG with others) or without overlap.
  *   strides   : HOST array of 12 (without k: 6) element strides of the batch,
  *               head and token dimensions of q, q_out, k, k_out, each a
  *               non-negative multiple of 8.
@@ -301,7 +301,8 @@ attn_status attn_rope(const void* q, const void* k, void* q_out, void* k_out,
  *               to position kv_lens[b] - n + i.
  *   strides   : HOST array of 6 (without q: 4) element strides of the head and
  *               token dimensions of k, v, q, each a non-negative multiple of 8.
- *   q_out     : [Hq, total, d] contiguous, written; may be q.
+ *   q_out     : [Hq, total, d] contiguous, written; may be q if q is contiguous
+ *               (ATTN_ERR_INVALID_ARG if it is not), and overlaps no other input.
  *   table     : NULL (no rotation; positions NULL, rot ignored), or as in
  *               attn_rope: keys and queries are turned on the way.
  *   positions : DEVICE int32 [n_axes, total], or NULL: the position in the

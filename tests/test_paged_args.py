@@ -61,6 +61,49 @@ def test_append_refusals(L, change, want):
     assert L.attn_append_kv(*dict(APPEND, **change).values()) == want
 
 
+# the refusals above once more with operands that lie apart, so that each is due
+# to its own change alone
+P1, P2, P3, P4 = (ctypes.c_void_p(x << 20) for x in (2, 3, 4, 5))
+ROPE_APART = dict(ROPE, k=P1, oq=P2, ok=P3)
+APPEND_APART = dict(APPEND, v=P1, q=P2, oq=P3, kp=P4, vp=ctypes.c_void_p(6 << 20))
+
+
+@pytest.mark.parametrize("change,want", test_rope_refusals.pytestmark[0].args[1])
+def test_rope_refusals_of_operands_apart(L, change, want):
+    assert L.attn_rope(*dict(ROPE_APART, **change).values()) == want
+
+
+@pytest.mark.parametrize("change,want", test_append_refusals.pytestmark[0].args[1])
+def test_append_refusals_of_operands_apart(L, change, want):
+    assert L.attn_append_kv(*dict(APPEND_APART, **change).values()) == want
+
+
+def _i64(*s):
+    return (ctypes.c_int64 * len(s))(*s)
+
+
+# q, k views of a projection [B, N, heads, d]; contiguous outputs
+ROPE_VIEWS = _i64(8 * 512, 64, 512, 4 * 8 * 64, 8 * 64, 64, 8 * 512, 64, 512, 2 * 8 * 64, 8 * 64, 64)
+
+
+@pytest.mark.parametrize("change", [
+    dict(oq=P, strides=ROPE_VIEWS), dict(ok=P1, strides=ROPE_VIEWS), dict(oq=P1), dict(ok=P),
+    dict(ok=P2), dict(oq=P, strides=_i64(64, 64, 64, 64, 64, 128, 64, 64, 64, 64, 64, 64)),
+    dict(oq=P, B=1, pos_batches=1, strides=_i64(0, 64, 512, 0, 128, 512, 0, 64, 64, 0, 64, 64)),
+    dict(ok=P1, N=1, strides=_i64(64, 64, 0, 64, 64, 0, 128, 64, 0, 256, 64, 64))])
+def test_rope_refuses_outputs_over_inputs_of_another_layout(L, change):
+    assert L.attn_rope(*dict(ROPE_APART, **change).values()) == INVALID
+
+
+@pytest.mark.parametrize("change", [
+    dict(oq=P2), dict(oq=P2, strides=_i64(64, 512, 64, 512, 64, 512)),  # rows by token, by head
+    dict(oq=P2, Hq=2, strides=_i64(576, 64, 576, 64, 640, 64)),
+    dict(oq=P2, total=1, strides=_i64(64, 0, 64, 0, 128, 0)),
+    dict(oq=P), dict(oq=P1), dict(oq=P4), dict(oq=ctypes.c_void_p(6 << 20))])
+def test_append_refuses_turned_queries_over_inputs(L, change):
+    assert L.attn_append_kv(*dict(APPEND_APART, **change).values()) == INVALID
+
+
 PAGED = dict(q=P, kp=P, vp=P, o=P, lse=P, table=P, cu=P, kv=P, ws=P, ws_bytes=1 << 40, n_seq=2,
              max_q=4, total=9, n_pages=8, page=16, max_pages=4, Hq=4, Hkv=2, d=64, causal=1,
              scale=0.1, dtype=1, stream=None)

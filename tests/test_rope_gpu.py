@@ -248,3 +248,42 @@ def test_append_reports_lengths_and_offsets_out_of_range(attn_lib):
     attn_lib.append_kv(k, v, kp.clone(), vp.clone(), table, cuda(cu), cuda(lens))
     st, detail = attn_lib.poll_status()
     assert st == 1 and detail >> 16 == 3777
+
+
+def test_outputs_over_inputs(attn_lib):
+    """Outputs at the address of their input: the same layout works, whatever
+    the strides of dimensions of size 1; another one is refused and leaves the
+    input alone."""
+    d, dt = 64, torch.bfloat16
+    table = _table(attn_lib, d, 1)
+    for heads, n in ((4, 30), (4, 1), (1, 30)):
+        pos = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+        rows = _normal((n, heads, d), dt, heads + n)  # by token
+        q, flat = rows.transpose(0, 1), rows.view(heads, n, d)
+        keep, want = rows.clone(), attn_lib.rope(q.contiguous(), None, pos, table)[0]
+        kp, vp = _cache(2, 1, 64, d, dt, 1)
+        kv = _normal((1, n, d), dt, 3)
+        cuda = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+        batch = kp, vp, cuda([[0]]), cuda([0, n]), cuda([n])
+        if heads > 1 and n > 1:
+            for call in (lambda: attn_lib.rope(q, None, pos, table, out_q=flat),
+                         lambda: attn_lib.append_kv(kv, kv, *batch, table=table, q=q, out_q=flat)):
+                with pytest.raises(attn_lib.AttnError) as e:
+                    call()
+                assert e.value.status == 1 and torch.equal(rows, keep)
+        else:
+            attn_lib.rope(q, None, pos, table, out_q=flat)
+            assert torch.equal(flat, want)
+            rows.copy_(keep)
+            attn_lib.append_kv(kv, kv, *batch, table=table, q=q, out_q=flat)
+            assert torch.equal(flat, want)
+            rows.copy_(keep)
+        attn_lib.rope(q, None, pos, table, out_q=q)
+        assert torch.equal(q, want)
+        full = keep.transpose(0, 1).contiguous()
+        attn_lib.append_kv(kv, kv, *batch, table=table, q=full, out_q=full)
+        assert torch.equal(full, want)
+        with pytest.raises(attn_lib.AttnError):
+            attn_lib.append_kv(full, full, *(t.expand(2, heads, 64, d).contiguous() for t in batch[:2]),
+                               *batch[2:], table=table, q=want, out_q=full)
+    assert attn_lib.poll_status() == (0, 0)
