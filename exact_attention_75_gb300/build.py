@@ -6,19 +6,24 @@ decoding-step calls (_binding.so) with the host compiler.
 Each .cu file under csrc/ is compiled in parallel to an object file in
 ``_build/``, then linked into ``_build/libattn.so`` (CUDA runtime linked
 statically; the driver API is reached through cudaGetDriverEntryPointByVersion,
-so the library loads on machines without a GPU driver).  csrc/binding.cpp is
-compiled against the installed torch and Python headers.  A file is recompiled
+so the library loads on machines without a GPU driver).  A file is recompiled
 only when it, or a header under csrc/ or include/, is newer than its object.
+csrc/binding.cpp is compiled against the installed torch and Python headers,
+again when those change; the library is linked whatever becomes of it, and
+without torch it is left out.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -55,8 +60,6 @@ def _compile(src: str, obj: str, verbose: bool) -> str:
 
 
 def _compile_binding(src: str, out: str) -> str:
-    import sysconfig
-
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -76,6 +79,25 @@ def _compile_binding(src: str, out: str) -> str:
     return r.stderr
 
 
+def _read(path: str) -> Optional[str]:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _torch() -> Optional[str]:
+    """What _binding.so is compiled against: Python's ABI, torch's place and
+    version.  None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    root = os.path.dirname(spec.origin)
+    with open(os.path.join(root, "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{root}\n{f.read()}"
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if needed) and return the path of libattn.so."""
     os.makedirs(BUILD, exist_ok=True)
@@ -90,23 +112,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
             jobs[s] = o
     src = os.path.join(CSRC, "binding.cpp")
     header = os.path.getmtime(os.path.join(INCLUDE, "attn.h"))
-    bind = force or not os.path.exists(BINDING) or \
-        os.path.getmtime(BINDING) < max(os.path.getmtime(src), header)
-    if jobs or bind:
-        with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + bind)) as ex:
-            futs = {ex.submit(_compile_binding, src, BINDING): src} if bind else {}
-            futs.update({ex.submit(_compile, s, o, verbose): s for s, o in jobs.items()})
-            for f in cf.as_completed(futs):
-                log = f.result()
-                if verbose and log:
-                    sys.stderr.write(log)
-    if jobs or not os.path.exists(LIB):
-        tmp = LIB + ".tmp"
-        r = subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs,
-                           capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
-        os.replace(tmp, LIB)
+    stamp, against = BINDING + ".txt", _torch()
+    if against is None:
+        sys.stderr.write("torch is not installed: the Python entry of the rotary and paged calls "
+                         "(_binding.so) is not built\n")
+    bind = against is not None and (
+        force or not os.path.exists(BINDING) or _read(stamp) != against or
+        os.path.getmtime(BINDING) < max(os.path.getmtime(src), header))
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, len(jobs) + bind))) as ex:
+        binding = ex.submit(_compile_binding, src, BINDING) if bind else None
+        for f in cf.as_completed([ex.submit(_compile, s, o, verbose) for s, o in jobs.items()]):
+            log = f.result()
+            if verbose and log:
+                sys.stderr.write(log)
+        if jobs or not os.path.exists(LIB):
+            tmp = LIB + ".tmp"
+            r = subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs,
+                               capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
+            os.replace(tmp, LIB)
+        if binding is not None:
+            binding.result()
+            with open(stamp, "w") as f:
+                f.write(against)
     return LIB
 
 
