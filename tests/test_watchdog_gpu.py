@@ -153,3 +153,55 @@ def test_decoding_kernel_winds_down_when_waits_run_out(attn_lib):
                                            w.causal, w.scale, 4)
         assert np.max(np.abs(to64(Op[:, b, h]) - O_ref[:, 0, 0])) <= 2e-2
         assert np.max(np.abs(to64(Lp[:, b, h]) - L_ref[:, 0, 0])) <= 5e-3
+
+
+@pytest.mark.parametrize("kind,dtype,d", [("tile", "bf16", 128), ("tile", "fp16", 64),
+                                          ("tile", "bf16", 96), ("shares", "bf16", 128),
+                                          ("shares", "fp16", 128), ("cluster", "bf16", 128),
+                                          ("cluster", "fp16", 128)])
+def test_paged_kernels_wind_down_when_waits_run_out(attn_lib, kind, dtype, d):
+    """The same for attention over a paged cache: chunks on the tile kernel
+    (its producer waits a block's products, over 1 us, for each slot), decoding
+    in equal shares, and the form that runs in clusters (300 items, a cluster
+    of one CTA each).  Waits of clusters are short: a few in ten launches have
+    one over 1 us while L2 is being written back and another stream copies,
+    with larger clusters none.  A launch whose waits run out reports
+    ATTN_ERR_TIMEOUT at a wait of that kernel, and the next one at the normal
+    limit gives the bits of an undisturbed one."""
+    import test_paged_gpu as pg
+    lens, Hq, Hkv = {"tile": ([(300, 3000)] * 3, 16, 8), "shares": ([(1, 3000)] * 40, 16, 8),
+                     "cluster": ([(1, 900)] * 300, 1, 1)}[kind]
+    x = pg.make(lens, Hq, Hkv, d, 64, dtype, seed=d)
+    assert (pg.workspace_bytes(attn_lib, x) == 0) == (kind == "cluster")
+    want, want_lse = pg.run(attn_lib, x, True)
+    assert attn_lib.poll_status() == (0, 0)
+    # waits; the drains (66, 69, 70, 73) keep a longer limit
+    waits = {67, 68, 71, 72, 74, 75} if kind == "tile" else {65}
+    sites, want_sites = [], 1 if kind == "cluster" else 3
+    flush = torch.empty(1 << 29, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    attn_lib.set_wait_limit_us(1)
+    try:
+        for _ in range(400):
+            flush.fill_(1)
+            if kind == "cluster":
+                torch.cuda.synchronize()
+                with torch.cuda.stream(side):
+                    flush[1 << 28:].copy_(flush[:1 << 28])
+            pg.run(attn_lib, x, True)
+            torch.cuda.synchronize()
+            st, detail = attn_lib.poll_status()
+            assert st in (0, 4), (st, hex(detail))
+            if st == 4:
+                sites.append(detail >> 8 & 0xFF)
+                if len(sites) == want_sites:
+                    break
+    finally:
+        attn_lib.set_wait_limit_us(0)
+    assert set(sites) <= waits, sites
+    got, got_lse = pg.run(attn_lib, x, True)
+    assert attn_lib.poll_status() == (0, 0)
+    assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
+    if kind == "cluster" and not sites:
+        pytest.skip("no wait of the clusters outlasted 1 us")
+    assert len(sites) == want_sites
