@@ -638,3 +638,46 @@ def test_nan_key_reaches_the_rows_that_see_it(attn_lib, dtype, d, lens, reach, H
     assert attn_lib.poll_status() == (0, 0)
     assert torch.isnan(o[:, hit]).all() and torch.isnan(lse[:, hit]).all()
     assert torch.equal(o[:, ~hit], clean_o[:, ~hit]) and torch.equal(lse[:, ~hit], clean_lse[:, ~hit])
+
+
+def parts_of(attn, x, causal):
+    """O, LSE and the numbers of parts of the items that the call split, read
+    from the descriptions at the head of its workspace (per CTA and slot: parts
+    in all, 0 where the slot is empty)."""
+    ws = torch.zeros(workspace_bytes(attn, x), dtype=torch.uint8, device="cuda")
+    o, lse = run(attn, x, causal, workspace=ws)
+    few = x["max_q"] * (x["q"].shape[0] // x["k"].shape[1]) <= 16
+    ctas = 2 * 160 if few else 160
+    desc = ws[:ctas * 64].view(torch.int32).view(ctas, 2, 2, 4)
+    return o, lse, set(desc[:, :, 0, 0].flatten().tolist()) - {0}
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("lens,Hq,Hkv,parts", [
+    ([(17, 600)], 1, 1, (2, 4)), ([(33, 2000)], 2, 1, (5, 8)), ([(200, 1900)], 1, 1, (5, 8)),
+    ([(20, 3500)], 2, 1, (9, 16)), ([(64, 3900)], 7, 1, (9, 16)), ([(130, 3000), (1, 40)], 2, 2, (9, 16)),
+    ([(40, 16000)], 2, 1, (17, 160)), ([(250, 9000)], 1, 1, (17, 160)),
+    ([(64, 12000), (5, 9000), (0, 3)], 4, 2, (17, 160)), ([(300, 130)] * 9, 1, 1, None)])
+def test_chunks_in_many_parts(attn_lib, causal, dtype, d, lens, Hq, Hkv, parts):
+    """The join of tiles at every number of parts it has a form for, the last
+    parts seen by none of a causal item's first rows."""
+    x = make(lens, Hq, Hkv, d, 32, dtype, seed=101 + d, pad=2)
+    o, lse, got = parts_of(attn_lib, x, causal)
+    assert attn_lib.poll_status() == (0, 0)
+    if parts is not None:
+        assert any(parts[0] <= n <= parts[1] for n in got), got
+    check(x, o, lse, causal)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("lens,Hq,Hkv,parts", [
+    ([(1, 4600)] * 38, 4, 4, (2, 4)), ([(2, 4500)] * 10, 8, 4, (5, 16)),
+    ([(1, 9000), (1, 70)], 8, 1, (17, 320))])
+def test_few_rows_in_many_parts(attn_lib, dtype, d, lens, Hq, Hkv, parts):
+    """The join of decoding items at every number of parts it has a form for."""
+    x = widen(make(lens, Hq, Hkv, d, 64, dtype, seed=103 + d, pad=1))
+    o, lse, got = parts_of(attn_lib, x, True)
+    assert attn_lib.poll_status() == (0, 0)
+    assert any(parts[0] <= n <= parts[1] for n in got), got
+    check(x, o, lse, True)
