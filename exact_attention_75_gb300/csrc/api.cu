@@ -443,24 +443,34 @@ bool same_layout(const int64_t* s, const int64_t* t, const int64_t* n, int dims)
 }
 
 // A decoding batch runs in clusters of 8, 4, 2 or 1 CTAs an item (sequence and
-// key/value head), as many as are resident at once, while the block table
-// reaches no further than kPagedClusterKeys a CTA (a long sequence among short
-// ones keeps its cluster's CTAs to itself).  Measured per call in a graph,
-// clusters against equal shares (bf16, d = 128):
-//   4 items (8 CTAs each)   64 keys 5.1 / 6.0 us, 1024 5.8 / 8.3, 4096 10.1 / 8.9,
-//                           8192 16.0 / 10.0
-//   36 items (8)            256 keys 6.0 / 8.4, 4096 17.3 / 19.6
+// key/value head), as many as are resident at once on 152 SMs (of fewer, the
+// last clusters wait), while the block table reaches no further than
+// kPagedClusterKeys a CTA (a long sequence among short ones keeps its cluster's
+// CTAs to itself), and where the clusters leave CTAs idle that equal shares
+// would use, no further than kPagedClusterKeysIdle.  Measured per call in a
+// graph, clusters against equal shares (bf16, d = 128, all sequences as long as
+// the table):
+//   4 items (8 CTAs each)   256 keys 5.4 / 7.0 us, 1024 6.2 / 7.6, 2048 7.6 / 7.8,
+//                           4096 10.6 / 8.2
+//   16 items (8)            1024 keys 7.0 / 8.5, 2048 8.6 / 8.6, 4096 12.1 / 10.6
+//   24 items (8)            2048 keys 8.9 / 9.6, 4096 12.2 / 12.2, 8192 19.3 / 18.1
+//   36 items (8)            1024 keys 7.5 / 9.4, 4096 12.6 / 14.3
 //   38 items (8: the last clusters wait)  256 keys 10.7 / 8.4
-//   40 items (4)            256 keys 5.9 / 8.4, 2048 13.6 / 14.9
-//   80 items (2)            256 keys 6.4 / 8.6, 1024 13.4 / 15.0
-//   300 items (1)           256 keys 11.3 / 16.0, 1024 29.0 / 33.3, 256 to 1024
-//                           keys 23.2 / 25.5
-// Without a graph a call in shares takes the host 9 to 10 us at least (two
-// launches and a workspace), in clusters 6.
+//   40 items (4)            256 keys 5.9 / 7.7, 1024 8.4 / 9.5, 2048 11.7 / 11.4
+//                           (d = 64: 9.4 / 10.2), 4096 18.1 / 15.3
+//   56 items (4)            1024 keys 8.6 / 10.4, 2048 11.9 / 13.2
+//   80 items (2)            256 keys 6.4 / 8.2, 1024 11.3 / 11.6, 2048 17.9 / 15.1
+//   160 items (1)           256 keys 7.0 / 9.9, 1024 16.9 / 16.1
+//   300 items (1)           256 keys 7.6 / 11.8, 1024 28.4 / 32.2
+// and with lengths of a quarter of the table's up to it 300 items of 1024 keys
+// 23.2 / 25.5.  Without a graph a call in shares takes the host 9 to 10 us at
+// least (two launches and a workspace), in clusters 6.
 constexpr int kPagedClusterWide = 288;  // resident CTAs in clusters of 8 or 4
 constexpr int kPagedClusterCtas = 300;
 constexpr int64_t kPagedClusterKeys = 512;      // times the CTAs of an item,
 constexpr int64_t kPagedClusterKeysMin = 1024;  // at least
+constexpr int64_t kPagedClusterKeysIdle = 2048;
+constexpr int kPagedClusterFull = 192;          // CTAs that fill most of the card
 
 int log2_of(int pow2) {
   int n = 0;
@@ -499,8 +509,11 @@ struct PagedPlan {
     cluster = decode ? kPagedCluster : 0;
     while (cluster > 0 && items * cluster > (cluster > 2 ? kPagedClusterWide : kPagedClusterCtas))
       cluster >>= 1;
-    const int64_t keys = kPagedClusterKeys * cluster;
-    if (max_keys > (keys > kPagedClusterKeysMin ? keys : kPagedClusterKeysMin)) cluster = 0;
+    int64_t keys = kPagedClusterKeys * cluster;
+    if (keys < kPagedClusterKeysMin) keys = kPagedClusterKeysMin;
+    if (items * cluster < kPagedClusterFull && keys > kPagedClusterKeysIdle)
+      keys = kPagedClusterKeysIdle;
+    if (max_keys > keys) cluster = 0;
     const size_t ctas = cluster ? 0 : (decode ? 2 * kPagedMaxSms : kPagedMaxSms);
     const size_t rows = 2 * ctas * (decode ? kPagedRows : kPagedTileRows);
     ml = 4 * ctas * sizeof(int4);

@@ -158,3 +158,13 @@ def test_binding_refuses_cpu_tensors():
         attn.append_kv(q, q, pages, pages, i(1, 2), i(2), i(1))
     with pytest.raises(ValueError):
         attn.fwd_paged(q, pages, pages, i(1, 2), i(2), i(1), 1)
+
+
+@pytest.mark.parametrize("n_seq,Hkv,keys,clusters", [
+    (1, 4, 2048, True), (1, 4, 4096, False), (4, 4, 4096, False), (6, 4, 4096, True),
+    (9, 4, 4096, True), (9, 4, 8192, False), (10, 4, 1024, True), (10, 4, 2048, True),
+    (14, 4, 2048, True), (20, 4, 1024, True), (75, 4, 1024, True), (75, 4, 2048, False)])
+def test_decoding_batches_in_clusters(L, n_seq, Hkv, keys, clusters):
+    """Clusters (which need no workspace) where they measured faster: few keys
+    a CTA, and a short reach where they leave CTAs idle."""
+    assert (attn.fwd_paged_workspace_bytes(n_seq, 1, keys, 4 * Hkv, Hkv, 128) == 0) == clusters
