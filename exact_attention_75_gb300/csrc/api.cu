@@ -645,7 +645,7 @@ size_t attn_fwd_paged_workspace_bytes(int n_seq, int max_q, int64_t max_keys, in
                                       int d) {
   if (n_seq < 1 || max_q < 1 || max_keys < 1 || max_keys > (1 << 29)) return 0;
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (int64_t)n_seq * Hkv > 0x7FFFFFFF) return 0;
-  if (d != 64 && d != 96 && d != 128) return 0;
+  if ((d != 64 && d != 96 && d != 128) || Hq / Hkv > kPagedMaxGroup) return 0;
   return PagedPlan(n_seq, max_q, max_keys, Hkv, Hq / Hkv, d).bytes;
 }
 

@@ -131,6 +131,12 @@ def test_workspace_sizes(L):
         assert attn.fwd_paged_workspace_bytes(*bad) == 0
 
 
+def test_workspace_of_sizes_the_call_refuses(L):
+    assert attn.fwd_paged_workspace_bytes(1, 40, 64, 128, 1, 64) > 0
+    assert attn.fwd_paged_workspace_bytes(1, 40, 64, 129, 1, 64) == 0
+    assert attn.fwd_paged_workspace_bytes(1, 1, 64, 258, 2, 64) == 0
+
+
 def test_rope_table_is_the_angle_per_position():
     t = attn.rope_table(32, theta=500.0, axes=[0] * 4 + [1] * 6 + [2] * 6, device="cpu")
     assert t.shape == (2, 16) and t.dtype == torch.int64
