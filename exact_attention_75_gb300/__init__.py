@@ -549,7 +549,8 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     kv_lens[b] positions of its pages (layouts as in append_kv; Hkv divides
     Hq).  causal: the rows are the last positions, row i of n sees keys
     j <= i + kv_lens[b] - n.  A row that sees no key gets O = 0, LSE = -inf;
-    rows behind the last sequence are left as they were.  workspace: uint8,
+    rows behind the last sequence are left as they were.  The probabilities are
+    rounded to q's dtype before the product with v, as in fwd.  workspace: uint8,
     fwd_paged_workspace_bytes long; calls that may overlap need their own."""
     return _binding().fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, max_q,
                                 causal, scale, out, lse, workspace)

@@ -3,8 +3,8 @@
 // stream, like the package's ctypes functions, but compiled: these calls are
 // made once per layer and token in decoding, where the time of a call is the
 // host's.  Measured on the Grace host, a call after the other with outputs
-// allocated: an append of 64 tokens 4.2 us (19.5 with the same checks in Python
-// and ctypes), attention of one decoding sequence 7 us (20).
+// allocated: an append of 64 tokens 5.3 to 6.0 us (19.5 with the same checks in
+// Python and ctypes), attention of one decoding sequence 6.9 to 7.3 (20).
 //
 // The functions of libattn.so are handed over by address (init), so that both
 // routes use one loaded library.

@@ -18,9 +18,9 @@
 // shares leaves a partial result per share: an unnormalised O and the (m, l)
 // of each row, in slot 0 of a CTA that continues it and slot 1 of the CTA that
 // begins it, each described in desc.  The join kernel combines an item's parts
-// in key order, so equal calls give equal bits; a CTA of it takes a slice of
-// the item that its counterpart had a part of, so the join is shared out as
-// evenly as the parts are.
+// in an order that their number fixes, so equal calls give equal bits; a CTA of
+// it takes a slice of the item that its counterpart had a part of, so the join
+// is shared out as evenly as the parts are.
 #pragma once
 
 #include <cuda.h>
@@ -36,9 +36,9 @@ constexpr int kPagedMaxSms = 160;  // bound of the grids (two CTAs per SM at mos
 constexpr int kPagedRows = 16;
 // Rows of an item of the tile kernel (two query tiles).
 constexpr int kPagedTileRows = 256;
-// Keys of a block there (rows of the tensor-map box).
+// Keys of a block of the warp-level kernel (rows of its tensor-map box).
 constexpr int kPagedBlock = 16;
-// CTAs at most that share an item of a small batch there.
+// CTAs at most that share an item of a small batch on the warp-level kernel.
 constexpr int kPagedCluster = 8;
 // Query heads per key/value head at most.
 constexpr int kPagedMaxGroup = 128;
@@ -121,8 +121,10 @@ __device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
 // KEY1, KEY2: cost of a key in an item whose rows fill one query tile or
 // reach into the second (the last item of a sequence may have one tile, all
 // before it have two); OVERHEAD: of an item's prologue and epilogue.  SINGLE:
-// an item holds all new tokens of its sequence (the general form finds the
-// same; three sequences of 65536 keys take 31.4 us with it, 31.0 without).
+// an item holds all new tokens of its sequence.  The general form finds the
+// same shares, and the short one saves every CTA 0.3 to 0.5 us of its start:
+// three sequences of 65536 keys, d = 64, take 30.8 us with SINGLE and 31.3
+// without, four of 4096 keys 7.8 and 8.2.
 template <int UNIT_, int KEY1_, int KEY2_, int OVERHEAD_, bool SINGLE_>
 struct PagedCost {
   static constexpr int UNIT = UNIT_, KEY1 = KEY1_, KEY2 = KEY2_, OVERHEAD = OVERHEAD_;

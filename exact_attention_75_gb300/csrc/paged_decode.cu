@@ -305,7 +305,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
 
-      // O += P V
+      // O += P V.  P is rounded to the inputs' 16 bits, as in the dense kernels:
+      // at most eps / 2 of sum_j P_ij |v_j| (l sums the unrounded values).  For
+      // 64 sequences of up to 8192 keys in bf16 the relative error of O is 0.0022,
+      // of which the output's own rounding, with P in 32 bits, makes 0.0017; two
+      // 16-bit terms for P would double the products.
       uint32_t pa[4];
       pa[0] = pack2<BF16>(sc[0][0], sc[0][1]);
       pa[1] = hiB ? pack2<BF16>(sc[0][2], sc[0][3]) : 0u;

@@ -1,6 +1,8 @@
 // Joins the partial results of paged attention items whose keys several CTAs
-// shared.  Per row, over the item's parts in key order,
-//   M = max m_k,  l = sum l_k 2^(m_k - M),  O = sum O_k 2^(m_k - M) / l.
+// shared.  Per row, over the item's parts,
+//   M = max m_k,  l = sum l_k 2^(m_k - M),  O = sum O_k 2^(m_k - M) / l,
+// few parts in key order, many in strided runs whose sums are then added up:
+// the number of parts alone fixes the order.
 //
 // A warp takes a segment of 32 (row, four columns) elements, contiguous in
 // every part (512 bytes a read), up to four parts in flight at a time; where

@@ -451,6 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
           const float2 sc2 = make_float2(sl2, sl2);
+          // P goes to tensor memory in the inputs' 16 bits, what the product with
+          // V takes (at most eps / 2 of sum_j P_ij |v_j|; l sums the unrounded
+          // values); two 16-bit terms for P would double that product.
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];

@@ -347,8 +347,10 @@ size_t attn_fwd_paged_workspace_bytes(int n_seq, int max_q, int64_t max_keys, in
  * A value row that is infinite or NaN may reach every row of its sequence.
  * A row with a score of NaN at a key it sees (a NaN or infinite query or key)
  * has O and LSE NaN.
- * Partial results are joined in key order: equal calls give equal bits (the
- * split depends on all lengths of the batch).  d in {64, 96, 128}.
+ * Partial results are joined in a fixed order: equal calls give equal bits
+ * (the split depends on all lengths of the batch).  Scores, sums and partial
+ * results are fp32; the probabilities are rounded to q's type before the
+ * product with V, as in attn_fwd.  d in {64, 96, 128}.
  * Cite: the FlashAttention-2 review, "Insights" and "Discussion Points"
  * (paged key/value caches; a decoding kernel that splits the keys).
  */
@@ -427,8 +429,10 @@ attn_status attn_fwd_fp8(const void* q8, const void* k8, const void* v8t, const 
  * since the last poll (the kernel then skipped the rest of its work and
  * released its resources; outputs are incomplete), ATTN_ERR_CUDA if the
  * synchronisation failed, ATTN_ERR_INVALID_ARG if a device-side argument
- * check failed (variable-length offsets), else ATTN_OK.  `detail` (may be
- * NULL) receives the raw status word: code | site << 8 | block index << 16.
+ * check failed (variable-length offsets, site 60; the lengths, offsets and
+ * page numbers of the paged calls, sites 63 and 64), else ATTN_OK.  `detail`
+ * (may be NULL) receives the raw status word: code | site << 8 | block index
+ * << 16 (at sites 60, 63 and 64 the index of the sequence).
  */
 attn_status attn_poll_device_status(void* stream, uint32_t* detail);
 
