@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "dependent.cuh"
 #include "mma16.cuh"
 #include "paged.cuh"
 #include "sm103_ptx.cuh"

@@ -36,6 +36,7 @@
 #include <cstdint>
 
 #include "attn.h"
+#include "dependent.cuh"
 #include "rotary.cuh"
 #include "sm103_ptx.cuh"
 #include "smem_attr.cuh"
