@@ -24,7 +24,7 @@ import torch
 
 __all__ = ["AttnError", "lib", "lib_path", "fwd", "fwd_split", "fwd_kv", "merge", "bwd", "fwd_varlen",
            "bwd_varlen", "bwd_workspace_bytes", "rope_table", "rope", "rope_bwd", "append_kv", "fwd_paged",
-           "fwd_paged_workspace_bytes", "quantize_fp8", "fwd_fp8", "poll_status", "set_wait_limit_us",
+           "fwd_paged_workspace_bytes", "append_kv4", "read_kv4", "fwd_paged4", "quantize_fp8", "fwd_fp8", "poll_status", "set_wait_limit_us",
            "selftest_wait_timeout", "num_sms", "STATUS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -74,6 +74,9 @@ def lib() -> ctypes.CDLL:
         "attn_append_kv": ([vp] * 11 + [i, vp] + [i] * 11 + [vp], i),
         "attn_fwd_paged_workspace_bytes": ([i, i, ctypes.c_int64, i, i, i], sz),
         "attn_fwd_paged": ([vp] * 9 + [sz] + [i] * 10 + [f, i, vp], i),
+        "attn_append_kv4": ([vp] * 11 + [i, vp] + [i] * 11 + [vp], i),
+        "attn_read_kv4": ([vp] * 7 + [i] * 8 + [vp], i),
+        "attn_fwd_paged4": ([vp] * 9 + [sz] + [i] * 10 + [f, i, vp], i),
         "attn_quantize_fp8": ([vp, vp, vp, i, i, i, i, i, vp, i, vp], i),
         "attn_fwd_fp8": ([vp] * 8 + [i, i, i, i, i, f, vp], i),
         "attn_poll_device_status": ([vp, u32p], i),
@@ -109,7 +112,8 @@ def _binding():
         loader.exec_module(mod)
         L = lib()
         mod.init(AttnError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
-            "attn_rope", "attn_append_kv", "attn_fwd_paged", "attn_fwd_paged_workspace_bytes")))
+            "attn_rope", "attn_append_kv", "attn_fwd_paged", "attn_fwd_paged_workspace_bytes",
+            "attn_append_kv4", "attn_read_kv4", "attn_fwd_paged4")))
         _bind = mod
     return _bind
 
@@ -527,7 +531,7 @@ def append_kv(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: 
     are left as they were.  out_q: contiguous; it may be q if q is, and must not
     overlap the inputs otherwise."""
     return _binding().append_kv(k, v, k_pages, v_pages, block_table, cu_seqlens, kv_lens, table,
-                                positions, interleaved, q, out_q)
+                                positions, interleaved, q, out_q, False)
 
 
 def fwd_paged_workspace_bytes(n_seq: int, max_q: int, max_keys: int, Hq: int, Hkv: int,
@@ -553,7 +557,51 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     rounded to q's dtype before the product with v, as in fwd.  workspace: uint8,
     fwd_paged_workspace_bytes long; calls that may overlap need their own."""
     return _binding().fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, max_q,
-                                causal, scale, out, lse, workspace)
+                                causal, scale, out, lse, workspace, False)
+
+
+def append_kv4(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+               block_table: torch.Tensor, cu_seqlens: torch.Tensor, kv_lens: torch.Tensor,
+               table: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+               interleaved: bool = False, q: Optional[torch.Tensor] = None,
+               out_q: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """append_kv into a cache held in 4 bits: k_pages, v_pages uint8
+    [n_pages,Hkv,page,5d/8], d in {64, 96, 128}; the other arguments as there.
+
+    A row is d/2 bytes of codes (channel 2i in the low half of byte i), then for
+    each 32 channels a scale s and a minimum m in k's dtype; a code c stands
+    for m + c s, with m = min x, s = (max x - m) / 15 over the group's values
+    and c the nearest code.  What append_kv would store is what is quantized.
+    A group with an infinity or a NaN stands for NaN."""
+    return _binding().append_kv(k, v, k_pages, v_pages, block_table, cu_seqlens, kv_lens, table,
+                                positions, interleaved, q, out_q, True)
+
+
+def read_kv4(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+             cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, total: int,
+             dtype: torch.dtype = torch.bfloat16, out_k: Optional[torch.Tensor] = None,
+             out_v: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows of a 4-bit cache (see append_kv4) back in 16 bits: k, v
+    [Hkv,total,d] of dtype, which is the one that was appended, packed like
+    append_kv4's input.  Rows cu_seqlens[b]..cu_seqlens[b+1] are the last of
+    the kv_lens[b] cached positions of sequence b (with cu_seqlens the running
+    sum of kv_lens: all of them); rows behind the last sequence are left as
+    they were."""
+    return _binding().read_kv4(k_pages, v_pages, block_table, cu_seqlens, kv_lens, total, dtype,
+                               out_k, out_v)
+
+
+def fwd_paged4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+               block_table: torch.Tensor, cu_seqlens: torch.Tensor, kv_lens: torch.Tensor,
+               max_q: int, causal: bool = False, scale: Optional[float] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """fwd_paged over a cache held in 4 bits (see append_kv4).  Values take part
+    as read_kv4 gives them, keys unrounded (in chunks of more than 16 query
+    rows a key/value head to 2^-12); q has the dtype that was appended.
+    Arguments, masking and workspace (fwd_paged_workspace_bytes) as there."""
+    return _binding().fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, max_q,
+                                causal, scale, out, lse, workspace, True)
 
 
 def num_sms() -> int:

@@ -10,6 +10,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "append4.cuh"
 #include "attn.h"
 #include "bwd.cuh"
 #include "decode.cuh"
@@ -522,6 +523,149 @@ struct PagedPlan {
   }
 };
 
+PackedBatch packed_batch(const DeviceInfo* di, const int32_t* block_table,
+                         const int32_t* cu_seqlens, const int32_t* kv_lens, int n_seq,
+                         int max_pages, int n_pages, int page, int total) {
+  return {block_table, cu_seqlens, kv_lens, di->status, n_seq, max_pages, n_pages, log2_of(page),
+          total};
+}
+
+// attn_append_kv, and attn_append_kv4 (kv4).
+attn_status append_call(const void* k, const void* v, const void* q, void* q_out,
+                        const int64_t* strides, void* k_pages, void* v_pages,
+                        const int32_t* block_table, const int32_t* cu_seqlens,
+                        const int32_t* kv_lens, const int32_t* positions, int n_axes,
+                        const int64_t* table, int rot, int interleaved, int n_seq, int total,
+                        int n_pages, int page, int max_pages, int Hq, int Hkv, int d,
+                        attn_dtype dtype, void* stream, bool kv4) {
+  if (!aligned16(k) || !aligned16(v) || strides == nullptr) return ATTN_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (q == nullptr) != (Hq == 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (q != nullptr && (!aligned16(q) || !aligned16(q_out))) return ATTN_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype) || (interleaved & ~1)) return ATTN_ERR_INVALID_ARG;
+  if (kv4 ? (d != 64 && d != 96 && d != 128) : !head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
+  if (table != nullptr && !rotary_ok(table, rot, n_axes, d)) return ATTN_ERR_INVALID_ARG;
+  if (positions != nullptr && (table == nullptr || !aligned(positions, 4)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!strides_ok(strides, q != nullptr ? 6 : 4)) return ATTN_ERR_INVALID_ARG;
+  attn_status st = paged_args(k_pages, v_pages, block_table, cu_seqlens, kv_lens, n_seq, total,
+                              n_pages, page, max_pages, q != nullptr ? Hq : Hkv, Hkv);
+  if (st != ATTN_OK) return st;
+  if ((2 * (int64_t)Hkv + Hq) * total > 0x7FFFFFFF) return ATTN_ERR_INVALID_ARG;
+  if (q != nullptr) {
+    const int64_t n[2] = {Hq, total}, contiguous[2] = {(int64_t)total * d, d};
+    if (q_out == q && !same_layout(strides + 4, contiguous, n, 2)) return ATTN_ERR_INVALID_ARG;
+    if (q_out == k || q_out == v || q_out == k_pages || q_out == v_pages)
+      return ATTN_ERR_INVALID_ARG;
+  }
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != ATTN_OK) return st;
+  AppendLaunch a;
+  AppendParams& p = a.params;
+  p.src[0] = k;
+  p.src[1] = v;
+  p.src[2] = q;
+  for (int i = 0; i < (q != nullptr ? 3 : 2); ++i) {
+    p.sh[i] = strides[2 * i];
+    p.sn[i] = strides[2 * i + 1];
+  }
+  p.q_out = q_out;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.batch = packed_batch(di, block_table, cu_seqlens, kv_lens, n_seq, max_pages, n_pages, page,
+                         total);
+  p.positions = positions;
+  p.table = table;
+  p.n_axes = n_axes;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.rot = table != nullptr ? rot : 0;
+  a.bf16 = dtype == ATTN_BF16;
+  a.interleaved = interleaved != 0;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(kv4 ? launch_append4(a, di->num_sms) : launch_append(a, di->num_sms));
+}
+
+// attn_fwd_paged, and attn_fwd_paged4 (kv4).
+attn_status paged_call(const void* q, const void* k_pages, const void* v_pages, void* o,
+                       float* lse, const int32_t* block_table, const int32_t* cu_seqlens,
+                       const int32_t* kv_lens, void* workspace, size_t workspace_bytes,
+                       int n_seq, int max_q, int total, int n_pages, int page, int max_pages,
+                       int Hq, int Hkv, int d, int causal, float scale, attn_dtype dtype,
+                       void* stream, bool kv4) {
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (!dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  attn_status st = paged_args(k_pages, v_pages, block_table, cu_seqlens, kv_lens, n_seq, total,
+                              n_pages, page, max_pages, Hq, Hkv);
+  if (st != ATTN_OK) return st;
+  if (max_q < 1 || max_q > total) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 96 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (Hq / Hkv > kPagedMaxGroup) return ATTN_ERR_UNSUPPORTED;
+  const PagedPlan plan(n_seq, max_q, (int64_t)max_pages * page, Hkv, Hq / Hkv, d);
+  if (plan.bytes > 0 && (workspace_bytes < plan.bytes || !aligned(workspace, 256)))
+    return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != ATTN_OK) return st;
+  const CUtensorMapDataType dt =
+      dtype == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  PagedLaunch a;
+  PagedParams& p = a.params;
+  p.q = q;
+  p.k4 = static_cast<const uint8_t*>(k_pages);
+  p.v4 = static_cast<const uint8_t*>(v_pages);
+  p.o = o;
+  p.lse = lse;
+  p.status = di->status;
+  p.block_table = block_table;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.n_seq = n_seq;
+  p.total = total;
+  p.max_q = max_q;
+  p.n_pages = n_pages;
+  p.page = page;
+  p.page_log2 = log2_of(page);
+  p.max_pages = max_pages;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.causal = causal;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p.desc = reinterpret_cast<int4*>(w);
+  p.part_ml = reinterpret_cast<float*>(w + plan.ml);
+  p.part_o = reinterpret_cast<float*>(w + plan.o);
+  const bool decode = plan.decode;
+  p.min_share = decode ? 128 : 1024;
+  const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
+  p.cluster = plan.cluster;
+  a.grid = plan.cluster ? n_seq * Hkv * plan.cluster : (decode ? 2 * sms : sms);
+  a.stream = static_cast<cudaStream_t>(stream);
+  // the cost of the largest batch of these sizes stays in 63 bits
+  const int64_t keys = 4 * ((int64_t)max_pages * page + 1024);
+  const int64_t items = (((int64_t)total * p.G) / 64 + n_seq) * Hkv;
+  if (keys > INT64_MAX / items) return ATTN_ERR_INVALID_ARG;
+  const int64_t heads = (int64_t)n_pages * Hkv;
+  const int box = decode ? kPagedBlock : (page < 128 ? page : 128);
+  if (!kv4 && (!encode_3d(&a.tmK, k_pages, dt, 2, d, page, heads, 64, box) ||
+               !encode_3d(&a.tmV, v_pages, dt, 2, d, page, heads, 64, box)))
+    return ATTN_ERR_CUDA;
+  if (!decode && !encode_3d(&a.tmQ, q, dt, 2, d, total, Hq, 64, 128 / p.G,
+                            CU_TENSOR_MAP_SWIZZLE_128B, p.G))
+    return ATTN_ERR_CUDA;
+  const bool bf16 = dtype == ATTN_BF16;
+  auto main = decode ? (kv4 ? launch_paged4_decode : launch_paged_decode)
+                     : (kv4 ? launch_paged4_tile : launch_paged_tile);
+  cudaError_t e = main(a, d, bf16);
+  if (e == cudaSuccess && plan.cluster == 0) e = launch_paged_join(a, d, bf16, decode);
+  return launch_result(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -584,61 +728,51 @@ attn_status attn_append_kv(const void* k, const void* v, const void* q, void* q_
                            const int64_t* table, int rot, int interleaved, int n_seq, int total,
                            int n_pages, int page, int max_pages, int Hq, int Hkv, int d,
                            attn_dtype dtype, void* stream) {
-  if (!aligned16(k) || !aligned16(v) || strides == nullptr) return ATTN_ERR_INVALID_ARG;
-  if ((q == nullptr) != (q_out == nullptr) || (q == nullptr) != (Hq == 0))
+  return append_call(k, v, q, q_out, strides, k_pages, v_pages, block_table, cu_seqlens,
+                     kv_lens, positions, n_axes, table, rot, interleaved, n_seq, total, n_pages,
+                     page, max_pages, Hq, Hkv, d, dtype, stream, false);
+}
+
+attn_status attn_append_kv4(const void* k, const void* v, const void* q, void* q_out,
+                            const int64_t* strides, void* k_pages, void* v_pages,
+                            const int32_t* block_table, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, const int32_t* positions, int n_axes,
+                            const int64_t* table, int rot, int interleaved, int n_seq, int total,
+                            int n_pages, int page, int max_pages, int Hq, int Hkv, int d,
+                            attn_dtype dtype, void* stream) {
+  return append_call(k, v, q, q_out, strides, k_pages, v_pages, block_table, cu_seqlens,
+                     kv_lens, positions, n_axes, table, rot, interleaved, n_seq, total, n_pages,
+                     page, max_pages, Hq, Hkv, d, dtype, stream, true);
+}
+
+attn_status attn_read_kv4(const void* k_pages, const void* v_pages, void* k, void* v,
+                          const int32_t* block_table, const int32_t* cu_seqlens,
+                          const int32_t* kv_lens, int n_seq, int total, int n_pages, int page,
+                          int max_pages, int Hkv, int d, attn_dtype dtype, void* stream) {
+  if (!aligned16(k) || !aligned16(v) || !dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
+  if (k == v || k == k_pages || k == v_pages || v == k_pages || v == v_pages)
     return ATTN_ERR_INVALID_ARG;
-  if (q != nullptr && (!aligned16(q) || !aligned16(q_out))) return ATTN_ERR_INVALID_ARG;
-  if (!dtype_ok(dtype) || (interleaved & ~1)) return ATTN_ERR_INVALID_ARG;
-  if (!head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
-  if (table != nullptr && !rotary_ok(table, rot, n_axes, d)) return ATTN_ERR_INVALID_ARG;
-  if (positions != nullptr && (table == nullptr || !aligned(positions, 4)))
-    return ATTN_ERR_INVALID_ARG;
-  if (!strides_ok(strides, q != nullptr ? 6 : 4)) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 96 && d != 128) return ATTN_ERR_UNSUPPORTED;
   attn_status st = paged_args(k_pages, v_pages, block_table, cu_seqlens, kv_lens, n_seq, total,
-                              n_pages, page, max_pages, q != nullptr ? Hq : Hkv, Hkv);
+                              n_pages, page, max_pages, Hkv, Hkv);
   if (st != ATTN_OK) return st;
-  if ((2 * (int64_t)Hkv + Hq) * total > 0x7FFFFFFF) return ATTN_ERR_INVALID_ARG;
-  if (q != nullptr) {
-    const int64_t n[2] = {Hq, total}, contiguous[2] = {(int64_t)total * d, d};
-    if (q_out == q && !same_layout(strides + 4, contiguous, n, 2)) return ATTN_ERR_INVALID_ARG;
-    if (q_out == k || q_out == v || q_out == k_pages || q_out == v_pages)
-      return ATTN_ERR_INVALID_ARG;
-  }
+  if (2 * (int64_t)Hkv * total > 0x7FFFFFFF) return ATTN_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;
   st = device_info(&di);
   if (st != ATTN_OK) return st;
-  AppendLaunch a;
-  AppendParams& p = a.params;
-  p.src[0] = k;
-  p.src[1] = v;
-  p.src[2] = q;
-  for (int i = 0; i < (q != nullptr ? 3 : 2); ++i) {
-    p.sh[i] = strides[2 * i];
-    p.sn[i] = strides[2 * i + 1];
-  }
-  p.q_out = q_out;
-  p.k_pages = k_pages;
-  p.v_pages = v_pages;
-  p.block_table = block_table;
-  p.cu_seqlens = cu_seqlens;
-  p.kv_lens = kv_lens;
-  p.positions = positions;
-  p.table = table;
-  p.status = di->status;
-  p.n_axes = n_axes;
-  p.n_seq = n_seq;
-  p.max_pages = max_pages;
-  p.n_pages = n_pages;
-  p.page_log2 = log2_of(page);
-  p.total = total;
-  p.Hq = Hq;
+  Read4Launch a;
+  Read4Params& p = a.params;
+  p.batch = packed_batch(di, block_table, cu_seqlens, kv_lens, n_seq, max_pages, n_pages, page,
+                         total);
+  p.k_pages = static_cast<const uint8_t*>(k_pages);
+  p.v_pages = static_cast<const uint8_t*>(v_pages);
+  p.k = k;
+  p.v = v;
   p.Hkv = Hkv;
   p.d = d;
-  p.rot = table != nullptr ? rot : 0;
   a.bf16 = dtype == ATTN_BF16;
-  a.interleaved = interleaved != 0;
   a.stream = static_cast<cudaStream_t>(stream);
-  return launch_result(launch_append(a, di->num_sms));
+  return launch_result(launch_read4(a, di->num_sms));
 }
 
 size_t attn_fwd_paged_workspace_bytes(int n_seq, int max_q, int64_t max_keys, int Hq, int Hkv,
@@ -655,71 +789,20 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
                            int n_seq, int max_q, int total, int n_pages, int page, int max_pages,
                            int Hq, int Hkv, int d, int causal, float scale, attn_dtype dtype,
                            void* stream) {
-  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_INVALID_ARG;
-  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
-  if (!dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
-  attn_status st = paged_args(k_pages, v_pages, block_table, cu_seqlens, kv_lens, n_seq, total,
-                              n_pages, page, max_pages, Hq, Hkv);
-  if (st != ATTN_OK) return st;
-  if (max_q < 1 || max_q > total) return ATTN_ERR_INVALID_ARG;
-  if (d != 64 && d != 96 && d != 128) return ATTN_ERR_UNSUPPORTED;
-  if (Hq / Hkv > kPagedMaxGroup) return ATTN_ERR_UNSUPPORTED;
-  const PagedPlan plan(n_seq, max_q, (int64_t)max_pages * page, Hkv, Hq / Hkv, d);
-  if (plan.bytes > 0 && (workspace_bytes < plan.bytes || !aligned(workspace, 256)))
-    return ATTN_ERR_INVALID_ARG;
-  DeviceInfo* di = nullptr;
-  st = device_info(&di);
-  if (st != ATTN_OK) return st;
-  const CUtensorMapDataType dt =
-      dtype == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  PagedLaunch a;
-  PagedParams& p = a.params;
-  p.q = q;
-  p.o = o;
-  p.lse = lse;
-  p.status = di->status;
-  p.block_table = block_table;
-  p.cu_seqlens = cu_seqlens;
-  p.kv_lens = kv_lens;
-  p.n_seq = n_seq;
-  p.total = total;
-  p.max_q = max_q;
-  p.n_pages = n_pages;
-  p.page = page;
-  p.page_log2 = log2_of(page);
-  p.max_pages = max_pages;
-  p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.causal = causal;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.wait_limit_ns = g_wait_limit_ns.load();
-  uint8_t* w = static_cast<uint8_t*>(workspace);
-  p.desc = reinterpret_cast<int4*>(w);
-  p.part_ml = reinterpret_cast<float*>(w + plan.ml);
-  p.part_o = reinterpret_cast<float*>(w + plan.o);
-  const bool decode = plan.decode;
-  p.min_share = decode ? 128 : 1024;
-  const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
-  p.cluster = plan.cluster;
-  a.grid = plan.cluster ? n_seq * Hkv * plan.cluster : (decode ? 2 * sms : sms);
-  a.stream = static_cast<cudaStream_t>(stream);
-  // the cost of the largest batch of these sizes stays in 63 bits
-  const int64_t keys = 4 * ((int64_t)max_pages * page + 1024);
-  const int64_t items = (((int64_t)total * p.G) / 64 + n_seq) * Hkv;
-  if (keys > INT64_MAX / items) return ATTN_ERR_INVALID_ARG;
-  const int64_t heads = (int64_t)n_pages * Hkv;
-  const int box = decode ? kPagedBlock : (page < 128 ? page : 128);
-  if (!encode_3d(&a.tmK, k_pages, dt, 2, d, page, heads, 64, box) ||
-      !encode_3d(&a.tmV, v_pages, dt, 2, d, page, heads, 64, box))
-    return ATTN_ERR_CUDA;
-  if (!decode && !encode_3d(&a.tmQ, q, dt, 2, d, total, Hq, 64, 128 / p.G,
-                            CU_TENSOR_MAP_SWIZZLE_128B, p.G))
-    return ATTN_ERR_CUDA;
-  const bool bf16 = dtype == ATTN_BF16;
-  cudaError_t e = decode ? launch_paged_decode(a, d, bf16) : launch_paged_tile(a, d, bf16);
-  if (e == cudaSuccess && plan.cluster == 0) e = launch_paged_join(a, d, bf16, decode);
-  return launch_result(e);
+  return paged_call(q, k_pages, v_pages, o, lse, block_table, cu_seqlens, kv_lens, workspace,
+                    workspace_bytes, n_seq, max_q, total, n_pages, page, max_pages, Hq, Hkv, d,
+                    causal, scale, dtype, stream, false);
+}
+
+attn_status attn_fwd_paged4(const void* q, const void* k_pages, const void* v_pages, void* o,
+                            float* lse, const int32_t* block_table, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, void* workspace, size_t workspace_bytes,
+                            int n_seq, int max_q, int total, int n_pages, int page, int max_pages,
+                            int Hq, int Hkv, int d, int causal, float scale, attn_dtype dtype,
+                            void* stream) {
+  return paged_call(q, k_pages, v_pages, o, lse, block_table, cu_seqlens, kv_lens, workspace,
+                    workspace_bytes, n_seq, max_q, total, n_pages, page, max_pages, Hq, Hkv, d,
+                    causal, scale, dtype, stream, true);
 }
 
 }  // extern "C"

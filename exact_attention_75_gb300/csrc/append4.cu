@@ -1,0 +1,253 @@
+// New keys and values into a paged cache held in 4 bits (kv4.cuh), turned by
+// their positions on the way, and rows of that cache back in 16 bits.
+//
+// The append reads and turns like the 16-bit one (rotary.cu): a thread owns 16
+// channels of a token, as two pieces of 8, and walks up to 16 heads.  What it
+// would store there is what is quantized here, so keys are rounded to 16 bits
+// between the turn and the groups.  A group of 32 channels is four pieces,
+// which the half-split rotation leaves with up to four threads of the token:
+// each piece's minimum and maximum go to shared memory, and every thread
+// takes its group's from there, four heads between two barriers.
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "append4.cuh"
+#include "dependent.cuh"
+#include "kv4.cuh"
+#include "packed.cuh"
+#include "rotary.cuh"
+#include "turn.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kBatch = 4;  // heads whose rows are read together
+
+// The extremes of a piece; NaN where it holds one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float from16(uint32_t x) {
+  return BF16 ? __uint_as_float(x << 16) : __half2float(__ushort_as_half((unsigned short)x));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t to16(float x) {
+  return BF16 ? pack_bf16x2(x, 0.f) : pack_f16x2(x, 0.f);
+}
+
+// s in the low half, m in the high.
+template <bool BF16>
+__device__ __forceinline__ uint32_t kv4_params(float lo, float hi) {
+  uint32_t s = to16<BF16>(__fdiv_rn(hi - lo, 15.f));
+  const uint32_t m = to16<BF16>(lo);  // exact: one of the values
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+  if (s >= kInf) return 0x7FFF7FFFu;
+  // s rounded up may carry code 15 past the type's range
+  if (to16<BF16>(fmaf(15.f, from16<BF16>(s), lo)) == kInf) --s;
+  return s | m << 16;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t par) {
+  const float m = from16<BF16>(par >> 16), s = from16<BF16>(par & 0xFFFFu);
+  const float by = s > 0.f ? s : INFINITY;  // one value: code 0
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w |= (uint32_t)fminf(rintf(__fdiv_rn(x[i] - m, by)), 15.f) << (4 * i);
+  return w;
+}
+
+template <bool BF16, bool INTER>
+__global__ void __launch_bounds__(kThreads, 4) append4_kernel(const AppendParams p) {
+  __shared__ float2 range[2][kBatch][2 * kThreads];  // of each token's pieces
+  grid_wait();
+  grid_release();
+  if (blockIdx.x >= p.token_blocks) {  // as in the 16-bit append
+    const int64_t b = (int64_t)(blockIdx.x - p.token_blocks) * kThreads + threadIdx.x;
+    if (b < p.batch.n_seq) packed_check(p.batch, b);
+    return;
+  }
+  // A token's threads lie in one block; the threads left over, and those of
+  // tokens that are not stored, walk along to the barriers.
+  const int per_row = p.d / 16, tokens = kThreads / per_row;
+  const int group = blockIdx.x % p.head_groups;
+  const int own = threadIdx.x / per_row, c = threadIdx.x % per_row;
+  const int64_t t64 = (int64_t)(blockIdx.x / p.head_groups) * tokens + own;
+  const bool token = own < tokens && t64 < p.batch.total;
+  const int t = token ? (int)t64 : 0;
+  const Pieces s = pieces<INTER>(c, p.rot);
+  // heads in the order k, v, q
+  const int h0 = group * p.group_heads;
+  const int count = min(p.group_heads, 2 * p.Hkv + p.Hq - h0);
+  auto which = [&](int h) { return h < p.Hkv ? 0 : (h < 2 * p.Hkv ? 1 : 2); };
+  uint4 lo[2][kBatch], hi[2][kBatch];
+  auto load = [&](uint4 (&l)[kBatch], uint4 (&h)[kBatch], int at) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (at + i >= count || !token) break;
+      const int w = which(h0 + at + i);
+      const uint16_t* x = static_cast<const uint16_t*>(p.src[w]) +
+                          (h0 + at + i - w * p.Hkv) * p.sh[w] + (int64_t)t * p.sn[w];
+      l[i] = *reinterpret_cast<const uint4*>(x + s.lo);
+      h[i] = *reinterpret_cast<const uint4*>(x + s.hi);
+    }
+  };
+  load(lo[0], hi[0], 0);
+
+  PackedPlace at = {p.batch.n_seq, false, false, 0, -1};
+  if (token) at = packed_place(p.batch, t);
+  if (at.b < p.batch.n_seq && !at.stored && c == 0 && group == 0)
+    report_bad(p.batch.status, at.in_seq ? kBadPage : kBadBatch, at.b);
+
+  float cs[8], sn[8];
+  if (s.turn && at.in_seq) {
+    angles(p.table, p.rot / 2, c,
+           [&](int axis) {
+             return p.positions == nullptr
+                        ? (int)at.pos
+                        : __ldg(p.positions +
+                                (int64_t)min(max(axis, 0), p.n_axes - 1) * p.batch.total + t);
+           },
+           cs, sn);
+  }
+  const int page_row = (int)at.pos & ((1 << p.batch.page_log2) - 1);
+  const int row_bytes = kv4_row(p.d);
+  const int base = own * 2 * per_row;  // the token's pieces in range
+  auto store = [&](uint4 (&l)[kBatch], uint4 (&hh)[kBatch], int first, int buf) {
+    if (first >= count) return;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (first + i >= count || !at.in_seq) break;
+      const int w = which(h0 + first + i);
+      const int h = h0 + first + i - w * p.Hkv;
+      if (s.turn && w != 1) turn_pieces<BF16, INTER>(l[i], hh[i], cs, sn);
+      if (w == 2) {
+        uint16_t* y = static_cast<uint16_t*>(p.q_out) + ((int64_t)h * p.batch.total + t) * p.d;
+        *reinterpret_cast<uint4*>(y + s.lo) = l[i];
+        *reinterpret_cast<uint4*>(y + s.hi) = hh[i];
+        continue;
+      }
+      float x[8];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        unpack8<BF16>(half ? hh[i] : l[i], x);
+        float a = x[0], b = x[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) {
+          a = min_nan(a, x[e]);
+          b = max_nan(b, x[e]);
+        }
+        range[buf][i][base + (half ? s.hi : s.lo) / 8] = make_float2(a, b);
+      }
+    }
+    if (h0 + first >= 2 * p.Hkv) return;  // queries alone
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (first + i >= count || !at.stored) break;
+      const int w = which(h0 + first + i);
+      if (w == 2) break;
+      const int h = h0 + first + i - w * p.Hkv;
+      uint8_t* y = static_cast<uint8_t*>(w ? p.v_pages : p.k_pages) +
+                   ((((int64_t)at.page * p.Hkv + h) << p.batch.page_log2) + page_row) * row_bytes;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int ch = half ? s.hi : s.lo;
+        const float2* r = &range[buf][i][base + ch / kKv4Group * 4];
+        const float a = min_nan(min_nan(r[0].x, r[1].x), min_nan(r[2].x, r[3].x));
+        const float b = max_nan(max_nan(r[0].y, r[1].y), max_nan(r[2].y, r[3].y));
+        const uint32_t par = kv4_params<BF16>(a, b);
+        float x[8];
+        unpack8<BF16>(half ? hh[i] : l[i], x);
+        *reinterpret_cast<uint32_t*>(y + ch / 2) = quantize8<BF16>(x, par);
+        if (ch % kKv4Group == 0)
+          *reinterpret_cast<uint32_t*>(y + p.d / 2 + ch / kKv4Group * 4) = par;
+      }
+    }
+  };
+  // The barrier of a batch also says that the one before last has been read.
+  for (int first = 0; first < count; first += 2 * kBatch) {
+    load(lo[1], hi[1], first + kBatch);
+    store(lo[0], hi[0], first, 0);
+    load(lo[0], hi[0], first + 2 * kBatch);
+    store(lo[1], hi[1], first + kBatch, 1);
+  }
+}
+
+// A thread owns a code word (8 channels) of a token and walks its heads.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) read4_kernel(const Read4Params p) {
+  grid_wait();
+  grid_release();
+  if (blockIdx.x >= p.token_blocks) {
+    const int64_t b = (int64_t)(blockIdx.x - p.token_blocks) * kThreads + threadIdx.x;
+    if (b < p.batch.n_seq) packed_check(p.batch, b);
+    return;
+  }
+  const int words = p.d / 8;
+  const int group = blockIdx.x % p.head_groups;
+  const int64_t idx = (int64_t)(blockIdx.x / p.head_groups) * kThreads + threadIdx.x;
+  const int64_t t64 = idx / words;
+  if (t64 >= p.batch.total) return;
+  const int t = (int)t64, c = (int)(idx % words);
+  const PackedPlace at = packed_place(p.batch, t);
+  if (at.b == p.batch.n_seq) return;
+  if (!at.stored) {
+    if (c == 0 && group == 0)
+      report_bad(p.batch.status, at.in_seq ? kBadPage : kBadBatch, at.b);
+    return;
+  }
+  const int page_row = (int)at.pos & ((1 << p.batch.page_log2) - 1);
+  const int row_bytes = kv4_row(p.d);
+  const int h0 = group * p.group_heads, h1 = min(h0 + p.group_heads, 2 * p.Hkv);
+#pragma unroll 4
+  for (int i = h0; i < h1; ++i) {  // heads in the order k, v
+    const int w = i >= p.Hkv, h = i - w * p.Hkv;
+    const uint8_t* x = (w ? p.v_pages : p.k_pages) +
+                       ((((int64_t)at.page * p.Hkv + h) << p.batch.page_log2) + page_row) * row_bytes;
+    const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(x) + c);
+    const uint32_t par = __ldg(reinterpret_cast<const uint32_t*>(x + p.d / 2) + c / 4);
+    uint16_t* y = static_cast<uint16_t*>(w ? p.v : p.k) + ((int64_t)h * p.batch.total + t) * p.d;
+    reinterpret_cast<uint4*>(y)[c] = kv4_word<BF16>(code, par);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append4(const AppendLaunch& a, int num_sms) {
+  AppendParams p = a.params;
+  const int heads = 2 * p.Hkv + p.Hq, tokens = kThreads / (p.d / 16);
+  const int64_t bx = ((int64_t)p.batch.total + tokens - 1) / tokens;
+  p.group_heads = heads_per_block(bx, heads, num_sms);
+  p.head_groups = (heads + p.group_heads - 1) / p.group_heads;
+  p.token_blocks = (unsigned)(bx * p.head_groups);
+  const dim3 grid(p.token_blocks + ((unsigned)p.batch.n_seq + kThreads - 1) / kThreads);
+  auto kern = a.bf16 ? (a.interleaved ? append4_kernel<true, true> : append4_kernel<true, false>)
+                     : (a.interleaved ? append4_kernel<false, true> : append4_kernel<false, false>);
+  return launch_dependent(kern, grid, kThreads, 0, a.stream, p);
+}
+
+cudaError_t launch_read4(const Read4Launch& a, int num_sms) {
+  Read4Params p = a.params;
+  const int64_t bx = ((int64_t)p.batch.total * (p.d / 8) + kThreads - 1) / kThreads;
+  p.group_heads = heads_per_block(bx, 2 * p.Hkv, num_sms);
+  p.head_groups = (2 * p.Hkv + p.group_heads - 1) / p.group_heads;
+  p.token_blocks = (unsigned)(bx * p.head_groups);
+  const dim3 grid(p.token_blocks + ((unsigned)p.batch.n_seq + kThreads - 1) / kThreads);
+  return launch_dependent(a.bf16 ? read4_kernel<true> : read4_kernel<false>, grid, kThreads, 0,
+                          a.stream, p);
+}
+
+}  // namespace attn

@@ -16,6 +16,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -28,6 +29,9 @@ constexpr int kMaxAxes = 8;  // position axes of a rotary table
 decltype(&attn_rope) p_rope = nullptr;
 decltype(&attn_append_kv) p_append = nullptr;
 decltype(&attn_fwd_paged) p_paged = nullptr;
+decltype(&attn_append_kv4) p_append4 = nullptr;
+decltype(&attn_read_kv4) p_read4 = nullptr;
+decltype(&attn_fwd_paged4) p_paged4 = nullptr;
 decltype(&attn_fwd_paged_workspace_bytes) p_paged_bytes = nullptr;
 PyObject* g_error = nullptr;  // the package's AttnError
 
@@ -193,19 +197,12 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 struct Paged {
   at::Tensor k_pages, v_pages, blocks, cu, kv;
 
-  // x: packed new tokens [H, total, d]
+  // x: the tensor whose device the batch lies on.  a: k_pages, v_pages (the
+  // caller checks them), block_table, cu_seqlens, kv_lens.
   Paged(PyObject* const* a, const at::Tensor& x)
       : k_pages(required(a[0], "k_pages")), v_pages(required(a[1], "v_pages")),
         blocks(required(a[2], "block_table")), cu(required(a[3], "cu_seqlens")),
         kv(required(a[4], "kv_lens")) {
-    need(x.dim() == 3, "packed tensors must be [H, total, d]");
-    dtype_of(x);
-    need(x.is_cuda() && like(k_pages, x) && like(v_pages, x),
-         "tokens and pages must be CUDA tensors of one dtype on one device");
-    need(k_pages.dim() == 4 && k_pages.sizes() == v_pages.sizes() && k_pages.size(3) == x.size(2),
-         "k_pages, v_pages must be [n_pages, Hkv, page, d] with the tokens' d");
-    need(k_pages.is_contiguous() && v_pages.is_contiguous(),
-         "k_pages, v_pages must be contiguous");
     need(kv.dim() == 1 && kv.size(0) >= 1 && blocks.dim() == 2 && blocks.size(0) == kv.size(0) &&
              cu.dim() == 1 && cu.size(0) == kv.size(0) + 1,
          "block_table must be [n_seq, max_pages], cu_seqlens [n_seq + 1], kv_lens [n_seq]");
@@ -213,15 +210,41 @@ struct Paged {
          "block_table, cu_seqlens and kv_lens must be contiguous int32 tensors on the tokens' "
          "device");
   }
+  // Packed new tokens x [H, total, d] of a cache in 16 bits, or in 4 (kv4).
+  Paged(PyObject* const* a, const at::Tensor& x, bool kv4) : Paged(a, tokens(x)) {
+    if (kv4) {
+      need(k_pages.device() == x.device() && v_pages.device() == x.device() &&
+               k_pages.scalar_type() == at::kByte && v_pages.scalar_type() == at::kByte,
+           "k_pages, v_pages must be uint8 tensors on the tokens' device");
+      need(x.size(2) % 32 == 0 && k_pages.dim() == 4 && k_pages.sizes() == v_pages.sizes() &&
+               k_pages.size(3) == x.size(2) / 8 * 5,
+           "k_pages, v_pages must be [n_pages, Hkv, page, 5 d / 8] with the tokens' d");
+    } else {
+      need(like(k_pages, x) && like(v_pages, x),
+           "tokens and pages must be CUDA tensors of one dtype on one device");
+      need(k_pages.dim() == 4 && k_pages.sizes() == v_pages.sizes() &&
+               k_pages.size(3) == x.size(2),
+           "k_pages, v_pages must be [n_pages, Hkv, page, d] with the tokens' d");
+    }
+    need(k_pages.is_contiguous() && v_pages.is_contiguous(),
+         "k_pages, v_pages must be contiguous");
+  }
+  static const at::Tensor& tokens(const at::Tensor& x) {
+    need(x.dim() == 3, "packed tensors must be [H, total, d]");
+    dtype_of(x);
+    need(x.is_cuda(), "tokens and pages must be CUDA tensors of one dtype on one device");
+    return x;
+  }
 };
 
 // append_kv(k, v, k_pages, v_pages, block_table, cu_seqlens, kv_lens, table,
-//           positions, interleaved, q, out_q) -> q' or None
+//           positions, interleaved, q, out_q, 4 bits) -> q' or None
 PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 12);
+  arguments(n, 13);
   const at::Tensor k = required(a[0], "k"), v = required(a[1], "v");
-  const Paged c(a + 2, k);
+  const bool kv4 = truth(a[12]);
+  const Paged c(a + 2, k, kv4);
   const at::Tensor table = tensor(a[7], "table"), pos = tensor(a[8], "positions");
   const at::Tensor q = tensor(a[10], "q");
   at::Tensor oq = tensor(a[11], "out_q");
@@ -250,26 +273,65 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(oq.sizes() == q.sizes() && like(oq, q) && oq.is_contiguous(),
          "out_q must be contiguous with q's shape, dtype and device");
   }
-  check(p_append(ptr(k), ptr(v), ptr(q), ptr(oq), st, ptr(c.k_pages), ptr(c.v_pages),
-                 ptr_as<int32_t>(c.blocks), ptr_as<int32_t>(c.cu), ptr_as<int32_t>(c.kv),
-                 ptr_as<int32_t>(pos), pos.defined() ? (int)pos.size(0) : 1,
-                 ptr_as<int64_t>(table), rot, truth(a[9]), size(c.kv.size(0)), size(total),
-                 size(c.k_pages.size(0)), size(c.k_pages.size(2)), size(c.blocks.size(1)),
-                 q.defined() ? size(q.size(0)) : 0, size(Hkv), size(d), dtype_of(k),
-                 stream_of(k)),
-        "attn_append_kv");
+  check((kv4 ? p_append4 : p_append)(
+            ptr(k), ptr(v), ptr(q), ptr(oq), st, ptr(c.k_pages), ptr(c.v_pages),
+            ptr_as<int32_t>(c.blocks), ptr_as<int32_t>(c.cu), ptr_as<int32_t>(c.kv),
+            ptr_as<int32_t>(pos), pos.defined() ? (int)pos.size(0) : 1, ptr_as<int64_t>(table),
+            rot, truth(a[9]), size(c.kv.size(0)), size(total), size(c.k_pages.size(0)),
+            size(c.k_pages.size(2)), size(c.blocks.size(1)), q.defined() ? size(q.size(0)) : 0,
+            size(Hkv), size(d), dtype_of(k), stream_of(k)),
+        kv4 ? "attn_append_kv4" : "attn_append_kv");
   if (!q.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(oq);
   END_HANDLE_TH_ERRORS
 }
 
+// read_kv4(k_pages, v_pages, block_table, cu_seqlens, kv_lens, total, dtype, k, v) -> (k, v)
+PyObject* read_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 9);
+  const at::Tensor pages = required(a[0], "k_pages");
+  need(pages.is_cuda(), "all tensors must be on the same CUDA device");
+  const Paged c(a, pages);
+  need(pages.scalar_type() == at::kByte && like(c.v_pages, pages) && pages.dim() == 4 &&
+           pages.sizes() == c.v_pages.sizes() && pages.size(3) % 20 == 0 &&
+           pages.is_contiguous() && c.v_pages.is_contiguous(),
+       "k_pages, v_pages must be contiguous uint8 [n_pages, Hkv, page, 5 d / 8]");
+  const int64_t total = integer(a[5], "total"), Hkv = pages.size(1), d = pages.size(3) / 5 * 8;
+  need(total >= 1 && Hkv >= 1, "tensors must not be empty");
+  if (!THPDtype_Check(a[6])) fail(PyExc_TypeError, "dtype must be a torch.dtype");
+  const at::ScalarType type = reinterpret_cast<THPDtype*>(a[6])->scalar_type;
+  if (type != at::kHalf && type != at::kBFloat16)
+    fail(PyExc_TypeError, "dtype must be float16 or bfloat16");
+  at::Tensor k = tensor(a[7], "out_k"), v = tensor(a[8], "out_v");
+  c10::cuda::CUDAGuard guard(pages.device());
+  for (at::Tensor* t : {&k, &v}) {
+    if (!t->defined()) *t = at::empty({Hkv, total, d}, pages.options().dtype(type));
+    need(t->dim() == 3 && t->size(0) == Hkv && t->size(1) == total && t->size(2) == d &&
+             t->scalar_type() == type && t->device() == pages.device() && t->is_contiguous(),
+         "out_k, out_v must be contiguous [Hkv, total, d] tensors of dtype on the pages' device");
+  }
+  check(p_read4(ptr(pages), ptr(c.v_pages), ptr(k), ptr(v), ptr_as<int32_t>(c.blocks),
+                ptr_as<int32_t>(c.cu), ptr_as<int32_t>(c.kv), size(c.kv.size(0)), size(total),
+                size(pages.size(0)), size(pages.size(2)), size(c.blocks.size(1)), size(Hkv),
+                size(d), dtype_of(k), stream_of(pages)),
+        "attn_read_kv4");
+  PyObject* pair = PyTuple_New(2);
+  if (pair == nullptr) return nullptr;
+  PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(k));
+  PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(v));
+  return pair;
+  END_HANDLE_TH_ERRORS
+}
+
 // fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, max_q, causal,
-//           scale, out, lse, workspace) -> (out, lse)
+//           scale, out, lse, workspace, 4 bits) -> (out, lse)
 PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 12);
+  arguments(n, 13);
   const at::Tensor q = required(a[0], "q");
-  const Paged c(a + 1, q);
+  const bool kv4 = truth(a[12]);
+  const Paged c(a + 1, q, kv4);
   const int max_q = integer(a[6], "max_q");
   at::Tensor out = tensor(a[9], "out"), lse = tensor(a[10], "lse");
   at::Tensor ws = tensor(a[11], "workspace");
@@ -301,12 +363,13 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         p_paged_bytes(n_seq, max_q, (int64_t)max_pages * page, size(H), size(Hkv), size(d));
     if (bytes > 0) ws = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
   }
-  check(p_paged(ptr(q), ptr(c.k_pages), ptr(c.v_pages), ptr(out), ptr_as<float>(lse),
-                ptr_as<int32_t>(c.blocks), ptr_as<int32_t>(c.cu), ptr_as<int32_t>(c.kv), ptr(ws),
-                ws.defined() ? (size_t)ws.numel() : 0, n_seq, max_q, size(total),
-                size(c.k_pages.size(0)), page, max_pages, size(H), size(Hkv), size(d),
-                truth(a[7]), (float)scale, dtype_of(q), stream_of(q)),
-        "attn_fwd_paged");
+  check((kv4 ? p_paged4 : p_paged)(
+            ptr(q), ptr(c.k_pages), ptr(c.v_pages), ptr(out), ptr_as<float>(lse),
+            ptr_as<int32_t>(c.blocks), ptr_as<int32_t>(c.cu), ptr_as<int32_t>(c.kv), ptr(ws),
+            ws.defined() ? (size_t)ws.numel() : 0, n_seq, max_q, size(total),
+            size(c.k_pages.size(0)), page, max_pages, size(H), size(Hkv), size(d), truth(a[7]),
+            (float)scale, dtype_of(q), stream_of(q)),
+        kv4 ? "attn_fwd_paged4" : "attn_fwd_paged");
   PyObject* pair = PyTuple_New(2);
   if (pair == nullptr) return nullptr;
   PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(out));
@@ -315,20 +378,25 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+template <typename F>
+void take(F& to, PyObject* address) {
+  void* f = PyLong_AsVoidPtr(address);
+  if (f == nullptr) fail(PyExc_TypeError, "function addresses are wanted");
+  to = reinterpret_cast<F>(f);
+}
+
 // init(AttnError, addresses of attn_rope, attn_append_kv, attn_fwd_paged,
-//      attn_fwd_paged_workspace_bytes)
+//      attn_fwd_paged_workspace_bytes, attn_append_kv4, attn_read_kv4, attn_fwd_paged4)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 5);
-  void* f[4];
-  for (int i = 0; i < 4; ++i) {
-    f[i] = PyLong_AsVoidPtr(a[i + 1]);
-    if (f[i] == nullptr) fail(PyExc_TypeError, "function addresses are wanted");
-  }
-  p_rope = reinterpret_cast<decltype(p_rope)>(f[0]);
-  p_append = reinterpret_cast<decltype(p_append)>(f[1]);
-  p_paged = reinterpret_cast<decltype(p_paged)>(f[2]);
-  p_paged_bytes = reinterpret_cast<decltype(p_paged_bytes)>(f[3]);
+  arguments(n, 8);
+  take(p_rope, a[1]);
+  take(p_append, a[2]);
+  take(p_paged, a[3]);
+  take(p_paged_bytes, a[4]);
+  take(p_append4, a[5]);
+  take(p_read4, a[6]);
+  take(p_paged4, a[7]);
   Py_INCREF(a[0]);
   Py_XSETREF(g_error, a[0]);
   Py_RETURN_NONE;
@@ -341,7 +409,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<rope>("rope"), method<append_kv>("append_kv"),
-                           method<fwd_paged>("fwd_paged"), method<init>("init"),
+                           method<read_kv4>("read_kv4"), method<fwd_paged>("fwd_paged"),
+                           method<init>("init"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods};
 

@@ -1,0 +1,97 @@
+// A key/value cache held in 4 bits: the format of a row and its way back to 16
+// bits.
+//
+// A row of D channels takes 5 D / 8 bytes: D / 2 bytes of codes (channel 2 i in
+// the low half of byte i), then for each 32 channels a scale s and a minimum m
+// in the cache's 16-bit type T.  A code c in 0..15 stands for m + c s.  The
+// quantizer (append4.cu) sets, over the 32 values x of a group,
+//   m = min x,  s = RN_T((max x - m) / 15),  c = min(RN((x - m) / s), 15),
+// so m is a value of the group and x is off by s / 2 at most, but at the
+// largest, where the rounding of s may add 15 half steps of s.  A group with an
+// infinity or a NaN, or whose range passes fp32, has s = m = NaN: all of it
+// stands for NaN.
+//
+// Values take part in products as RN_T(m + c s), one fused multiply-add of two
+// 16-bit values at a time: half a step of T, the error that a 16-bit cache has in
+// the first place.  Keys do not: an error of 2^-9 a channel would show in the
+// log-sum-exp (1e-4 of it in bf16).  The decoding kernel multiplies by the
+// codes, c - 8 being exact in T, and applies s and m to each group's product in 32
+// bits; the tile kernel widens keys to fp16 (2^-12).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace attn {
+
+constexpr int kKv4Group = 32;
+constexpr int kv4_row(int d) { return d / 2 + d / 8; }  // bytes
+
+#ifdef __CUDACC__
+
+// Two codes (bits 0-3 and 16-19 of w) less ZERO as 16-bit numbers: their bits in
+// the mantissa of 2^7 (bf16) or 2^10 (fp16), less that power and ZERO.
+template <bool BF16, int ZERO>
+__device__ __forceinline__ uint32_t kv4_codes(uint32_t w) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("sub.rn.bf16x2 %0, %1, %2;"
+        : "=r"(r)
+        : "r"((w & 0x000F000Fu) | 0x43004300u), "r"(0x43004300u + 0x10001u * ZERO));
+  else
+    asm("sub.rn.f16x2 %0, %1, %2;"
+        : "=r"(r)
+        : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(0x64006400u + 0x10001u * ZERO));
+  return r;
+}
+
+// What two codes stand for.
+template <bool BF16>
+__device__ __forceinline__ uint32_t kv4_values(uint32_t w, uint32_t s, uint32_t m) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(kv4_codes<true, 0>(w)), "r"(s), "r"(m));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(kv4_codes<false, 0>(w)), "r"(s), "r"(m));
+  return r;
+}
+
+// Two 16-bit values in 32 bits.
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  if constexpr (BF16)
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+
+// 2^k that takes the finite number of bits `top` (>= 0) to 2^14 .. 2^15, where fp16
+// has 28 binades of full precision below it, and 2^-k.  Both are normal numbers;
+// zero is left where it is.
+__device__ __forceinline__ float2 to_fp16_range(uint32_t top) {
+  const uint32_t e = top == 0u ? 127u + 14u : top >> 23;
+  const uint32_t up = min(268u - e, 253u);
+  return make_float2(__uint_as_float(up << 23), __uint_as_float((254u - up) << 23));
+}
+
+// Bits of |x|, 0 for infinities and NaN: ordered like the numbers.
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+  return b < 0x7F800000u ? b : 0u;
+}
+
+// The eight values of a code word in channel order; par: s and m of its group.
+template <bool BF16>
+__device__ __forceinline__ uint4 kv4_word(uint32_t w, uint32_t par) {
+  const uint32_t s = __byte_perm(par, par, 0x1010), m = __byte_perm(par, par, 0x3232);
+  uint32_t v[4];  // channels i and i + 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = kv4_values<BF16>(w >> (4 * i), s, m);
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+
+#endif  // __CUDACC__
+
+}  // namespace attn

@@ -45,6 +45,8 @@ constexpr int kPagedMaxGroup = 128;
 
 struct PagedParams {
   const void* q;            // [Hkv * G, total, D]
+  const uint8_t* k4;        // [n_pages, Hkv, page, 5 D / 8] of a cache in 4 bits (kv4.cuh)
+  const uint8_t* v4;
   void* o;                  // [Hkv * G, total, D]
   float* lse;               // [Hkv * G, total]
   uint32_t* status;         // device status word
@@ -77,6 +79,9 @@ struct PagedLaunch {
 cudaError_t launch_paged_decode(const PagedLaunch& a, int d, bool bf16);
 cudaError_t launch_paged_tile(const PagedLaunch& a, int d, bool bf16);
 cudaError_t launch_paged_join(const PagedLaunch& a, int d, bool bf16, bool decode);
+// The same over a cache in 4 bits (params.k4, v4; tmK, tmV are not used).
+cudaError_t launch_paged4_decode(const PagedLaunch& a, int d, bool bf16);
+cudaError_t launch_paged4_tile(const PagedLaunch& a, int d, bool bf16);
 
 #ifdef __CUDACC__
 

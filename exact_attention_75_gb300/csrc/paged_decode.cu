@@ -25,17 +25,16 @@
 #include "dependent.cuh"
 #include "mma16.cuh"
 #include "paged.cuh"
+#include "paged_rows.cuh"
 #include "sm103_ptx.cuh"
 #include "smem_attr.cuh"
 
 namespace attn {
 
+using namespace rows;
+
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kKeys = kPagedBlock;
-constexpr int kMeet = 4;                // rows that meet in shared memory at a time
 constexpr int kBoxBytes = kKeys * 128;  // one 64-column chunk of a block's K or V
 
 template <int D>
@@ -45,9 +44,8 @@ struct PagedDecodeLayout {
   static constexpr int kSlots = D == 64 ? 6 : 3;              // ring depth of each warp
   static constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
   // Where the warps' results meet: kMeet rows of O each (padded), m and l.
-  static constexpr int kRowStride = D + 4;
   static constexpr int kMeetOff = kRingBytes;
-  static constexpr int kMlOff = kMeetOff + kWarps * kMeet * kRowStride * 4;
+  static constexpr int kMlOff = kMeetOff + kWarps * kMeet * kRowStride<D> * 4;
   static constexpr int kBarOff = kMlOff + kWarps * kMeet * 8;  // one mbarrier per slot
   static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;
   static constexpr int kBytes = kFlagOff + 16 + 1024;  // + room to align the base
@@ -57,22 +55,6 @@ struct PagedDecodeLayout {
 // Byte offset of 16-byte piece `piece` of row `row` in a staged block.
 __device__ __forceinline__ uint32_t sw_off(int row, int piece) {
   return (uint32_t)((piece >> 3) * kBoxBytes + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
-}
-
-// An item is a sequence's key/value head; the warps take the 16-key blocks of
-// its kUnit-key cost blocks in turn.
-constexpr int kUnit = kWarps * kKeys;
-using Cost = PagedCost<kUnit, 1, 1, 128, true>;
-using Walk = PagedWalk<Cost>;
-
-__device__ __forceinline__ int warp_blocks(const Walk& w, int warp) {
-  const int keys = min(w.u1 * kUnit, w.sq.klen) - w.u0 * kUnit;
-  const int nb = (max(keys, 0) + kKeys - 1) / kKeys;
-  return nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;
-}
-// First key of the warp's block j.
-__device__ __forceinline__ int first_key(const Walk& w, int warp, int j) {
-  return w.u0 * kUnit + (warp + j * kWarps) * kKeys;
 }
 
 // CLUSTER: an item is shared by the p.cluster CTAs of a cluster, which join
@@ -103,71 +85,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tmV);
   }
   grid_wait();
-  Walk w;
-  if constexpr (CLUSTER) {
-    const int item = blockIdx.x / p.cluster, rank = blockIdx.x - item * p.cluster;
-    w.b = item / p.Hkv;
-    w.head = item - w.b * p.Hkv;
-    w.sq = paged_seq(p, w.b);
-    w.nb = (w.sq.klen + kUnit - 1) / kUnit;
-    w.u0 = (int)((long long)rank * w.nb / p.cluster);
-    w.u1 = (int)((long long)(rank + 1) * w.nb / p.cluster);
-    w.x0 = 0;
-    w.take = 1;
-    w.left = w.sq.qlen > 0 ? 1 : 0;
-    if (threadIdx.x == 0 && rank == 0 && w.head == 0) paged_check(p, w.b);
-    __syncthreads();
-  } else {
-    if (threadIdx.x == 0) paged_clear(p);
-    w = paged_start<Cost, kThreads>(p, p.max_q);
-  }
+  Walk w = start_rows<CLUSTER>(p);
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
-  // The warp's stream of blocks runs over the pieces without a break: ahead
-  // walks it as far as the ring reaches.  Lane i holds the page of the piece's
-  // block 32 n + i, so that a table read's latency is paid once in 32 blocks.
-  // issued, it: blocks issued to and taken from the ring.
-  Walk ahead = w;
-  int aj = 0, an = w.left > 0 ? warp_blocks(w, warp) : 0, pages = -1;
-  uint32_t issued = 0, it = 0;
-  auto find_next = [&]() {  // settles ahead on its next block, or on left <= 0
-    while (ahead.left > 0 && aj >= an) {
-      ahead.advance(p, p.max_q);
-      an = warp_blocks(ahead, warp);
-      aj = 0;
-    }
-    if (ahead.left > 0 && (aj & 31) == 0) {
-      const int j = aj + lane;
-      pages = j < an ? __ldg(p.block_table + (size_t)ahead.b * p.max_pages +
-                             (first_key(ahead, warp, j) >> p.page_log2))
-                     : -1;
-    }
-  };
+  // it: blocks taken from the ring.
+  BlockStream stream(p, w, warp, lane);
+  uint32_t it = 0;
   auto issue = [&]() {
-    if (ahead.left <= 0) return;
-    const int page = __shfl_sync(0xffffffffu, pages, aj & 31);
-    if (lane == 0) {
-      const int s = (int)(issued % NS);
+    stream.issue(p, warp, lane, [&](int page, int head, int y) {
+      const int s = (int)(stream.issued % NS);
       const uint32_t dk = ring + (uint32_t)(s * L::kSlotBytes);
       const uint32_t dv = dk + L::kChunks * kBoxBytes;
-      const bool ok = page >= 0 && page < p.n_pages;
-      if (!ok)
-        atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(ahead.b, 0xFFFF) << 16));
-      const int z = ok ? page * p.Hkv + ahead.head : -1;  // -1: the box reads zeros
-      const int y = first_key(ahead, warp, aj) & (p.page - 1);
+      const int z = page >= 0 ? page * p.Hkv + head : -1;  // -1: the box reads zeros
       mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
 #pragma unroll
       for (int c = 0; c < L::kChunks; ++c) {
         tma_load_3d(dk + c * kBoxBytes, &tmK, bar(s), c * 64, y, z);
         tma_load_3d(dv + c * kBoxBytes, &tmV, bar(s), c * 64, y, z);
       }
-    }
-    ++issued;
-    ++aj;
-    find_next();
+    });
   };
-  find_next();
   for (int i = 0; i < NS; ++i) issue();
 
   float* meet = reinterpret_cast<float*>(smem + L::kMeetOff);
@@ -182,11 +120,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int nbw = warp_blocks(w, warp);
     const PagedSeq sq = w.sq;
     const int rows = min(kPagedRows, sq.qlen * p.G);
-    // Row r of the item: new token r / G, query head r % G of the group.
-    auto grow = [&](int r) -> size_t {
-      const int i = r / p.G, h = r - i * p.G;
-      return (size_t)(w.head * p.G + h) * p.total + sq.s0 + i;
-    };
+    auto grow = [&](int r) { return row_of(p, w, r); };
     const int r0 = lane >> 2, cq = 2 * (lane & 3);
     const uint16_t* qa_ = static_cast<const uint16_t*>(p.q) + (r0 < rows ? grow(r0) * D : 0);
     const uint16_t* qb_ =
@@ -200,12 +134,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       qa[ks][2] = r0 < rows ? *reinterpret_cast<const uint32_t*>(qa_ + c + 8) : 0u;
       qa[ks][3] = r0 + 8 < rows ? *reinterpret_cast<const uint32_t*>(qb_ + c + 8) : 0u;
     }
-    // Last key each of the thread's two rows sees (-1: a padding row, or one
-    // before the first key).
-    auto last_key = [&](int r) {
-      if (r >= rows) return -1;
-      return min(p.causal ? r / p.G + sq.klen - sq.qlen : sq.klen, sq.klen - 1);
-    };
+    auto last_key = [&](int r) { return r < rows ? last_key_of(p, sq, r) : -1; };
     const int limA = last_key(r0), limB = last_key(r0 + 8);
     const bool hiB = rows > 8;
 
@@ -341,13 +270,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     lB += __shfl_xor_sync(0xffffffffu, lB, 2);
 
     // The warps' (O, m, l) meet in shared memory, kMeet rows at a time.
-    const bool whole = !CLUSTER && w.whole();
-    const size_t slot = 2 * (size_t)blockIdx.x + (w.x0 == 0 ? 1 : 0);
-    if (!CLUSTER && !whole && threadIdx.x == 0) w.describe(p, 0);
+    if (!CLUSTER && !w.whole() && threadIdx.x == 0) w.describe(p, 0);
     for (int pass = 0; pass * kMeet < rows; ++pass) {
       if (pass > 0) __syncthreads();
       if ((r0 >> 2) == (pass & 1)) {
-        float* ro = meet + (warp * kMeet + (r0 & 3)) * L::kRowStride + cq;
+        float* ro = meet + (warp * kMeet + (r0 & 3)) * kRowStride<D> + cq;
 #pragma unroll
         for (int dn = 0; dn < DN; ++dn)
           *reinterpret_cast<float2*>(ro + 8 * dn) =
@@ -356,93 +283,16 @@ __global__ void __launch_bounds__(kThreads, 2)
           meet_ml[warp * kMeet + (r0 & 3)] = pass < 2 ? make_float2(mA, lA) : make_float2(mB, lB);
       }
       __syncthreads();
-      for (int idx = threadIdx.x; idx < kMeet * (D / 4); idx += kThreads) {
-        const int mr = idx / (D / 4), c = idx % (D / 4) * 4;
-        const int r = pass * kMeet + mr;
-        if (r >= rows) break;
-        float M = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) M = fmaxf(M, meet_ml[k * kMeet + mr].x);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lsum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-          const float2 ml = meet_ml[k * kMeet + mr];
-          const float f = paged_weight(ml.x, ml.y, M);
-          lsum += f * ml.y;
-          const float4 x =
-              *reinterpret_cast<const float4*>(meet + (k * kMeet + mr) * L::kRowStride + c);
-          acc.x += f * x.x;
-          acc.y += f * x.y;
-          acc.z += f * x.z;
-          acc.w += f * x.w;
-        }
-        if constexpr (CLUSTER) {
-          *reinterpret_cast<float4*>(part + r * D + c) = acc;
-          if (c == 0) part_ml[r] = make_float2(M, lsum);
-        } else if (whole) {
-          const float inv = paged_inverse(lsum);
-          const size_t gr = grow(r);
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + c) = make_uint2(
-              pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-          if (c == 0) p.lse[gr] = paged_lse(M, lsum);
-        } else {
-          *reinterpret_cast<float4*>(p.part_o + (slot * kPagedRows + r) * D + c) = acc;
-          if (c == 0)
-            *reinterpret_cast<float2*>(p.part_ml + (slot * kPagedRows + r) * 2) =
-                make_float2(M, lsum);
-        }
-      }
+      meet_rows<D, BF16, CLUSTER>(p, w, meet, meet_ml, part, part_ml, pass, rows);
     }
   }
-  if constexpr (CLUSTER) {
-    if (w.sq.qlen > 0) {  // the same in every CTA of the cluster
-      cluster_sync();
-      const int rows = min(kPagedRows, w.sq.qlen * p.G);
-      const int rank = blockIdx.x % p.cluster;
-      for (int e = rank * kThreads + threadIdx.x; !given_up && e < rows * (D / 4);
-           e += p.cluster * kThreads) {
-        const int r = e / (D / 4), c = e % (D / 4) * 4;
-        float2 ml[kPagedCluster];
-        float4 x[kPagedCluster];
-#pragma unroll
-        for (int k = 0; k < kPagedCluster; ++k) {
-          ml[k] = make_float2(-INFINITY, 0.f);
-          if (k >= p.cluster) continue;
-          ml[k] = cluster_load2(smem_u32(part_ml + r), k);
-          x[k] = cluster_load4(smem_u32(part + r * D + c), k);
-        }
-        float M = ml[0].x;
-#pragma unroll
-        for (int k = 1; k < kPagedCluster; ++k) M = fmaxf(M, ml[k].x);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lsum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kPagedCluster; ++k) {
-          if (k >= p.cluster) continue;
-          const float f = paged_weight(ml[k].x, ml[k].y, M);
-          lsum += f * ml[k].y;
-          acc.x += f * x[k].x;
-          acc.y += f * x[k].y;
-          acc.z += f * x[k].z;
-          acc.w += f * x[k].w;
-        }
-        const float inv = paged_inverse(lsum);
-        const int i = r / p.G, h = r - i * p.G;
-        const size_t gr = (size_t)(w.head * p.G + h) * p.total + w.sq.s0 + i;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + gr * D + c) = make_uint2(
-            pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-        if (c == 0) p.lse[gr] = paged_lse(M, lsum);
-      }
-      cluster_sync();  // the others have read this CTA's part
-    }
-  }
+  if constexpr (CLUSTER) join_cluster<D, BF16>(p, w, part, part_ml, given_up);
   // After an abort, copies still on their way must land before the CTA exits.
   Watchdog dw = wd;
   volatile int never = 0;
   dw.abort_flag = &never;
   dw.limit_ns = drain_limit_ns(wd.limit_ns);
-  for (; it < issued; ++it) mbar_wait(bar((int)(it % NS)), (it / NS) & 1, dw, 66);
+  for (; it < stream.issued; ++it) mbar_wait(bar((int)(it % NS)), (it / NS) & 1, dw, 66);
   grid_release();
 }
 

@@ -14,6 +14,17 @@
 // tile 0 / 1, warp 8 TMA producer, warp 9 tcgen05 issuer, warp 10 relay of
 // the TMA completions (and of the zeroing behind a sequence's last key).
 //
+// Over a cache held in 4 bits (KV4; kv4.cuh) warps 12-15 take the producer's place
+// for K and V: a thread owns a key of the block, has the next block's row on its way
+// to registers, and stores the widened row where TMA would have put it.  The rest
+// of the pipeline does not differ.  With 16 warps a thread has 128 registers, not the
+// 168 in which a softmax thread holds a row of 128 scores: it holds half, and reads
+// the other half twice, for the maximum and for the exponentials.  Keys widened to
+// bf16 would be off by 2^-9, which shows in the log-sum-exp, so the scores of a bf16
+// cache are a product in fp16 (keys off by 2^-12): the widening warps scale every 32
+// keys, and the softmax threads each their query, by a power of two into fp16's range,
+// and the scores are scaled back where they are scaled anyway.
+//
 // Bound, like the dense forward, by the softmax and products of 128-row tiles:
 // a key block of two tiles takes 1.55 to 1.75 us (d = 128; d = 96 1.65), of one
 // 1.06.  Measured, kernel and join, bf16: 4096 new tokens over 16384 keys, 16
@@ -28,6 +39,7 @@
 #include <cstdint>
 
 #include "dependent.cuh"
+#include "kv4.cuh"
 #include "mma16.cuh"
 #include "paged.cuh"
 #include "sm103_ptx.cuh"
@@ -38,10 +50,12 @@ namespace attn {
 
 namespace {
 
-constexpr int kThreads = 352;
+template <bool KV4>
+constexpr int kTileThreads = KV4 ? 512 : 352;
 constexpr int kWarpProducer = 8;
 constexpr int kWarpMma = 9;
 constexpr int kWarpRelay = 10;
+constexpr int kWarpWiden = 12;  // first of four
 constexpr uint32_t kBarKv = 1, kBarP = 2;  // issuer <-> relay, issuer <-> softmax t
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
 constexpr int kRows = kPagedTileRows;
@@ -57,9 +71,15 @@ struct PagedTileLayout {
   static constexpr int kBarOff = kStageOff + 8 * kStageBytes;
   static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kOFull = 6, kDrain = 8;
   static constexpr int kKvFull = 9, kKvEmpty = 9 + kSlots;
-  static constexpr int kNumBars = 9 + 2 * kSlots;
+  static constexpr int kQReady = 9 + 2 * kSlots;  // queries of a 4-bit cache, scaled
+  static constexpr int kNumBars = kQReady + 2;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr int kBytes = kMiscOff + 16;
+  // Scales of 4 x 32 keys by block of a 4-bit cache.  The widening warps are at
+  // most kSlots / 2 + 1 blocks past one whose scores are read.
+  static constexpr int kScales = 8;
+  static_assert(kScales > kSlots / 2 + 1, "a scale is read before it is written again");
+  static constexpr int kScaleOff = (kMiscOff + 16 + 15) / 16 * 16;
+  static constexpr int kBytes = kScaleOff + kScales * 16;
   static constexpr int kDynSmem = kBytes + 1024;  // + alignment slack
   static_assert(kDynSmem + 256 <= 232448, "shared memory budget (227 KB) exceeded");
 };
@@ -85,13 +105,117 @@ struct Walk : PagedWalk<Cost> {
   }
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ float row_max32(const uint32_t (&s)[32]) {
+  auto at = [&](int i) { return __uint_as_float(s[i]); };
+  float m[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) m[a] = fmax3(at(3 * a), at(3 * a + 1), at(3 * a + 2));
+#pragma unroll
+  for (int i = 12; i < 28; i += 8) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) m[a] = fmax3(m[a], at(i + 2 * a), at(i + 2 * a + 1));
+  }
+  m[0] = fmax3(m[0], at(28), at(29));
+  m[1] = fmax3(m[1], at(30), at(31));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// A row of a 4-bit cache: its code words, then its groups' scales and minima.
+template <int D>
+struct Row4 {
+  uint32_t w[kv4_row(D) / 4];
+
+  __device__ __forceinline__ void load(const uint8_t* x) {  // null: a row of zeros
+    constexpr int N = kv4_row(D) / 4;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = 0u;
+    if (x == nullptr) return;
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<uint4*>(w + i) = __ldg(reinterpret_cast<const uint4*>(x) + i / 4);
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2)
+        *reinterpret_cast<uint2*>(w + i) = __ldg(reinterpret_cast<const uint2*>(x) + i / 2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(x) + i);
+    }
+  }
+  __device__ __forceinline__ uint32_t& param(int c) { return w[D / 8 + c]; }
+  // The bits of the largest finite number that a code of the row can stand for
+  // (of a bf16 cache).
+  __device__ __forceinline__ uint32_t top() {
+    uint32_t b = 0u;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const float2 par = unpack2<true>(param(c));
+      b = max(b, max(finite_bits(par.y), finite_bits(fmaf(15.f, par.x, par.y))));
+    }
+    return b;
+  }
+  // Scales and minima of a bf16 cache as fp16, times f.
+  __device__ __forceinline__ void to_fp16(float f) {
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const float2 par = unpack2<true>(param(c));
+      param(c) = pack_f16x2(par.x * f, par.y * f);
+    }
+  }
+  // Widened, as row `row` of a tile in shared memory.
+  template <bool BF16>
+  __device__ __forceinline__ void widen(uint8_t* tile, int row) {
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+      *reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
+                                (((c & 7) ^ (row & 7)) << 4)) =
+          kv4_word<BF16>(w[c], param(c / 4));
+  }
+};
+
+// Row `row` of a tile of bf16 queries as fp16, scaled into its range: the factor
+// that undoes it.
+template <int D>
+__device__ __forceinline__ float query_to_fp16(uint8_t* tile, int row) {
+  auto piece = [&](int c) {
+    return reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
+                                    (((c & 7) ^ (row & 7)) << 4));
+  };
+  uint32_t top = 0u;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *piece(c);
+    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2<true>(y[i]);
+      top = max(top, max(finite_bits(v.x), finite_bits(v.y)));
+    }
+  }
+  const float2 f = to_fp16_range(top);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *piece(c);
+    uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2<true>(y[i]);
+      y[i] = pack_f16x2(v.x * f.x, v.y * f.x);
+    }
+    *piece(c) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  return f.y;
+}
+
+template <int D, bool BF16, bool KV4>
+__global__ void __launch_bounds__(kTileThreads<KV4>, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
   using L = PagedTileLayout<D>;
   constexpr int kChunks = kPaddedD<D> / 64;
+  constexpr bool kScaled = KV4 && BF16;  // scores are a product in fp16
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -105,18 +229,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
   const int TT = 128 / p.G;  // tokens of a query tile
+  float4* const scales = reinterpret_cast<float4*>(smem + L::kScaleOff);
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(L::kQFull + t), 1);
       mbar_init(bar(L::kQEmpty + t), 1);
+      mbar_init(bar(L::kQReady + t), 4);
       mbar_init(bar(L::kSFull + t), 1);
       mbar_init(bar(L::kOFull + t), 1);
     }
     mbar_init(bar(L::kDrain), 1);
     for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(bar(L::kKvFull + s), 1);
+      mbar_init(bar(L::kKvFull + s), KV4 ? 4 : 1);
       mbar_init(bar(L::kKvEmpty + s), 1);
     }
     mbar_fence_init();
@@ -131,244 +257,310 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   if (threadIdx.x == 0) paged_clear(p);
   Walk w;
-  static_cast<PagedWalk<Cost>&>(w) = paged_start<Cost, kThreads>(p, 2 * TT);  // a CTA barrier
+  // (a CTA barrier)
+  static_cast<PagedWalk<Cost>&>(w) = paged_start<Cost, kTileThreads<KV4>>(p, 2 * TT);
   if (w.left > 0) w.tiles(p, TT);
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
-
-  if (warp == kWarpProducer) {
-    // ------------------------------------------------------ TMA producer ---
-    const int box_rows = min(p.page, 128);
-    const int boxes = 128 / box_rows;
-    uint32_t kv_it = 0, q_it[2] = {0, 0};
-    bool ok = true;
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
-    for (; w.left > 0 && ok; w.next(p, TT)) {
-      const int nbmax = max(w.n[0], w.n[1]);
-      if (nbmax == 0) continue;
-      // The page of the lane's box of key block kb, read ahead of its use: -2
-      // past the sequence.
-      auto box_page = [&](int kb) {
-        const int key0 = kb * 128 + lane * box_rows;
-        return lane < boxes && key0 < w.sq.klen
-                   ? __ldg(p.block_table + (size_t)w.b * p.max_pages + (key0 >> p.page_log2))
-                   : -2;
-      };
-      int page = box_page(w.u0);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (w.n[t] == 0) continue;
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(bar(L::kQEmpty + t), (q_it[t] & 1) ^ 1, wd, 67));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(L::kQFull + t), (uint32_t)(kChunks * TT * p.G * 128));
-          const uint32_t dst = sbase + L::kQOff + t * L::kTileBytes;
-#pragma unroll
-          for (int h = 0; h < kChunks; ++h)
-            tma_load_3d(dst + h * 16384, &tmQ, bar(L::kQFull + t), h * 64,
-                        w.sq.s0 + (2 * w.item + t) * TT, w.head * p.G);
+  if (warp >= kWarpProducer) {
+    if (warp == kWarpProducer) {
+      // ------------------------------------------------------ TMA producer ---
+      const int box_rows = min(p.page, 128);
+      const int boxes = 128 / box_rows;
+      uint32_t kv_it = 0, q_it[2] = {0, 0};
+      bool ok = true;
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        if (!KV4) {
+          tma_prefetch_desc(&tmK);
+          tma_prefetch_desc(&tmV);
         }
-        ++q_it[t];
       }
-      for (int j = 0; j < nbmax && ok; ++j) {
-        const int y = (w.u0 + j) * 128 & (p.page - 1);  // 0 unless a page holds two blocks
-        const int next = j + 1 < nbmax ? box_page(w.u0 + j + 1) : -2;
-        // tensor-map page index; -1 (zeros) past the sequence or for a page
-        // outside the cache
-        const bool in_cache = page >= 0 && page < p.n_pages;
-        if (!in_cache && page != -2)
-          atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(w.b, 0xFFFF) << 16));
-        const int z = in_cache ? page * p.Hkv + w.head : -1;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          const uint32_t slot = kv_it % L::kSlots;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvEmpty + slot),
-                                                 ((kv_it / L::kSlots) & 1) ^ 1, wd, 68));
+      for (; w.left > 0 && ok; w.next(p, TT)) {
+        const int nbmax = max(w.n[0], w.n[1]);
+        if (nbmax == 0) continue;
+        // The page of the lane's box of key block kb, read ahead of its use: -2
+        // past the sequence.
+        auto box_page = [&](int kb) {
+          const int key0 = kb * 128 + lane * box_rows;
+          return lane < boxes && key0 < w.sq.klen
+                     ? __ldg(p.block_table + (size_t)w.b * p.max_pages + (key0 >> p.page_log2))
+                     : -2;
+        };
+        int page = KV4 ? -2 : box_page(w.u0);
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (w.n[t] == 0) continue;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(bar(L::kQEmpty + t), (q_it[t] & 1) ^ 1, wd, 67));
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar(L::kKvFull + slot), L::kTileBytes);
-          __syncwarp();
-          if (lane < boxes) {
-            const uint32_t dst = sbase + L::kKvOff + slot * L::kTileBytes + lane * box_rows * 128;
-#pragma unroll
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(L::kQFull + t), (uint32_t)(kChunks * TT * p.G * 128));
+            const uint32_t dst = sbase + L::kQOff + t * L::kTileBytes;
+  #pragma unroll
             for (int h = 0; h < kChunks; ++h)
-              tma_load_3d(dst + h * 16384, which ? &tmV : &tmK, bar(L::kKvFull + slot), h * 64,
-                          y, z);
+              tma_load_3d(dst + h * 16384, &tmQ, bar(L::kQFull + t), h * 64,
+                          w.sq.s0 + (2 * w.item + t) * TT, w.head * p.G);
           }
-          ++kv_it;
+          ++q_it[t];
         }
-        page = next;
-      }
-    }
-    // Drain: every copy this warp issued must have landed before the CTA may
-    // exit (only matters after an abort; otherwise all were consumed).
-    Watchdog dw = wd;
-    volatile int never = 0;
-    dw.abort_flag = &never;
-    dw.limit_ns = drain_limit_ns(wd.limit_ns);
-    const uint32_t first = kv_it > (uint32_t)L::kSlots ? kv_it - L::kSlots : 0u;
-    for (uint32_t it = first; it < kv_it; ++it)
-      mbar_wait(bar(L::kKvFull + it % L::kSlots), (it / L::kSlots) & 1, dw, 69);
-    for (int t = 0; t < 2; ++t)
-      if (q_it[t] > 0) mbar_wait(bar(L::kQFull + t), (q_it[t] - 1) & 1, dw, 70);
-    __syncwarp();
-  } else if (warp == kWarpRelay) {
-    // ---------------------------------------------------------- TMA relay ---
-    // Waits for the TMA completions the issuer needs and meets it at named
-    // barrier kBarKv: per piece [Q tiles + K_0], then per block [V_j + K_{j+1}].
-    // After an abort the schedule is still walked to the end (waits skipped),
-    // so that every rendezvous pairs up.
-    const int box_rows = min(p.page, 128);
-    uint32_t kv_it = 0, q_it[2] = {0, 0};
-    bool aborted = false;
-    auto kv_ready = [&]() {
-      const uint32_t slot = kv_it % L::kSlots;
-      const uint32_t par = (kv_it / L::kSlots) & 1;
-      ++kv_it;
-      if (!aborted)
-        aborted = !__all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull + slot), par, wd, 71));
-      return slot;
-    };
-    for (; w.left > 0; w.next(p, TT)) {
-      const int nbmax = max(w.n[0], w.n[1]);
-      if (!w.nothing() && !w.whole() && lane == 0) w.describe(p, 2 * w.item * TT);
-      if (nbmax == 0) continue;  // the same skip in every role
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (w.n[t] == 0) continue;
-        const uint32_t par = q_it[t] & 1;
-        ++q_it[t];
-        if (aborted) continue;
-        aborted = !__all_sync(0xffffffffu, mbar_wait(bar(L::kQFull + t), par, wd, 72));
-      }
-      kv_ready();
-      aborted = named_bar_or(kBarKv, 64, aborted);
-      for (int j = 0; j < nbmax; ++j) {
-        const uint32_t vslot = kv_ready();
-        const int valid = w.sq.klen - (w.u0 + j) * 128;  // rows of V that are keys
-        if (valid < 128 && !aborted) {
-          // Rows past the sequence's last key hold whatever their page held
-          // (P is 0 there, but 0 x NaN is not): zero them, up to the end of
-          // the last key's box (later boxes read zeros).
-          const int end = (valid + box_rows - 1) / box_rows * box_rows;
-          uint8_t* tile = smem + L::kKvOff + vslot * L::kTileBytes;
-          for (int i = lane; i < (end - valid) * 8 * kChunks; i += 32) {
-            const int row = valid + i / (8 * kChunks), pc = i % (8 * kChunks);
-            *reinterpret_cast<uint4*>(tile + (pc >> 3) * 16384 + row * 128 + (pc & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
-        if (j + 1 < nbmax) kv_ready();
-        aborted = named_bar_or(kBarKv, 64, aborted);
-      }
-    }
-  } else if (warp == kWarpMma) {
-    // ---------------------------------------------------- tcgen05 issuer ---
-    constexpr uint32_t kIdS = idesc_f16(128, 128, BF16, false, false);
-    constexpr uint32_t kIdO = idesc_f16(128, D, BF16, false, true);
-    uint32_t kv_it = 0;
-    bool aborted = false;
-    bool issued = false;
-    const uint64_t qdesc0 = kmajor_base(sbase + L::kQOff);
-    const uint64_t qdesc1 = kmajor_base(sbase + L::kQOff + L::kTileBytes);
-    auto issue_s = [&](int t, uint32_t kaddr) {
-      const uint64_t kd = kmajor_base(kaddr);
-      const uint64_t qd = t ? qdesc1 : qdesc0;
-      const uint32_t dcol = tbase + 128 * t;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma_f16_ss(dcol, desc_plus(qd, kmajor16_off(kk)), desc_plus(kd, kmajor16_off(kk)), kIdS,
-                   kk > 0);
-    };
-    auto issue_pv = [&](int t, uint32_t vaddr, uint32_t acc0) {
-      const uint32_t ocol = tbase + 256 + kPaddedD<D> * t;
-      const uint32_t pcol = tbase + 128 * t;
-      const uint64_t vd = mnmajor_base(vaddr);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // 16 keys per MMA
-        mma_f16_ts(ocol, pcol + kk * 8, desc_plus(vd, mnmajor16_off(kk)), kIdO,
-                   kk > 0 ? 1u : acc0);
-    };
-    for (; w.left > 0; w.next(p, TT)) {
-      const int nb0 = w.n[0], nb1 = w.n[1];
-      const int nbmax = max(nb0, nb1);
-      if (nbmax == 0) continue;  // the same skip in every role
-      aborted = named_bar_or(kBarKv, 64, aborted);
-      uint32_t kslot = kv_it % L::kSlots;
-      ++kv_it;
-      if (!aborted) {
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t kaddr = sbase + L::kKvOff + kslot * L::kTileBytes;
-          if (nb0 > 0) {
-            issue_s(0, kaddr);
-            mma_commit(bar(L::kSFull + 0));
-            if (nb0 == 1) mma_commit(bar(L::kQEmpty + 0));
-          }
-          if (nb1 > 0) {
-            issue_s(1, kaddr);
-            mma_commit(bar(L::kSFull + 1));
-            if (nb1 == 1) mma_commit(bar(L::kQEmpty + 1));
-          }
-          mma_commit(bar(L::kKvEmpty + kslot));
-        }
-        issued = true;
-        __syncwarp();
-      }
-      for (int j = 0; j < nbmax; ++j) {
-        // V_j and (if any) K_{j+1} are in shared memory.
-        aborted = named_bar_or(kBarKv, 64, aborted);
-        const uint32_t vslot = kv_it % L::kSlots;
-        ++kv_it;
-        const bool have_next = j + 1 < nbmax;
-        if (have_next) {
-          kslot = kv_it % L::kSlots;
-          ++kv_it;
-        }
-        const uint32_t vaddr = sbase + L::kKvOff + vslot * L::kTileBytes;
-        const uint32_t kaddr = sbase + L::kKvOff + kslot * L::kTileBytes;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int nbt = t ? nb1 : nb0;
-          if (j >= nbt) continue;
-          // P_t(j) is in tensor memory.
-          aborted = named_bar_or(kBarP + t, 160, aborted);
-          if (aborted) continue;
-          tc_fence_after();
-          if (lane == 0) {
-            issue_pv(t, vaddr, j > 0 ? 1u : 0u);
-            if (j == nbt - 1) mma_commit(bar(L::kOFull + t));
-            if (j + 1 < nbt) {
-              issue_s(t, kaddr);
-              mma_commit(bar(L::kSFull + t));
-              if (j + 1 == nbt - 1) mma_commit(bar(L::kQEmpty + t));
+        for (int j = 0; !KV4 && j < nbmax && ok; ++j) {
+          const int y = (w.u0 + j) * 128 & (p.page - 1);  // 0 unless a page holds two blocks
+          const int next = j + 1 < nbmax ? box_page(w.u0 + j + 1) : -2;
+          // tensor-map page index; -1 (zeros) past the sequence or for a page
+          // outside the cache
+          const bool in_cache = page >= 0 && page < p.n_pages;
+          if (!in_cache && page != -2)
+            atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(w.b, 0xFFFF) << 16));
+          const int z = in_cache ? page * p.Hkv + w.head : -1;
+  #pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            const uint32_t slot = kv_it % L::kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvEmpty + slot),
+                                                   ((kv_it / L::kSlots) & 1) ^ 1, wd, 68));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(L::kKvFull + slot), L::kTileBytes);
+            __syncwarp();
+            if (lane < boxes) {
+              const uint32_t dst = sbase + L::kKvOff + slot * L::kTileBytes + lane * box_rows * 128;
+  #pragma unroll
+              for (int h = 0; h < kChunks; ++h)
+                tma_load_3d(dst + h * 16384, which ? &tmV : &tmK, bar(L::kKvFull + slot), h * 64,
+                            y, z);
             }
+            ++kv_it;
           }
-          __syncwarp();
-        }
-        if (!aborted) {
-          if (lane == 0) {
-            mma_commit(bar(L::kKvEmpty + vslot));
-            if (have_next) mma_commit(bar(L::kKvEmpty + kslot));
-          }
-          __syncwarp();
+          page = next;
         }
       }
-    }
-    // Drain: wait until every MMA issued above has completed.
-    if (lane == 0 && issued) {
-      mma_commit(bar(L::kDrain));
+      // Drain: every copy this warp issued must have landed before the CTA may
+      // exit (only matters after an abort; otherwise all were consumed).
       Watchdog dw = wd;
       volatile int never = 0;
       dw.abort_flag = &never;
       dw.limit_ns = drain_limit_ns(wd.limit_ns);
-      mbar_wait(bar(L::kDrain), 0, dw, 73);
+      const uint32_t first = kv_it > (uint32_t)L::kSlots ? kv_it - L::kSlots : 0u;
+      for (uint32_t it = first; it < kv_it; ++it)
+        mbar_wait(bar(L::kKvFull + it % L::kSlots), (it / L::kSlots) & 1, dw, 69);
+      for (int t = 0; t < 2; ++t)
+        if (q_it[t] > 0) mbar_wait(bar(L::kQFull + t), (q_it[t] - 1) & 1, dw, 70);
+      __syncwarp();
+    } else if (KV4 && warp > kWarpRelay) {
+      // ------------------------------------------------ widening of K and V ---
+      const int row = threadIdx.x - 32 * kWarpWiden;  // key of the block; < 0: warp 11, idle
+      uint32_t kv_it = 0;
+      bool ok = row >= 0;
+      for (; w.left > 0 && ok; w.next(p, TT)) {
+        const int nbmax = max(w.n[0], w.n[1]);
+        if (nbmax == 0) continue;  // the same skip in every role
+        // The page of the thread's key of the piece's block j: -2 past the sequence
+        // or the piece.
+        auto key_page = [&](int j) {
+          const int key = (w.u0 + j) * 128 + row;
+          return j < nbmax && key < w.sq.klen
+                     ? __ldg(p.block_table + (size_t)w.b * p.max_pages + (key >> p.page_log2))
+                     : -2;
+        };
+        // Where its row lies in the cache; a page outside it gives zeros.
+        auto find = [&](int page, int j) -> int64_t {
+          if (page >= 0 && page < p.n_pages)
+            return ((((int64_t)page * p.Hkv + w.head) << p.page_log2) +
+                    (((w.u0 + j) * 128 + row) & (p.page - 1))) * kv4_row(D);
+          if (page != -2)
+            atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(w.b, 0xFFFF) << 16));
+          return -1;
+        };
+        auto put = [&](Row4<D>& x, bool key) {
+          const uint32_t slot = kv_it % L::kSlots;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvEmpty + slot),
+                                                 ((kv_it / L::kSlots) & 1) ^ 1, wd, 78));
+          if (!ok) return;
+          uint8_t* const tile = smem + L::kKvOff + slot * L::kTileBytes;
+          if (kScaled && key) {
+            const float2 f = to_fp16_range(__reduce_max_sync(0xffffffffu, x.top()));
+            if (lane == 0)
+              reinterpret_cast<float*>(scales + kv_it / 2 % L::kScales)[row >> 5] = f.y;
+            x.to_fp16(f.x);
+            x.template widen<false>(tile, row);
+          } else {
+            x.template widen<BF16>(tile, row);
+          }
+          fence_proxy_async_smem();  // before the products read it
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kKvFull + slot));
+          ++kv_it;
+        };
+        // Each row is asked for a block before it is widened, its page two before.
+        int64_t at = find(key_page(0), 0);
+        int page = key_page(1);
+        Row4<D> k, v;
+        k.load(at < 0 ? nullptr : p.k4 + at);
+        v.load(at < 0 ? nullptr : p.v4 + at);
+        for (int j = 0; j < nbmax && ok; ++j) {
+          at = find(page, j + 1);
+          page = key_page(j + 2);
+          put(k, true);
+          k.load(at < 0 ? nullptr : p.k4 + at);
+          if (!ok) break;
+          put(v, false);
+          v.load(at < 0 ? nullptr : p.v4 + at);
+        }
+      }
+    } else if (warp == kWarpRelay) {
+      // ---------------------------------------------------------- TMA relay ---
+      // Waits for the TMA completions the issuer needs and meets it at named
+      // barrier kBarKv: per piece [Q tiles + K_0], then per block [V_j + K_{j+1}].
+      // After an abort the schedule is still walked to the end (waits skipped),
+      // so that every rendezvous pairs up.
+      const int box_rows = min(p.page, 128);
+      uint32_t kv_it = 0, q_it[2] = {0, 0};
+      bool aborted = false;
+      auto kv_ready = [&]() {
+        const uint32_t slot = kv_it % L::kSlots;
+        const uint32_t par = (kv_it / L::kSlots) & 1;
+        ++kv_it;
+        if (!aborted)
+          aborted = !__all_sync(0xffffffffu, mbar_wait(bar(L::kKvFull + slot), par, wd, 71));
+        return slot;
+      };
+      for (; w.left > 0; w.next(p, TT)) {
+        const int nbmax = max(w.n[0], w.n[1]);
+        if (!w.nothing() && !w.whole() && lane == 0) w.describe(p, 2 * w.item * TT);
+        if (nbmax == 0) continue;  // the same skip in every role
+  #pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (w.n[t] == 0) continue;
+          const uint32_t par = q_it[t] & 1;
+          ++q_it[t];
+          if (aborted) continue;
+          const int full = kScaled ? L::kQReady : L::kQFull;
+          aborted = !__all_sync(0xffffffffu, mbar_wait(bar(full + t), par, wd, 72));
+        }
+        kv_ready();
+        aborted = named_bar_or(kBarKv, 64, aborted);
+        for (int j = 0; j < nbmax; ++j) {
+          const uint32_t vslot = kv_ready();
+          const int valid = w.sq.klen - (w.u0 + j) * 128;  // rows of V that are keys
+          if (!KV4 && valid < 128 && !aborted) {
+            // Rows past the sequence's last key hold whatever their page held
+            // (P is 0 there, but 0 x NaN is not): zero them, up to the end of
+            // the last key's box (later boxes read zeros).
+            const int end = (valid + box_rows - 1) / box_rows * box_rows;
+            uint8_t* tile = smem + L::kKvOff + vslot * L::kTileBytes;
+            for (int i = lane; i < (end - valid) * 8 * kChunks; i += 32) {
+              const int row = valid + i / (8 * kChunks), pc = i % (8 * kChunks);
+              *reinterpret_cast<uint4*>(tile + (pc >> 3) * 16384 + row * 128 + (pc & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+          if (j + 1 < nbmax) kv_ready();
+          aborted = named_bar_or(kBarKv, 64, aborted);
+        }
+      }
+    } else if (warp == kWarpMma) {
+      // ---------------------------------------------------- tcgen05 issuer ---
+      constexpr uint32_t kIdS = idesc_f16(128, 128, BF16 && !KV4, false, false);
+      constexpr uint32_t kIdO = idesc_f16(128, D, BF16, false, true);
+      uint32_t kv_it = 0;
+      bool aborted = false;
+      bool issued = false;
+      const uint64_t qdesc0 = kmajor_base(sbase + L::kQOff);
+      const uint64_t qdesc1 = kmajor_base(sbase + L::kQOff + L::kTileBytes);
+      auto issue_s = [&](int t, uint32_t kaddr) {
+        const uint64_t kd = kmajor_base(kaddr);
+        const uint64_t qd = t ? qdesc1 : qdesc0;
+        const uint32_t dcol = tbase + 128 * t;
+  #pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss(dcol, desc_plus(qd, kmajor16_off(kk)), desc_plus(kd, kmajor16_off(kk)), kIdS,
+                     kk > 0);
+      };
+      auto issue_pv = [&](int t, uint32_t vaddr, uint32_t acc0) {
+        const uint32_t ocol = tbase + 256 + kPaddedD<D> * t;
+        const uint32_t pcol = tbase + 128 * t;
+        const uint64_t vd = mnmajor_base(vaddr);
+  #pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // 16 keys per MMA
+          mma_f16_ts(ocol, pcol + kk * 8, desc_plus(vd, mnmajor16_off(kk)), kIdO,
+                     kk > 0 ? 1u : acc0);
+      };
+      for (; w.left > 0; w.next(p, TT)) {
+        const int nb0 = w.n[0], nb1 = w.n[1];
+        const int nbmax = max(nb0, nb1);
+        if (nbmax == 0) continue;  // the same skip in every role
+        aborted = named_bar_or(kBarKv, 64, aborted);
+        uint32_t kslot = kv_it % L::kSlots;
+        ++kv_it;
+        if (!aborted) {
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t kaddr = sbase + L::kKvOff + kslot * L::kTileBytes;
+            if (nb0 > 0) {
+              issue_s(0, kaddr);
+              mma_commit(bar(L::kSFull + 0));
+              if (nb0 == 1) mma_commit(bar(L::kQEmpty + 0));
+            }
+            if (nb1 > 0) {
+              issue_s(1, kaddr);
+              mma_commit(bar(L::kSFull + 1));
+              if (nb1 == 1) mma_commit(bar(L::kQEmpty + 1));
+            }
+            mma_commit(bar(L::kKvEmpty + kslot));
+          }
+          issued = true;
+          __syncwarp();
+        }
+        for (int j = 0; j < nbmax; ++j) {
+          // V_j and (if any) K_{j+1} are in shared memory.
+          aborted = named_bar_or(kBarKv, 64, aborted);
+          const uint32_t vslot = kv_it % L::kSlots;
+          ++kv_it;
+          const bool have_next = j + 1 < nbmax;
+          if (have_next) {
+            kslot = kv_it % L::kSlots;
+            ++kv_it;
+          }
+          const uint32_t vaddr = sbase + L::kKvOff + vslot * L::kTileBytes;
+          const uint32_t kaddr = sbase + L::kKvOff + kslot * L::kTileBytes;
+  #pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int nbt = t ? nb1 : nb0;
+            if (j >= nbt) continue;
+            // P_t(j) is in tensor memory.
+            aborted = named_bar_or(kBarP + t, 160, aborted);
+            if (aborted) continue;
+            tc_fence_after();
+            if (lane == 0) {
+              issue_pv(t, vaddr, j > 0 ? 1u : 0u);
+              if (j == nbt - 1) mma_commit(bar(L::kOFull + t));
+              if (j + 1 < nbt) {
+                issue_s(t, kaddr);
+                mma_commit(bar(L::kSFull + t));
+                if (j + 1 == nbt - 1) mma_commit(bar(L::kQEmpty + t));
+              }
+            }
+            __syncwarp();
+          }
+          if (!aborted) {
+            if (lane == 0) {
+              mma_commit(bar(L::kKvEmpty + vslot));
+              if (have_next) mma_commit(bar(L::kKvEmpty + kslot));
+            }
+            __syncwarp();
+          }
+        }
+      }
+      // Drain: wait until every MMA issued above has completed.
+      if (lane == 0 && issued) {
+        mma_commit(bar(L::kDrain));
+        Watchdog dw = wd;
+        volatile int never = 0;
+        dw.abort_flag = &never;
+        dw.limit_ns = drain_limit_ns(wd.limit_ns);
+        mbar_wait(bar(L::kDrain), 0, dw, 73);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // --------------------------------------------------- softmax warpgroups ---
     const int t = warp >> 2;          // query tile of the pair
@@ -376,13 +568,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_addr = tbase + lane_base + 128u * t;
     const uint32_t o_addr = tbase + lane_base + 256u + kPaddedD<D> * t;
-    const float sl2 = p.scale_log2;
+    float sl2 = p.scale_log2;
     const int gi = r / TT, ti = r - gi * TT;  // query head of the group, token of the tile
-    uint32_t s_it = 0, o_it = 0;
+    uint32_t s_it = 0, o_it = 0, blocks = 0;  // blocks: key blocks of the pieces before
     bool aborted = false;
     for (; w.left > 0; w.next(p, TT)) {
       if (w.nothing()) continue;
       const int nb = w.n[t];
+      const uint32_t block0 = blocks;
+      blocks += max(w.n[0], w.n[1]);
       const int token = (2 * w.item + t) * TT + ti;
       const bool live = gi < p.G && token < w.sq.qlen;
       const size_t grow = (size_t)(w.head * p.G + gi) * p.total + w.sq.s0 + token;
@@ -407,6 +601,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int koff = p.causal ? w.sq.klen - w.sq.qlen : w.sq.klen;
       const int lim = min(token + koff, w.sq.klen - 1);  // last key the row sees
       const int lim0 = min(token - ti + koff, w.sq.klen - 1);  // of the tile's first token
+      if constexpr (kScaled) {
+        if (!aborted)
+          aborted = !__all_sync(0xffffffffu, mbar_wait(bar(L::kQFull + t), o_it & 1, wd, 79));
+        if (!aborted) {
+          sl2 = p.scale_log2 * query_to_fp16<D>(smem + L::kQOff + t * L::kTileBytes, r);
+          fence_proxy_async_smem();  // before the products read it
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kQReady + t));
+        }
+      }
       float m = -INFINITY;  // running max of the log2-scaled scores (reference value)
       float l = 0.f;        // running sum of exp2(x - m)
       for (int j = 0; j < nb; ++j) {
@@ -416,23 +620,49 @@ __global__ void __launch_bounds__(kThreads, 1)
           aborted = !__all_sync(0xffffffffu, mbar_wait(bar(L::kSFull + t), spar, wd, 74));
         if (!aborted) {
           tc_fence_after();
-          uint32_t sr[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, sr[c]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) reg_fence32(sr[c]);
-          float s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(sr[c][i]);
           const int kbase = (w.u0 + j) * 128;
-          if (kbase + 127 > lim0) {
+          // Scores 32 c .. of the row, those that it does not see -inf.
+          constexpr int kHeld = KV4 ? 2 : 4;  // chunks of 32 in registers at a time
+          uint32_t sr[kHeld][32];
+          auto read_scores = [&](int c0) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = (kbase + c > lim) ? -INFINITY : s[c];
+            for (int c = 0; c < kHeld; ++c) tmem_ld32(s_addr + (c0 + c) * 32, sr[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kHeld; ++c) reg_fence32(sr[c]);
+            if (kbase + 127 > lim0) {
+#pragma unroll
+              for (int c = 0; c < kHeld; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (kbase + (c0 + c) * 32 + i > lim) sr[c][i] = 0xFF800000u;
+            }
+          };
+          // What takes chunk c's scores to base 2: 1e-37 .. 1e37, since a masked
+          // score times 0 would be NaN (a product that needs more is 0 or inf anyway).
+          float to2[4] = {sl2, sl2, sl2, sl2};
+          if constexpr (kScaled) {
+            const float4 f = scales[(block0 + j) % L::kScales];
+            const float by[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) to2[c] = fminf(fmaxf(sl2 * by[c], 1e-37f), 1e37f);
           }
-          const float m_blk = row_max128(s) * sl2;
+          float m_blk;
+          if constexpr (KV4) {
+            auto held_max = [&](int c0) {
+              return fmaxf(row_max32(sr[0]) * to2[c0], row_max32(sr[1]) * to2[c0 + 1]);
+            };
+            read_scores(2);
+            m_blk = held_max(2);
+            read_scores(0);
+            m_blk = fmaxf(m_blk, held_max(0));
+          } else {
+            read_scores(0);
+            float x[kHeld * 32];
+#pragma unroll
+            for (int i = 0; i < kHeld * 32; ++i) x[i] = __uint_as_float(sr[i / 32][i % 32]);
+            m_blk = row_max128(x) * sl2;
+          }
           // Raise the reference max where the block's exceeds it by more than
           // the threshold; O and l of those rows are rescaled by alpha.
           bool rescale = false;
@@ -451,23 +681,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 nm2 = make_float2(-mref, -mref);
           float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
-          const float2 sc2 = make_float2(sl2, sl2);
           // P goes to tensor memory in the inputs' 16 bits, what the product with
           // V takes (at most eps / 2 of sum_j P_ij |v_j|; l sums the unrounded
           // values); two 16-bit terms for P would double that product.
+          // P_c lies over scores that have been read: chunks 0 and 1 over the first.
+          auto exponentials = [&](int c0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
+            for (int c = 0; c < kHeld; ++c) {
+              uint32_t pk[16];
+              const float2 sc2 = make_float2(to2[c0 + c], to2[c0 + c]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x =
-                  __ffma2_rn(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc2, nm2);
-              const float p0 = ex2_approx(x.x);
-              const float p1 = ex2_approx(x.y);
-              rs2[i & 3] = __fadd2_rn(rs2[i & 3], make_float2(p0, p1));
-              pk[i] = pack2<BF16>(p0, p1);
+              for (int i = 0; i < 16; ++i) {
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c][2 * i]),
+                                                        __uint_as_float(sr[c][2 * i + 1])),
+                                            sc2, nm2);
+                const float p0 = ex2_approx(x.x);
+                const float p1 = ex2_approx(x.y);
+                rs2[i & 3] = __fadd2_rn(rs2[i & 3], make_float2(p0, p1));
+                pk[i] = pack2<BF16>(p0, p1);
+              }
+              tmem_st16(s_addr + (c0 + c) * 16, pk);
             }
-            tmem_st16(s_addr + c * 16, pk);
+          };
+          exponentials(0);
+          if constexpr (KV4) {
+            read_scores(2);
+            exponentials(2);
           }
           const float2 rsum =
               __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
@@ -573,30 +812,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool BF16>
-cudaError_t launch_db(const PagedLaunch& a) {
+template <int D, bool BF16, bool KV4>
+cudaError_t launch_dbk(const PagedLaunch& a) {
   using L = PagedTileLayout<D>;
-  auto kern = paged_tile_kernel<D, BF16>;
+  auto kern = paged_tile_kernel<D, BF16, KV4>;
   static DeviceFlags configured;
   cudaError_t e = ensure_dyn_smem(kern, L::kDynSmem, configured);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3((unsigned)a.grid), kThreads, L::kDynSmem, a.stream, a.tmQ,
-                          a.tmK, a.tmV, a.params);
+  return launch_dependent(kern, dim3((unsigned)a.grid), kTileThreads<KV4>, L::kDynSmem, a.stream,
+                          a.tmQ, a.tmK, a.tmV, a.params);
 }
 
-template <int D>
-cudaError_t launch_d(const PagedLaunch& a, bool bf16) {
-  return bf16 ? launch_db<D, true>(a) : launch_db<D, false>(a);
+template <int D, bool KV4>
+cudaError_t launch_dk(const PagedLaunch& a, bool bf16) {
+  return bf16 ? launch_dbk<D, true, KV4>(a) : launch_dbk<D, false, KV4>(a);
+}
+
+template <bool KV4>
+cudaError_t launch_k(const PagedLaunch& a, int d, bool bf16) {
+  switch (d) {
+    case 64: return launch_dk<64, KV4>(a, bf16);
+    case 96: return launch_dk<96, KV4>(a, bf16);
+    default: return launch_dk<128, KV4>(a, bf16);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_tile(const PagedLaunch& a, int d, bool bf16) {
-  switch (d) {
-    case 64: return launch_d<64>(a, bf16);
-    case 96: return launch_d<96>(a, bf16);
-    default: return launch_d<128>(a, bf16);
-  }
+  return launch_k<false>(a, d, bf16);
+}
+
+cudaError_t launch_paged4_tile(const PagedLaunch& a, int d, bool bf16) {
+  return launch_k<true>(a, d, bf16);
 }
 
 }  // namespace attn

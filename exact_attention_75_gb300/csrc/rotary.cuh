@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "packed.cuh"
+
 namespace attn {
 
 constexpr int kMaxAxes = 8;  // position axes
@@ -43,13 +45,10 @@ struct AppendParams {
   void* q_out;             // [heads, total, D] contiguous (null: no q)
   void* k_pages;           // [n_pages, Hkv, page, D]
   void* v_pages;
-  const int* block_table;  // [n_seq, max_pages]
-  const int* cu_seqlens;   // [n_seq + 1]
-  const int* kv_lens;      // [n_seq]
+  PackedBatch batch;
   const int* positions;    // [n_axes, total]; null: the position in the cache on every axis
   const int64_t* table;    // null: no rotation
-  uint32_t* status;
-  int n_axes, n_seq, max_pages, n_pages, page_log2, total, Hq, Hkv, d, rot;
+  int n_axes, Hq, Hkv, d, rot;
   int group_heads, head_groups;
   unsigned token_blocks;   // the blocks behind them check the batch
 };
@@ -61,5 +60,9 @@ struct AppendLaunch {
 };
 
 cudaError_t launch_append(const AppendLaunch& a, int num_sms);
+
+// The same into a 4-bit cache (kv4.cuh): k_pages, v_pages [n_pages, Hkv, page, 5 D / 8]
+// bytes.  d in {64, 96, 128}.
+cudaError_t launch_append4(const AppendLaunch& a, int num_sms);
 
 }  // namespace attn

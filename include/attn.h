@@ -362,6 +362,62 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
                            void* stream);
 
 /*
+ * A paged cache held in 4 bits, shared by attn_append_kv4, attn_read_kv4 and
+ * attn_fwd_paged4 (attn_kv_weights and attn_evict_kv take it too):
+ *   k_pages, v_pages : [n_pages, Hkv, page, 5 d / 8] bytes, 16-byte aligned;
+ *                 d in {64, 96, 128}.  A row is d / 2 bytes of codes (channel
+ *                 2i in the low half of byte i), then for each 32 channels a
+ *                 scale s and a minimum m in the 16-bit type that was appended
+ *                 (`dtype`); a code c stands for m + c s.
+ * Over the 32 values x of a group: m = min x, s = RN16((max x - m) / 15),
+ * c = min(RN((x - m) / s), 15) in fp32 (0 where s = 0), so that a value is off
+ * by s / 2, the largest by 15 half steps of s's rounding more.  A group that
+ * holds an infinity or a NaN, or whose range passes fp32, stands for NaN.
+ * The other arrays of the batch are those of the 16-bit cache (attn_append_kv).
+ *
+ * attn_append_kv4: as attn_append_kv, with the same arguments.  What that
+ * would store (keys turned and rounded to 16 bits) is what is quantized.
+ * Cite: "8.3 FlashAttention-3", section 5.1 (a scale per block of values), as
+ * attn_append_kv.
+ */
+attn_status attn_append_kv4(const void* k, const void* v, const void* q, void* q_out,
+                            const int64_t* strides, void* k_pages, void* v_pages,
+                            const int32_t* block_table, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, const int32_t* positions, int n_axes,
+                            const int64_t* table, int rot, int interleaved, int n_seq, int total,
+                            int n_pages, int page, int max_pages, int Hq, int Hkv, int d,
+                            attn_dtype dtype, void* stream);
+
+/*
+ * Rows of a 4-bit cache back in 16 bits: the counterpart of attn_append_kv4
+ * for the last cu_seqlens[b+1] - cu_seqlens[b] positions of each sequence (with
+ * cu_seqlens the running sum of kv_lens, the whole cache).
+ *   k, v : [Hkv, total, d] of `dtype`, written, each RN16(m + c s); rows behind
+ *          the last sequence, and rows whose page is none of the cache, are left
+ *          as they were.  Neither overlaps the other or the pages.
+ * 2 Hkv total < 2^31.
+ */
+attn_status attn_read_kv4(const void* k_pages, const void* v_pages, void* k, void* v,
+                          const int32_t* block_table, const int32_t* cu_seqlens,
+                          const int32_t* kv_lens, int n_seq, int total, int n_pages, int page,
+                          int max_pages, int Hkv, int d, attn_dtype dtype, void* stream);
+
+/*
+ * attn_fwd_paged over a 4-bit cache, with the same arguments, workspace
+ * (attn_fwd_paged_workspace_bytes), masking and promises.  Values are what
+ * attn_read_kv4 gives, RN16(m + c s); keys are m + c s, in chunks of more than
+ * 16 query rows a key/value head to 2^-12 of a channel (and to 2^-38 of the largest
+ * channel of the 32 cached positions 32 i .. 32 i + 31).
+ * Cite: as attn_fwd_paged, and "8.3 FlashAttention-3", section 5.1.
+ */
+attn_status attn_fwd_paged4(const void* q, const void* k_pages, const void* v_pages, void* o,
+                            float* lse, const int32_t* block_table, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, void* workspace, size_t workspace_bytes,
+                            int n_seq, int max_q, int total, int n_pages, int page, int max_pages,
+                            int Hq, int Hkv, int d, int causal, float scale, attn_dtype dtype,
+                            void* stream);
+
+/*
  * Backward pass that allocates nothing (no counterpart on the pages: it is a
  * library convenience, not part of the method).
  *
