@@ -24,7 +24,8 @@ import torch
 
 __all__ = ["AttnError", "lib", "lib_path", "fwd", "fwd_split", "fwd_kv", "merge", "bwd", "fwd_varlen",
            "bwd_varlen", "bwd_workspace_bytes", "rope_table", "rope", "rope_bwd", "append_kv", "fwd_paged",
-           "fwd_paged_workspace_bytes", "append_kv4", "read_kv4", "fwd_paged4", "quantize_fp8", "fwd_fp8", "poll_status", "set_wait_limit_us",
+           "fwd_paged_workspace_bytes", "append_kv4", "read_kv4", "fwd_paged4", "kv_weights",
+           "evict_kv", "quantize_fp8", "fwd_fp8", "poll_status", "set_wait_limit_us",
            "selftest_wait_timeout", "num_sms", "STATUS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -77,6 +78,8 @@ def lib() -> ctypes.CDLL:
         "attn_append_kv4": ([vp] * 11 + [i, vp] + [i] * 11 + [vp], i),
         "attn_read_kv4": ([vp] * 7 + [i] * 8 + [vp], i),
         "attn_fwd_paged4": ([vp] * 9 + [sz] + [i] * 10 + [f, i, vp], i),
+        "attn_kv_weights": ([vp] * 7 + [i] * 11 + [f, i, vp], i),
+        "attn_evict_kv": ([vp] * 7 + [i] * 10 + [vp], i),
         "attn_quantize_fp8": ([vp, vp, vp, i, i, i, i, i, vp, i, vp], i),
         "attn_fwd_fp8": ([vp] * 8 + [i, i, i, i, i, f, vp], i),
         "attn_poll_device_status": ([vp, u32p], i),
@@ -113,7 +116,8 @@ def _binding():
         L = lib()
         mod.init(AttnError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "attn_rope", "attn_append_kv", "attn_fwd_paged", "attn_fwd_paged_workspace_bytes",
-            "attn_append_kv4", "attn_read_kv4", "attn_fwd_paged4")))
+            "attn_append_kv4", "attn_read_kv4", "attn_fwd_paged4", "attn_kv_weights",
+            "attn_evict_kv")))
         _bind = mod
     return _bind
 
@@ -602,6 +606,46 @@ def fwd_paged4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     Arguments, masking and workspace (fwd_paged_workspace_bytes) as there."""
     return _binding().fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, max_q,
                                 causal, scale, out, lse, workspace, True)
+
+
+def kv_weights(q: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor,
+               cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, lse: torch.Tensor,
+               weights: torch.Tensor, max_q: int, causal: bool = False,
+               scale: Optional[float] = None) -> torch.Tensor:
+    """Adds the attention weights of a call's rows to those of the cached
+    positions: weights float32 [n_pages,Hkv,page], in place (and returned).
+    Position j of a sequence and key/value head gets the sum of
+    exp(scale q_i . k_j - lse_i) over the sequence's rows i and the head's query
+    heads, on top of what it had; the positions of the call's own rows (the
+    last ones) start from 0.
+
+    q [Hq,total,d], packed by cu_seqlens, and lse [Hq,total] as fwd_paged (or
+    fwd_paged4) took and gave them, or the last rows of prompts alone with their
+    lse; k_pages a cache in 16 bits or in 4 (uint8).  Sequences without rows and
+    positions past a length are left as they were.  Sequences of one call that
+    share a page leave there the weights of either."""
+    return _binding().kv_weights(q, k_pages, block_table, cu_seqlens, kv_lens, lse, weights, max_q,
+                                 causal, scale)
+
+
+def evict_kv(k_pages: torch.Tensor, v_pages: torch.Tensor, weights: torch.Tensor,
+             block_table: torch.Tensor, kv_lens: torch.Tensor, budget: int, sinks: int = 0,
+             recent: int = 0, kept: Optional[torch.Tensor] = None,
+             new_lens: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Cuts every sequence of a paged cache (16 bits, or 4 in uint8) to at most
+    budget positions, head by head: the first sinks stay, the last recent, and of
+    those between the heaviest by weights (see kv_weights; of equal ones the
+    lowest positions, a NaN the heaviest).  They move to positions 0..budget-1
+    in order, rows of k_pages, v_pages and weights, in place; the rows behind
+    stay as they were.  Returns kept int32 [n_seq,Hkv,budget], the positions
+    that stay (-1 behind the last), and new_lens int32 [n_seq], the lengths
+    to go on with: min(kv_lens, budget); it must not be kv_lens itself.
+
+    Afterwards a row's place says nothing of its position in the text: give
+    append_kv positions of its own.  Pages past the new lengths are free for
+    other sequences; a page that two sequences share must not be evicted from."""
+    return _binding().evict_kv(k_pages, v_pages, weights, block_table, kv_lens, budget, sinks,
+                               recent, kept, new_lens)
 
 
 def num_sms() -> int:

@@ -16,8 +16,10 @@
 #include "decode.cuh"
 #include "fp8.cuh"
 #include "fwd.cuh"
+#include "kv4.cuh"
 #include "merge.cuh"
 #include "paged.cuh"
+#include "retain.cuh"
 #include "rotary.cuh"
 #include "sm103_ptx.cuh"
 
@@ -523,6 +525,39 @@ struct PagedPlan {
   }
 };
 
+// The batch of the calls that attend over a paged cache.
+PagedParams paged_params(const DeviceInfo* di, const int32_t* block_table,
+                         const int32_t* cu_seqlens, const int32_t* kv_lens, int n_seq, int max_q,
+                         int total, int n_pages, int page, int max_pages, int Hq, int Hkv,
+                         int causal, float scale) {
+  PagedParams p = {};
+  p.status = di->status;
+  p.block_table = block_table;
+  p.cu_seqlens = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.n_seq = n_seq;
+  p.total = total;
+  p.max_q = max_q;
+  p.n_pages = n_pages;
+  p.page = page;
+  p.page_log2 = log2_of(page);
+  p.max_pages = max_pages;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.causal = causal;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  return p;
+}
+
+// Whether the cost of the largest batch of these sizes, in keys and tiles of
+// rows, stays in 63 bits.
+bool paged_cost_ok(int n_seq, int total, int page, int max_pages, int group, int Hkv) {
+  const int64_t keys = 4 * ((int64_t)max_pages * page + 1024);
+  const int64_t items = (((int64_t)total * group) / 64 + n_seq) * Hkv;
+  return keys <= INT64_MAX / items;
+}
+
 PackedBatch packed_batch(const DeviceInfo* di, const int32_t* block_table,
                          const int32_t* cu_seqlens, const int32_t* kv_lens, int n_seq,
                          int max_pages, int n_pages, int page, int total) {
@@ -615,27 +650,13 @@ attn_status paged_call(const void* q, const void* k_pages, const void* v_pages, 
       dtype == ATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   PagedLaunch a;
   PagedParams& p = a.params;
+  p = paged_params(di, block_table, cu_seqlens, kv_lens, n_seq, max_q, total, n_pages, page,
+                   max_pages, Hq, Hkv, causal, scale);
   p.q = q;
   p.k4 = static_cast<const uint8_t*>(k_pages);
   p.v4 = static_cast<const uint8_t*>(v_pages);
   p.o = o;
   p.lse = lse;
-  p.status = di->status;
-  p.block_table = block_table;
-  p.cu_seqlens = cu_seqlens;
-  p.kv_lens = kv_lens;
-  p.n_seq = n_seq;
-  p.total = total;
-  p.max_q = max_q;
-  p.n_pages = n_pages;
-  p.page = page;
-  p.page_log2 = log2_of(page);
-  p.max_pages = max_pages;
-  p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.causal = causal;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.wait_limit_ns = g_wait_limit_ns.load();
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.desc = reinterpret_cast<int4*>(w);
   p.part_ml = reinterpret_cast<float*>(w + plan.ml);
@@ -646,10 +667,7 @@ attn_status paged_call(const void* q, const void* k_pages, const void* v_pages, 
   p.cluster = plan.cluster;
   a.grid = plan.cluster ? n_seq * Hkv * plan.cluster : (decode ? 2 * sms : sms);
   a.stream = static_cast<cudaStream_t>(stream);
-  // the cost of the largest batch of these sizes stays in 63 bits
-  const int64_t keys = 4 * ((int64_t)max_pages * page + 1024);
-  const int64_t items = (((int64_t)total * p.G) / 64 + n_seq) * Hkv;
-  if (keys > INT64_MAX / items) return ATTN_ERR_INVALID_ARG;
+  if (!paged_cost_ok(n_seq, total, page, max_pages, p.G, Hkv)) return ATTN_ERR_INVALID_ARG;
   const int64_t heads = (int64_t)n_pages * Hkv;
   const int box = decode ? kPagedBlock : (page < 128 ? page : 128);
   if (!kv4 && (!encode_3d(&a.tmK, k_pages, dt, 2, d, page, heads, 64, box) ||
@@ -803,6 +821,85 @@ attn_status attn_fwd_paged4(const void* q, const void* k_pages, const void* v_pa
   return paged_call(q, k_pages, v_pages, o, lse, block_table, cu_seqlens, kv_lens, workspace,
                     workspace_bytes, n_seq, max_q, total, n_pages, page, max_pages, Hq, Hkv, d,
                     causal, scale, dtype, stream, true);
+}
+
+attn_status attn_kv_weights(const void* q, const void* k_pages, const float* lse, float* weights,
+                            const int32_t* block_table, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, int n_seq, int max_q, int total, int n_pages,
+                            int page, int max_pages, int Hq, int Hkv, int d, int bits, int causal,
+                            float scale, attn_dtype dtype, void* stream) {
+  if (!aligned16(q) || !aligned16(lse) || !aligned16(weights)) return ATTN_ERR_INVALID_ARG;
+  if ((causal & ~1) || (bits != 4 && bits != 16) || !dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (weights == lse || weights == q || weights == k_pages) return ATTN_ERR_INVALID_ARG;
+  attn_status st = paged_args(k_pages, k_pages, block_table, cu_seqlens, kv_lens, n_seq, total,
+                              n_pages, page, max_pages, Hq, Hkv);
+  if (st != ATTN_OK) return st;
+  if (max_q < 1 || max_q > total) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 96 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (Hq / Hkv > kPagedMaxGroup) return ATTN_ERR_UNSUPPORTED;
+  if (!paged_cost_ok(n_seq, total, page, max_pages, Hq / Hkv, Hkv)) return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != ATTN_OK) return st;
+  WeightsLaunch a;
+  PagedParams& p = a.params.paged;
+  p = paged_params(di, block_table, cu_seqlens, kv_lens, n_seq, max_q, total, n_pages, page,
+                   max_pages, Hq, Hkv, causal, scale);
+  p.q = q;
+  p.k4 = static_cast<const uint8_t*>(k_pages);
+  p.lse = const_cast<float*>(lse);  // read
+  a.params.k_pages = k_pages;
+  a.params.weights = weights;
+  a.grid = 2 * di->num_sms;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(launch_kv_weights(a, d, dtype == ATTN_BF16, bits == 4));
+}
+
+attn_status attn_evict_kv(void* k_pages, void* v_pages, float* weights, const int32_t* block_table,
+                          const int32_t* kv_lens, int32_t* kept, int32_t* new_lens, int n_seq,
+                          int n_pages, int page, int max_pages, int Hkv, int d, int bits,
+                          int budget, int sinks, int recent, void* stream) {
+  if (!aligned16(weights) || !aligned(kept, 4) || !aligned(new_lens, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (bits != 4 && bits != 16) return ATTN_ERR_INVALID_ARG;
+  if (k_pages == v_pages || weights == k_pages || weights == v_pages || new_lens == kv_lens ||
+      kept == kv_lens || kept == new_lens || kept == block_table || new_lens == block_table)
+    return ATTN_ERR_INVALID_ARG;
+  attn_status st = paged_args(k_pages, v_pages, block_table, kv_lens, kv_lens, n_seq, 1, n_pages,
+                              page, max_pages, Hkv, Hkv);
+  if (st != ATTN_OK) return st;
+  if (bits == 4 ? (d != 64 && d != 96 && d != 128) : !head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
+  if (budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+    return ATTN_ERR_INVALID_ARG;
+  if ((int64_t)n_seq * Hkv > 0x7FFFFFFF / kEvictCluster) return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  st = device_info(&di);
+  if (st != ATTN_OK) return st;
+  EvictLaunch a;
+  EvictParams& p = a.params;
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  p.weights = weights;
+  p.block_table = block_table;
+  p.kv_lens = kv_lens;
+  p.kept = kept;
+  p.new_lens = new_lens;
+  p.status = di->status;
+  p.n_seq = n_seq;
+  p.n_pages = n_pages;
+  p.page_log2 = log2_of(page);
+  p.max_pages = max_pages;
+  p.Hkv = Hkv;
+  p.budget = budget;
+  p.sinks = sinks;
+  p.recent = recent;
+  a.row_bytes = bits == 4 ? kv4_row(d) : 2 * d;
+  // as many CTAs an item as are resident together, two per SM
+  a.cluster = kEvictCluster;
+  while (a.cluster > 1 && (int64_t)n_seq * Hkv * a.cluster > 2 * di->num_sms) a.cluster >>= 1;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return launch_result(launch_evict(a));
 }
 
 }  // extern "C"

@@ -32,6 +32,8 @@ decltype(&attn_fwd_paged) p_paged = nullptr;
 decltype(&attn_append_kv4) p_append4 = nullptr;
 decltype(&attn_read_kv4) p_read4 = nullptr;
 decltype(&attn_fwd_paged4) p_paged4 = nullptr;
+decltype(&attn_kv_weights) p_weights = nullptr;
+decltype(&attn_evict_kv) p_evict = nullptr;
 decltype(&attn_fwd_paged_workspace_bytes) p_paged_bytes = nullptr;
 PyObject* g_error = nullptr;  // the package's AttnError
 
@@ -378,6 +380,97 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Weights of a cache's positions.
+at::Tensor weights_of(PyObject* o, const at::Tensor& pages) {
+  const at::Tensor w = required(o, "weights");
+  need(w.scalar_type() == at::kFloat && w.device() == pages.device() && w.is_contiguous() &&
+           w.dim() == 3 && w.size(0) == pages.size(0) && w.size(1) == pages.size(1) &&
+           w.size(2) == pages.size(2),
+       "weights must be a contiguous float32 [n_pages, Hkv, page] tensor on the pages' device");
+  return w;
+}
+
+// kv_weights(q, k_pages, block_table, cu_seqlens, kv_lens, lse, weights, max_q, causal,
+//            scale) -> weights
+PyObject* kv_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 10);
+  const at::Tensor q = required(a[0], "q"), pages = required(a[1], "k_pages");
+  const bool kv4 = pages.scalar_type() == at::kByte;
+  PyObject* const batch[5] = {a[1], a[1], a[2], a[3], a[4]};
+  const Paged c(batch, q, kv4);
+  const at::Tensor lse = required(a[5], "lse"), w = weights_of(a[6], pages);
+  const int max_q = integer(a[7], "max_q");
+  const int64_t H = q.size(0), total = q.size(1), d = q.size(2), Hkv = pages.size(1);
+  need(q.is_contiguous(), "q must be contiguous [Hq, total, d]");
+  need(Hkv >= 1 && H >= 1 && H % Hkv == 0,
+       "the number of key/value heads must divide the query heads");
+  need(max_q >= 1 && max_q <= total, "max_q must lie in [1, total]");
+  need(lse.dim() == 2 && lse.size(0) == H && lse.size(1) == total &&
+           lse.scalar_type() == at::kFloat && lse.device() == q.device() && lse.is_contiguous(),
+       "lse must be a contiguous float32 [Hq, total] tensor on q's device");
+  double scale = 1.0 / std::sqrt((double)d);
+  if (a[9] != Py_None) {
+    scale = PyFloat_AsDouble(a[9]);
+    if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+  }
+  c10::cuda::CUDAGuard guard(q.device());
+  check(p_weights(ptr(q), ptr(pages), ptr_as<float>(lse), ptr_as<float>(w),
+                  ptr_as<int32_t>(c.blocks), ptr_as<int32_t>(c.cu), ptr_as<int32_t>(c.kv),
+                  size(c.kv.size(0)), max_q, size(total), size(pages.size(0)),
+                  size(pages.size(2)), size(c.blocks.size(1)), size(H), size(Hkv), size(d),
+                  kv4 ? 4 : 16, truth(a[8]), (float)scale, dtype_of(q), stream_of(q)),
+        "attn_kv_weights");
+  return THPVariable_Wrap(w);
+  END_HANDLE_TH_ERRORS
+}
+
+// evict_kv(k_pages, v_pages, weights, block_table, kv_lens, budget, sinks, recent, kept,
+//          new_lens) -> (kept, new_lens)
+PyObject* evict_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 10);
+  const at::Tensor k = required(a[0], "k_pages"), v = required(a[1], "v_pages");
+  const at::Tensor blocks = required(a[3], "block_table"), kv = required(a[4], "kv_lens");
+  const bool kv4 = k.scalar_type() == at::kByte;
+  if (!kv4) dtype_of(k);
+  need(k.is_cuda() && like(v, k) && k.dim() == 4 && k.sizes() == v.sizes() &&
+           k.is_contiguous() && v.is_contiguous() && k.numel() > 0,
+       "k_pages, v_pages must be contiguous CUDA tensors [n_pages, Hkv, page, d], or uint8 "
+       "[n_pages, Hkv, page, 5 d / 8], on one device");
+  need(!kv4 || k.size(3) % 20 == 0, "rows of a 4-bit cache have 5 d / 8 bytes");
+  const at::Tensor w = weights_of(a[2], k);
+  need(kv.dim() == 1 && kv.size(0) >= 1 && blocks.dim() == 2 && blocks.size(0) == kv.size(0) &&
+           ints_on(blocks, at::kInt, k) && ints_on(kv, at::kInt, k),
+       "block_table [n_seq, max_pages] and kv_lens [n_seq] must be contiguous int32 tensors on the "
+       "pages' device");
+  const int budget = integer(a[5], "budget"), sinks = integer(a[6], "sinks");
+  const int recent = integer(a[7], "recent");
+  need(budget >= 1 && sinks >= 0 && recent >= 0 && (int64_t)sinks + recent <= budget,
+       "budget must be positive and hold sinks and recent");
+  at::Tensor kept = tensor(a[8], "kept"), lens = tensor(a[9], "new_lens");
+  c10::cuda::CUDAGuard guard(k.device());
+  if (!kept.defined()) kept = at::empty({kv.size(0), k.size(1), budget}, kv.options());
+  if (!lens.defined()) lens = at::empty({kv.size(0)}, kv.options());
+  need(kept.dim() == 3 && kept.size(0) == kv.size(0) && kept.size(1) == k.size(1) &&
+           kept.size(2) == budget && ints_on(kept, at::kInt, k),
+       "kept must be a contiguous int32 [n_seq, Hkv, budget] tensor on the pages' device");
+  need(lens.dim() == 1 && lens.size(0) == kv.size(0) && ints_on(lens, at::kInt, k),
+       "new_lens must be a contiguous int32 [n_seq] tensor on the pages' device");
+  check(p_evict(ptr(k), ptr(v), ptr_as<float>(w), ptr_as<int32_t>(blocks), ptr_as<int32_t>(kv),
+                ptr_as<int32_t>(kept), ptr_as<int32_t>(lens), size(kv.size(0)), size(k.size(0)),
+                size(k.size(2)), size(blocks.size(1)), size(k.size(1)),
+                size(kv4 ? k.size(3) / 5 * 8 : k.size(3)), kv4 ? 4 : 16, budget, sinks, recent,
+                stream_of(k)),
+        "attn_evict_kv");
+  PyObject* pair = PyTuple_New(2);
+  if (pair == nullptr) return nullptr;
+  PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(kept));
+  PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(lens));
+  return pair;
+  END_HANDLE_TH_ERRORS
+}
+
 template <typename F>
 void take(F& to, PyObject* address) {
   void* f = PyLong_AsVoidPtr(address);
@@ -386,10 +479,11 @@ void take(F& to, PyObject* address) {
 }
 
 // init(AttnError, addresses of attn_rope, attn_append_kv, attn_fwd_paged,
-//      attn_fwd_paged_workspace_bytes, attn_append_kv4, attn_read_kv4, attn_fwd_paged4)
+//      attn_fwd_paged_workspace_bytes, attn_append_kv4, attn_read_kv4, attn_fwd_paged4,
+//      attn_kv_weights, attn_evict_kv)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 8);
+  arguments(n, 10);
   take(p_rope, a[1]);
   take(p_append, a[2]);
   take(p_paged, a[3]);
@@ -397,6 +491,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   take(p_append4, a[5]);
   take(p_read4, a[6]);
   take(p_paged4, a[7]);
+  take(p_weights, a[8]);
+  take(p_evict, a[9]);
   Py_INCREF(a[0]);
   Py_XSETREF(g_error, a[0]);
   Py_RETURN_NONE;
@@ -410,6 +506,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<rope>("rope"), method<append_kv>("append_kv"),
                            method<read_kv4>("read_kv4"), method<fwd_paged>("fwd_paged"),
+                           method<kv_weights>("kv_weights"), method<evict_kv>("evict_kv"),
                            method<init>("init"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods};

@@ -1,0 +1,322 @@
+// Accumulated attention weights of a paged cache's positions: for position j of a
+// sequence and one of its key/value heads
+//   w_j = [j is older than the call's tokens] w_j + sum over the sequence's new
+//         rows i and the head's query heads of exp(scale q_i k_j - LSE_i).
+//
+// The log-sum-exp is given, so each key is read once and no row waits for another:
+// a warp takes 16 keys and all rows that see them, 8 at a time.  The product is
+//   S^T = K Q^T  (A = 16 keys x 16 channels, B = 8 query rows),
+// keys going from memory straight into the operand's registers (a lane reads 16
+// bytes of keys g and g + 8; the contraction may take the channels in any order), the
+// next block's while this one is multiplied.  The sum over rows stays in the lane
+// that has the key, and four lanes add theirs up at the end: no atomics, the
+// same bits from run to run.
+//
+// Of a cache in 4 bits (kv4.cuh) the product is taken with c - 8, and s and m + 8 s
+// are applied to each group of 32 channels in 32 bits; the queries' sums over a
+// group, which m takes, are a product with ones.
+//
+// Work.  A block of 16 keys costs kRead + its tiles of 8 rows; the blocks of all
+// sequences and heads laid end to end are shared out evenly over the grid, and
+// the warps of a CTA take its blocks in turn.
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "dependent.cuh"
+#include "kv4.cuh"
+#include "mma16.cuh"
+#include "paged.cuh"
+#include "retain.cuh"
+#include "sm103_ptx.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = 16;  // of a block: never past the end of a page
+constexpr int kRead = 3;   // cost of reading a block, in tiles of 8 rows
+
+// A sequence's part of the line.
+struct Line {
+  PagedSeq sq;
+  int blocks, cost;  // key blocks of a head, cost of each
+  __device__ __forceinline__ Line(const PagedParams& p, int b) : sq(paged_seq(p, b)) {
+    blocks = sq.qlen > 0 ? (sq.klen + kKeys - 1) / kKeys : 0;
+    cost = kRead + (int)(((long long)sq.qlen * p.G + 7) / 8);
+  }
+  __device__ __forceinline__ long long head() const { return (long long)blocks * cost; }
+};
+
+// The CTA's share [begin, end) of the line, the first sequence of it and where
+// that one begins.
+struct Share {
+  long long begin, end, at;
+  int b;
+};
+
+__device__ __forceinline__ Share find_share(const PagedParams& p) {
+  __shared__ long long warp_sum[kWarps];
+  __shared__ Share share;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (p.n_seq + kThreads - 1) / kThreads;
+  const int b0 = min(tid * run, p.n_seq), b1 = min(b0 + run, p.n_seq);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    sum += Line(p, b).head() * p.Hkv;
+    if (blockIdx.x == 0) paged_check(p, b);
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += up;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  if (tid == 0) share = {0, 0, 0, 0};
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    all += warp_sum[w];
+  }
+  const long long part = (all + gridDim.x - 1) / gridDim.x;
+  const long long s = part * blockIdx.x;
+  long long at = before + incl - sum;
+  if (s < all && s >= at && s < at + sum) {
+    int b = b0;
+    for (;; ++b) {
+      const long long line = Line(p, b).head() * p.Hkv;
+      if (s < at + line) break;
+      at += line;
+    }
+    share = {s, min(s + part, all), at, b};
+  }
+  __syncthreads();
+  return share;
+}
+
+// A block's keys as operand A: register pairs of row g (h = 0) and g + 8.
+template <int D, bool KV4>
+struct Keys {
+  static constexpr int C = D / 32;
+  uint4 x[2][KV4 ? 1 : C];     // 16 bits: channels 32 c + 8 t ..
+  uint32_t code[2][KV4 ? C : 1], par[2][KV4 ? C : 1];
+  float old[2];                // the weights so far
+  size_t slot;                 // of the block's first key in weights; valid only
+  bool valid;
+
+  // page: of the block, key0: its first key
+  template <typename Params>
+  __device__ __forceinline__ void load(const Params& a, int page, int head, int key0, int g,
+                                       int t) {
+    const PagedParams& p = a.paged;
+    valid = page >= 0 && page < p.n_pages;
+    if (!valid) return;
+    slot = (((size_t)page * p.Hkv + head) << p.page_log2) + (key0 & (p.page - 1));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const size_t row = slot + g + 8 * h;
+      if constexpr (KV4) {
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(p.k4 + row * kv4_row(D));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          code[h][c] = __ldg(k + 4 * c + t);
+          par[h][c] = __ldg(k + D / 8 + c);
+        }
+      } else {
+        const uint4* k = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(a.k_pages) + row * D);
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[h][c] = __ldg(k + 4 * c + t);
+      }
+      old[h] = a.weights[row];
+    }
+  }
+};
+
+template <int D, bool BF16, bool KV4>
+__global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsParams a) {
+  constexpr int C = D / 32;
+  const PagedParams& p = a.paged;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  grid_wait();
+  const Share share = find_share(p);
+  const int step_i = 8 / p.G, step_h = 8 % p.G;  // tokens and heads between tiles
+  constexpr uint32_t kOnes = BF16 ? 0x3F803F80u : 0x3C003C00u;
+  const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
+
+  long long at = share.at;  // where sequence b begins
+  for (int b = share.b; at < share.end; ++b) {
+    const Line line(p, b);
+    const PagedSeq sq = line.sq;
+    const long long whole = line.head();
+    const int rows = sq.qlen * p.G;
+    for (int head = 0; head < p.Hkv && whole > 0; ++head, at += whole) {
+      if (at + whole <= share.begin || at >= share.end) continue;
+      // blocks whose first unit of cost lies in the share
+      const int u0 = (int)((max(share.begin - at, 0LL) + line.cost - 1) / line.cost);
+      const int u1 = (int)((min(share.end - at, whole) + line.cost - 1) / line.cost);
+      auto page_of = [&](int u) {
+        return u < u1 ? __ldg(p.block_table + (size_t)b * p.max_pages +
+                              (u * kKeys >> p.page_log2))
+                      : -2;
+      };
+      auto get = [&](Keys<D, KV4>& k, int page, int u) {
+        k.load(a, page, head, u * kKeys, g, t);
+        if (!k.valid && page != -2 && lane == 0)
+          atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(b, 0xFFFF) << 16));
+      };
+      int u = u0 + warp;
+      Keys<D, KV4> k;
+      get(k, page_of(u), u);
+      int page = page_of(u + kWarps);
+      // Queries of a tile: rows 8 n + g; and of rows 8 n + 2 t and the next the
+      // log-sum-exp and the last key seen.
+      uint4 q[C];
+      float qsum[C][2], lse[2];
+      int lim[2];
+      int qi, qh, ri[2], rh[2];  // token and head of those rows
+      auto first_tile = [&]() {
+        qi = g / p.G, qh = g - qi * p.G;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ri[e] = (2 * t + e) / p.G, rh[e] = 2 * t + e - ri[e] * p.G;
+      };
+      auto next = [&](int& i, int& h) {
+        i += step_i;
+        h += step_h;
+        if (h >= p.G) h -= p.G, ++i;
+      };
+      auto load_tile = [&]() {
+#pragma unroll
+        for (int c = 0; c < C; ++c) q[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (qi < sq.qlen) {
+          const uint4* x = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(p.q) +
+              ((size_t)(head * p.G + qh) * p.total + sq.s0 + qi) * D);
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            q[c] = __ldg(x + 4 * c + t);
+            if constexpr (KV4) {  // channel pairs (i, i + 4), as the codes have them
+              const uint4 y = q[c];
+              q[c] = make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632),
+                                __byte_perm(y.y, y.w, 0x5410), __byte_perm(y.y, y.w, 0x7632));
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool live = ri[e] < sq.qlen;
+          lim[e] = !live ? -1 : min(p.causal ? ri[e] + sq.klen - sq.qlen : sq.klen, sq.klen - 1);
+          lse[e] = !live ? 0.f
+                         : 1.4426950408889634f *
+                               __ldg(p.lse + (size_t)(head * p.G + rh[e]) * p.total + sq.s0 + ri[e]);
+        }
+        if constexpr (KV4) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816<BF16>(y, ones, q[c].x, q[c].y);
+            mma16816<BF16>(y, ones, q[c].z, q[c].w);
+            qsum[c][0] = y[0];
+            qsum[c][1] = y[1];
+          }
+        }
+      };
+      first_tile();
+      if (rows <= 8) load_tile();
+
+      for (; u < u1; u += kWarps) {
+        const Keys<D, KV4> cur = k;
+        get(k, page, u + kWarps);
+        page = page_of(u + 2 * kWarps);
+        if (!cur.valid) continue;
+        const int key0 = u * kKeys;
+        // 4 bits: the codes less 8 in 16, and s, m + 8 s
+        uint32_t v[KV4 ? C : 1][2][4];
+        float2 par[KV4 ? C : 1][2];
+        if constexpr (KV4) {
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              par[c][h] = unpack2<BF16>(cur.par[h][c]);
+              par[c][h].y = fmaf(8.f, par[c][h].x, par[c][h].y);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[c][h][i] = kv4_codes<BF16, 8>(cur.code[h][c] >> (4 * i));
+            }
+        }
+        float sum[2] = {0.f, 0.f};
+        if (rows > 8) first_tile();
+        for (int r = 0; r < rows; r += 8) {
+          if (rows > 8) load_tile();
+          float x[4] = {0.f, 0.f, 0.f, 0.f};  // key g + 8 (e / 2), row 2 t + e % 2 of the tile
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            if constexpr (KV4) {
+              const uint32_t a0[4] = {v[c][0][0], v[c][1][0], v[c][0][1], v[c][1][1]};
+              const uint32_t a1[4] = {v[c][0][2], v[c][1][2], v[c][0][3], v[c][1][3]};
+              float y[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<BF16>(y, a0, q[c].x, q[c].y);
+              mma16816<BF16>(y, a1, q[c].z, q[c].w);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[e] = fmaf(par[c][e >> 1].y, qsum[c][e & 1], fmaf(par[c][e >> 1].x, y[e], x[e]));
+            } else {
+              const uint32_t a0[4] = {cur.x[0][c].x, cur.x[1][c].x, cur.x[0][c].y, cur.x[1][c].y};
+              const uint32_t a1[4] = {cur.x[0][c].z, cur.x[1][c].z, cur.x[0][c].w, cur.x[1][c].w};
+              mma16816<BF16>(x, a0, q[c].x, q[c].y);
+              mma16816<BF16>(x, a1, q[c].z, q[c].w);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float w = ex2_approx(fmaf(x[e], p.scale_log2, -lse[e & 1]));
+            // (a select: an unseen key may hold anything)
+            if (key0 + g + 8 * (e >> 1) <= lim[e & 1]) sum[e >> 1] += w;
+          }
+          if (rows > 8) {
+            next(qi, qh);
+            next(ri[0], rh[0]);
+            next(ri[1], rh[1]);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+          sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+          const int key = key0 + g + 8 * h;
+          if (t == 0 && key < sq.klen)
+            a.weights[cur.slot + g + 8 * h] = key < sq.klen - sq.qlen ? cur.old[h] + sum[h] : sum[h];
+        }
+      }
+    }
+  }
+  grid_release();
+}
+
+template <int D, bool BF16>
+cudaError_t launch_db(const WeightsLaunch& a, bool kv4) {
+  return launch_dependent(kv4 ? kv_weights_kernel<D, BF16, true> : kv_weights_kernel<D, BF16, false>,
+                          dim3((unsigned)a.grid), kThreads, 0, a.stream, a.params);
+}
+
+template <int D>
+cudaError_t launch_d(const WeightsLaunch& a, bool bf16, bool kv4) {
+  return bf16 ? launch_db<D, true>(a, kv4) : launch_db<D, false>(a, kv4);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_weights(const WeightsLaunch& a, int d, bool bf16, bool kv4) {
+  switch (d) {
+    case 64: return launch_d<64>(a, bf16, kv4);
+    case 96: return launch_d<96>(a, bf16, kv4);
+    default: return launch_d<128>(a, bf16, kv4);
+  }
+}
+
+}  // namespace attn

@@ -418,6 +418,56 @@ attn_status attn_fwd_paged4(const void* q, const void* k_pages, const void* v_pa
                             void* stream);
 
 /*
+ * Accumulated attention weights of a paged cache, what an eviction goes by:
+ *   weights : [n_pages, Hkv, page] fp32, read and written: of position j of a
+ *             sequence and key/value head
+ *               w_j = [j < kv_lens[b] - n] w_j + sum exp(scale q_i . k_j - lse_i)
+ *             over the sequence's n rows and the head's query heads.  The call's
+ *             own n positions, the last ones, start from 0.
+ *   q, lse  : [Hq, total, d] and what attn_fwd_paged (attn_fwd_paged4) wrote for
+ *             them, [Hq, total]; or the last rows of a prompt alone with
+ *             their lse, packed by a cu_seqlens of their own.
+ *   k_pages : a cache in 16 bits (bits = 16) or 4 (bits = 4).
+ * Sequences without new rows, and positions behind a length, are left as they
+ * were.  Masking, the other arguments and the device checks are those of
+ * attn_fwd_paged; a row that sees no key adds nothing.  Sums are fp32 and their
+ * order is fixed.  Sequences of one call that share a page leave there the
+ * weights of either.  weights overlaps no input.
+ * Cite: the FlashAttention-2 review, "Methods" (the probabilities are recomputed
+ * from the log-sum-exp) and "Insights" (key/value caches).
+ */
+attn_status attn_kv_weights(const void* q, const void* k_pages, const float* lse, float* weights,
+                            const int32_t* block_table, const int32_t* cu_seqlens,
+                            const int32_t* kv_lens, int n_seq, int max_q, int total, int n_pages,
+                            int page, int max_pages, int Hq, int Hkv, int d, int bits, int causal,
+                            float scale, attn_dtype dtype, void* stream);
+
+/*
+ * Eviction from a paged cache by accumulated weight.  Of each sequence of more
+ * than `budget` positions and each key/value head there stay the first `sinks`,
+ * the last `recent`, and of those between the heaviest budget - sinks - recent
+ * (of equal ones the lowest positions; a NaN weight is the heaviest).  They move
+ * to positions 0 .. budget - 1, in order: rows of k_pages, v_pages and weights.
+ * Shorter sequences stay as they are, and so do the rows behind the budget.
+ *   k_pages, v_pages : [n_pages, Hkv, page, d] in 16 bits (bits = 16; d in {64, 96, 128,
+ *              192, 256}) or [n_pages, Hkv, page, 5 d / 8] bytes (bits = 4; d in {64, 96,
+ *              128}), written in place.
+ *   kept     : [n_seq, Hkv, budget], written: the positions that stay, -1
+ *              behind the last.
+ *   new_lens : [n_seq], written: min(kv_lens[b], budget); not kv_lens itself.
+ *   0 <= sinks, recent; sinks + recent <= budget; 1 <= budget.
+ * Heads keep positions of their own, so that afterwards a row's place says
+ * nothing of its position in the text: keys appended later take `positions`.
+ * Pages of an evicted sequence belong to it alone (shared ones are left with
+ * bytes of either).  Lengths and pages are checked as in attn_append_kv.
+ * Cite: as attn_kv_weights.
+ */
+attn_status attn_evict_kv(void* k_pages, void* v_pages, float* weights, const int32_t* block_table,
+                          const int32_t* kv_lens, int32_t* kept, int32_t* new_lens, int n_seq,
+                          int n_pages, int page, int max_pages, int Hkv, int d, int bits,
+                          int budget, int sinks, int recent, void* stream);
+
+/*
  * Backward pass that allocates nothing (no counterpart on the pages: it is a
  * library convenience, not part of the method).
  *

@@ -5,7 +5,7 @@ reference legs may import this package.  The CUDA library neither imports nor
 links anything here; the two share no code.  See ``oracle/attention.py`` for
 what each function computes, the passages it follows and how it is pinned, and
 ``oracle/paged.py`` for rotary positions and the paged cache, ``oracle/kv4.py``
-for the cache in 4 bits.
+for the cache in 4 bits, ``oracle/retain.py`` for attention weights and eviction.
 """
 from .attention import *  # noqa: F401,F403
 from .attention import __all__ as _attention
@@ -13,5 +13,7 @@ from .kv4 import *  # noqa: F401,F403
 from .kv4 import __all__ as _kv4
 from .paged import *  # noqa: F401,F403
 from .paged import __all__ as _paged
+from .retain import *  # noqa: F401,F403
+from .retain import __all__ as _retain
 
-__all__ = _attention + _kv4 + _paged
+__all__ = _attention + _kv4 + _paged + _retain
