@@ -13,10 +13,11 @@
 //
 // Values take part in products as RN_T(m + c s), one fused multiply-add of two
 // 16-bit values at a time: half a step of T, the error that a 16-bit cache has in
-// the first place.  Keys do not: an error of 2^-9 a channel would show in the
-// log-sum-exp (1e-4 of it in bf16).  The decoding kernel multiplies by the
-// codes, c - 8 being exact in T, and applies s and m to each group's product in 32
-// bits; the tile kernel widens keys to fp16 (2^-12).
+// the first place.  Keys do not: an error of 2^-9 a channel, even of 2^-12, shows in
+// the log-sum-exp of a short sequence.  The codes less 8 have three significant
+// bits, so their product with a query, and with a scale of 8 bits, is exact, and
+//   q . k = sum over groups of  sum q (c - 8) s  +  (m + 8 s) sum q,
+// the second part in 32 bits or split into 16-bit terms.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -66,12 +67,13 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
     return __half22float2(*reinterpret_cast<const __half2*>(&x));
 }
 
-// 2^k that takes the finite number of bits `top` (>= 0) to 2^14 .. 2^15, where fp16
-// has 28 binades of full precision below it, and 2^-k.  Both are normal numbers;
-// zero is left where it is.
+// 2^k that takes the finite number of bits `top` (>= 0) to 2^T .. 2^(T + 1), and 2^-k.
+// Both are normal numbers; zero is left where it is.  (fp16 has full precision down
+// to 2^-14 and steps of 2^-24 below.)
+template <int T>
 __device__ __forceinline__ float2 to_fp16_range(uint32_t top) {
-  const uint32_t e = top == 0u ? 127u + 14u : top >> 23;
-  const uint32_t up = min(268u - e, 253u);
+  const uint32_t e = top == 0u ? 127u + T : top >> 23;
+  const uint32_t up = min(254u + T - e, 253u);
   return make_float2(__uint_as_float(up << 23), __uint_as_float((254u - up) << 23));
 }
 
@@ -88,6 +90,16 @@ __device__ __forceinline__ uint4 kv4_word(uint32_t w, uint32_t par) {
   uint32_t v[4];  // channels i and i + 4
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = kv4_values<BF16>(w >> (4 * i), s, m);
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+
+// The eight codes of a word less 8, times the two s in fp16, in channel order.
+__device__ __forceinline__ uint4 kv4_scaled_word(uint32_t w, uint32_t s) {
+  uint32_t v[4];  // channels i and i + 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(kv4_codes<false, 8>(w >> (4 * i))), "r"(s));
   return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
                     __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }

@@ -19,11 +19,15 @@
 // to registers, and stores the widened row where TMA would have put it.  The rest
 // of the pipeline does not differ.  With 16 warps a thread has 128 registers, not the
 // 168 in which a softmax thread holds a row of 128 scores: it holds half, and reads
-// the other half twice, for the maximum and for the exponentials.  Keys widened to
-// bf16 would be off by 2^-9, which shows in the log-sum-exp, so the scores of a bf16
-// cache are a product in fp16 (keys off by 2^-12): the widening warps scale every 32
-// keys, and the softmax threads each their query, by a power of two into fp16's range,
-// and the scores are scaled back where they are scaled anyway.
+// the other half twice, for the maximum and for the exponentials.
+//
+// Keys of a 4-bit cache have more bits than a 16-bit operand (kv4.cuh).  Their
+// scores are a product in fp16 of d + 16 columns: (c - 8) s by the query, exact, and
+// behind them, for each group, m + 8 s by the query's sum over the group, both in two
+// terms (three products).  The scale of an fp16 cache has 11 bits; its upper 8 and
+// its lower 3 make a tile of keys each.  Powers of two bring every 32 keys, and each
+// query, into fp16's range; the scores are scaled back where they are scaled anyway.
+// The softmax threads prepare their queries' rows.
 //
 // Bound, like the dense forward, by the softmax and products of 128-row tiles:
 // a key block of two tiles takes 1.55 to 1.75 us (d = 128; d = 96 1.65), of one
@@ -59,19 +63,25 @@ constexpr int kWarpWiden = 12;  // first of four
 constexpr uint32_t kBarKv = 1, kBarP = 2;  // issuer <-> relay, issuer <-> softmax t
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
 constexpr int kRows = kPagedTileRows;
-constexpr int kStageBytes = 32 * 128;      // a softmax warp's rows on their way out
+constexpr int kExtraBytes = 128 * 32;      // 16 columns more of a tile (KV4)
 
-template <int D>
+template <int D, bool KV4>
 struct PagedTileLayout {
   static constexpr int kTileBytes = 128 * kPaddedD<D> * 2;
   static constexpr int kSlots = D == 64 ? 8 : 4;  // K/V ring
   static constexpr int kQOff = 0;
   static constexpr int kKvOff = 2 * kTileBytes;
-  static constexpr int kStageOff = kKvOff + kSlots * kTileBytes;
+  static constexpr int kQExtraOff = kKvOff + kSlots * kTileBytes;
+  static constexpr int kExtras = kSlots / 2;      // blocks of the ring at most
+  static constexpr int kKExtraOff = kQExtraOff + (KV4 ? 2 * kExtraBytes : 0);
+  // A softmax warp's rows on their way out, 32 or 64 columns at a time.
+  static constexpr int kStageCols = KV4 ? 1 : 2;
+  static constexpr int kStageBytes = 32 * 64 * kStageCols;
+  static constexpr int kStageOff = kKExtraOff + (KV4 ? kExtras * kExtraBytes : 0);
   static constexpr int kBarOff = kStageOff + 8 * kStageBytes;
   static constexpr int kQFull = 0, kQEmpty = 2, kSFull = 4, kOFull = 6, kDrain = 8;
   static constexpr int kKvFull = 9, kKvEmpty = 9 + kSlots;
-  static constexpr int kQReady = 9 + 2 * kSlots;  // queries of a 4-bit cache, scaled
+  static constexpr int kQReady = 9 + 2 * kSlots;  // queries for a 4-bit cache
   static constexpr int kNumBars = kQReady + 2;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   // Scales of 4 x 32 keys by block of a 4-bit cache.  The widening warps are at
@@ -120,6 +130,21 @@ __device__ __forceinline__ float row_max32(const uint32_t (&s)[32]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// x as the sum of two fp16 numbers (22 bits of it), the first in the low half.
+__device__ __forceinline__ uint32_t two_terms(float x) {
+  const float hi = unpack2<false>(pack_f16x2(x, 0.f)).x;
+  return pack_f16x2(x, x - hi);
+}
+
+// Row `row` of a tile's 16 further columns (32 bytes a row, 32-byte swizzle): columns
+// 0-7, then 8-11; the last four are 0.
+__device__ __forceinline__ void store_extra(uint8_t* extra, int row, uint4 a, uint2 b) {
+  uint4* const x = reinterpret_cast<uint4*>(extra + row * 32);
+  const int swap = row >> 2 & 1;
+  x[swap] = a;
+  x[swap ^ 1] = make_uint4(b.x, b.y, 0u, 0u);
+}
+
 // A row of a 4-bit cache: its code words, then its groups' scales and minima.
 template <int D>
 struct Row4 {
@@ -143,29 +168,51 @@ struct Row4 {
       for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(x) + i);
     }
   }
-  __device__ __forceinline__ uint32_t& param(int c) { return w[D / 8 + c]; }
-  // The bits of the largest finite number that a code of the row can stand for
-  // (of a bf16 cache).
-  __device__ __forceinline__ uint32_t top() {
+  __device__ __forceinline__ uint32_t param(int c) const { return w[D / 8 + c]; }
+  // The bits of the largest finite number that key() has to hold.
+  template <bool BF16>
+  __device__ __forceinline__ uint32_t top() const {
     uint32_t b = 0u;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
-      const float2 par = unpack2<true>(param(c));
-      b = max(b, max(finite_bits(par.y), finite_bits(fmaf(15.f, par.x, par.y))));
+      const float2 par = unpack2<BF16>(param(c));
+      b = max(b, max(finite_bits(8.f * par.x), finite_bits(fmaf(8.f, par.x, par.y))));
     }
     return b;
   }
-  // Scales and minima of a bf16 cache as fp16, times f.
-  __device__ __forceinline__ void to_fp16(float f) {
+  // Row `row` of a tile of keys times f: the codes less 8, times the upper 8 bits of
+  // the scale or what these leave of it (LOW).
+  template <bool BF16, bool LOW>
+  __device__ __forceinline__ void key(uint8_t* tile, int row, float f) const {
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const float2 par = unpack2<true>(param(c));
-      param(c) = pack_f16x2(par.x * f, par.y * f);
+    for (int g = 0; g < D / 32; ++g) {
+      const float s = unpack2<BF16>(param(g)).x * f;
+      const float hi = __uint_as_float(__float_as_uint(s) & 0xFFFF0000u);
+      const uint32_t by = LOW ? pack_f16x2(s - hi, s - hi) : pack_f16x2(hi, hi);
+#pragma unroll
+      for (int c = 4 * g; c < 4 * g + 4; ++c)
+        *reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
+                                  (((c & 7) ^ (row & 7)) << 4)) = kv4_scaled_word(w[c], by);
     }
   }
-  // Widened, as row `row` of a tile in shared memory.
+  // Its columns behind: m + 8 s in two terms, the first of them once more.
   template <bool BF16>
-  __device__ __forceinline__ void widen(uint8_t* tile, int row) {
+  __device__ __forceinline__ void key_extra(uint8_t* extra, int row, float f) const {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < D / 32; ++g) {
+      const float2 par = unpack2<BF16>(param(g));
+      x[g] = fmaf(8.f, par.x, par.y) * f;
+    }
+    uint32_t two[4];  // first and second term
+#pragma unroll
+    for (int g = 0; g < 4; ++g) two[g] = two_terms(x[g]);
+    store_extra(extra, row, make_uint4(two[0], two[1], two[2], two[3]),
+                make_uint2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[2], two[3], 0x5410)));
+  }
+  // Widened values, as row `row` of a tile in shared memory.
+  template <bool BF16>
+  __device__ __forceinline__ void value(uint8_t* tile, int row) const {
 #pragma unroll
     for (int c = 0; c < D / 8; ++c)
       *reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
@@ -174,10 +221,11 @@ struct Row4 {
   }
 };
 
-// Row `row` of a tile of bf16 queries as fp16, scaled into its range: the factor
-// that undoes it.
-template <int D>
-__device__ __forceinline__ float query_to_fp16(uint8_t* tile, int row) {
+// Row `row` of a tile of queries as fp16, scaled into its range with room for sums
+// of 32, and the sums over its groups as the columns behind: the first term twice,
+// the second.  The factor that undoes the scaling.
+template <int D, bool BF16>
+__device__ __forceinline__ float query_row(uint8_t* tile, uint8_t* extra, int row) {
   auto piece = [&](int c) {
     return reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
                                     (((c & 7) ^ (row & 7)) << 4));
@@ -189,23 +237,41 @@ __device__ __forceinline__ float query_to_fp16(uint8_t* tile, int row) {
     const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 v = unpack2<true>(y[i]);
+      const float2 v = unpack2<BF16>(y[i]);
       top = max(top, max(finite_bits(v.x), finite_bits(v.y)));
     }
   }
-  const float2 f = to_fp16_range(top);
+  const float2 f = to_fp16_range<9>(top);
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
     const uint4 x = *piece(c);
     uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 v = unpack2<true>(y[i]);
-      y[i] = pack_f16x2(v.x * f.x, v.y * f.x);
+      float2 v = unpack2<BF16>(y[i]);
+      v.x *= f.x;
+      v.y *= f.x;
+      sum[c / 4] += v.x + v.y;
+      y[i] = pack_f16x2(v.x, v.y);
     }
     *piece(c) = make_uint4(y[0], y[1], y[2], y[3]);
   }
+  uint32_t two[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) two[g] = two_terms(sum[g]);
+  store_extra(extra, row,
+              make_uint4(__byte_perm(two[0], 0u, 0x1010), __byte_perm(two[1], 0u, 0x1010),
+                         __byte_perm(two[2], 0u, 0x1010), __byte_perm(two[3], 0u, 0x1010)),
+              make_uint2(__byte_perm(two[0], two[1], 0x7632), __byte_perm(two[2], two[3], 0x7632)));
   return f.y;
+}
+
+// Descriptor of 16 further columns (store_extra): 8 rows of 32 bytes every 256, the
+// 32-byte swizzle (bit 4 of the address changes with bit 7).
+__device__ __forceinline__ uint64_t extra_desc(uint32_t addr) {
+  constexpr uint64_t kSwizzles = 7ull << 61, kSwizzle32 = 6ull << 61;
+  return (sdesc_sw128(addr, 16, 256) & ~kSwizzles) | kSwizzle32;
 }
 
 template <int D, bool BF16, bool KV4>
@@ -213,9 +279,9 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
-  using L = PagedTileLayout<D>;
+  using L = PagedTileLayout<D, KV4>;
   constexpr int kChunks = kPaddedD<D> / 64;
-  constexpr bool kScaled = KV4 && BF16;  // scores are a product in fp16
+  constexpr int kKeyTiles = KV4 && !BF16 ? 2 : 1;  // tiles of a block's keys
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -369,25 +435,30 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
             atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(w.b, 0xFFFF) << 16));
           return -1;
         };
-        auto put = [&](Row4<D>& x, bool key) {
+        // The next slot of the ring, filled by `write`.
+        auto put = [&](auto write) {
           const uint32_t slot = kv_it % L::kSlots;
           ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvEmpty + slot),
                                                  ((kv_it / L::kSlots) & 1) ^ 1, wd, 78));
           if (!ok) return;
-          uint8_t* const tile = smem + L::kKvOff + slot * L::kTileBytes;
-          if (kScaled && key) {
-            const float2 f = to_fp16_range(__reduce_max_sync(0xffffffffu, x.top()));
-            if (lane == 0)
-              reinterpret_cast<float*>(scales + kv_it / 2 % L::kScales)[row >> 5] = f.y;
-            x.to_fp16(f.x);
-            x.template widen<false>(tile, row);
-          } else {
-            x.template widen<BF16>(tile, row);
-          }
+          write(smem + L::kKvOff + slot * L::kTileBytes);
           fence_proxy_async_smem();  // before the products read it
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kKvFull + slot));
           ++kv_it;
+        };
+        auto put_key = [&](const Row4<D>& x) {
+          const uint32_t block = kv_it / (kKeyTiles + 1);
+          const float2 f =
+              to_fp16_range<14>(__reduce_max_sync(0xffffffffu, x.template top<BF16>()));
+          put([&](uint8_t* tile) {
+            if (lane == 0) reinterpret_cast<float*>(scales + block % L::kScales)[row >> 5] = f.y;
+            x.template key_extra<BF16>(
+                smem + L::kKExtraOff + block % L::kExtras * kExtraBytes, row, f.x);
+            x.template key<BF16, false>(tile, row, f.x);
+          });
+          if (kKeyTiles == 2 && ok)
+            put([&](uint8_t* tile) { x.template key<BF16, true>(tile, row, f.x); });
         };
         // Each row is asked for a block before it is widened, its page two before.
         int64_t at = find(key_page(0), 0);
@@ -398,10 +469,10 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
         for (int j = 0; j < nbmax && ok; ++j) {
           at = find(page, j + 1);
           page = key_page(j + 2);
-          put(k, true);
+          put_key(k);
           k.load(at < 0 ? nullptr : p.k4 + at);
           if (!ok) break;
-          put(v, false);
+          put([&](uint8_t* tile) { v.template value<BF16>(tile, row); });
           v.load(at < 0 ? nullptr : p.v4 + at);
         }
       }
@@ -432,10 +503,10 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           const uint32_t par = q_it[t] & 1;
           ++q_it[t];
           if (aborted) continue;
-          const int full = kScaled ? L::kQReady : L::kQFull;
+          const int full = KV4 ? L::kQReady : L::kQFull;
           aborted = !__all_sync(0xffffffffu, mbar_wait(bar(full + t), par, wd, 72));
         }
-        kv_ready();
+        for (int i = 0; i < kKeyTiles; ++i) kv_ready();
         aborted = named_bar_or(kBarKv, 64, aborted);
         for (int j = 0; j < nbmax; ++j) {
           const uint32_t vslot = kv_ready();
@@ -453,7 +524,7 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
             }
             fence_proxy_async_smem();
           }
-          if (j + 1 < nbmax) kv_ready();
+          for (int i = 0; i < kKeyTiles && j + 1 < nbmax; ++i) kv_ready();
           aborted = named_bar_or(kBarKv, 64, aborted);
         }
       }
@@ -466,14 +537,31 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
       bool issued = false;
       const uint64_t qdesc0 = kmajor_base(sbase + L::kQOff);
       const uint64_t qdesc1 = kmajor_base(sbase + L::kQOff + L::kTileBytes);
-      auto issue_s = [&](int t, uint32_t kaddr) {
-        const uint64_t kd = kmajor_base(kaddr);
+      // S_t of the block whose keys begin in ring slot kslot; its number, for the
+      // columns behind.
+      auto slot_addr = [&](uint32_t slot) {
+        return sbase + L::kKvOff + slot % L::kSlots * L::kTileBytes;
+      };
+      auto issue_s = [&](int t, uint32_t kslot, uint32_t block) {
         const uint64_t qd = t ? qdesc1 : qdesc0;
         const uint32_t dcol = tbase + 128 * t;
-  #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_f16_ss(dcol, desc_plus(qd, kmajor16_off(kk)), desc_plus(kd, kmajor16_off(kk)), kIdS,
-                     kk > 0);
+#pragma unroll
+        for (int n = 0; n < kKeyTiles; ++n) {
+          const uint64_t kd = kmajor_base(slot_addr(kslot + n));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16_ss(dcol, desc_plus(qd, kmajor16_off(kk)), desc_plus(kd, kmajor16_off(kk)),
+                       kIdS, kk > 0 || n > 0);
+        }
+        if constexpr (KV4)
+          mma_f16_ss(dcol, extra_desc(sbase + L::kQExtraOff + t * kExtraBytes),
+                     extra_desc(sbase + L::kKExtraOff + block % L::kExtras * kExtraBytes), kIdS,
+                     1u);
+      };
+      auto free_keys = [&](uint32_t kslot) {
+#pragma unroll
+        for (int n = 0; n < kKeyTiles; ++n)
+          mma_commit(bar(L::kKvEmpty + (kslot + n) % L::kSlots));
       };
       auto issue_pv = [&](int t, uint32_t vaddr, uint32_t acc0) {
         const uint32_t ocol = tbase + 256 + kPaddedD<D> * t;
@@ -490,22 +578,22 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
         if (nbmax == 0) continue;  // the same skip in every role
         aborted = named_bar_or(kBarKv, 64, aborted);
         uint32_t kslot = kv_it % L::kSlots;
-        ++kv_it;
+        uint32_t block = kv_it / (kKeyTiles + 1);
+        kv_it += kKeyTiles;
         if (!aborted) {
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t kaddr = sbase + L::kKvOff + kslot * L::kTileBytes;
             if (nb0 > 0) {
-              issue_s(0, kaddr);
+              issue_s(0, kslot, block);
               mma_commit(bar(L::kSFull + 0));
               if (nb0 == 1) mma_commit(bar(L::kQEmpty + 0));
             }
             if (nb1 > 0) {
-              issue_s(1, kaddr);
+              issue_s(1, kslot, block);
               mma_commit(bar(L::kSFull + 1));
               if (nb1 == 1) mma_commit(bar(L::kQEmpty + 1));
             }
-            mma_commit(bar(L::kKvEmpty + kslot));
+            free_keys(kslot);
           }
           issued = true;
           __syncwarp();
@@ -518,10 +606,10 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           const bool have_next = j + 1 < nbmax;
           if (have_next) {
             kslot = kv_it % L::kSlots;
-            ++kv_it;
+            block = kv_it / (kKeyTiles + 1);
+            kv_it += kKeyTiles;
           }
-          const uint32_t vaddr = sbase + L::kKvOff + vslot * L::kTileBytes;
-          const uint32_t kaddr = sbase + L::kKvOff + kslot * L::kTileBytes;
+          const uint32_t vaddr = slot_addr(vslot);
   #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int nbt = t ? nb1 : nb0;
@@ -534,7 +622,7 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
               issue_pv(t, vaddr, j > 0 ? 1u : 0u);
               if (j == nbt - 1) mma_commit(bar(L::kOFull + t));
               if (j + 1 < nbt) {
-                issue_s(t, kaddr);
+                issue_s(t, kslot, block);
                 mma_commit(bar(L::kSFull + t));
                 if (j + 1 == nbt - 1) mma_commit(bar(L::kQEmpty + t));
               }
@@ -544,7 +632,7 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           if (!aborted) {
             if (lane == 0) {
               mma_commit(bar(L::kKvEmpty + vslot));
-              if (have_next) mma_commit(bar(L::kKvEmpty + kslot));
+              if (have_next) free_keys(kslot);
             }
             __syncwarp();
           }
@@ -601,11 +689,12 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
       const int koff = p.causal ? w.sq.klen - w.sq.qlen : w.sq.klen;
       const int lim = min(token + koff, w.sq.klen - 1);  // last key the row sees
       const int lim0 = min(token - ti + koff, w.sq.klen - 1);  // of the tile's first token
-      if constexpr (kScaled) {
+      if constexpr (KV4) {
         if (!aborted)
           aborted = !__all_sync(0xffffffffu, mbar_wait(bar(L::kQFull + t), o_it & 1, wd, 79));
         if (!aborted) {
-          sl2 = p.scale_log2 * query_to_fp16<D>(smem + L::kQOff + t * L::kTileBytes, r);
+          sl2 = p.scale_log2 * query_row<D, BF16>(smem + L::kQOff + t * L::kTileBytes,
+                                                  smem + L::kQExtraOff + t * kExtraBytes, r);
           fence_proxy_async_smem();  // before the products read it
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kQReady + t));
@@ -641,7 +730,7 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           // What takes chunk c's scores to base 2: 1e-37 .. 1e37, since a masked
           // score times 0 would be NaN (a product that needs more is 0 or inf anyway).
           float to2[4] = {sl2, sl2, sl2, sl2};
-          if constexpr (kScaled) {
+          if constexpr (KV4) {
             const float4 f = scales[(block0 + j) % L::kScales];
             const float by[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
@@ -746,14 +835,19 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
       tc_fence_after();
       if (whole) {
         const float inv_l = paged_inverse(l);
-        // Rows go out through the warp's stage, 64 columns at a time (swizzled
-        // 16-byte pieces), so that a store covers whole 128-byte row pieces:
-        // a lane per row would write 16 bytes of 32 lines.
-        uint8_t* const stage = smem + L::kStageOff + warp * kStageBytes;
+        // Rows go out through the warp's stage, so that a store covers whole row
+        // pieces of 64 or 128 bytes: a lane per row would write 16 bytes of 32
+        // lines.
+        constexpr int kPitch = 64 * L::kStageCols;
+        uint8_t* const stage = smem + L::kStageOff + warp * L::kStageBytes;
+        auto place = [&](int row, int pc) {  // of a 16-byte piece, spread over the banks
+          const int x = kPitch == 128 ? row & 7 : row >> 1 & 3;
+          return reinterpret_cast<uint4*>(stage + row * kPitch + ((pc ^ x) << 4));
+        };
 #pragma unroll
-        for (int c0 = 0; c0 < D / 32; c0 += 2) {
-          constexpr int kPieces = 8;
-          const int pieces = D / 32 - c0 >= 2 ? kPieces : kPieces / 2;  // of a row
+        for (int c0 = 0; c0 < D / 32; c0 += L::kStageCols) {
+          constexpr int kPieces = 4 * L::kStageCols;
+          const int pieces = D / 32 - c0 >= L::kStageCols ? kPieces : kPieces / 2;  // of a row
 #pragma unroll
           for (int c = c0; c < c0 + pieces / 4; ++c) {
             uint32_t raw[32];
@@ -765,17 +859,14 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
               for (int i = 0; i < 4; ++i)
                 pk[i] = pack2<BF16>(__uint_as_float(raw[8 * v + 2 * i]) * inv_l,
                                     __uint_as_float(raw[8 * v + 2 * i + 1]) * inv_l);
-              const int pc = (c - c0) * 4 + v;
-              *reinterpret_cast<uint4*>(stage + lane * 128 + ((pc ^ (lane & 7)) << 4)) =
-                  make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              *place(lane, (c - c0) * 4 + v) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < pieces; ++i) {
             const int row = i * (32 / pieces) + lane / pieces, pc = lane % pieces;
-            const uint4 x =
-                *reinterpret_cast<const uint4*>(stage + row * 128 + ((pc ^ (row & 7)) << 4));
+            const uint4 x = *place(row, pc);
             const int at = __shfl_sync(0xffffffffu, live ? (int)grow : -1, row);
             if (at >= 0)
               *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (size_t)at * D + c0 * 32 +
@@ -814,7 +905,7 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
 
 template <int D, bool BF16, bool KV4>
 cudaError_t launch_dbk(const PagedLaunch& a) {
-  using L = PagedTileLayout<D>;
+  using L = PagedTileLayout<D, KV4>;
   auto kern = paged_tile_kernel<D, BF16, KV4>;
   static DeviceFlags configured;
   cudaError_t e = ensure_dyn_smem(kern, L::kDynSmem, configured);

@@ -2,11 +2,12 @@
 path vs the fp64 oracle.
 
 Attention: the cases are those of the 16-bit cache (test_paged_gpu.py).  Keys are
-the exact m + c s, values that in 16 bits.  A score's error d_j (u = finfo.eps / 2):
+the exact m + c s, values that in 16 bits.  A score's error d_j (u = finfo.eps / 2),
+with M = scale max sum |q| (|m + 8 s| + 8 s):
 * few rows: a group's product with c - 8 sums 32 exact products, and s and m + 8 s are
-  applied in fp32: at most 48 2^-24 of M = scale max sum |q| (|m + 8 s| + 8 s);
-* chunks: keys are rounded to fp16 (2^-12 of each), then d products are summed:
-  (2^-12 + d 2^-24) M with M = scale max sum |q| |k|.
+  applied in fp32: at most 48 2^-24 M;
+* chunks: 2 d exact products and 12 more are summed in fp32, and of m + 8 s and the
+  sum of q two terms of 11 bits are taken each: (2 d + 16) 2^-24 M + 2^-20 M.
 With e = 2^-20 + n 2^-24 + d_j for the exponential and the sums as there,
 |LSE - LSE_ref| <= e + 2^-23 |LSE| and, P_ij being off by d_j and by the row's
 l, |O - O_ref| <= (u + 2 e) A + u |O|.  P may exceed 1 by 2^8, which scales its
@@ -85,11 +86,10 @@ def check4(x, o, lse, causal, scale=None):
     k, v = exact4(x["k4"], dt), unpack4(x["v4"], dt)
     O, L, A, _ = oracle.attention_paged(to64(x["q"]), k.cpu().numpy(), to64(v), x["table"].cpu().numpy(), cu, kv,
                                         causal, scale)
-    if x["max_q"] * (x["q"].shape[0] // k.shape[1]) <= 16:
-        s, m, _ = parts4(x["k4"], dt)
-        err = 48 * 2.0 ** -24 * largest(x, causal, scale, (m + 8 * s).abs() + 8 * s)
-    else:
-        err = (2.0 ** -12 + d * 2.0 ** -24) * largest(x, causal, scale, k.abs())
+    s, m, _ = parts4(x["k4"], dt)
+    few = x["max_q"] * (x["q"].shape[0] // k.shape[1]) <= 16
+    err = (48 * 2.0 ** -24 if few else (2 * d + 16) * 2.0 ** -24 + 2.0 ** -20) * \
+        largest(x, causal, scale, (m + 8 * s).abs() + 8 * s)
     live = slice(0, int(cu[-1]))
     u = torch.finfo(dt).eps / 2
     e = 2.0 ** -20 + int(kv.max()) * 2.0 ** -24 + err
