@@ -662,7 +662,7 @@ attn_status paged_call(const void* q, const void* k_pages, const void* v_pages, 
   p.part_ml = reinterpret_cast<float*>(w + plan.ml);
   p.part_o = reinterpret_cast<float*>(w + plan.o);
   const bool decode = plan.decode;
-  p.min_share = decode ? 128 : 1024;
+  p.min_share = !decode ? kPagedTileShare : (kv4 ? kPaged4Share : kPagedShare);
   const int sms = di->num_sms < kPagedMaxSms ? di->num_sms : kPagedMaxSms;
   p.cluster = plan.cluster;
   a.grid = plan.cluster ? n_seq * Hkv * plan.cluster : (decode ? 2 * sms : sms);

@@ -38,6 +38,9 @@ constexpr int kPagedRows = 16;
 constexpr int kPagedTileRows = 256;
 // Keys of a block of the warp-level kernel (rows of its tensor-map box).
 constexpr int kPagedBlock = 16;
+// Least shares of the three kernels: at least their cost blocks (the warps' key blocks,
+// the tile kernel's 128 keys at their weights).
+constexpr int kPagedShare = 128, kPaged4Share = 192, kPagedTileShare = 1024;
 // CTAs at most that share an item of a small batch on the warp-level kernel.
 constexpr int kPagedCluster = 8;
 // Query heads per key/value head at most.
@@ -59,7 +62,7 @@ struct PagedParams {
   float* part_o;            // [grid][2][rows][D], of the tile kernel [grid][2][D / 4][rows][4]
   int n_seq, total, max_q, n_pages, page, page_log2, max_pages, Hkv, G;
   int causal;               // query i of n sees keys j <= i + kv_len - n
-  int min_share;            // least share, at least one key block
+  int min_share;            // least share
   int cluster;              // CTAs of an item's cluster (decoding kernel; 0: equal shares)
   float scale_log2;         // scale * log2(e)
   unsigned long long wait_limit_ns;

@@ -2,8 +2,8 @@
 // key/value head) over a paged cache held in 4 bits (kv4.cuh).
 //
 // The work is cut and the results meet as in the 16-bit kernel (paged_rows.cuh,
-// paged_decode.cu), and each warp streams its 16-key blocks through a ring, here
-// as two plain bulk copies of 16 rows.  Since a row is 5/8 byte a channel, the
+// paged_decode.cu), and each warp streams its 32-key blocks through a ring, here
+// as plain bulk copies of 16 rows.  Since a row is 5/8 byte a channel, the
 // instructions that widen it are what competes with HBM: a card at full rate
 // hands an SM a block every 111 cycles (d = 128), 444 issue slots for 4096
 // values.  So the product is turned round against the 16-bit kernel's:
@@ -43,23 +43,28 @@ using namespace rows;
 
 namespace {
 
+constexpr int kKeys = 2 * kUnit;  // of a block
+// Warps of a CTA by 8-row tiles: what two CTAs an SM leave registers for.
+template <int NT>
+constexpr int kWarps = NT == 1 ? 6 : 4;
 constexpr float kRaise = 8.f;  // log2 units
 
-template <int D>
+template <int D, int W>
 struct Paged4Layout {
   static constexpr int kRow = kv4_row(D);
-  static constexpr int kHalfBytes = kKeys * kRow;       // a block's K or V
-  static constexpr int kSlotBytes = 2 * kHalfBytes;
-  static constexpr int kSlots = D == 64 ? 16 : (D == 96 ? 12 : 10);  // ring depth of each warp
-  static constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
+  static constexpr int kUnitBytes = kUnit * kRow;   // K or V of 16 keys
+  static constexpr int kSlotBytes = 4 * kUnitBytes;  // K, K, V, V of a block
+  static constexpr int kSlots = 100 * 1024 / (W * kSlotBytes);  // ring depth of each warp
+  static constexpr int kRingBytes = W * kSlots * kSlotBytes;
   static constexpr int kMeetOff = kRingBytes;
-  static constexpr int kMlOff = kMeetOff + kWarps * kMeet * kRowStride<D> * 4;
-  static constexpr int kBarOff = kMlOff + kWarps * kMeet * 8;
-  static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;
+  static constexpr int kMlOff = kMeetOff + W * kMeet * kRowStride<D> * 4;
+  static constexpr int kBarOff = kMlOff + W * kMeet * 8;
+  static constexpr int kFlagOff = kBarOff + W * kSlots * 8;
   static constexpr int kBytes = kFlagOff + 16 + 128;  // + room to align the base
-  static_assert(kHalfBytes % 16 == 0 && kRingBytes % 128 == 0, "bulk copies");
+  static_assert(kUnitBytes % 16 == 0 && kRingBytes % 128 == 0, "bulk copies");
   static_assert(kRingBytes >= kPagedRows * (D * 4 + 8), "a cluster's part lies over the ring");
   static_assert(kBytes + 256 <= 113 * 1024, "two CTAs per SM");
+  static_assert(W * kKeys <= kPaged4Share, "a share holds a cost block");
 };
 
 // Bytes global -> shared (both addresses and the size multiples of 16),
@@ -120,8 +125,9 @@ __device__ __forceinline__ void load_pairs(const uint8_t* a, const uint8_t* b, u
 
 // NT: 8-row tiles of query rows.  CLUSTER as in the 16-bit kernel.
 template <int D, bool BF16, int NT, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 2) paged4_decode_kernel(const PagedParams p) {
-  using L = Paged4Layout<D>;
+__global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const PagedParams p) {
+  constexpr int W = kWarps<NT>;
+  using L = Paged4Layout<D, W>;
   constexpr int KS = D / 16;  // k-steps of S^T, 16-channel tiles of O^T
   constexpr int C = D / 32;   // a lane's words of a key, half words of a value row
   constexpr int NS = L::kSlots;
@@ -137,35 +143,44 @@ __global__ void __launch_bounds__(kThreads, 2) paged4_decode_kernel(const PagedP
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < kWarps * NS; ++i) mbar_init(sbase + L::kBarOff + 8u * i, 1);
+    for (int i = 0; i < W * NS; ++i) mbar_init(sbase + L::kBarOff + 8u * i, 1);
     mbar_fence_init();
   }
   grid_wait();
-  Walk w = start_rows<CLUSTER>(p);
+  Walk<W, kKeys> w = start_rows<W, kKeys, CLUSTER>(p);
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
+  const float raise_by = kRaise / p.scale_log2;
   uint8_t* const ring = smem + warp * NS * L::kSlotBytes;
   const uint32_t ring_addr = smem_u32(ring);
 
   // Block n of the warp's stream lies in slot n % NS; the ring is full until the
   // stream ends, so the slot that is read is the one that is filled next.
-  BlockStream stream(p, w, warp, lane);
+  BlockStream<W, kKeys> stream(p, w, warp, lane);
   uint32_t it = 0;         // blocks taken from the ring
   int slot = 0;            // it % NS
   uint32_t parity = 0;     // (it / NS) & 1
   auto issue = [&](int s) {
-    stream.issue(p, warp, lane, [&](int page, int head, int y) {
-      // a page outside the cache: any of it, reported
-      const size_t row = (((size_t)max(page, 0) * p.Hkv + head) << p.page_log2) + y;
-      const uint32_t dst = ring_addr + (uint32_t)(s * L::kSlotBytes);
-      mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
-      bulk_load(dst, p.k4 + row * L::kRow, L::kHalfBytes, bar(s));
-      bulk_load(dst + L::kHalfBytes, p.v4 + row * L::kRow, L::kHalfBytes, bar(s));
-    });
+    if (!stream.more()) return;
+    // Lanes 0 to 3 copy a unit of K or V each, of a page outside the cache (reported)
+    // any one; what the second unit of a block past the sequence has is not read
+    // but as numbers that count nothing.
+    const int page0 = stream.page(p, 0, lane), page1 = stream.page(p, 1, lane);
+    const int pages = page1 == -2 ? 1 : 2;
+    if (lane == 0) mbar_arrive_expect_tx(bar(s), (uint32_t)(2 * pages * L::kUnitBytes));
+    __syncwarp();
+    const int u = lane & 1;
+    if (lane < 4 && u < pages) {
+      const size_t row = (((size_t)max(u ? page1 : page0, 0) * p.Hkv + stream.ahead.head)
+                          << p.page_log2) + stream.row(p, u, warp);
+      bulk_load(ring_addr + (uint32_t)(s * L::kSlotBytes + lane * L::kUnitBytes),
+                (lane < 2 ? p.k4 : p.v4) + row * L::kRow, L::kUnitBytes, bar(s));
+    }
+    stream.next(p, warp, lane);
   };
   for (int i = 0; i < NS; ++i) issue(i);
 
   float* meet = reinterpret_cast<float*>(smem + L::kMeetOff);
-  float2* meet_ml = reinterpret_cast<float2*>(smem + L::kMlOff);  // [kWarps][kMeet]
+  float2* meet_ml = reinterpret_cast<float2*>(smem + L::kMlOff);  // [W][kMeet]
   // The CTA's part of a cluster's item, over the idle ring: O, (m, l) by row.
   float* part = reinterpret_cast<float*>(smem);
   float2* part_ml = reinterpret_cast<float2*>(smem + kPagedRows * D * 4);
@@ -214,12 +229,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged4_decode_kernel(const PagedP
     const int lim0 = last_key_of(p, sq, 0);
 
     float o[NT][KS][4];
-    float m[NT][2], l[NT][2];
+    // The reference of a row's exponentials, what it is subtracted as (0 before there
+    // is one), the product beyond which it is raised; the sum of the exponentials.
+    float m[NT][2], ref[NT][2], limit[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = limit[nt][0] = limit[nt][1] = -INFINITY;
+      ref[nt][0] = ref[nt][1] = 0.f;
       l[nt][0] = l[nt][1] = 0.f;
     }
     bool aborted = false;
@@ -230,73 +248,79 @@ __global__ void __launch_bounds__(kThreads, 2) paged4_decode_kernel(const PagedP
         break;
       }
       ++it;
-      const uint8_t* const tk = ring + slot * L::kSlotBytes;
-      const uint8_t* const tv = tk + L::kHalfBytes;
+      const uint8_t* const block = ring + slot * L::kSlotBytes;
       const int key0 = first_key(w, warp, j);
 
-      // S^T: x[nt][e] is row 8 nt + 2 t + e % 2, key key0 + g + 8 (e / 2).
-      uint32_t kw[2][C], kp[2][C];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* row = tk + (g + 8 * h) * L::kRow;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          kw[h][c] = reinterpret_cast<const uint32_t*>(row)[4 * c + t];
-        load_words<C>(row + D / 2, kp[h]);
-      }
-      float x[NT][4];
+      // S^T: x[nt][4 u + e] is row 8 nt + 2 t + e % 2, key key0 + 16 u + g + 8 (e / 2).
+      float x[NT][8];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+        for (int e = 0; e < 8; ++e) x[nt][e] = 0.f;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        uint32_t v[2][4];
-        float2 par[2];  // s, m + 8 s
+      for (int u = 0; u < 2; ++u) {
+        uint32_t kw[2][C], kp[2][C];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          par[h] = unpack2<BF16>(kp[h][c]);
-          par[h].y = fmaf(8.f, par[h].x, par[h].y);
+          const uint8_t* row = block + u * L::kUnitBytes + (g + 8 * h) * L::kRow;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[h][i] = kv4_codes<BF16, 8>(kw[h][c] >> (4 * i));
+          for (int c = 0; c < C; ++c) kw[h][c] = reinterpret_cast<const uint32_t*>(row)[4 * c + t];
+          load_words<C>(row + D / 2, kp[h]);
         }
-        const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]};
-        const uint32_t a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float y[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816<BF16>(y, a0, qb[nt][2 * c][0], qb[nt][2 * c][1]);
-          mma16816<BF16>(y, a1, qb[nt][2 * c + 1][0], qb[nt][2 * c + 1][1]);
+        for (int c = 0; c < C; ++c) {
+          uint32_t v[2][4];
+          float2 par[2];  // s, m + 8 s
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[nt][e] = fmaf(par[e >> 1].y, qsum[nt][c][e & 1], fmaf(par[e >> 1].x, y[e], x[nt][e]));
+          for (int h = 0; h < 2; ++h) {
+            par[h] = unpack2<BF16>(kp[h][c]);
+            par[h].y = fmaf(8.f, par[h].x, par[h].y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][i] = kv4_codes<BF16, 8>(kw[h][c] >> (4 * i));
+          }
+          const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]};
+          const uint32_t a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816<BF16>(y, a0, qb[nt][2 * c][0], qb[nt][2 * c][1]);
+            mma16816<BF16>(y, a1, qb[nt][2 * c + 1][0], qb[nt][2 * c + 1][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[nt][4 * u + e] = fmaf(par[e >> 1].y, qsum[nt][c][e & 1],
+                                      fmaf(par[e >> 1].x, y[e], x[nt][4 * u + e]));
+          }
         }
       }
 
       // Online softmax.
+      if (key0 + kKeys - 1 > lim0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (key0 + g + 8 * (e >> 1) > lim[nt][e & 1]) x[nt][e] = -INFINITY;
+      }
       bool raise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[nt][e] *= p.scale_log2;
-          if (key0 + kKeys - 1 > lim0 && key0 + g + 8 * (e >> 1) > lim[nt][e & 1])
-            x[nt][e] = -INFINITY;
-          raise |= x[nt][e] > m[nt][e & 1] + kRaise;
-        }
+        for (int e = 0; e < 8; ++e) raise |= x[nt][e] > limit[nt][e & 1];
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float b = fmaxf(x[nt][e], x[nt][e + 2]);
+            float b = fmaxf(fmaxf(x[nt][e], x[nt][e + 2]), fmaxf(x[nt][e + 4], x[nt][e + 6]));
             b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 4));
             b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 8));
             b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 16));
             // (by the row's own scores alone: no row's bits depend on another's)
-            if (!(b > m[nt][e] + kRaise)) continue;
-            const float alpha = ex2_approx(m[nt][e] - b);
-            m[nt][e] = b;
+            if (!(b > limit[nt][e])) continue;
+            const float n = b * p.scale_log2;
+            const float alpha = ex2_approx(m[nt][e] - n);
+            m[nt][e] = ref[nt][e] = n;
+            limit[nt][e] = b + raise_by;
             l[nt][e] *= alpha;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
@@ -307,61 +331,65 @@ __global__ void __launch_bounds__(kThreads, 2) paged4_decode_kernel(const PagedP
       }
       // P is rounded to 16 bits for its product, as in the 16-bit kernel; l sums
       // the unrounded values.
-      uint32_t pb[NT][2];
+      uint32_t pb[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-          x[nt][e] = ex2_approx(x[nt][e] - ref);
+        for (int e = 0; e < 8; ++e) {
+          x[nt][e] = ex2_approx(fmaf(x[nt][e], p.scale_log2, -ref[nt][e & 1]));
           l[nt][e & 1] += x[nt][e];
         }
-        pb[nt][0] = transpose8(pack2<BF16>(x[nt][0], x[nt][1]));
-        pb[nt][1] = transpose8(pack2<BF16>(x[nt][2], x[nt][3]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          pb[nt][i] = transpose8(pack2<BF16>(x[nt][2 * i], x[nt][2 * i + 1]));
       }
 
       // O^T += V^T P^T.
-      uint32_t vw[2][C], vp[2][2][kSplit ? C : 1];  // keys 2 t, 2 t + 1 and those 8 behind
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* a = tv + (2 * t + 8 * h) * L::kRow;
-        load_pairs<C>(a + g * (D / 16), a + L::kRow + g * (D / 16), vw[h]);
+      for (int u = 0; u < 2; ++u) {
+        uint32_t vw[2][C], vp[2][2][kSplit ? C : 1];  // keys 2 t, 2 t + 1 and those 8 behind
 #pragma unroll
-        for (int c = 0; c < (kSplit ? C : 1); ++c) {
-          const int group = (C * g + c) / 8;
-          uint32_t p0 = reinterpret_cast<const uint32_t*>(a + D / 2)[group];
-          uint32_t p1 = reinterpret_cast<const uint32_t*>(a + L::kRow + D / 2)[group];
-          if (key0 + kKeys > sq.klen) {
-            // Rows past the sequence's last key hold whatever the page held (P
-            // is 0 there, but 0 x NaN is not): they stand for 0.
-            if (key0 + 2 * t + 8 * h >= sq.klen) p0 = 0u;
-            if (key0 + 2 * t + 1 + 8 * h >= sq.klen) p1 = 0u;
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* a = block + (2 + u) * L::kUnitBytes + (2 * t + 8 * h) * L::kRow;
+          load_pairs<C>(a + g * (D / 16), a + L::kRow + g * (D / 16), vw[h]);
+#pragma unroll
+          for (int c = 0; c < (kSplit ? C : 1); ++c) {
+            const int group = (C * g + c) / 8;
+            uint32_t p0 = reinterpret_cast<const uint32_t*>(a + D / 2)[group];
+            uint32_t p1 = reinterpret_cast<const uint32_t*>(a + L::kRow + D / 2)[group];
+            if (key0 + kKeys > sq.klen) {
+              // Rows past the sequence's last key hold whatever the page, or the slot,
+              // held (P is 0 there, but 0 x NaN is not): they stand for 0.
+              const int key = key0 + 16 * u + 2 * t + 8 * h;
+              if (key >= sq.klen) p0 = 0u;
+              if (key + 1 >= sq.klen) p1 = 0u;
+            }
+            vp[h][0][c] = __byte_perm(p0, p1, 0x5410);
+            vp[h][1][c] = __byte_perm(p0, p1, 0x7632);
           }
-          vp[h][0][c] = __byte_perm(p0, p1, 0x5410);
-          vp[h][1][c] = __byte_perm(p0, p1, 0x7632);
         }
-      }
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        uint32_t v[2][4];
+        for (int c = 0; c < C; ++c) {
+          uint32_t v[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[h][i] = kv4_values<BF16>(vw[h][c] >> (4 * i), vp[h][0][kSplit ? c : 0],
-                                       vp[h][1][kSplit ? c : 0]);
-        const uint32_t a0[4] = {v[0][0], v[0][1], v[1][0], v[1][1]};
-        const uint32_t a1[4] = {v[0][2], v[0][3], v[1][2], v[1][3]};
+            for (int i = 0; i < 4; ++i)
+              v[h][i] = kv4_values<BF16>(vw[h][c] >> (4 * i), vp[h][0][kSplit ? c : 0],
+                                         vp[h][1][kSplit ? c : 0]);
+          const uint32_t a0[4] = {v[0][0], v[0][1], v[1][0], v[1][1]};
+          const uint32_t a1[4] = {v[0][2], v[0][3], v[1][2], v[1][3]};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816<BF16>(o[nt][2 * c], a0, pb[nt][0], pb[nt][1]);
-          mma16816<BF16>(o[nt][2 * c + 1], a1, pb[nt][0], pb[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<BF16>(o[nt][2 * c], a0, pb[nt][2 * u], pb[nt][2 * u + 1]);
+            mma16816<BF16>(o[nt][2 * c + 1], a1, pb[nt][2 * u], pb[nt][2 * u + 1]);
+          }
         }
       }
 
       // The slot is read: refill it with the next block of the stream.
       __syncwarp();
-      if (lane == 0) fence_proxy_async_smem();
+      if (lane < 4) fence_proxy_async_smem();  // the lanes that copy
       issue(slot);
       if (++slot == NS) {
         slot = 0;
@@ -418,12 +446,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged4_decode_kernel(const PagedP
 
 template <int D, bool BF16, int NT, bool CLUSTER>
 cudaError_t launch_dbnc(const PagedLaunch& a) {
-  using L = Paged4Layout<D>;
+  using L = Paged4Layout<D, kWarps<NT>>;
   static DeviceFlags configured;
   auto kern = paged4_decode_kernel<D, BF16, NT, CLUSTER>;
   cudaError_t e = ensure_dyn_smem(kern, L::kBytes, configured);
   if (e != cudaSuccess) return e;
-  return launch_clusters(kern, CLUSTER ? a.params.cluster : 1, dim3((unsigned)a.grid), kThreads,
+  return launch_clusters(kern, CLUSTER ? a.params.cluster : 1, dim3((unsigned)a.grid), kWarps<NT> * 32,
                          L::kBytes, a.stream, a.params);
 }
 

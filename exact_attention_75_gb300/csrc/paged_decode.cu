@@ -35,6 +35,9 @@ using namespace rows;
 
 namespace {
 
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = kUnit;  // of a block
 constexpr int kBoxBytes = kKeys * 128;  // one 64-column chunk of a block's K or V
 
 template <int D>
@@ -50,6 +53,7 @@ struct PagedDecodeLayout {
   static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;
   static constexpr int kBytes = kFlagOff + 16 + 1024;  // + room to align the base
   static_assert(kRingBytes % 1024 == 0 && kBytes + 256 <= 113 * 1024, "two CTAs per SM");
+  static_assert(kWarps * kKeys <= kPagedShare, "a share holds a cost block");
 };
 
 // Byte offset of 16-byte piece `piece` of row `row` in a staged block.
@@ -85,26 +89,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     tma_prefetch_desc(&tmV);
   }
   grid_wait();
-  Walk w = start_rows<CLUSTER>(p);
+  Walk<kWarps, kKeys> w = start_rows<kWarps, kKeys, CLUSTER>(p);
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
   // it: blocks taken from the ring.
-  BlockStream stream(p, w, warp, lane);
+  BlockStream<kWarps, kKeys> stream(p, w, warp, lane);
   uint32_t it = 0;
   auto issue = [&]() {
-    stream.issue(p, warp, lane, [&](int page, int head, int y) {
+    if (!stream.more()) return;
+    const int page = stream.page(p, 0, lane);
+    if (lane == 0) {
       const int s = (int)(stream.issued % NS);
       const uint32_t dk = ring + (uint32_t)(s * L::kSlotBytes);
       const uint32_t dv = dk + L::kChunks * kBoxBytes;
-      const int z = page >= 0 ? page * p.Hkv + head : -1;  // -1: the box reads zeros
+      const int z = page >= 0 ? page * p.Hkv + stream.ahead.head : -1;  // -1: the box reads zeros
+      const int y = stream.row(p, 0, warp);
       mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
 #pragma unroll
       for (int c = 0; c < L::kChunks; ++c) {
         tma_load_3d(dk + c * kBoxBytes, &tmK, bar(s), c * 64, y, z);
         tma_load_3d(dv + c * kBoxBytes, &tmV, bar(s), c * 64, y, z);
       }
-    });
+    }
+    stream.next(p, warp, lane);
   };
   for (int i = 0; i < NS; ++i) issue();
 

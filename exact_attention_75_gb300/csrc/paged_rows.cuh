@@ -1,7 +1,7 @@
 // What the decoding kernels over a paged cache share, whatever it is held in:
 // items of at most 16 query rows (a sequence's key/value head), their keys shared
-// out in 16-key blocks over the warps of a CTA and the CTAs of a cluster or of
-// the whole grid, and how the warps' and the CTAs' results meet.
+// out in blocks over the warps of a CTA and the CTAs of a cluster or of the whole
+// grid, and how the warps' and the CTAs' results meet.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -15,40 +15,41 @@
 namespace attn {
 namespace rows {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kKeys = kPagedBlock;
-constexpr int kMeet = 4;  // rows that meet in shared memory at a time
+constexpr int kUnit = kPagedBlock;  // keys that never lie in two pages
+constexpr int kMeet = 4;            // rows that meet in shared memory at a time
 template <int D>
 constexpr int kRowStride = D + 4;  // floats of a row there
 
-// An item is a sequence's key/value head; the warps take the 16-key blocks of
-// its kUnit-key cost blocks in turn.
-constexpr int kUnit = kWarps * kKeys;
-using Cost = PagedCost<kUnit, 1, 1, 128, true>;
-using Walk = PagedWalk<Cost>;
+// An item is a sequence's key/value head; the W warps of a CTA take the blocks (K
+// keys each) of its cost blocks (one block for each warp) in turn.
+template <int W, int K>
+using Cost = PagedCost<W * K, 1, 1, 128, true>;
+template <int W, int K>
+struct Walk : PagedWalk<Cost<W, K>> {};
 
-__device__ __forceinline__ int warp_blocks(const Walk& w, int warp) {
-  const int keys = min(w.u1 * kUnit, w.sq.klen) - w.u0 * kUnit;
-  const int nb = (max(keys, 0) + kKeys - 1) / kKeys;
-  return nb > warp ? (nb - warp + kWarps - 1) / kWarps : 0;
+template <int W, int K>
+__device__ __forceinline__ int warp_blocks(const Walk<W, K>& w, int warp) {
+  const int keys = min(w.u1 * W * K, w.sq.klen) - w.u0 * W * K;
+  const int nb = (max(keys, 0) + K - 1) / K;
+  return nb > warp ? (nb - warp + W - 1) / W : 0;
 }
 // First key of the warp's block j.
-__device__ __forceinline__ int first_key(const Walk& w, int warp, int j) {
-  return w.u0 * kUnit + (warp + j * kWarps) * kKeys;
+template <int W, int K>
+__device__ __forceinline__ int first_key(const Walk<W, K>& w, int warp, int j) {
+  return (w.u0 * W + warp + j * W) * K;
 }
 
 // Where the CTA starts.  CLUSTER: an item is shared by the p.cluster CTAs of a
 // cluster; otherwise the grid takes equal shares of the whole batch.
-template <bool CLUSTER>
-__device__ __forceinline__ Walk start_rows(const PagedParams& p) {
-  Walk w;
+template <int W, int K, bool CLUSTER>
+__device__ __forceinline__ Walk<W, K> start_rows(const PagedParams& p) {
+  Walk<W, K> w;
   if constexpr (CLUSTER) {
     const int item = blockIdx.x / p.cluster, rank = blockIdx.x - item * p.cluster;
     w.b = item / p.Hkv;
     w.head = item - w.b * p.Hkv;
     w.sq = paged_seq(p, w.b);
-    w.nb = (w.sq.klen + kUnit - 1) / kUnit;
+    w.nb = (w.sq.klen + W * K - 1) / (W * K);
     w.u0 = (int)((long long)rank * w.nb / p.cluster);
     w.u1 = (int)((long long)(rank + 1) * w.nb / p.cluster);
     w.x0 = 0;
@@ -58,24 +59,51 @@ __device__ __forceinline__ Walk start_rows(const PagedParams& p) {
     __syncthreads();
   } else {
     if (threadIdx.x == 0) paged_clear(p);
-    w = paged_start<Cost, kThreads>(p, p.max_q);
+    static_cast<PagedWalk<Cost<W, K>>&>(w) = paged_start<Cost<W, K>, W * 32>(p, p.max_q);
   }
   return w;
 }
 
 // A warp's blocks in order, over the borders of pieces: it walks ahead of the
-// kernel as far as the warp's ring reaches.  Lane i holds the page of the
-// piece's block 32 n + i, so that a table read's latency is paid once in 32
-// blocks.
+// kernel as far as the warp's ring reaches.  The lanes hold the pages of the next
+// 32 units (a block has K / kUnit), so that a table read's latency is paid once for
+// them.
+template <int W, int K>
 struct BlockStream {
-  Walk ahead;
+  static constexpr int kUnits = K / kUnit;
+  Walk<W, K> ahead;
   int j, n, pages;
   uint32_t issued;
 
-  __device__ __forceinline__ BlockStream(const PagedParams& p, const Walk& w, int warp, int lane)
-      : ahead(w), j(0), n(w.left > 0 ? warp_blocks(w, warp) : 0), pages(-1), issued(0) {
+  __device__ __forceinline__ BlockStream(const PagedParams& p, const Walk<W, K>& w, int warp,
+                                         int lane)
+      : ahead(w), j(0), n(w.left > 0 ? warp_blocks(w, warp) : 0), pages(-2), issued(0) {
     settle(p, warp, lane);
   }
+  // Whether there is a block to issue.
+  __device__ __forceinline__ bool more() const { return ahead.left > 0; }
+  // The page of unit u of the block: -1 if it is none of the cache (lane 0 reports
+  // it), -2 if the unit lies past the sequence.
+  __device__ __forceinline__ int page(const PagedParams& p, int u, int lane) const {
+    const int page = __shfl_sync(0xffffffffu, pages, (j * kUnits + u) & 31);
+    if (page >= p.n_pages || page == -1) {
+      if (lane == 0)
+        atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(ahead.b, 0xFFFF) << 16));
+      return -1;
+    }
+    return page;
+  }
+  // The unit's first row in its page.
+  __device__ __forceinline__ int row(const PagedParams& p, int u, int warp) const {
+    return (first_key(ahead, warp, j) + u * kUnit) & (p.page - 1);
+  }
+  __device__ __forceinline__ void next(const PagedParams& p, int warp, int lane) {
+    ++issued;
+    ++j;
+    settle(p, warp, lane);
+  }
+
+ private:
   // Goes to the next block, or to left <= 0.
   __device__ __forceinline__ void settle(const PagedParams& p, int warp, int lane) {
     while (ahead.left > 0 && j >= n) {
@@ -83,33 +111,20 @@ struct BlockStream {
       n = warp_blocks(ahead, warp);
       j = 0;
     }
-    if (ahead.left > 0 && (j & 31) == 0) {
-      const int i = j + lane;
-      pages = i < n ? __ldg(p.block_table + (size_t)ahead.b * p.max_pages +
-                            (first_key(ahead, warp, i) >> p.page_log2))
-                    : -1;
+    if (ahead.left > 0 && (j * kUnits & 31) == 0) {
+      const int at = j + lane / kUnits;
+      const int key = first_key(ahead, warp, at) + lane % kUnits * kUnit;
+      pages = at < n && key < ahead.sq.klen
+                  ? max(__ldg(p.block_table + (size_t)ahead.b * p.max_pages +
+                              (key >> p.page_log2)), -1)
+                  : -2;
     }
-  }
-  // Lane 0 copies the next block: copy(page, -1 if it is none of the cache;
-  // head; the block's first row in the page).
-  template <typename Copy>
-  __device__ __forceinline__ void issue(const PagedParams& p, int warp, int lane, Copy copy) {
-    if (ahead.left <= 0) return;
-    const int page = __shfl_sync(0xffffffffu, pages, j & 31);
-    if (lane == 0) {
-      const bool ok = page >= 0 && page < p.n_pages;
-      if (!ok)
-        atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(ahead.b, 0xFFFF) << 16));
-      copy(ok ? page : -1, ahead.head, first_key(ahead, warp, j) & (p.page - 1));
-    }
-    ++issued;
-    ++j;
-    settle(p, warp, lane);
   }
 };
 
 // Row r of the item in q, o and lse: new token r / G, query head r % G of the group.
-__device__ __forceinline__ size_t row_of(const PagedParams& p, const Walk& w, int r) {
+template <int W, int K>
+__device__ __forceinline__ size_t row_of(const PagedParams& p, const Walk<W, K>& w, int r) {
   const int i = r / p.G, h = r - i * p.G;
   return (size_t)(w.head * p.G + h) * p.total + w.sq.s0 + i;
 }
@@ -129,25 +144,25 @@ __device__ __forceinline__ void store_row(const PagedParams& p, size_t row, int 
 }
 
 // Combines the warps' results (O, m, l) of rows pass * kMeet .. of the piece,
-// which lie in meet and meet_ml [kWarps][kMeet]: the item's rows, the CTA's
+// which lie in meet and meet_ml [W][kMeet]: the item's rows, the CTA's
 // part of a cluster's item (part, part_ml, by row), or a part for the join kernel.
-template <int D, bool BF16, bool CLUSTER>
-__device__ __forceinline__ void meet_rows(const PagedParams& p, const Walk& w, const float* meet,
-                                          const float2* meet_ml, float* part, float2* part_ml,
-                                          int pass, int rows) {
+template <int D, bool BF16, bool CLUSTER, int W, int K>
+__device__ __forceinline__ void meet_rows(const PagedParams& p, const Walk<W, K>& w,
+                                          const float* meet, const float2* meet_ml, float* part,
+                                          float2* part_ml, int pass, int rows) {
   const bool whole = !CLUSTER && w.whole();
   const size_t slot = 2 * (size_t)blockIdx.x + (w.x0 == 0 ? 1 : 0);
-  for (int idx = threadIdx.x; idx < kMeet * (D / 4); idx += kThreads) {
+  for (int idx = threadIdx.x; idx < kMeet * (D / 4); idx += W * 32) {
     const int mr = idx / (D / 4), c = idx % (D / 4) * 4;
     const int r = pass * kMeet + mr;
     if (r >= rows) break;
     float M = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) M = fmaxf(M, meet_ml[k * kMeet + mr].x);
+    for (int k = 0; k < W; ++k) M = fmaxf(M, meet_ml[k * kMeet + mr].x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float lsum = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
+    for (int k = 0; k < W; ++k) {
       const float2 ml = meet_ml[k * kMeet + mr];
       const float f = paged_weight(ml.x, ml.y, M);
       lsum += f * ml.y;
@@ -173,16 +188,16 @@ __device__ __forceinline__ void meet_rows(const PagedParams& p, const Walk& w, c
 }
 
 // Joins the parts of a cluster's item through its CTAs' shared memory.
-template <int D, bool BF16>
-__device__ __forceinline__ void join_cluster(const PagedParams& p, const Walk& w,
+template <int D, bool BF16, int W, int K>
+__device__ __forceinline__ void join_cluster(const PagedParams& p, const Walk<W, K>& w,
                                              const float* part, const float2* part_ml,
                                              bool given_up) {
   if (w.sq.qlen == 0) return;  // the same in every CTA of the cluster
   cluster_sync();
   const int rows = min(kPagedRows, w.sq.qlen * p.G);
   const int rank = blockIdx.x % p.cluster;
-  for (int e = rank * kThreads + threadIdx.x; !given_up && e < rows * (D / 4);
-       e += p.cluster * kThreads) {
+  for (int e = rank * W * 32 + threadIdx.x; !given_up && e < rows * (D / 4);
+       e += p.cluster * W * 32) {
     const int r = e / (D / 4), c = e % (D / 4) * 4;
     float2 ml[kPagedCluster];
     float4 x[kPagedCluster];
