@@ -12,8 +12,8 @@
 // stands for NaN.
 //
 // Values take part in products as RN_T(m + c s), one fused multiply-add of two
-// 16-bit values at a time: half a step of T, the error that a 16-bit cache has in
-// the first place.  Keys do not: an error of 2^-9 a channel, even of 2^-12, shows in
+// 16-bit values at a time, or as m and RN_T(c s): half a step of T, the error that a
+// 16-bit cache has in the first place.  Keys do not: an error of 2^-9 a channel, even of 2^-12, shows in
 // the log-sum-exp of a short sequence.  The codes less 8 have three significant
 // bits, so their product with a query, and with a scale of 8 bits, is exact, and
 //   q . k = sum over groups of  sum q (c - 8) s  +  (m + 8 s) sum q,
@@ -31,6 +31,14 @@ constexpr int kv4_row(int d) { return d / 2 + d / 8; }  // bytes
 
 #ifdef __CUDACC__
 
+// (w & mask) | bits, as the one instruction that it is (the compiler makes two of
+// them where both are constants).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  return r;
+}
+
 // Two codes (bits 0-3 and 16-19 of w) less ZERO as 16-bit numbers: their bits in
 // the mantissa of 2^7 (bf16) or 2^10 (fp16), less that power and ZERO.
 template <bool BF16, int ZERO>
@@ -39,23 +47,64 @@ __device__ __forceinline__ uint32_t kv4_codes(uint32_t w) {
   if constexpr (BF16)
     asm("sub.rn.bf16x2 %0, %1, %2;"
         : "=r"(r)
-        : "r"((w & 0x000F000Fu) | 0x43004300u), "r"(0x43004300u + 0x10001u * ZERO));
+        : "r"(and_or(w, 0x000F000Fu, 0x43004300u)), "r"(0x43004300u + 0x10001u * ZERO));
   else
     asm("sub.rn.f16x2 %0, %1, %2;"
         : "=r"(r)
-        : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(0x64006400u + 0x10001u * ZERO));
+        : "r"(and_or(w, 0x000F000Fu, 0x64006400u)), "r"(0x64006400u + 0x10001u * ZERO));
   return r;
 }
 
-// What two codes stand for.
+// The codes of a word less 8 in fp16, nibbles i and i + 4 side by side; those of odd i
+// times 16, since their bits are taken where they stand (one shift a word, not three).
+__device__ __forceinline__ void kv4_centred(uint32_t w, uint32_t (&v)[4]) {
+  const uint32_t x[2] = {w, w >> 8};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    asm("sub.rn.f16x2 %0, %1, %2;"
+        : "=r"(v[2 * i])
+        : "r"(and_or(x[i], 0x000F000Fu, 0x64006400u)), "r"(0x64086408u));
+    asm("sub.rn.f16x2 %0, %1, %2;"
+        : "=r"(v[2 * i + 1])
+        : "r"(and_or(x[i], 0x00F000F0u, 0x64006400u)), "r"(0x64806480u));
+  }
+}
+
+// What the codes of a word stand for, nibbles i and i + 4 side by side.
 template <bool BF16>
-__device__ __forceinline__ uint32_t kv4_values(uint32_t w, uint32_t s, uint32_t m) {
-  uint32_t r;
-  if constexpr (BF16)
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(kv4_codes<true, 0>(w)), "r"(s), "r"(m));
-  else
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(kv4_codes<false, 0>(w)), "r"(s), "r"(m));
-  return r;
+__device__ __forceinline__ void kv4_values(uint32_t w, uint32_t s, uint32_t m, uint32_t (&v)[4]) {
+  if constexpr (BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+          : "=r"(v[i])
+          : "r"(kv4_codes<true, 0>(w >> (4 * i))), "r"(s), "r"(m));
+  } else {
+    const uint32_t x[2] = {w, w >> 8};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t c;
+      if (i & 1)  // (1024 + 16 c) / 16 - 64
+        asm("fma.rn.f16x2 %0, %1, %2, %3;"
+            : "=r"(c)
+            : "r"(and_or(x[i / 2], 0x00F000F0u, 0x64006400u)), "r"(0x2C002C00u), "r"(0xD400D400u));
+      else
+        c = kv4_codes<false, 0>(x[i / 2]);
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(c), "r"(s), "r"(m));
+    }
+  }
+}
+
+// c s of a word's codes in bf16, nibbles i and i + 4 side by side, each rounded once:
+// (128 + c) s - 128 s, the second product being exact.
+__device__ __forceinline__ void kv4_steps(uint32_t w, uint32_t s, uint32_t (&v)[4]) {
+  uint32_t base;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(base) : "r"(s), "r"(0xC300C300u));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(v[i])
+        : "r"(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), "r"(s), "r"(base));
 }
 
 // Two 16-bit values in 32 bits.
@@ -88,8 +137,7 @@ template <bool BF16>
 __device__ __forceinline__ uint4 kv4_word(uint32_t w, uint32_t par) {
   const uint32_t s = __byte_perm(par, par, 0x1010), m = __byte_perm(par, par, 0x3232);
   uint32_t v[4];  // channels i and i + 4
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = kv4_values<BF16>(w >> (4 * i), s, m);
+  kv4_values<BF16>(w, s, m, v);
   return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
                     __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }

@@ -19,8 +19,11 @@
 //      operand register;
 //   V: it reads channels g D/8 .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9; two keys'
 //      half words side by side give the pairs of keys that an operand holds.
-// A group's product is taken with c - 8, and s and m + 8 s of its keys are applied to
-// it and to the sum of the query's channels in 32 bits: keys lose nothing.
+// A group's product is taken with c - 8 in fp16, the query scaled into its range by a
+// power of two, and s and m + 8 s of its keys are applied to it and to the sum of the
+// query's channels in 32 bits: keys lose nothing.
+// Values are m + c s rounded to 16 bits, or, in bf16, c s rounded, and m by a product of
+// its own: (128 + c) s - 128 s is one instruction where c s + m takes two.
 // P leaves the softmax by keys and is wanted by rows: one 8 x 8 transpose for 8
 // keys.
 //
@@ -85,39 +88,45 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-// N 32-bit words from shared memory.
+// N 32-bit words from shared memory, at an address of that space (a generic one
+// costs 64-bit arithmetic and a look at what it points to).
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* x, uint32_t (&w)[N]) {
+__device__ __forceinline__ void load_words(uint32_t a, uint32_t (&w)[N]) {
   if constexpr (N == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(x);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(a)
+                 : "memory");
   } else if constexpr (N == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(x);
-    w[0] = v.x, w[1] = v.y;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(x)[i];
+    for (int i = 0; i < N; ++i)
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(a + 4 * i) : "memory");
   }
 }
+__device__ __forceinline__ uint32_t load_word(uint32_t a) {
+  uint32_t w[1];
+  load_words<1>(a, w);
+  return w[0];
+}
 
-// The codes of 4 C channels of two keys (a: the first's, b: the second's), the
+// The codes of 4 C channels of two keys (at a: the first's, at b: the second's), the
 // first key's in the low halves.
 template <int C>
-__device__ __forceinline__ void load_pairs(const uint8_t* a, const uint8_t* b, uint32_t (&w)[C]) {
+__device__ __forceinline__ void load_pairs(uint32_t a, uint32_t b, uint32_t (&w)[C]) {
   if constexpr (C == 3) {
+    auto half = [](uint32_t at) {
+      uint16_t x;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+      return (uint32_t)x;
+    };
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      w[c] = (uint32_t)reinterpret_cast<const uint16_t*>(a)[c] |
-             (uint32_t)reinterpret_cast<const uint16_t*>(b)[c] << 16;
+    for (int c = 0; c < C; ++c) w[c] = half(a + 2 * c) | half(b + 2 * c) << 16;
   } else {
     uint32_t x[C / 2], y[C / 2];
-    if constexpr (C == 4) {
-      load_words<2>(a, x);
-      load_words<2>(b, y);
-    } else {
-      x[0] = *reinterpret_cast<const uint32_t*>(a);
-      y[0] = *reinterpret_cast<const uint32_t*>(b);
-    }
+    load_words<C / 2>(a, x);
+    load_words<C / 2>(b, y);
 #pragma unroll
     for (int c = 0; c < C; ++c) w[c] = __byte_perm(x[c / 2], y[c / 2], c & 1 ? 0x7632 : 0x5410);
   }
@@ -132,12 +141,15 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
   constexpr int C = D / 32;   // a lane's words of a key, half words of a value row
   constexpr int NS = L::kSlots;
   constexpr bool kSplit = D == 96;  // a lane's channels of V lie in more than one group
+  constexpr int G = kSplit ? C : 1;  // scales and minima of them
+  constexpr int M = BF16 ? (G + 1) / 2 : 0;  // products of the minima: two to a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                              ~static_cast<uintptr_t>(127));
   const uint32_t sbase = smem_u32(smem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kFlagOff);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the warp's number as one value, which the compiler can keep for the whole warp)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   auto bar = [&](int s) { return sbase + L::kBarOff + 8u * (uint32_t)(warp * NS + s); };
 
@@ -149,9 +161,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
   grid_wait();
   Walk<W, kKeys> w = start_rows<W, kKeys, CLUSTER>(p);
   Watchdog wd{p.status, abort_flag, p.wait_limit_ns};
-  const float raise_by = kRaise / p.scale_log2;
-  uint8_t* const ring = smem + warp * NS * L::kSlotBytes;
-  const uint32_t ring_addr = smem_u32(ring);
+  const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
   // Block n of the warp's stream lies in slot n % NS; the ring is full until the
   // stream ends, so the slot that is read is the one that is filled next.
@@ -161,19 +171,24 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
   uint32_t parity = 0;     // (it / NS) & 1
   auto issue = [&](int s) {
     if (!stream.more()) return;
-    // Lanes 0 to 3 copy a unit of K or V each, of a page outside the cache (reported)
-    // any one; what the second unit of a block past the sequence has is not read
-    // but as numbers that count nothing.
+    // A page outside the cache (reported): any of it.  Past the sequence a unit is
+    // what its page holds, or, in a page of its own, what the slot held: numbers that
+    // count nothing.
     const int page0 = stream.page(p, 0, lane), page1 = stream.page(p, 1, lane);
-    const int pages = page1 == -2 ? 1 : 2;
-    if (lane == 0) mbar_arrive_expect_tx(bar(s), (uint32_t)(2 * pages * L::kUnitBytes));
-    __syncwarp();
-    const int u = lane & 1;
-    if (lane < 4 && u < pages) {
-      const size_t row = (((size_t)max(u ? page1 : page0, 0) * p.Hkv + stream.ahead.head)
-                          << p.page_log2) + stream.row(p, u, warp);
-      bulk_load(ring_addr + (uint32_t)(s * L::kSlotBytes + lane * L::kUnitBytes),
-                (lane < 2 ? p.k4 : p.v4) + row * L::kRow, L::kUnitBytes, bar(s));
+    if (lane == 0) {
+      auto copy = [&](int page, int u, int units) {
+        const size_t row = (((size_t)max(page, 0) * p.Hkv + stream.ahead.head) << p.page_log2) +
+                           stream.row(p, u, warp);
+        const uint32_t dst = ring + (uint32_t)(s * L::kSlotBytes + u * L::kUnitBytes);
+        const uint32_t bytes = (uint32_t)(units * L::kUnitBytes);
+        bulk_load(dst, p.k4 + row * L::kRow, bytes, bar(s));
+        bulk_load(dst + 2 * L::kUnitBytes, p.v4 + row * L::kRow, bytes, bar(s));
+      };
+      const bool two = p.page == kUnit;  // a unit a page
+      const int units = two && page1 == -2 ? 1 : 2;
+      mbar_arrive_expect_tx(bar(s), (uint32_t)(2 * units * L::kUnitBytes));
+      copy(page0, 0, two ? 1 : 2);
+      if (two && units == 2) copy(page1, 1, 1);
     }
     stream.next(p, warp, lane);
   };
@@ -191,34 +206,56 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     const int nbw = warp_blocks(w, warp);
     const PagedSeq sq = w.sq;
     const int rows = min(kPagedRows, sq.qlen * p.G);
-    // Q^T: of row 8 nt + g the channels that the lane has of the keys; and the
-    // sums over each group of rows 8 nt + 2 t and the next.
+    // Q^T: of row 8 nt + g the channels that the lane has of the keys, those of odd
+    // nibbles over 16 (kv4_centred); of rows 8 nt + 2 t and the next the sums over each
+    // group, and what takes their products to base 2 (1e-37 .. 1e37, as in the tile
+    // kernel).
     uint32_t qb[NT][KS][2];
-    float qsum[NT][C][2];
+    float2 qsum[NT][C], to2[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = 8 * nt + g;
       const uint16_t* q =
           static_cast<const uint16_t*>(p.q) + (r < rows ? row_of(p, w, r) * D + 8 * t : 0);
+      uint4 x[C];
+      uint32_t top = 0u;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) x = *reinterpret_cast<const uint4*>(q + 32 * c);
-        qb[nt][2 * c][0] = __byte_perm(x.x, x.z, 0x5410);
-        qb[nt][2 * c][1] = __byte_perm(x.x, x.z, 0x7632);
-        qb[nt][2 * c + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-        qb[nt][2 * c + 1][1] = __byte_perm(x.y, x.w, 0x7632);
-        float sum = 0.f;
+        x[c] = r < rows ? *reinterpret_cast<const uint4*>(q + 32 * c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 f = unpack2<BF16>(reinterpret_cast<const uint32_t*>(&x)[i]);
-          sum += f.x + f.y;
+          const float2 f = unpack2<BF16>(y[i]);
+          top = max(top, max(finite_bits(f.x), finite_bits(f.y)));
+        }
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float2 f = to_fp16_range<9>(top);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        float z[8], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = unpack2<BF16>(y[i]);
+          z[2 * i] = v.x * f.x;
+          z[2 * i + 1] = v.y * f.x;
+          sum += z[2 * i] + z[2 * i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float by = i & 1 ? 0.0625f : 1.f;
+          qb[nt][2 * c + i / 2][i & 1] = pack_f16x2(z[i] * by, z[i + 4] * by);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qsum[nt][c][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-        qsum[nt][c][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        qsum[nt][c] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t),
+                                  __shfl_sync(0xffffffffu, sum, 8 * t + 4));
       }
+      const float by = fminf(fmaxf(p.scale_log2 * f.y, 1e-37f), 1e37f);
+      to2[nt] = make_float2(__shfl_sync(0xffffffffu, by, 8 * t),
+                            __shfl_sync(0xffffffffu, by, 8 * t + 4));
     }
     // Last key that rows 8 nt + 2 t and the next see, and the item's first row.
     int lim[NT][2];
@@ -229,16 +266,20 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     const int lim0 = last_key_of(p, sq, 0);
 
     float o[NT][KS][4];
+    float om[NT][BF16 ? M : 1][4];  // what the minima add to the lane's channels
     // The reference of a row's exponentials, what it is subtracted as (0 before there
     // is one), the product beyond which it is raised; the sum of the exponentials.
-    float m[NT][2], ref[NT][2], limit[NT][2], l[NT][2];
+    float m[NT][2], ref[NT][2], limit[NT][2];
+    float2 l[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < M; ++i) om[nt][i][0] = om[nt][i][1] = om[nt][i][2] = om[nt][i][3] = 0.f;
       m[nt][0] = m[nt][1] = limit[nt][0] = limit[nt][1] = -INFINITY;
       ref[nt][0] = ref[nt][1] = 0.f;
-      l[nt][0] = l[nt][1] = 0.f;
+      l[nt] = make_float2(0.f, 0.f);
     }
     bool aborted = false;
 #pragma unroll 1
@@ -248,23 +289,23 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
         break;
       }
       ++it;
-      const uint8_t* const block = ring + slot * L::kSlotBytes;
+      const uint32_t block = ring + (uint32_t)(slot * L::kSlotBytes);
       const int key0 = first_key(w, warp, j);
 
-      // S^T: x[nt][4 u + e] is row 8 nt + 2 t + e % 2, key key0 + 16 u + g + 8 (e / 2).
-      float x[NT][8];
+      // S^T: x[nt][2 u + h] is rows 8 nt + 2 t and the next, key key0 + 16 u + 8 h + g.
+      float2 x[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[nt][e] = 0.f;
+        for (int i = 0; i < 4; ++i) x[nt][i] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t kw[2][C], kp[2][C];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint8_t* row = block + u * L::kUnitBytes + (g + 8 * h) * L::kRow;
+          const uint32_t row = block + u * L::kUnitBytes + (g + 8 * h) * L::kRow;
 #pragma unroll
-          for (int c = 0; c < C; ++c) kw[h][c] = reinterpret_cast<const uint32_t*>(row)[4 * c + t];
+          for (int c = 0; c < C; ++c) kw[h][c] = load_word(row + 16 * c + 4 * t);
           load_words<C>(row + D / 2, kp[h]);
         }
 #pragma unroll
@@ -275,57 +316,68 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
           for (int h = 0; h < 2; ++h) {
             par[h] = unpack2<BF16>(kp[h][c]);
             par[h].y = fmaf(8.f, par[h].x, par[h].y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[h][i] = kv4_codes<BF16, 8>(kw[h][c] >> (4 * i));
+            kv4_centred(kw[h][c], v[h]);
           }
           const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]};
           const uint32_t a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float y[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816<BF16>(y, a0, qb[nt][2 * c][0], qb[nt][2 * c][1]);
-            mma16816<BF16>(y, a1, qb[nt][2 * c + 1][0], qb[nt][2 * c + 1][1]);
+            mma16816<false>(y, a0, qb[nt][2 * c][0], qb[nt][2 * c][1]);
+            mma16816<false>(y, a1, qb[nt][2 * c + 1][0], qb[nt][2 * c + 1][1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[nt][4 * u + e] = fmaf(par[e >> 1].y, qsum[nt][c][e & 1],
-                                      fmaf(par[e >> 1].x, y[e], x[nt][4 * u + e]));
+            for (int h = 0; h < 2; ++h) {
+              float2& z = x[nt][2 * u + h];
+              z = __ffma2_rn(make_float2(par[h].x, par[h].x), make_float2(y[2 * h], y[2 * h + 1]), z);
+              z = __ffma2_rn(make_float2(par[h].y, par[h].y), qsum[nt][c], z);
+            }
           }
         }
       }
 
       // Online softmax.
       if (key0 + kKeys - 1 > lim0) {
+        asm volatile("");  // few blocks: a branch, not selects in every one
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (key0 + g + 8 * (e >> 1) > lim[nt][e & 1]) x[nt][e] = -INFINITY;
+          for (int i = 0; i < 4; ++i) {
+            if (key0 + g + 8 * i > lim[nt][0]) x[nt][i].x = -INFINITY;
+            if (key0 + g + 8 * i > lim[nt][1]) x[nt][i].y = -INFINITY;
+          }
       }
       bool raise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) raise |= x[nt][e] > limit[nt][e & 1];
+        for (int i = 0; i < 4; ++i)
+          raise |= x[nt][i].x > limit[nt][0] || x[nt][i].y > limit[nt][1];
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float b = fmaxf(fmaxf(x[nt][e], x[nt][e + 2]), fmaxf(x[nt][e + 4], x[nt][e + 6]));
+            auto at = [&](int i) { return e ? x[nt][i].y : x[nt][i].x; };
+            float b = fmaxf(fmaxf(at(0), at(1)), fmaxf(at(2), at(3)));
             b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 4));
             b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 8));
             b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, 16));
             // (by the row's own scores alone: no row's bits depend on another's)
             if (!(b > limit[nt][e])) continue;
-            const float n = b * p.scale_log2;
+            const float by = e ? to2[nt].y : to2[nt].x, n = b * by;
             const float alpha = ex2_approx(m[nt][e] - n);
             m[nt][e] = ref[nt][e] = n;
-            limit[nt][e] = b + raise_by;
-            l[nt][e] *= alpha;
+            limit[nt][e] = b + kRaise / by;
+            (e ? l[nt].y : l[nt].x) *= alpha;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
               o[nt][i][e] *= alpha;
               o[nt][i][e + 2] *= alpha;
+            }
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+              om[nt][i][e] *= alpha;
+              om[nt][i][e + 2] *= alpha;
             }
           }
       }
@@ -335,48 +387,69 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[nt][e] = ex2_approx(fmaf(x[nt][e], p.scale_log2, -ref[nt][e & 1]));
-          l[nt][e & 1] += x[nt][e];
+        for (int i = 0; i < 4; ++i) {
+          float2 z = __ffma2_rn(x[nt][i], to2[nt], make_float2(-ref[nt][0], -ref[nt][1]));
+          z = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+          l[nt] = __fadd2_rn(l[nt], z);
+          pb[nt][i] = transpose8(pack2<BF16>(z.x, z.y));
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          pb[nt][i] = transpose8(pack2<BF16>(x[nt][2 * i], x[nt][2 * i + 1]));
       }
 
       // O^T += V^T P^T.
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        uint32_t vw[2][C], vp[2][2][kSplit ? C : 1];  // keys 2 t, 2 t + 1 and those 8 behind
+        // keys 2 t, 2 t + 1 and those 8 behind: codes, and s and m of each key
+        uint32_t vw[2][C], vp[2][2][G];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint8_t* a = block + (2 + u) * L::kUnitBytes + (2 * t + 8 * h) * L::kRow;
+          const uint32_t a = block + (2 + u) * L::kUnitBytes + (2 * t + 8 * h) * L::kRow;
           load_pairs<C>(a + g * (D / 16), a + L::kRow + g * (D / 16), vw[h]);
 #pragma unroll
-          for (int c = 0; c < (kSplit ? C : 1); ++c) {
-            const int group = (C * g + c) / 8;
-            uint32_t p0 = reinterpret_cast<const uint32_t*>(a + D / 2)[group];
-            uint32_t p1 = reinterpret_cast<const uint32_t*>(a + L::kRow + D / 2)[group];
-            if (key0 + kKeys > sq.klen) {
-              // Rows past the sequence's last key hold whatever the page, or the slot,
-              // held (P is 0 there, but 0 x NaN is not): they stand for 0.
-              const int key = key0 + 16 * u + 2 * t + 8 * h;
-              if (key >= sq.klen) p0 = 0u;
-              if (key + 1 >= sq.klen) p1 = 0u;
-            }
-            vp[h][0][c] = __byte_perm(p0, p1, 0x5410);
-            vp[h][1][c] = __byte_perm(p0, p1, 0x7632);
+          for (int n = 0; n < G; ++n) {
+            const int group = (C * g + n) / 8;
+            vp[h][0][n] = load_word(a + D / 2 + 4 * group);
+            vp[h][1][n] = load_word(a + L::kRow + D / 2 + 4 * group);
           }
+        }
+        if (key0 + kKeys > sq.klen) {
+          asm volatile("");
+          // Rows past the sequence's last key hold whatever the page, or the slot,
+          // held (P is 0 there, but 0 x NaN is not): they stand for 0.
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int n = 0; n < G; ++n)
+                if (key0 + 16 * u + 2 * t + 8 * h + e >= sq.klen) vp[h][e][n] = 0u;
+        }
+        uint32_t sc[2][G], lo[2][G];  // scales and minima of two keys side by side
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int n = 0; n < G; ++n) {
+            sc[h][n] = __byte_perm(vp[h][0][n], vp[h][1][n], 0x5410);
+            lo[h][n] = __byte_perm(vp[h][0][n], vp[h][1][n], 0x7632);
+          }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          // row g of the tile: group 2 i of the lane's, row g + 8: the next
+          const int n = 2 * i + 1;
+          const uint32_t a[4] = {lo[0][2 * i], n < G ? lo[0][n % G] : 0u, lo[1][2 * i],
+                                 n < G ? lo[1][n % G] : 0u};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816<BF16>(om[nt][i], a, pb[nt][2 * u], pb[nt][2 * u + 1]);
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           uint32_t v[2][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              v[h][i] = kv4_values<BF16>(vw[h][c] >> (4 * i), vp[h][0][kSplit ? c : 0],
-                                         vp[h][1][kSplit ? c : 0]);
+          for (int h = 0; h < 2; ++h) {
+            const int n = kSplit ? c : 0;
+            if constexpr (BF16) kv4_steps(vw[h][c], sc[h][n], v[h]);
+            else kv4_values<BF16>(vw[h][c], sc[h][n], lo[h][n], v[h]);
+          }
           const uint32_t a0[4] = {v[0][0], v[0][1], v[1][0], v[1][1]};
           const uint32_t a1[4] = {v[0][2], v[0][3], v[1][2], v[1][3]};
 #pragma unroll
@@ -389,7 +462,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
 
       // The slot is read: refill it with the next block of the stream.
       __syncwarp();
-      if (lane < 4) fence_proxy_async_smem();  // the lanes that copy
+      if (lane == 0) fence_proxy_async_smem();
       issue(slot);
       if (++slot == NS) {
         slot = 0;
@@ -402,13 +475,21 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     if (given_up) break;
 
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
-        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+      for (int off = 4; off < 32; off <<= 1) {
+        l[nt].x += __shfl_xor_sync(0xffffffffu, l[nt].x, off);
+        l[nt].y += __shfl_xor_sync(0xffffffffu, l[nt].y, off);
       }
+      if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          const int n = kSplit ? i / 2 : 0;  // the lane's group of tile i
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][i][e] += om[nt][n / 2][(e & 1) + 2 * (n & 1)];
+        }
+      }
+    }
 
     // The warps' (O, m, l) meet in shared memory, kMeet rows at a time.  The
     // lane's channels of row 8 nt + 2 t + e are g D/8 .. in the order of the tiles
@@ -427,7 +508,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
           for (int c = 0; c < C; ++c)
             ro[c] = make_float4(o[nt][2 * c][e], o[nt][2 * c][e + 2], o[nt][2 * c + 1][e],
                                 o[nt][2 * c + 1][e + 2]);
-          if (g == 0) meet_ml[mr] = make_float2(m[nt][e], l[nt][e]);
+          if (g == 0) meet_ml[mr] = make_float2(m[nt][e], e ? l[nt].y : l[nt].x);
         }
       }
       __syncthreads();

@@ -404,10 +404,10 @@ attn_status attn_read_kv4(const void* k_pages, const void* v_pages, void* k, voi
 
 /*
  * attn_fwd_paged over a 4-bit cache, with the same arguments, workspace
- * (attn_fwd_paged_workspace_bytes), masking and promises.  Values are what
- * attn_read_kv4 gives, RN16(m + c s); keys are m + c s unrounded (in chunks of more
- * than 16 query rows a key/value head a channel may be off by 2^-38 of the largest
- * of the 32 cached positions 32 i .. 32 i + 31, or of its query's largest).
+ * (attn_fwd_paged_workspace_bytes), masking and promises.  Values take part as
+ * RN16(m + c s), or as m + RN16(c s); keys as m + c s unrounded (a channel may be off
+ * by 2^-34 of its query's largest and, in chunks of more than 16 query rows a
+ * key/value head, by 2^-38 of the largest of the 32 cached positions 32 i .. 32 i + 31).
  * Cite: as attn_fwd_paged, and "8.3 FlashAttention-3", section 5.1.
  */
 attn_status attn_fwd_paged4(const void* q, const void* k_pages, const void* v_pages, void* o,

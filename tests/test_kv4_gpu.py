@@ -1,16 +1,17 @@
 """The paged cache in 4 bits: append, reading back, and attention over it, CUDA
 path vs the fp64 oracle.
 
-Attention: the cases are those of the 16-bit cache (test_paged_gpu.py).  Keys are
-the exact m + c s, values that in 16 bits.  A score's error d_j (u = finfo.eps / 2),
-with M = scale max sum |q| (|m + 8 s| + 8 s):
+Attention: the cases are those of the 16-bit cache (test_paged_gpu.py), keys and
+values the exact m + c s.  With u = finfo.eps / 2, a value is rounded to u (|v|), or c s
+is, to u (c s): together with P's rounding at most u of A = sum P (|v| + max(|v|, c s)).
+A score's error d_j, with M = scale max sum |q| (|m + 8 s| + 8 s):
 * few rows: a group's product with c - 8 sums 32 exact products, and s and m + 8 s are
   applied in fp32: at most 48 2^-24 M;
 * chunks: 2 d exact products and 12 more are summed in fp32, and of m + 8 s and the
   sum of q two terms of 11 bits are taken each: (2 d + 16) 2^-24 M + 2^-20 M.
 With e = 2^-20 + n 2^-24 + d_j for the exponential and the sums as there,
 |LSE - LSE_ref| <= e + 2^-23 |LSE| and, P_ij being off by d_j and by the row's
-l, |O - O_ref| <= (u + 2 e) A + u |O|.  P may exceed 1 by 2^8, which scales its
+l, |O - O_ref| <= (u + 2 e) (1 + u) A + u |O|.  P may exceed 1 by 2^8, which scales its
 rounding and l alike.
 
 Append: the scale and the minimum have to be those of the definition, and a code
@@ -83,9 +84,12 @@ def check4(x, o, lse, causal, scale=None):
     dt, d = x["q"].dtype, x["q"].shape[2]
     scale = d ** -0.5 if scale is None else scale
     cu, kv = x["cu"].cpu().numpy(), x["kv"].cpu().numpy()
-    k, v = exact4(x["k4"], dt), unpack4(x["v4"], dt)
-    O, L, A, _ = oracle.attention_paged(to64(x["q"]), k.cpu().numpy(), to64(v), x["table"].cpu().numpy(), cu, kv,
-                                        causal, scale)
+    k, v = exact4(x["k4"], dt), exact4(x["v4"], dt)
+    args = x["table"].cpu().numpy(), cu, kv, causal, scale
+    O, L, _, _ = oracle.attention_paged(to64(x["q"]), k.cpu().numpy(), to64(v), *args)
+    s, m, c = parts4(x["v4"], dt)
+    A = oracle.attention_paged(to64(x["q"]), k.cpu().numpy(), to64(v.abs() + torch.maximum(v.abs(), c * s)),
+                               *args)[0]
     s, m, _ = parts4(x["k4"], dt)
     few = x["max_q"] * (x["q"].shape[0] // k.shape[1]) <= 16
     err = (48 * 2.0 ** -24 if few else (2 * d + 16) * 2.0 ** -24 + 2.0 ** -20) * \
@@ -94,7 +98,7 @@ def check4(x, o, lse, causal, scale=None):
     u = torch.finfo(dt).eps / 2
     e = 2.0 ** -20 + int(kv.max()) * 2.0 ** -24 + err
     got, ref = to64(o)[:, live], O[:, live]
-    tol = (u + 2 * e) * A[:, live] + u * np.abs(ref) + torch.finfo(dt).smallest_normal * u
+    tol = (u + 2 * e) * (1 + u) * A[:, live] + u * np.abs(ref) + torch.finfo(dt).smallest_normal * u
     assert np.isfinite(got).all()
     assert (np.abs(got - ref) <= tol).all(), float(np.max(np.abs(got - ref) - tol))
     gl, rl = to64(lse)[:, live], L[:, live]
