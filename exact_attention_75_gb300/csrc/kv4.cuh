@@ -14,10 +14,12 @@
 // Values take part in products as RN_T(m + c s), one fused multiply-add of two
 // 16-bit values at a time, or as m and RN_T(c s): half a step of T, the error that a
 // 16-bit cache has in the first place.  Keys do not: an error of 2^-9 a channel, even of 2^-12, shows in
-// the log-sum-exp of a short sequence.  The codes less 8 have three significant
-// bits, so their product with a query, and with a scale of 8 bits, is exact, and
-//   q . k = sum over groups of  sum q (c - 8) s  +  (m + 8 s) sum q,
-// the second part in 32 bits or split into 16-bit terms.
+// the log-sum-exp of a short sequence.  A code's product with a query is exact, and
+// so is that of c - 8, which has three significant bits, with a scale of 8 bits; so
+//   q . k = sum over groups of  s sum q c  +  m sum q
+// is taken with s and m in 32 bits (decoding), or as
+//           sum over groups of  sum q ((c - 8) s)  +  (m + 8 s) sum q
+// with the second part split into 16-bit terms (chunks).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -55,19 +57,16 @@ __device__ __forceinline__ uint32_t kv4_codes(uint32_t w) {
   return r;
 }
 
-// The codes of a word less 8 in fp16, nibbles i and i + 4 side by side; those of odd i
-// times 16, since their bits are taken where they stand (one shift a word, not three).
-__device__ __forceinline__ void kv4_centred(uint32_t w, uint32_t (&v)[4]) {
+// The codes of a word in fp16, nibbles i and i + 4 side by side; those of odd i times
+// 16, since their bits are taken where they stand (one shift a word, not three).
+__device__ __forceinline__ void kv4_halves(uint32_t w, uint32_t (&v)[4]) {
   const uint32_t x[2] = {w, w >> 8};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 4; ++i)
     asm("sub.rn.f16x2 %0, %1, %2;"
-        : "=r"(v[2 * i])
-        : "r"(and_or(x[i], 0x000F000Fu, 0x64006400u)), "r"(0x64086408u));
-    asm("sub.rn.f16x2 %0, %1, %2;"
-        : "=r"(v[2 * i + 1])
-        : "r"(and_or(x[i], 0x00F000F0u, 0x64006400u)), "r"(0x64806480u));
-  }
+        : "=r"(v[i])
+        : "r"(and_or(x[i / 2], i & 1 ? 0x00F000F0u : 0x000F000Fu, 0x64006400u)),
+          "r"(0x64006400u));
 }
 
 // What the codes of a word stand for, nibbles i and i + 4 side by side.

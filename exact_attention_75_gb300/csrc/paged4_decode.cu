@@ -19,8 +19,8 @@
 //      operand register;
 //   V: it reads channels g D/8 .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9; two keys'
 //      half words side by side give the pairs of keys that an operand holds.
-// A group's product is taken with c - 8 in fp16, the query scaled into its range by a
-// power of two, and s and m + 8 s of its keys are applied to it and to the sum of the
+// A group's product is taken with the codes in fp16, the query scaled into its range by
+// a power of two, and s and m of its keys are applied to it and to the sum of the
 // query's channels in 32 bits: keys lose nothing.
 // Values are m + c s rounded to 16 bits, or, in bf16, c s rounded, and m by a product of
 // its own: (128 + c) s - 128 s is one instruction where c s + m takes two.
@@ -174,17 +174,17 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     // A page outside the cache (reported): any of it.  Past the sequence a unit is
     // what its page holds, or, in a page of its own, what the slot held: numbers that
     // count nothing.
-    const int page0 = stream.page(p, 0, lane), page1 = stream.page(p, 1, lane);
+    const bool two = p.page == kUnit;  // a unit a page
+    const int page0 = stream.page(p, 0, lane), page1 = two ? stream.page(p, 1, lane) : 0;
     if (lane == 0) {
       auto copy = [&](int page, int u, int units) {
         const size_t row = (((size_t)max(page, 0) * p.Hkv + stream.ahead.head) << p.page_log2) +
-                           stream.row(p, u, warp);
+                           stream.row(p, u);
         const uint32_t dst = ring + (uint32_t)(s * L::kSlotBytes + u * L::kUnitBytes);
         const uint32_t bytes = (uint32_t)(units * L::kUnitBytes);
         bulk_load(dst, p.k4 + row * L::kRow, bytes, bar(s));
         bulk_load(dst + 2 * L::kUnitBytes, p.v4 + row * L::kRow, bytes, bar(s));
       };
-      const bool two = p.page == kUnit;  // a unit a page
       const int units = two && page1 == -2 ? 1 : 2;
       mbar_arrive_expect_tx(bar(s), (uint32_t)(2 * units * L::kUnitBytes));
       copy(page0, 0, two ? 1 : 2);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     const PagedSeq sq = w.sq;
     const int rows = min(kPagedRows, sq.qlen * p.G);
     // Q^T: of row 8 nt + g the channels that the lane has of the keys, those of odd
-    // nibbles over 16 (kv4_centred); of rows 8 nt + 2 t and the next the sums over each
+    // nibbles over 16 (kv4_halves); of rows 8 nt + 2 t and the next the sums over each
     // group, and what takes their products to base 2 (1e-37 .. 1e37, as in the tile
     // kernel).
     uint32_t qb[NT][KS][2];
@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
       l[nt] = make_float2(0.f, 0.f);
     }
     bool aborted = false;
+    int key0 = first_key(w, warp, 0) - W * kKeys;
 #pragma unroll 1
     for (int j = 0; j < nbw; ++j) {
       if (!__all_sync(0xffffffffu, mbar_wait(bar(slot), parity, wd, 76))) {
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
       }
       ++it;
       const uint32_t block = ring + (uint32_t)(slot * L::kSlotBytes);
-      const int key0 = first_key(w, warp, j);
+      key0 += W * kKeys;
 
       // S^T: x[nt][2 u + h] is rows 8 nt + 2 t and the next, key key0 + 16 u + 8 h + g.
       float2 x[NT][4];
@@ -311,12 +312,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           uint32_t v[2][4];
-          float2 par[2];  // s, m + 8 s
+          float2 par[2];  // s, m
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             par[h] = unpack2<BF16>(kp[h][c]);
-            par[h].y = fmaf(8.f, par[h].x, par[h].y);
-            kv4_centred(kw[h][c], v[h]);
+            kv4_halves(kw[h][c], v[h]);
           }
           const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]};
           const uint32_t a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float2& z = x[nt][2 * u + h];
-              z = __ffma2_rn(make_float2(par[h].x, par[h].x), make_float2(y[2 * h], y[2 * h + 1]), z);
-              z = __ffma2_rn(make_float2(par[h].y, par[h].y), qsum[nt][c], z);
+              z.x = fmaf(par[h].y, qsum[nt][c].x, fmaf(par[h].x, y[2 * h], z.x));
+              z.y = fmaf(par[h].y, qsum[nt][c].y, fmaf(par[h].x, y[2 * h + 1], z.y));
             }
           }
         }

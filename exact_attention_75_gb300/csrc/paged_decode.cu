@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t dk = ring + (uint32_t)(s * L::kSlotBytes);
       const uint32_t dv = dk + L::kChunks * kBoxBytes;
       const int z = page >= 0 ? page * p.Hkv + stream.ahead.head : -1;  // -1: the box reads zeros
-      const int y = stream.row(p, 0, warp);
+      const int y = stream.row(p, 0);
       mbar_arrive_expect_tx(bar(s), L::kSlotBytes);
 #pragma unroll
       for (int c = 0; c < L::kChunks; ++c) {
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int dn = 0; dn < DN; ++dn) o[dn][0] = o[dn][1] = o[dn][2] = o[dn][3] = 0.f;
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
     bool aborted = false;
+    int key0 = first_key(w, warp, 0) - kWarps * kKeys;
 #pragma unroll 1
     for (int j = 0; j < nbw; ++j) {
       const int s = (int)(it % NS);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++it;
       const uint32_t tk = ring + (uint32_t)(s * L::kSlotBytes);
       const uint32_t tv = tk + L::kChunks * kBoxBytes;
-      const int key0 = first_key(w, warp, j);
+      key0 += kWarps * kKeys;
       if (key0 + kKeys > sq.klen) {
         // Rows past the sequence's last key hold whatever the page held (P is
         // 0 there, but 0 x NaN is not): zero those rows of V.

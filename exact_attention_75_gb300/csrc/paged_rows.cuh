@@ -72,20 +72,21 @@ template <int W, int K>
 struct BlockStream {
   static constexpr int kUnits = K / kUnit;
   Walk<W, K> ahead;
-  int j, n, pages;
+  int key, left;  // the block's first key; blocks of the piece, this one included
+  int pages, at;  // at: the lane that holds the page of the block's first unit
   uint32_t issued;
 
   __device__ __forceinline__ BlockStream(const PagedParams& p, const Walk<W, K>& w, int warp,
                                          int lane)
-      : ahead(w), j(0), n(w.left > 0 ? warp_blocks(w, warp) : 0), pages(-2), issued(0) {
-    settle(p, warp, lane);
+      : ahead(w), key(0), left(0), pages(-2), at(0), issued(0) {
+    if (w.left > 0) begin(p, warp, lane);
   }
   // Whether there is a block to issue.
-  __device__ __forceinline__ bool more() const { return ahead.left > 0; }
+  __device__ __forceinline__ bool more() const { return left > 0; }
   // The page of unit u of the block: -1 if it is none of the cache (lane 0 reports
   // it), -2 if the unit lies past the sequence.
   __device__ __forceinline__ int page(const PagedParams& p, int u, int lane) const {
-    const int page = __shfl_sync(0xffffffffu, pages, (j * kUnits + u) & 31);
+    const int page = __shfl_sync(0xffffffffu, pages, at + u);
     if (page >= p.n_pages || page == -1) {
       if (lane == 0)
         atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(ahead.b, 0xFFFF) << 16));
@@ -94,31 +95,39 @@ struct BlockStream {
     return page;
   }
   // The unit's first row in its page.
-  __device__ __forceinline__ int row(const PagedParams& p, int u, int warp) const {
-    return (first_key(ahead, warp, j) + u * kUnit) & (p.page - 1);
+  __device__ __forceinline__ int row(const PagedParams& p, int u) const {
+    return (key + u * kUnit) & (p.page - 1);
   }
   __device__ __forceinline__ void next(const PagedParams& p, int warp, int lane) {
     ++issued;
-    ++j;
-    settle(p, warp, lane);
+    key += W * K;
+    at += kUnits;
+    if (--left == 0) {
+      ahead.advance(p, p.max_q);
+      if (ahead.left > 0) begin(p, warp, lane);
+    } else if (at == 32) {
+      read(p, lane);
+    }
   }
 
  private:
-  // Goes to the next block, or to left <= 0.
-  __device__ __forceinline__ void settle(const PagedParams& p, int warp, int lane) {
-    while (ahead.left > 0 && j >= n) {
+  // Goes to the first block of the warp from the current piece on, if there is one.
+  __device__ __forceinline__ void begin(const PagedParams& p, int warp, int lane) {
+    while ((left = warp_blocks(ahead, warp)) == 0) {
       ahead.advance(p, p.max_q);
-      n = warp_blocks(ahead, warp);
-      j = 0;
+      if (ahead.left <= 0) return;
     }
-    if (ahead.left > 0 && (j * kUnits & 31) == 0) {
-      const int at = j + lane / kUnits;
-      const int key = first_key(ahead, warp, at) + lane % kUnits * kUnit;
-      pages = at < n && key < ahead.sq.klen
-                  ? max(__ldg(p.block_table + (size_t)ahead.b * p.max_pages +
-                              (key >> p.page_log2)), -1)
-                  : -2;
-    }
+    key = first_key(ahead, warp, 0);
+    read(p, lane);
+  }
+  // The pages of the next 32 units, as many as the piece has blocks for.
+  __device__ __forceinline__ void read(const PagedParams& p, int lane) {
+    const int n = lane / kUnits, k = key + n * W * K + lane % kUnits * kUnit;
+    at = 0;
+    pages = n < left && k < ahead.sq.klen
+                ? max(__ldg(p.block_table + (size_t)ahead.b * p.max_pages + (k >> p.page_log2)),
+                      -1)
+                : -2;
   }
 };
 

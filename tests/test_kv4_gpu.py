@@ -4,11 +4,12 @@ path vs the fp64 oracle.
 Attention: the cases are those of the 16-bit cache (test_paged_gpu.py), keys and
 values the exact m + c s.  With u = finfo.eps / 2, a value is rounded to u (|v|), or c s
 is, to u (c s): together with P's rounding at most u of A = sum P (|v| + max(|v|, c s)).
-A score's error d_j, with M = scale max sum |q| (|m + 8 s| + 8 s):
-* few rows: a group's product with c - 8 sums 32 exact products, and s and m + 8 s are
-  applied in fp32: at most 48 2^-24 M;
+A score's error d_j:
+* few rows: a group's product with c sums 32 exact products, and s and m are applied
+  in fp32: at most 48 2^-24 M with M = scale max sum |q| (|m| + 15 s);
 * chunks: 2 d exact products and 12 more are summed in fp32, and of m + 8 s and the
-  sum of q two terms of 11 bits are taken each: (2 d + 16) 2^-24 M + 2^-20 M.
+  sum of q two terms of 11 bits are taken each: (2 d + 16) 2^-24 M + 2^-20 M with
+  M = scale max sum |q| (|m + 8 s| + 8 s).
 With e = 2^-20 + n 2^-24 + d_j for the exponential and the sums as there,
 |LSE - LSE_ref| <= e + 2^-23 |LSE| and, P_ij being off by d_j and by the row's
 l, |O - O_ref| <= (u + 2 e) (1 + u) A + u |O|.  P may exceed 1 by 2^8, which scales its
@@ -93,7 +94,7 @@ def check4(x, o, lse, causal, scale=None):
     s, m, _ = parts4(x["k4"], dt)
     few = x["max_q"] * (x["q"].shape[0] // k.shape[1]) <= 16
     err = (48 * 2.0 ** -24 if few else (2 * d + 16) * 2.0 ** -24 + 2.0 ** -20) * \
-        largest(x, causal, scale, (m + 8 * s).abs() + 8 * s)
+        largest(x, causal, scale, m.abs() + 15 * s if few else (m + 8 * s).abs() + 8 * s)
     live = slice(0, int(cu[-1]))
     u = torch.finfo(dt).eps / 2
     e = 2.0 ** -20 + int(kv.max()) * 2.0 ** -24 + err
