@@ -39,11 +39,11 @@ __device__ __forceinline__ uint32_t order(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t cluster_load(uint32_t addr, int rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];"
-               : "=r"(v)
-               : "r"(cluster_addr(addr, rank))
+__device__ __forceinline__ uint4 cluster_load(const uint32_t* x, int rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr(smem_u32(x), rank))
                : "memory");
   return v;
 }
@@ -69,12 +69,19 @@ struct Item {
   }
 };
 
+// A CTA's positions in runs of kHeld x kThreads, kHeld to a thread (kThreads apart,
+// so that a run is in order by (j, thread)); the first run's weights stay in
+// registers.
+constexpr int kHeld = 16;
+constexpr int kRun = kHeld * kThreads;
+
 __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictParams p,
                                                                    int cluster) {
-  __shared__ uint32_t count[kBins];  // of the CTA's positions, by digit
-  __shared__ uint32_t scan[kThreads / 32];
+  __shared__ __align__(16) uint32_t count[kBins];  // of the CTA's positions, by digit
+  __shared__ uint32_t scan[kHeld * kThreads / 32];
   __shared__ uint32_t chosen, above, own[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
   grid_wait();
   const Item it(p, cluster);
   int* const kept = p.kept + ((size_t)it.b * p.Hkv + it.head) * p.budget;
@@ -92,14 +99,23 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
   const int middle = it.n - p.sinks - p.recent;
   const int m0 = p.sinks + (int)((int64_t)middle * it.rank / cluster);
   const int m1 = p.sinks + (int)((int64_t)middle * (it.rank + 1) / cluster);
-  auto weight = [&](int at) {
-    const int64_t row = it.row(p, at);
-    if (row < 0) {
-      report_bad(p.status, kBadPage, it.b);
-      return 0u;
+  // The weights of a run that begins at r0, eight on their way together.
+  auto read = [&](int r0, uint32_t (&w)[kHeld]) {
+#pragma unroll
+    for (int j0 = 0; j0 < kHeld; j0 += 8) {
+      int64_t row[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = r0 + (j0 + j) * kThreads + tid;
+        row[j] = at < m1 ? it.row(p, at) : -2;
+        if (row[j] == -1) report_bad(p.status, kBadPage, it.b);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j0 + j] = row[j] >= 0 ? order(p.weights[row[j]]) : 0u;
     }
-    return order(p.weights[row]);
   };
+  uint32_t first[kHeld];
+  read(m0, first);
   // want: positions still to be chosen among those whose first digits are `prefix`;
   // more: of the CTA's positions those that lie above it.
   uint32_t want = (uint32_t)(p.budget - p.sinks - p.recent), prefix = 0, more = 0, equal = 0;
@@ -107,22 +123,34 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
     const int shift = digit == 0 ? 21 : (digit == 1 ? 10 : 0), bits = digit == 2 ? 10 : 11;
     for (int i = tid; i < kBins; i += kThreads) count[i] = 0u;
     __syncthreads();
-    for (int at = m0 + tid; at < m1; at += kThreads) {
-      const uint32_t w = weight(at);
-      if (digit == 0 || w >> (shift + bits) == prefix)
-        atomicAdd(count + (w >> shift & ((1u << bits) - 1)), 1u);
+    auto add = [&](int r0, const uint32_t (&w)[kHeld]) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+        if (r0 + j * kThreads + tid < m1 && (digit == 0 || w[j] >> (shift + bits) == prefix))
+          atomicAdd(count + (w[j] >> shift & ((1u << bits) - 1)), 1u);
+    };
+    add(m0, first);
+    for (int r0 = m0 + kRun; r0 < m1; r0 += kRun) {
+      uint32_t w[kHeld];
+      read(r0, w);
+      add(r0, w);
     }
     cluster_sync();
     // A thread has four digits, the largest first, and scans over the cluster's counts.
     const int top = kBins - 1 - 4 * tid;
-    uint32_t c[4], mine = 0, sum = 0;
+    uint4 got[kEvictCluster];  // all on their way together
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = 0u;
-      for (int r = 0; r < cluster; ++r) c[i] += cluster_load(smem_u32(count + top - i), r);
-      mine += count[top - i];
-      sum += c[i];
+    for (int r = 0; r < kEvictCluster; ++r)
+      got[r] = r < cluster ? cluster_load(count + top - 3, r) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t c[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int r = 0; r < kEvictCluster; ++r) {
+      c[0] += got[r].w;
+      c[1] += got[r].z;
+      c[2] += got[r].y;
+      c[3] += got[r].x;
     }
+    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
     uint32_t incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -135,29 +163,26 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
     uint32_t before = incl - sum;
     for (int w = 0; w < warp; ++w) before += scan[w];
     uint32_t here = 0;  // the CTA's positions above the chosen digit
-    if (before + sum < want) {
-      here = mine;
-    } else if (before < want) {
-      int i = 0;
-      for (; before + c[i] < want; ++i) {
-        before += c[i];
-        here += count[top - i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t mine = count[top - i];
+      if (before + c[i] < want) {
+        here += mine;
+      } else if (before < want) {  // one thread, one digit
+        chosen = (uint32_t)(top - i);
+        above = before;
+        own[1] = mine;
       }
-      chosen = (uint32_t)(top - i);
-      above = before;
-      own[1] = count[top - i];
+      before += c[i];
     }
-    if (here > 0) atomicAdd(own, here);
+    here = __reduce_add_sync(0xffffffffu, here);
+    if (lane == 0 && here > 0) atomicAdd(own, here);
     __syncthreads();
     prefix = prefix << bits | chosen;
     want -= above;
     more += own[0];
     equal = own[1];
     cluster_sync();  // the others have read this CTA's counts
-  }
-  if (want == 0) {  // nothing of the middle stays
-    prefix = 0xFFFFFFFFu;
-    more = equal = 0u;
   }
   // Of the CTAs before this one: what lies above the limit, what equals it.
   if (tid == 0) {
@@ -166,30 +191,58 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
   }
   cluster_sync();
   uint32_t gt = 0, eq = 0;
-  for (int r = 0; r < it.rank; ++r) {
-    gt += cluster_load(smem_u32(count), r);
-    eq += cluster_load(smem_u32(count + 1), r);
+#pragma unroll
+  for (int r = 0; r < kEvictCluster; ++r) {
+    if (r >= it.rank) break;
+    const uint4 x = cluster_load(count, r);
+    gt += x.x;
+    eq += x.y;
   }
   cluster_sync();  // the others have read
-  const uint32_t limit = prefix;
-  const bool none = want == 0;
-  for (int t0 = m0; t0 < m1 && !none; t0 += kThreads) {
-    const int at = t0 + tid;
-    const uint32_t w = at < m1 ? weight(at) : 0u;
-    const bool is_gt = at < m1 && w > limit, is_eq = at < m1 && w == limit;
-    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-    if (lane == 0) scan[warp] = (uint32_t)__popc(bg) | (uint32_t)__popc(be) << 16;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
+  for (int r0 = m0; r0 < m1 && want > 0; r0 += kRun) {  // (want 0: nothing of the middle stays)
+    if (r0 > m0) read(r0, first);
+    uint32_t above_in[kHeld], equal_in[kHeld];  // ballots
 #pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) {
-      if (k < warp) before += scan[k];
-      all += scan[k];
+    for (int j = 0; j < kHeld; ++j) {
+      const bool in = r0 + j * kThreads + tid < m1;
+      above_in[j] = __ballot_sync(0xffffffffu, in && first[j] > prefix);
+      equal_in[j] = __ballot_sync(0xffffffffu, in && first[j] == prefix);
+      if (lane == 0)
+        scan[j * kWarps + warp] =
+            (uint32_t)__popc(above_in[j]) | (uint32_t)__popc(equal_in[j]) << 16;
     }
-    const uint32_t under = (1u << lane) - 1;
-    const uint32_t g = gt + (before & 0xFFFFu) + __popc(bg & under);
-    const uint32_t e = eq + (before >> 16) + __popc(be & under);
-    if (is_gt || (is_eq && e < want)) kept[p.sinks + g + min(e, want)] = at;
+    __syncthreads();
+    // Each warp scans all counts of the run (kHeld x kWarps, in order), eight a lane.
+    constexpr int kEach = kHeld * kWarps / 32;
+    uint32_t part[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      part[i] = sum;
+      sum += scan[lane * kEach + i];
+    }
+    uint32_t incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += up;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+    const uint32_t before = incl - sum, under = (1u << lane) - 1;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int e = j * kWarps + warp;  // whose count comes before
+      uint32_t off = __shfl_sync(0xffffffffu, before, e / kEach);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const uint32_t x = __shfl_sync(0xffffffffu, part[i], e / kEach);
+        if (e % kEach == i) off += x;
+      }
+      const uint32_t g = gt + (off & 0xFFFFu) + __popc(above_in[j] & under);
+      const uint32_t q = eq + (off >> 16) + __popc(equal_in[j] & under);
+      const bool is_gt = above_in[j] >> lane & 1, is_eq = equal_in[j] >> lane & 1;
+      if (is_gt || (is_eq && q < want))
+        kept[p.sinks + g + min(q, want)] = r0 + j * kThreads + tid;
+    }
     gt += all & 0xFFFFu;
     eq += all >> 16;
     __syncthreads();
@@ -202,13 +255,13 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
 }
 
 // Vec: what a row is moved in, VPR: of them a row has.  A round moves the rows that
-// the cluster's threads hold UNROLL vectors of K or V each of.
+// the cluster's threads hold kUnroll vectors of K or V each of.
 template <typename Vec, int VPR>
 __global__ void __launch_bounds__(kThreads, 2) evict_move_kernel(const EvictParams p, int cluster) {
   constexpr int kUnroll = 8;
   constexpr int kPerCta = kUnroll * kThreads / (2 * VPR);  // rows of a round a CTA has
   constexpr int kVecs = kPerCta * 2 * VPR;
-  __shared__ int64_t from[kPerCta], to[kPerCta];
+  __shared__ int64_t from[2][kPerCta], to[2][kPerCta];
   const int tid = threadIdx.x;
   grid_wait();
   const Item it(p, cluster);
@@ -217,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_move_kernel(const EvictPara
     return;
   }
   const int* const kept = p.kept + ((size_t)it.b * p.Hkv + it.head) * p.budget;
-  for (int r0 = p.sinks; r0 < p.budget; r0 += kPerCta * cluster) {
-    // The round's rows of this CTA (from -1: it stays where it is).
+  // The rows of the round that begins at r0 (from -1: it stays where it is).
+  auto find = [&](int r0, int buf) {
     for (int i = tid; i < kPerCta; i += kThreads) {
       const int dst = r0 + it.rank * kPerCta + i;
       int64_t f = -1, t = -1;
@@ -233,36 +286,41 @@ __global__ void __launch_bounds__(kThreads, 2) evict_move_kernel(const EvictPara
           }
         }
       }
-      from[i] = f;
-      to[i] = t;
+      from[buf][i] = f;
+      to[buf][i] = t;
     }
-    __syncthreads();
+  };
+  find(p.sinks, 0);
+  __syncthreads();
+  int buf = 0;
+  for (int r0 = p.sinks; r0 < p.budget; r0 += kPerCta * cluster, buf ^= 1) {
     Vec x[kUnroll];
     float w[(kPerCta + kThreads - 1) / kThreads];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int v = u * kThreads + tid, i = v / (2 * VPR), c = v % (2 * VPR);
-      if (v >= kVecs || from[i] < 0) continue;
+      if (v >= kVecs || from[buf][i] < 0) continue;
       const uint8_t* pages = c < VPR ? p.k_pages : p.v_pages;
-      x[u] = *(reinterpret_cast<const Vec*>(pages) + from[i] * VPR + c % VPR);
+      x[u] = *(reinterpret_cast<const Vec*>(pages) + from[buf][i] * VPR + c % VPR);
     }
 #pragma unroll
     for (int j = 0; j < (kPerCta + kThreads - 1) / kThreads; ++j) {
       const int i = j * kThreads + tid;
-      if (i < kPerCta && from[i] >= 0) w[j] = p.weights[from[i]];
+      if (i < kPerCta && from[buf][i] >= 0) w[j] = p.weights[from[buf][i]];
     }
-    cluster_sync();  // every row of the round has been read
+    find(r0 + kPerCta * cluster, buf ^ 1);  // the next round's, while the rows are on their way
+    cluster_sync();                         // every row of the round has been read
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int v = u * kThreads + tid, i = v / (2 * VPR), c = v % (2 * VPR);
-      if (v >= kVecs || from[i] < 0) continue;
+      if (v >= kVecs || from[buf][i] < 0) continue;
       uint8_t* pages = c < VPR ? p.k_pages : p.v_pages;
-      *(reinterpret_cast<Vec*>(pages) + to[i] * VPR + c % VPR) = x[u];
+      *(reinterpret_cast<Vec*>(pages) + to[buf][i] * VPR + c % VPR) = x[u];
     }
 #pragma unroll
     for (int j = 0; j < (kPerCta + kThreads - 1) / kThreads; ++j) {
       const int i = j * kThreads + tid;
-      if (i < kPerCta && from[i] >= 0) p.weights[to[i]] = w[j];
+      if (i < kPerCta && from[buf][i] >= 0) p.weights[to[buf][i]] = w[j];
     }
     __syncthreads();  // from and to are read
   }

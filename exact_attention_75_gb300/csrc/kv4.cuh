@@ -26,6 +26,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "sm103_ptx.cuh"
+
 namespace attn {
 
 constexpr int kKv4Group = 32;
@@ -129,6 +131,45 @@ __device__ __forceinline__ float2 to_fp16_range(uint32_t top) {
 __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
   return b < 0x7F800000u ? b : 0u;
+}
+
+// A row of queries as the operand that meets kv4_halves: a quad of lanes has the row,
+// lane t channels 32 c + 8 t .. of each group in q[c], which become fp16 in channel
+// pairs (i, i + 4), scaled into its range by a power of two, those of odd i over 16.
+// sums: of the scaled row over each group.  Returns the factor that undoes the
+// scaling.  All lanes of the warp call this.
+template <bool BF16, int C>
+__device__ __forceinline__ float kv4_query(uint4 (&q)[C], float* sums) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint32_t y[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2<BF16>(y[i]);
+      top = max(top, max(finite_bits(f.x), finite_bits(f.y)));
+    }
+  }
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const float2 f = to_fp16_range<9>(top);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint32_t y[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+    float z[8], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2<BF16>(y[i]);
+      z[2 * i] = v.x * f.x;
+      z[2 * i + 1] = v.y * f.x;
+      sum += z[2 * i] + z[2 * i + 1];
+    }
+    q[c] = make_uint4(pack_f16x2(z[0], z[4]), pack_f16x2(z[1] * 0.0625f, z[5] * 0.0625f),
+                      pack_f16x2(z[2], z[6]), pack_f16x2(z[3] * 0.0625f, z[7] * 0.0625f));
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sums[c] = sum + __shfl_xor_sync(0xffffffffu, sum, 2);
+  }
+  return f.y;
 }
 
 // The eight values of a code word in channel order; par: s and m of its group.

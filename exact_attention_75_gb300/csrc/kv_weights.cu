@@ -4,7 +4,7 @@
 //         rows i and the head's query heads of exp(scale q_i k_j - LSE_i).
 //
 // The log-sum-exp is given, so each key is read once and no row waits for another:
-// a warp takes 16 keys and all rows that see them, 8 at a time.  The product is
+// a warp takes 16 keys and the rows that see them, 8 at a time.  The product is
 //   S^T = K Q^T  (A = 16 keys x 16 channels, B = 8 query rows),
 // keys going from memory straight into the operand's registers (a lane reads 16
 // bytes of keys g and g + 8; the contraction may take the channels in any order), the
@@ -12,9 +12,13 @@
 // that has the key, and four lanes add theirs up at the end: no atomics, the
 // same bits from run to run.
 //
-// Of a cache in 4 bits (kv4.cuh) the product is taken with c - 8, and s and m + 8 s
-// are applied to each group of 32 channels in 32 bits; the queries' sums over a
-// group, which m takes, are a product with ones.
+// Queries are put in shared memory as operands, 64 rows at a time (a tile a warp): a
+// warp's 8 rows of a decoding step then stay in registers, and the tiles of a longer
+// run are read by all warps for all their keys.  Each 64 rows go over the keys once;
+// from the second time on the keys come from L2.
+//
+// Of a cache in 4 bits (kv4.cuh) the product is taken with the codes in fp16, as in the
+// decoding kernel.
 //
 // Work.  A block of 16 keys costs kRead + its tiles of 8 rows; the blocks of all
 // sequences and heads laid end to end are shared out evenly over the grid, and
@@ -98,6 +102,11 @@ __device__ __forceinline__ Share find_share(const PagedParams& p) {
   return share;
 }
 
+// Last key that token i of a sequence sees.
+__device__ __forceinline__ int last_key(const PagedParams& p, const PagedSeq& sq, int i) {
+  return min(p.causal ? i + sq.klen - sq.qlen : sq.klen, sq.klen - 1);
+}
+
 // A block's keys as operand A: register pairs of row g (h = 0) and g + 8.
 template <int D, bool KV4>
 struct Keys {
@@ -137,17 +146,24 @@ struct Keys {
   }
 };
 
+// A row of queries beside its operand: the sums over its groups and what takes its
+// products to base 2 (KV4), its log-sum-exp in base 2, the last key it sees.
+struct RowInfo {
+  float qsum[4];
+  float to2, lse;
+  int lim, unused;
+};
+
 template <int D, bool BF16, bool KV4>
 __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsParams a) {
   constexpr int C = D / 32;
+  __shared__ uint4 tiles[kWarps][C][32];  // operand B of 8 rows: by lane
+  __shared__ __align__(16) RowInfo info[kWarps * 8];
   const PagedParams& p = a.paged;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   grid_wait();
   const Share share = find_share(p);
-  const int step_i = 8 / p.G, step_h = 8 % p.G;  // tokens and heads between tiles
-  constexpr uint32_t kOnes = BF16 ? 0x3F803F80u : 0x3C003C00u;
-  const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
 
   long long at = share.at;  // where sequence b begins
   for (int b = share.b; at < share.end; ++b) {
@@ -170,127 +186,103 @@ __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsPa
         if (!k.valid && page != -2 && lane == 0)
           atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(b, 0xFFFF) << 16));
       };
-      int u = u0 + warp;
-      Keys<D, KV4> k;
-      get(k, page_of(u), u);
-      int page = page_of(u + kWarps);
-      // Queries of a tile: rows 8 n + g; and of rows 8 n + 2 t and the next the
-      // log-sum-exp and the last key seen.
-      uint4 q[C];
-      float qsum[C][2], lse[2];
-      int lim[2];
-      int qi, qh, ri[2], rh[2];  // token and head of those rows
-      auto first_tile = [&]() {
-        qi = g / p.G, qh = g - qi * p.G;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) ri[e] = (2 * t + e) / p.G, rh[e] = 2 * t + e - ri[e] * p.G;
-      };
-      auto next = [&](int& i, int& h) {
-        i += step_i;
-        h += step_h;
-        if (h >= p.G) h -= p.G, ++i;
-      };
-      auto load_tile = [&]() {
-#pragma unroll
-        for (int c = 0; c < C; ++c) q[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (qi < sq.qlen) {
-          const uint4* x = reinterpret_cast<const uint4*>(
-              static_cast<const uint16_t*>(p.q) +
-              ((size_t)(head * p.G + qh) * p.total + sq.s0 + qi) * D);
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            q[c] = __ldg(x + 4 * c + t);
-            if constexpr (KV4) {  // channel pairs (i, i + 4), as the codes have them
-              const uint4 y = q[c];
-              q[c] = make_uint4(__byte_perm(y.x, y.z, 0x5410), __byte_perm(y.x, y.z, 0x7632),
-                                __byte_perm(y.y, y.w, 0x5410), __byte_perm(y.y, y.w, 0x7632));
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool live = ri[e] < sq.qlen;
-          lim[e] = !live ? -1 : min(p.causal ? ri[e] + sq.klen - sq.qlen : sq.klen, sq.klen - 1);
-          lse[e] = !live ? 0.f
-                         : 1.4426950408889634f *
-                               __ldg(p.lse + (size_t)(head * p.G + rh[e]) * p.total + sq.s0 + ri[e]);
-        }
-        if constexpr (KV4) {
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816<BF16>(y, ones, q[c].x, q[c].y);
-            mma16816<BF16>(y, ones, q[c].z, q[c].w);
-            qsum[c][0] = y[0];
-            qsum[c][1] = y[1];
-          }
-        }
-      };
-      first_tile();
-      if (rows <= 8) load_tile();
-
-      for (; u < u1; u += kWarps) {
-        const Keys<D, KV4> cur = k;
-        get(k, page, u + kWarps);
-        page = page_of(u + 2 * kWarps);
-        if (!cur.valid) continue;
-        const int key0 = u * kKeys;
-        // 4 bits: the codes less 8 in 16, and s, m + 8 s
-        uint32_t v[KV4 ? C : 1][2][4];
-        float2 par[KV4 ? C : 1][2];
-        if constexpr (KV4) {
+      for (int r0 = 0; r0 < rows; r0 += 8 * kWarps) {
+        // The first keys are on their way while the queries are prepared.
+        int u = u0 + warp;
+        Keys<D, KV4> k;
+        get(k, page_of(u), u);
+        int page = page_of(u + kWarps);
+        const int n_tiles = min(kWarps, (rows - r0 + 7) / 8);
+        __syncthreads();  // the tiles before have been read
+        if (warp < n_tiles) {
+          const int r = r0 + 8 * warp + g, i = r / p.G, h = r - i * p.G;
+          const bool live = i < sq.qlen;
+          const size_t row = live ? (size_t)(head * p.G + h) * p.total + sq.s0 + i : 0;
+          const uint4* x =
+              reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * D);
+          uint4 q[C];
 #pragma unroll
           for (int c = 0; c < C; ++c)
+            q[c] = live ? __ldg(x + 4 * c + t) : make_uint4(0u, 0u, 0u, 0u);
+          RowInfo ri = {};
+          ri.to2 = p.scale_log2;
+          if constexpr (KV4) {
+            const float undo = kv4_query<BF16, C>(q, ri.qsum);
+            ri.to2 = fminf(fmaxf(p.scale_log2 * undo, 1e-37f), 1e37f);
+          }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              par[c][h] = unpack2<BF16>(cur.par[h][c]);
-              par[c][h].y = fmaf(8.f, par[c][h].x, par[c][h].y);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[c][h][i] = kv4_codes<BF16, 8>(cur.code[h][c] >> (4 * i));
-            }
+          for (int c = 0; c < C; ++c) tiles[warp][c][lane] = q[c];
+          ri.lim = live ? last_key(p, sq, i) : -1;
+          ri.lse = live ? 1.4426950408889634f * __ldg(p.lse + row) : 0.f;
+          if (t == 0) info[8 * warp + g] = ri;
         }
-        float sum[2] = {0.f, 0.f};
-        if (rows > 8) first_tile();
-        for (int r = 0; r < rows; r += 8) {
-          if (rows > 8) load_tile();
-          float x[4] = {0.f, 0.f, 0.f, 0.f};  // key g + 8 (e / 2), row 2 t + e % 2 of the tile
+        __syncthreads();
+        uint4 q[C];
+        RowInfo ri[2];
+        auto load_tile = [&](int n) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            if constexpr (KV4) {
-              const uint32_t a0[4] = {v[c][0][0], v[c][1][0], v[c][0][1], v[c][1][1]};
-              const uint32_t a1[4] = {v[c][0][2], v[c][1][2], v[c][0][3], v[c][1][3]};
-              float y[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816<BF16>(y, a0, q[c].x, q[c].y);
-              mma16816<BF16>(y, a1, q[c].z, q[c].w);
+          for (int c = 0; c < C; ++c) q[c] = tiles[n][c][lane];
+          ri[0] = info[8 * n + 2 * t];
+          ri[1] = info[8 * n + 2 * t + 1];
+        };
+        if (n_tiles == 1) load_tile(0);
+
+        for (; u < u1; u += kWarps) {
+          const Keys<D, KV4> cur = k;
+          get(k, page, u + kWarps);
+          page = page_of(u + 2 * kWarps);
+          if (!cur.valid) continue;
+          const int key0 = u * kKeys;
+          uint32_t v[KV4 ? C : 1][2][4];  // 4 bits: the codes, and s and m
+          float2 par[KV4 ? C : 1][2];
+          if constexpr (KV4) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                x[e] = fmaf(par[c][e >> 1].y, qsum[c][e & 1], fmaf(par[c][e >> 1].x, y[e], x[e]));
-            } else {
-              const uint32_t a0[4] = {cur.x[0][c].x, cur.x[1][c].x, cur.x[0][c].y, cur.x[1][c].y};
-              const uint32_t a1[4] = {cur.x[0][c].z, cur.x[1][c].z, cur.x[0][c].w, cur.x[1][c].w};
-              mma16816<BF16>(x, a0, q[c].x, q[c].y);
-              mma16816<BF16>(x, a1, q[c].z, q[c].w);
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                par[c][h] = unpack2<BF16>(cur.par[h][c]);
+                kv4_halves(cur.code[h][c], v[c][h]);
+              }
+          }
+          float sum[2] = {0.f, 0.f};
+          for (int n = 0; n < n_tiles; ++n) {
+            if (n_tiles > 1) load_tile(n);
+            float x[4] = {0.f, 0.f, 0.f, 0.f};  // key g + 8 (e / 2), row 2 t + e % 2 of the tile
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+              if constexpr (KV4) {
+                const uint32_t a0[4] = {v[c][0][0], v[c][1][0], v[c][0][1], v[c][1][1]};
+                const uint32_t a1[4] = {v[c][0][2], v[c][1][2], v[c][0][3], v[c][1][3]};
+                float y[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<false>(y, a0, q[c].x, q[c].y);
+                mma16816<false>(y, a1, q[c].z, q[c].w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  x[e] = fmaf(par[c][e >> 1].y, ri[e & 1].qsum[c],
+                              fmaf(par[c][e >> 1].x, y[e], x[e]));
+              } else {
+                const uint32_t a0[4] = {cur.x[0][c].x, cur.x[1][c].x, cur.x[0][c].y, cur.x[1][c].y};
+                const uint32_t a1[4] = {cur.x[0][c].z, cur.x[1][c].z, cur.x[0][c].w, cur.x[1][c].w};
+                mma16816<BF16>(x, a0, q[c].x, q[c].y);
+                mma16816<BF16>(x, a1, q[c].z, q[c].w);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float w = ex2_approx(fmaf(x[e], ri[e & 1].to2, -ri[e & 1].lse));
+              // (a select: an unseen key may hold anything)
+              if (key0 + g + 8 * (e >> 1) <= ri[e & 1].lim) sum[e >> 1] += w;
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float w = ex2_approx(fmaf(x[e], p.scale_log2, -lse[e & 1]));
-            // (a select: an unseen key may hold anything)
-            if (key0 + g + 8 * (e >> 1) <= lim[e & 1]) sum[e >> 1] += w;
+          for (int h = 0; h < 2; ++h) {
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+            const int key = key0 + g + 8 * h;
+            if (t == 0 && key < sq.klen)
+              a.weights[cur.slot + g + 8 * h] =
+                  r0 > 0 || key < sq.klen - sq.qlen ? cur.old[h] + sum[h] : sum[h];
           }
-          if (rows > 8) {
-            next(qi, qh);
-            next(ri[0], rh[0]);
-            next(ri[1], rh[1]);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
-          sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
-          const int key = key0 + g + 8 * h;
-          if (t == 0 && key < sq.klen)
-            a.weights[cur.slot + g + 8 * h] = key < sq.klen - sq.qlen ? cur.old[h] + sum[h] : sum[h];
         }
       }
     }

@@ -206,9 +206,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     const int nbw = warp_blocks(w, warp);
     const PagedSeq sq = w.sq;
     const int rows = min(kPagedRows, sq.qlen * p.G);
-    // Q^T: of row 8 nt + g the channels that the lane has of the keys, those of odd
-    // nibbles over 16 (kv4_halves); of rows 8 nt + 2 t and the next the sums over each
-    // group, and what takes their products to base 2 (1e-37 .. 1e37, as in the tile
+    // Q^T: of row 8 nt + g the channels that the lane has of the keys (kv4_query); of
+    // rows 8 nt + 2 t and the next the sums over each group, and what takes their products to base 2 (1e-37 .. 1e37, as in the tile
     // kernel).
     uint32_t qb[NT][KS][2];
     float2 qsum[NT][C], to2[NT];
@@ -218,42 +217,21 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
       const uint16_t* q =
           static_cast<const uint16_t*>(p.q) + (r < rows ? row_of(p, w, r) * D + 8 * t : 0);
       uint4 x[C];
-      uint32_t top = 0u;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
+      for (int c = 0; c < C; ++c)
         x[c] = r < rows ? *reinterpret_cast<const uint4*>(q + 32 * c) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = unpack2<BF16>(y[i]);
-          top = max(top, max(finite_bits(f.x), finite_bits(f.y)));
-        }
-      }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float2 f = to_fp16_range<9>(top);
+      float sums[C];
+      const float undo = kv4_query<BF16, C>(x, sums);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-        float z[8], sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = unpack2<BF16>(y[i]);
-          z[2 * i] = v.x * f.x;
-          z[2 * i + 1] = v.y * f.x;
-          sum += z[2 * i] + z[2 * i + 1];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float by = i & 1 ? 0.0625f : 1.f;
-          qb[nt][2 * c + i / 2][i & 1] = pack_f16x2(z[i] * by, z[i + 4] * by);
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qsum[nt][c] = make_float2(__shfl_sync(0xffffffffu, sum, 8 * t),
-                                  __shfl_sync(0xffffffffu, sum, 8 * t + 4));
+        qb[nt][2 * c][0] = x[c].x;
+        qb[nt][2 * c][1] = x[c].y;
+        qb[nt][2 * c + 1][0] = x[c].z;
+        qb[nt][2 * c + 1][1] = x[c].w;
+        qsum[nt][c] = make_float2(__shfl_sync(0xffffffffu, sums[c], 8 * t),
+                                  __shfl_sync(0xffffffffu, sums[c], 8 * t + 4));
       }
-      const float by = fminf(fmaxf(p.scale_log2 * f.y, 1e-37f), 1e37f);
+      const float by = fminf(fmaxf(p.scale_log2 * undo, 1e-37f), 1e37f);
       to2[nt] = make_float2(__shfl_sync(0xffffffffu, by, 8 * t),
                             __shfl_sync(0xffffffffu, by, 8 * t + 4));
     }

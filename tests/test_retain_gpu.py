@@ -5,7 +5,7 @@ lse log2(e) and of the difference (each 2^-24 of its size, at most L = max |lse|
 max |s|), and the exponential's 2^-22; n terms are summed in fp32 (n 2^-24), and the
 sum is added to the weight (2^-24 of it).  d_j: over 16 bits, d exact products
 summed, d 2^-24 M with M = scale max sum |q| |k|; over 4 bits 48 2^-24 M with
-M = scale max sum |q| (|m + 8 s| + 8 s) (test_kv4_gpu.py).  So
+M = scale max sum |q| (|m| + 15 s) (test_kv4_gpu.py).  So
 |w - ref| <= (d_j + 2 L 2^-24 + 2^-21 + n 2^-24) new + 2^-24 ref.
 
 Eviction moves bytes: everything is equal.
@@ -55,7 +55,7 @@ def check(x, got, causal):
                                     x["table"].cpu().numpy(), cu, kv, causal, d ** -0.5)
     if x["bits"] == 4:
         s, m, _ = parts4(x["k"], dt)
-        err = 48 * 2.0 ** -24 * largest(x, causal, d ** -0.5, (m + 8 * s).abs() + 8 * s)
+        err = 48 * 2.0 ** -24 * largest(x, causal, d ** -0.5, m.abs() + 15 * s)
     else:
         err = d * 2.0 ** -24 * largest(x, causal, d ** -0.5, x["exact"].abs())
     lse = to64(x["lse"])[:, :int(cu[-1])]
