@@ -172,24 +172,33 @@ __device__ __forceinline__ float kv4_query(uint4 (&q)[C], float* sums) {
   return f.y;
 }
 
-// The eight values of a code word in channel order; par: s and m of its group.
-template <bool BF16>
+// The eight values of a code word, in channel order or (ORDER false) as channels 0, 4,
+// 1, 5, 2, 6, 3, 7; par: s and m of its group.
+template <bool BF16, bool ORDER = true>
 __device__ __forceinline__ uint4 kv4_word(uint32_t w, uint32_t par) {
   const uint32_t s = __byte_perm(par, par, 0x1010), m = __byte_perm(par, par, 0x3232);
   uint32_t v[4];  // channels i and i + 4
   kv4_values<BF16>(w, s, m, v);
+  if constexpr (!ORDER) return make_uint4(v[0], v[1], v[2], v[3]);
   return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
                     __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
-// The eight codes of a word less 8, times the two s in fp16, in channel order.
-__device__ __forceinline__ uint4 kv4_scaled_word(uint32_t w, uint32_t s) {
+// The eight codes of a word less 8, times the two s in fp16 (s / 16 in odd), as channels
+// 0, 4, 1, 5, 2, 6, 3, 7.
+__device__ __forceinline__ uint4 kv4_scaled_word(uint32_t w, uint32_t even, uint32_t odd) {
+  const uint32_t x[2] = {w, w >> 8};
   uint32_t v[4];  // channels i and i + 4
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(kv4_codes<false, 8>(w >> (4 * i))), "r"(s));
-  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+  for (int i = 0; i < 4; ++i) {
+    uint32_t c;  // times 16 for odd i
+    asm("sub.rn.f16x2 %0, %1, %2;"
+        : "=r"(c)
+        : "r"(and_or(x[i / 2], i & 1 ? 0x00F000F0u : 0x000F000Fu, 0x64006400u)),
+          "r"(i & 1 ? 0x64806480u : 0x64086408u));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(c), "r"(i & 1 ? odd : even));
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 #endif  // __CUDACC__

@@ -19,7 +19,9 @@
 // to registers, and stores the widened row where TMA would have put it.  The rest
 // of the pipeline does not differ.  With 16 warps a thread has 128 registers, not the
 // 168 in which a softmax thread holds a row of 128 scores: it holds half, and reads
-// the other half twice, for the maximum and for the exponentials.
+// the other half twice, for the maximum and for the exponentials.  The channels of a
+// word lie in a tile in the order in which its nibbles come out, 0, 4, 1, 5, 2, 6, 3, 7:
+// queries are put in that order too, and O is put back from it.
 //
 // Keys of a 4-bit cache have more bits than a 16-bit operand (kv4.cuh).  Their
 // scores are a product in fp16 of d + 16 columns: (c - 8) s by the query, exact, and
@@ -145,79 +147,89 @@ __device__ __forceinline__ void store_extra(uint8_t* extra, int row, uint4 a, ui
   x[swap ^ 1] = make_uint4(b.x, b.y, 0u, 0u);
 }
 
-// A row of a 4-bit cache: its code words, then its groups' scales and minima.
+// N words from global memory, aligned as rows of a 4-bit cache are.
+template <int N, int ALIGN>
+__device__ __forceinline__ void read_words(const uint8_t* x, uint32_t (&w)[N]) {
+  if constexpr (ALIGN % 16 == 0 && N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(x) + i / 4);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  } else if constexpr (ALIGN % 8 == 0 && N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(x) + i / 2);
+      w[i] = v.x, w[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(x) + i);
+  }
+}
+
+// A row of a 4-bit cache: its code words, and its groups' scales and minima.
 template <int D>
 struct Row4 {
-  uint32_t w[kv4_row(D) / 4];
+  uint32_t w[D / 8], par[D / 32];
 
   __device__ __forceinline__ void load(const uint8_t* x) {  // null: a row of zeros
-    constexpr int N = kv4_row(D) / 4;
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = 0u;
+    for (int i = 0; i < D / 8; ++i) w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) par[i] = 0u;
     if (x == nullptr) return;
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < N; i += 4)
-        *reinterpret_cast<uint4*>(w + i) = __ldg(reinterpret_cast<const uint4*>(x) + i / 4);
-    } else if constexpr (N % 2 == 0) {
-#pragma unroll
-      for (int i = 0; i < N; i += 2)
-        *reinterpret_cast<uint2*>(w + i) = __ldg(reinterpret_cast<const uint2*>(x) + i / 2);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(x) + i);
-    }
+    read_words<D / 8, kv4_row(D)>(x, w);
+    read_words<D / 32, kv4_row(D)>(x + D / 2, par);
   }
-  __device__ __forceinline__ uint32_t param(int c) const { return w[D / 8 + c]; }
   // The bits of the largest finite number that key() has to hold.
   template <bool BF16>
   __device__ __forceinline__ uint32_t top() const {
     uint32_t b = 0u;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
-      const float2 par = unpack2<BF16>(param(c));
-      b = max(b, max(finite_bits(8.f * par.x), finite_bits(fmaf(8.f, par.x, par.y))));
+      const float2 p = unpack2<BF16>(par[c]);
+      b = max(b, max(finite_bits(8.f * p.x), finite_bits(fmaf(8.f, p.x, p.y))));
     }
     return b;
   }
-  // Row `row` of a tile of keys times f: the codes less 8, times the upper 8 bits of
-  // the scale or what these leave of it (LOW).
+  // Where word c lies in row `row` of a tile.
+  static __device__ __forceinline__ uint4* place(uint8_t* tile, int row, int c) {
+    return reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
+                                    (((c & 7) ^ (row & 7)) << 4));
+  }
+  // Row `row` of a tile of keys times f: the codes less 8, times the upper 8 bits of the
+  // scale or what these leave of it (LOW).
   template <bool BF16, bool LOW>
   __device__ __forceinline__ void key(uint8_t* tile, int row, float f) const {
 #pragma unroll
     for (int g = 0; g < D / 32; ++g) {
-      const float s = unpack2<BF16>(param(g)).x * f;
+      const float s = unpack2<BF16>(par[g]).x * f;
       const float hi = __uint_as_float(__float_as_uint(s) & 0xFFFF0000u);
-      const uint32_t by = LOW ? pack_f16x2(s - hi, s - hi) : pack_f16x2(hi, hi);
+      const float by = LOW ? s - hi : hi;
+      const uint32_t even = pack_f16x2(by, by), odd = pack_f16x2(by * 0.0625f, by * 0.0625f);
 #pragma unroll
       for (int c = 4 * g; c < 4 * g + 4; ++c)
-        *reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
-                                  (((c & 7) ^ (row & 7)) << 4)) = kv4_scaled_word(w[c], by);
+        *place(tile, row, c) = kv4_scaled_word(w[c], even, odd);
     }
   }
   // Its columns behind: m + 8 s in two terms, the first of them once more.
   template <bool BF16>
   __device__ __forceinline__ void key_extra(uint8_t* extra, int row, float f) const {
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t two[4] = {0u, 0u, 0u, 0u};  // first and second term
 #pragma unroll
     for (int g = 0; g < D / 32; ++g) {
-      const float2 par = unpack2<BF16>(param(g));
-      x[g] = fmaf(8.f, par.x, par.y) * f;
+      const float2 p = unpack2<BF16>(par[g]);
+      two[g] = two_terms(fmaf(8.f, p.x, p.y) * f);
     }
-    uint32_t two[4];  // first and second term
-#pragma unroll
-    for (int g = 0; g < 4; ++g) two[g] = two_terms(x[g]);
     store_extra(extra, row, make_uint4(two[0], two[1], two[2], two[3]),
                 make_uint2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[2], two[3], 0x5410)));
   }
-  // Widened values, as row `row` of a tile in shared memory.
+  // Widened values.
   template <bool BF16>
   __device__ __forceinline__ void value(uint8_t* tile, int row) const {
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-      *reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
-                                (((c & 7) ^ (row & 7)) << 4)) =
-          kv4_word<BF16>(w[c], param(c / 4));
+    for (int c = 0; c < D / 8; ++c) *place(tile, row, c) = kv4_word<BF16, false>(w[c], par[c / 4]);
   }
 };
 
@@ -255,7 +267,9 @@ __device__ __forceinline__ float query_row(uint8_t* tile, uint8_t* extra, int ro
       sum[c / 4] += v.x + v.y;
       y[i] = pack_f16x2(v.x, v.y);
     }
-    *piece(c) = make_uint4(y[0], y[1], y[2], y[3]);
+    // channels (0, 1) (2, 3) (4, 5) (6, 7) as (0, 4) (1, 5) (2, 6) (3, 7)
+    *piece(c) = make_uint4(__byte_perm(y[0], y[2], 0x5410), __byte_perm(y[0], y[2], 0x7632),
+                           __byte_perm(y[1], y[3], 0x5410), __byte_perm(y[1], y[3], 0x7632));
   }
   uint32_t two[4];
 #pragma unroll
@@ -412,9 +426,10 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
       __syncwarp();
     } else if (KV4 && warp > kWarpRelay) {
       // ------------------------------------------------ widening of K and V ---
-      const int row = threadIdx.x - 32 * kWarpWiden;  // key of the block; < 0: warp 11, idle
-      uint32_t kv_it = 0;
-      bool ok = row >= 0;
+      const int row = threadIdx.x & 127;     // key of the block
+      constexpr int kTiles = kKeyTiles + 1;  // of a block in the ring: keys, values
+      uint32_t block = 0;
+      bool ok = warp >= kWarpWiden;  // warp 11 is idle
       for (; w.left > 0 && ok; w.next(p, TT)) {
         const int nbmax = max(w.n[0], w.n[1]);
         if (nbmax == 0) continue;  // the same skip in every role
@@ -426,7 +441,8 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
                      ? __ldg(p.block_table + (size_t)w.b * p.max_pages + (key >> p.page_log2))
                      : -2;
         };
-        // Where its row lies in the cache; a page outside it gives zeros.
+        // Where its row lies in the cache; -1 past the sequence and for a page outside
+        // the cache, which give zeros.
         auto find = [&](int page, int j) -> int64_t {
           if (page >= 0 && page < p.n_pages)
             return ((((int64_t)page * p.Hkv + w.head) << p.page_log2) +
@@ -435,44 +451,39 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
             atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(w.b, 0xFFFF) << 16));
           return -1;
         };
-        // The next slot of the ring, filled by `write`.
-        auto put = [&](auto write) {
-          const uint32_t slot = kv_it % L::kSlots;
+        // Tile n of the block's in the ring, filled by `write`.
+        auto put = [&](int n, auto write) {
+          const uint32_t it = block * kTiles + n, slot = it % L::kSlots;
           ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvEmpty + slot),
-                                                 ((kv_it / L::kSlots) & 1) ^ 1, wd, 78));
+                                                     ((it / L::kSlots) & 1) ^ 1, wd, 78));
           if (!ok) return;
           write(smem + L::kKvOff + slot * L::kTileBytes);
           fence_proxy_async_smem();  // before the products read it
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kKvFull + slot));
-          ++kv_it;
         };
-        auto put_key = [&](const Row4<D>& x) {
-          const uint32_t block = kv_it / (kKeyTiles + 1);
-          const float2 f =
-              to_fp16_range<14>(__reduce_max_sync(0xffffffffu, x.template top<BF16>()));
-          put([&](uint8_t* tile) {
-            if (lane == 0) reinterpret_cast<float*>(scales + block % L::kScales)[row >> 5] = f.y;
-            x.template key_extra<BF16>(
-                smem + L::kKExtraOff + block % L::kExtras * kExtraBytes, row, f.x);
-            x.template key<BF16, false>(tile, row, f.x);
-          });
-          if (kKeyTiles == 2 && ok)
-            put([&](uint8_t* tile) { x.template key<BF16, true>(tile, row, f.x); });
-        };
-        // Each row is asked for a block before it is widened, its page two before.
+        // A row is asked for a block before it is widened, its page two before.
         int64_t at = find(key_page(0), 0);
         int page = key_page(1);
         Row4<D> k, v;
         k.load(at < 0 ? nullptr : p.k4 + at);
         v.load(at < 0 ? nullptr : p.v4 + at);
-        for (int j = 0; j < nbmax && ok; ++j) {
+        for (int j = 0; j < nbmax && ok; ++j, ++block) {
           at = find(page, j + 1);
           page = key_page(j + 2);
-          put_key(k);
+          const float2 f =
+              to_fp16_range<14>(__reduce_max_sync(0xffffffffu, k.template top<BF16>()));
+          put(0, [&](uint8_t* tile) {
+            if (lane == 0) reinterpret_cast<float*>(scales + block % L::kScales)[row >> 5] = f.y;
+            k.template key_extra<BF16>(
+                smem + L::kKExtraOff + block % L::kExtras * kExtraBytes, row, f.x);
+            k.template key<BF16, false>(tile, row, f.x);
+          });
+          if (kKeyTiles == 2 && ok)
+            put(1, [&](uint8_t* tile) { k.template key<BF16, true>(tile, row, f.x); });
           k.load(at < 0 ? nullptr : p.k4 + at);
           if (!ok) break;
-          put([&](uint8_t* tile) { v.template value<BF16>(tile, row); });
+          put(kKeyTiles, [&](uint8_t* tile) { v.template value<BF16>(tile, row); });
           v.load(at < 0 ? nullptr : p.v4 + at);
         }
       }
@@ -658,6 +669,9 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
     const uint32_t o_addr = tbase + lane_base + 256u + kPaddedD<D> * t;
     float sl2 = p.scale_log2;
     const int gi = r / TT, ti = r - gi * TT;  // query head of the group, token of the tile
+    // The column of a word's channel i, 0 .. 7, and of channel i of 32.
+    auto column = [](int i) { return KV4 ? (i & 3) * 2 + (i >> 2) : i; };
+    auto at_column = [&](int i) { return (i & ~7) + column(i & 7); };
     uint32_t s_it = 0, o_it = 0, blocks = 0;  // blocks: key blocks of the pieces before
     bool aborted = false;
     for (; w.left > 0; w.next(p, TT)) {
@@ -857,8 +871,8 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
               uint32_t pk[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                pk[i] = pack2<BF16>(__uint_as_float(raw[8 * v + 2 * i]) * inv_l,
-                                    __uint_as_float(raw[8 * v + 2 * i + 1]) * inv_l);
+                pk[i] = pack2<BF16>(__uint_as_float(raw[8 * v + column(2 * i)]) * inv_l,
+                                    __uint_as_float(raw[8 * v + column(2 * i + 1)]) * inv_l);
               *place(lane, (c - c0) * 4 + v) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           }
@@ -884,8 +898,9 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           if (live) {  // the join reads no other rows
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-              part[(size_t)(c * 8 + v) * kRows + t * 128 + r] =
-                  make_uint4(raw[4 * v], raw[4 * v + 1], raw[4 * v + 2], raw[4 * v + 3]);
+              part[(size_t)(c * 8 + v) * kRows + t * 128 + r] = make_uint4(
+                  raw[at_column(4 * v)], raw[at_column(4 * v + 1)], raw[at_column(4 * v + 2)],
+                  raw[at_column(4 * v + 3)]);
           }
         }
         if (live) *ml = make_float2(m, l);
