@@ -7,13 +7,14 @@
 // between the turn and the groups.  A group of 32 channels is four pieces,
 // which the half-split rotation leaves with up to four threads of the token:
 // each piece's minimum and maximum go to shared memory, and every thread
-// takes its group's from there, four heads between two barriers.
+// takes its group's from there, two heads between two barriers.
 //
 // The instructions for a value are what can hold this back from the rate of its
 // bytes, so extremes are taken two values at a time in 16 bits (of 16-bit values they
 // are exact), and quotients by multiplying with the group's reciprocal and a
-// correction (divide): __fdiv_rn made the kernel take 132 us for a prompt of 16384
-// tokens, 16 + 8 + 8 heads of 128.
+// correction (divide).  A prompt of 16384 tokens, 16 + 8 + 8 heads of 128 in bf16: 132 us
+// with __fdiv_rn, 70 with divide, 62 with two heads between barriers and six blocks an SM
+// (four heads and four blocks, as in the 16-bit append, 65).
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -29,7 +30,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;  // heads whose rows are read together
+constexpr int kBatch = 2;  // heads whose rows are read together
 
 // The larger of two pairs of 16-bit values; NaN where one is.
 template <bool BF16>
@@ -68,12 +69,19 @@ __device__ __forceinline__ float divide(float x, float y, float reciprocal) {
   return fmaf(fmaf(-q, y, x), reciprocal, q);
 }
 
+// Outside that range, and where there is nothing to divide by.  Not inlined, as all
+// that is rare here: the instructions of the way that is taken have to fit their cache.
+__device__ __noinline__ float divide_any(float x, float y) { return __fdiv_rn(x, y); }
+__device__ __forceinline__ bool in_range(float y) { return y > 0x1p-60f && y < 0x1p60f; }
+
 // s in the low half, m in the high, for extremes -min, max.
 template <bool BF16>
 __device__ __forceinline__ uint32_t kv4_params(uint32_t ends) {
   const uint32_t m = (ends & 0xFFFFu) ^ 0x8000u;
   const float lo = from16<BF16>(m), hi = from16<BF16>(ends >> 16);
-  uint32_t s = to16<BF16>(__fdiv_rn(hi - lo, 15.f));
+  const float range = hi - lo;
+  uint32_t s =
+      to16<BF16>(in_range(range) ? divide(range, 15.f, 1.f / 15.f) : divide_any(range, 15.f));
   constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
   if (s >= kInf) return 0x7FFF7FFFu;
   // s rounded up may carry code 15 past the type's range
@@ -88,31 +96,38 @@ constexpr uint32_t magic_sum() {
   return w;
 }
 
-// The code word of eight values.
 template <bool BF16>
-__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], uint32_t par) {
-  const float m = from16<BF16>(par >> 16), s = from16<BF16>(par & 0xFFFFu);
-  constexpr uint32_t kMagic = magic_sum();
+__device__ __noinline__ uint32_t quantize8_any(uint4 x, float m, float s) {
+  float v[8];
+  unpack8<BF16>(x, v);
   uint32_t w = 0;
-  if (s > 0x1p-60f && s < 0x1p60f) {
-    const float reciprocal = __frcp_rn(s);
-    // q + 1.5 2^23 has the nearest whole number in its low bits
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = fminf(divide(x[i] - m, s, reciprocal), 15.f);
-      w += __float_as_uint(q + 0x1.8p23f) << (4 * i);
-    }
-    return w - kMagic;
-  }
   const float by = s > 0.f ? s : INFINITY;  // one value: code 0
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w |= (uint32_t)fminf(rintf(__fdiv_rn(x[i] - m, by)), 15.f) << (4 * i);
+  for (int i = 7; i >= 0; --i) w = w << 4 | (uint32_t)fminf(rintf(__fdiv_rn(v[i] - m, by)), 15.f);
   return w;
 }
 
+// The code word of eight values.
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantize8(const uint4& x, uint32_t par) {
+  const float m = from16<BF16>(par >> 16), s = from16<BF16>(par & 0xFFFFu);
+  // (of a normal number s no quotient passes 15.2, so that none has to be cut to 15)
+  if (!in_range(s) || (!BF16 && s < 0x1p-14f)) return quantize8_any<BF16>(x, m, s);
+  constexpr uint32_t kMagic = magic_sum();
+  const float reciprocal = __frcp_rn(s);
+  float v[8];
+  unpack8<BF16>(x, v);
+  uint32_t w = 0;
+  // q + 1.5 2^23 has the nearest whole number in its low bits
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = divide(v[i] - m, s, reciprocal);
+    w += __float_as_uint(q + 0x1.8p23f) << (4 * i);
+  }
+  return w - kMagic;
+}
+
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kThreads, 4) append4_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 6) append4_kernel(const AppendParams p) {
   __shared__ __align__(16) uint32_t ends[2][kBatch][2 * kThreads];  // of each token's pieces
   grid_wait();
   grid_release();
@@ -192,8 +207,9 @@ __global__ void __launch_bounds__(kThreads, 4) append4_kernel(const AppendParams
       const int w = which(h0 + first + i);
       if (w == 2) break;
       const int h = h0 + first + i - w * p.Hkv;
-      uint8_t* y = static_cast<uint8_t*>(w ? p.v_pages : p.k_pages) +
-                   ((((int64_t)at.page * p.Hkv + h) << p.batch.page_log2) + page_row) * row_bytes;
+      uint8_t* y =
+          static_cast<uint8_t*>(w ? p.v_pages : p.k_pages) +
+          ((((int64_t)at.page * p.Hkv + h) << p.batch.page_log2) + page_row) * row_bytes;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int ch = half ? s.hi : s.lo;
@@ -201,9 +217,7 @@ __global__ void __launch_bounds__(kThreads, 4) append4_kernel(const AppendParams
             &ends[buf][i][base + ch / kKv4Group * 4]);
         const uint32_t par =
             kv4_params<BF16>(max2<BF16>(max2<BF16>(r.x, r.y), max2<BF16>(r.z, r.w)));
-        float x[8];
-        unpack8<BF16>(half ? hh[i] : l[i], x);
-        *reinterpret_cast<uint32_t*>(y + ch / 2) = quantize8<BF16>(x, par);
+        *reinterpret_cast<uint32_t*>(y + ch / 2) = quantize8<BF16>(half ? hh[i] : l[i], par);
         if (ch % kKv4Group == 0)
           *reinterpret_cast<uint32_t*>(y + p.d / 2 + ch / kKv4Group * 4) = par;
       }

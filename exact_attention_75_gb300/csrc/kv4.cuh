@@ -13,9 +13,10 @@
 //
 // Values take part in products as RN_T(m + c s), one fused multiply-add of two
 // 16-bit values at a time, or as m and RN_T(c s): half a step of T, the error that a
-// 16-bit cache has in the first place.  Keys do not: an error of 2^-9 a channel, even of 2^-12, shows in
-// the log-sum-exp of a short sequence.  A code's product with a query is exact, and
-// so is that of c - 8, which has three significant bits, with a scale of 8 bits; so
+// 16-bit cache has in the first place.  Keys do not: an error of 2^-9 a channel, even
+// of 2^-12, shows in the log-sum-exp of a short sequence.  A code's product with a
+// query is exact, and so is that of c - 8, which has three significant bits, with a
+// scale of 8 bits; so
 //   q . k = sum over groups of  s sum q c  +  m sum q
 // is taken with s and m in 32 bits (decoding), or as
 //           sum over groups of  sum q ((c - 8) s)  +  (m + 8 s) sum q

@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsPa
 
 template <int D, bool BF16>
 cudaError_t launch_db(const WeightsLaunch& a, bool kv4) {
-  return launch_dependent(kv4 ? kv_weights_kernel<D, BF16, true> : kv_weights_kernel<D, BF16, false>,
-                          dim3((unsigned)a.grid), kThreads, 0, a.stream, a.params);
+  auto kern = kv4 ? kv_weights_kernel<D, BF16, true> : kv_weights_kernel<D, BF16, false>;
+  return launch_dependent(kern, dim3((unsigned)a.grid), kThreads, 0, a.stream, a.params);
 }
 
 template <int D>

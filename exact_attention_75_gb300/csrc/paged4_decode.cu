@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     const PagedSeq sq = w.sq;
     const int rows = min(kPagedRows, sq.qlen * p.G);
     // Q^T: of row 8 nt + g the channels that the lane has of the keys (kv4_query); of
-    // rows 8 nt + 2 t and the next the sums over each group, and what takes their products to base 2 (1e-37 .. 1e37, as in the tile
-    // kernel).
+    // rows 8 nt + 2 t and the next the sums over each group, and what takes their
+    // products to base 2 (1e-37 .. 1e37, as in the tile kernel).
     uint32_t qb[NT][KS][2];
     float2 qsum[NT][C], to2[NT];
 #pragma unroll
@@ -510,8 +510,8 @@ cudaError_t launch_dbnc(const PagedLaunch& a) {
   auto kern = paged4_decode_kernel<D, BF16, NT, CLUSTER>;
   cudaError_t e = ensure_dyn_smem(kern, L::kBytes, configured);
   if (e != cudaSuccess) return e;
-  return launch_clusters(kern, CLUSTER ? a.params.cluster : 1, dim3((unsigned)a.grid), kWarps<NT> * 32,
-                         L::kBytes, a.stream, a.params);
+  return launch_clusters(kern, CLUSTER ? a.params.cluster : 1, dim3((unsigned)a.grid),
+                         kWarps<NT> * 32, L::kBytes, a.stream, a.params);
 }
 
 template <int D, bool BF16, int NT>

@@ -223,7 +223,8 @@ struct Row4 {
       two[g] = two_terms(fmaf(8.f, p.x, p.y) * f);
     }
     store_extra(extra, row, make_uint4(two[0], two[1], two[2], two[3]),
-                make_uint2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[2], two[3], 0x5410)));
+                make_uint2(__byte_perm(two[0], two[1], 0x5410),
+                           __byte_perm(two[2], two[3], 0x5410)));
   }
   // Widened values.
   template <bool BF16>
