@@ -164,7 +164,10 @@ __global__ void __launch_bounds__(kThreads, 6) append4_kernel(const AppendParams
   load(lo[0], hi[0], 0);
 
   PackedPlace at = {p.batch.n_seq, false, false, 0, -1};
-  if (token) at = packed_place(p.batch, t);
+  if (token) {
+    at.b = packed_seq(p.batch, t);
+    if (at.b < p.batch.n_seq) at = packed_place(p.batch, at.b, t);
+  }
   if (at.b < p.batch.n_seq && !at.stored && c == 0 && group == 0)
     report_bad(p.batch.status, at.in_seq ? kBadPage : kBadBatch, at.b);
 
@@ -248,8 +251,9 @@ __global__ void __launch_bounds__(kThreads) read4_kernel(const Read4Params p) {
   const int64_t t64 = idx / words;
   if (t64 >= p.batch.total) return;
   const int t = (int)t64, c = (int)(idx % words);
-  const PackedPlace at = packed_place(p.batch, t);
-  if (at.b == p.batch.n_seq) return;
+  const int b = packed_seq(p.batch, t);
+  if (b == p.batch.n_seq) return;
+  const PackedPlace at = packed_place(p.batch, b, t);
   if (!at.stored) {
     if (c == 0 && group == 0)
       report_bad(p.batch.status, at.in_seq ? kBadPage : kBadBatch, at.b);

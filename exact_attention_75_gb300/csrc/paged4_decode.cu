@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
 
   // Block n of the warp's stream lies in slot n % NS; the ring is full until the
   // stream ends, so the slot that is read is the one that is filled next.
-  BlockStream<W, kKeys> stream(p, w, warp, lane);
+  BlockStream<W, kKeys, CLUSTER> stream(p, w, warp, lane);
   uint32_t it = 0;         // blocks taken from the ring
   int slot = 0;            // it % NS
   uint32_t parity = 0;     // (it / NS) & 1

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t ring = sbase + (uint32_t)(warp * NS * L::kSlotBytes);
 
   // it: blocks taken from the ring.
-  BlockStream<kWarps, kKeys> stream(p, w, warp, lane);
+  BlockStream<kWarps, kKeys, CLUSTER> stream(p, w, warp, lane);
   uint32_t it = 0;
   auto issue = [&]() {
     if (!stream.more()) return;

@@ -67,8 +67,8 @@ __device__ __forceinline__ Walk<W, K> start_rows(const PagedParams& p) {
 // A warp's blocks in order, over the borders of pieces: it walks ahead of the
 // kernel as far as the warp's ring reaches.  The lanes hold the pages of the next
 // 32 units (a block has K / kUnit), so that a table read's latency is paid once for
-// them.
-template <int W, int K>
+// them.  SINGLE: the CTA has one piece.
+template <int W, int K, bool SINGLE>
 struct BlockStream {
   static constexpr int kUnits = K / kUnit;
   Walk<W, K> ahead;
@@ -103,8 +103,10 @@ struct BlockStream {
     key += W * K;
     at += kUnits;
     if (--left == 0) {
-      ahead.advance(p, p.max_q);
-      if (ahead.left > 0) begin(p, warp, lane);
+      if constexpr (!SINGLE) {
+        ahead.advance(p, p.max_q);
+        if (ahead.left > 0) begin(p, warp, lane);
+      }
     } else if (at == 32) {
       read(p, lane);
     }
@@ -114,6 +116,7 @@ struct BlockStream {
   // Goes to the first block of the warp from the current piece on, if there is one.
   __device__ __forceinline__ void begin(const PagedParams& p, int warp, int lane) {
     while ((left = warp_blocks(ahead, warp)) == 0) {
+      if constexpr (SINGLE) return;
       ahead.advance(p, p.max_q);
       if (ahead.left <= 0) return;
     }

@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams 
 
   // While the rows are on their way: the token's place in the cache.  Of
   // padding nothing is written.
-  const PackedPlace at = packed_place(p.batch, t);
-  if (at.b == p.batch.n_seq) return;
+  const int b = packed_seq(p.batch, t);
+  if (b == p.batch.n_seq) return;
+  const PackedPlace at = packed_place(p.batch, b, t);
   if (!at.stored && c == 0 && group == 0)
     report_bad(p.batch.status, at.in_seq ? kBadPage : kBadBatch, at.b);
   if (!at.in_seq) return;
