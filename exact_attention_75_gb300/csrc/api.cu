@@ -863,14 +863,17 @@ attn_status attn_evict_kv(void* k_pages, void* v_pages, float* weights, const in
   if (!aligned16(weights) || !aligned(kept, 4) || !aligned(new_lens, 4))
     return ATTN_ERR_INVALID_ARG;
   if (bits != 4 && bits != 16) return ATTN_ERR_INVALID_ARG;
-  if (k_pages == v_pages || weights == k_pages || weights == v_pages || new_lens == kv_lens ||
-      kept == kv_lens || kept == new_lens || kept == block_table || new_lens == block_table)
+  const void* const held[5] = {k_pages, v_pages, weights, block_table, kv_lens};
+  for (const void* x : held)
+    if (kept == x || new_lens == x) return ATTN_ERR_INVALID_ARG;
+  if (k_pages == v_pages || weights == k_pages || weights == v_pages || kept == new_lens)
     return ATTN_ERR_INVALID_ARG;
   attn_status st = paged_args(k_pages, v_pages, block_table, kv_lens, kv_lens, n_seq, 1, n_pages,
                               page, max_pages, Hkv, Hkv);
   if (st != ATTN_OK) return st;
   if (bits == 4 ? (d != 64 && d != 96 && d != 128) : !head_dim_ok(d)) return ATTN_ERR_UNSUPPORTED;
-  if (budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+  if (budget < 1 || budget > (1 << 30) || sinks < 0 || recent < 0 ||
+      (int64_t)sinks + recent > budget)
     return ATTN_ERR_INVALID_ARG;
   if ((int64_t)n_seq * Hkv > 0x7FFFFFFF / kEvictCluster) return ATTN_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;

@@ -372,7 +372,9 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
  * Over the 32 values x of a group: m = min x, s = RN16((max x - m) / 15),
  * c = min(RN((x - m) / s), 15) in fp32 (0 where s = 0), so that a value is off
  * by s / 2, the largest by 15 half steps of s's rounding more.  A group that
- * holds an infinity or a NaN, or whose range passes fp32, stands for NaN.
+ * holds an infinity or a NaN, or whose range passes fp32, stands for NaN; the
+ * largest of a group, where s was rounded up, comes back as an infinity if what
+ * it stands for passes the type's range (fp16: from 65472 up).
  * The other arrays of the batch are those of the 16-bit cache (attn_append_kv).
  *
  * attn_append_kv4: as attn_append_kv, with the same arguments.  What that
@@ -407,7 +409,8 @@ attn_status attn_read_kv4(const void* k_pages, const void* v_pages, void* k, voi
  * (attn_fwd_paged_workspace_bytes), masking and promises.  Values take part as
  * RN16(m + c s), or as m + RN16(c s); keys as m + c s unrounded (a channel may be off
  * by 2^-34 of its query's largest and, in chunks of more than 16 query rows a
- * key/value head, by 2^-38 of the largest of the 32 cached positions 32 i .. 32 i + 31).
+ * key/value head, by 2^-38 of the largest of the 32 cached positions 32 i .. 32 i + 31;
+ * keys and queries of a bf16 cache stay below 2^100, or their scores may be NaN).
  * Cite: as attn_fwd_paged, and "8.3 FlashAttention-3", section 5.1.
  */
 attn_status attn_fwd_paged4(const void* q, const void* k_pages, const void* v_pages, void* o,
@@ -453,9 +456,9 @@ attn_status attn_kv_weights(const void* q, const void* k_pages, const float* lse
  *              192, 256}) or [n_pages, Hkv, page, 5 d / 8] bytes (bits = 4; d in {64, 96,
  *              128}), written in place.
  *   kept     : [n_seq, Hkv, budget], written: the positions that stay, -1
- *              behind the last.
+ *              behind the last.  Neither it nor new_lens overlaps another array.
  *   new_lens : [n_seq], written: min(kv_lens[b], budget); not kv_lens itself.
- *   0 <= sinks, recent; sinks + recent <= budget; 1 <= budget.
+ *   0 <= sinks, recent; sinks + recent <= budget; 1 <= budget <= 2^30.
  * Heads keep positions of their own, so that afterwards a row's place says
  * nothing of its position in the text: keys appended later take `positions`.
  * Pages of an evicted sequence belong to it alone (shared ones are left with

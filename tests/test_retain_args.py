@@ -41,7 +41,9 @@ EVICT = dict(kp=P, vp=P1, w=P2, table=P3, kv=P4, kept=P5, lens=ctypes.c_void_p(7
     (dict(n_pages=0), INVALID), (dict(max_pages=0), INVALID), (dict(Hkv=0), INVALID), (dict(page=20), UNSUPPORTED),
     (dict(d=80), UNSUPPORTED), (dict(d=192, bits=4), UNSUPPORTED), (dict(bits=2), INVALID), (dict(budget=0), INVALID),
     (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID), (dict(sinks=11), INVALID), (dict(budget=13), INVALID),
-    (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1, budget=2 ** 31 - 1), INVALID), (dict(n_seq=1 << 28), INVALID)])
+    (dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1, budget=2 ** 31 - 1), INVALID), (dict(n_seq=1 << 28), INVALID),
+    (dict(budget=(1 << 30) + 1), INVALID), (dict(budget=2 ** 31 - 1), INVALID), (dict(kept=P2), INVALID),
+    (dict(kept=P), INVALID), (dict(lens=P1), INVALID), (dict(lens=P2), INVALID)])
 def test_evict_refusals(L, change, want):  # noqa: F811
     assert L.attn_evict_kv(*dict(EVICT, **change).values()) == want
 
