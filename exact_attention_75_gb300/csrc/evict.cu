@@ -8,15 +8,25 @@
 //
 // Choice.  The n-th largest weight by its bits, most significant digits first
 // (11, 11 and 10 bits): each CTA counts its part of the positions by digit in
-// shared memory, the cluster adds the counts up, and the digit in which the n-th
-// lies is kept.  One more pass lists what lies above it, and of what equals it
-// as many as are wanted, a scan at a time.
+// shared memory, the CTAs add up a part of the counts each and give all of them the
+// sums, and the digit in which the n-th lies is kept.  One more pass lists what
+// lies above it, and of what equals it as many as are wanted.  Weights of the first
+// 8192 positions of a part stay in registers for all passes.  Bound by the chain of
+// these steps (two meetings of the cluster a digit), not by what it reads.
 //
 // Move.  Rows go to places that other rows may still have to be read from; but a
 // row only moves forward, so the rows go in order, as many at a time as the
 // cluster's registers hold: all of them are read, the cluster meets, all of them
 // are written.  No place written is a place still to be read, since that lies
-// behind every place written so far.
+// behind every place written so far.  Bound by HBM with many items, by a round's
+// latency (2.3 us) with few.
+//
+// 16 sequences of up to 8192 positions on 4 heads of 128 in 16 bits, half of them
+// kept, 58 us: choice 18, and 240 MB at 6 TB/s.  One sequence of 65536 on 8 heads of 64
+// in 4 bits, a quarter kept, 36 us: choice 17, five rounds.  Measured on the way:
+// every CTA reading all the CTAs' counts, 64 and 38; equal digits of a warp counted
+// together, 70 and 50; 16 vectors of a row's a thread in place of 8, 45 for the move
+// of the second, not 38.
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -31,6 +41,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kBins = 2048;
+static_assert(kBins == 4 * kThreads, "four digits a thread");
 
 // Weights as numbers that order alike: -0 is 0, NaN the heaviest.
 __device__ __forceinline__ uint32_t order(float w) {
@@ -46,6 +57,13 @@ __device__ __forceinline__ uint4 cluster_load(const uint32_t* x, int rank) {
                : "r"(cluster_addr(smem_u32(x), rank))
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ void cluster_store(const uint32_t* x, int rank, uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                   cluster_addr(smem_u32(x), rank)),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
 }
 
 // The cluster's item.
@@ -78,8 +96,9 @@ constexpr int kRun = kHeld * kThreads;
 __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictParams p,
                                                                    int cluster) {
   __shared__ __align__(16) uint32_t count[kBins];  // of the CTA's positions, by digit
+  __shared__ __align__(16) uint32_t total[kBins];  // of the cluster's
   __shared__ uint32_t scan[kHeld * kThreads / 32];
-  __shared__ uint32_t chosen, above, own[2];
+  __shared__ uint32_t chosen, above, own[2], all;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
   grid_wait();
@@ -103,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
   auto read = [&](int r0, uint32_t (&w)[kHeld]) {
 #pragma unroll
     for (int j0 = 0; j0 < kHeld; j0 += 8) {
+      if (r0 + j0 * kThreads >= m1) break;
       int64_t row[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -125,9 +145,11 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
     __syncthreads();
     auto add = [&](int r0, const uint32_t (&w)[kHeld]) {
 #pragma unroll
-      for (int j = 0; j < kHeld; ++j)
+      for (int j = 0; j < kHeld; ++j) {
+        if (r0 + j * kThreads >= m1) break;
         if (r0 + j * kThreads + tid < m1 && (digit == 0 || w[j] >> (shift + bits) == prefix))
           atomicAdd(count + (w[j] >> shift & ((1u << bits) - 1)), 1u);
+      }
     };
     add(m0, first);
     for (int r0 = m0 + kRun; r0 < m1; r0 += kRun) {
@@ -136,20 +158,24 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
       add(r0, w);
     }
     cluster_sync();
+    // Each CTA adds up a part of the digits, one load of four a thread, and gives the
+    // sums to all; neighbouring lanes have the same digits of different CTAs.
+    {
+      const int k = tid & (cluster - 1), at = (it.rank * (kThreads / cluster) + tid / cluster) * 4;
+      uint4 x = cluster_load(count + at, k);
+      for (int off = 1; off < cluster; off <<= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, off);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, off);
+        x.z += __shfl_xor_sync(0xffffffffu, x.z, off);
+        x.w += __shfl_xor_sync(0xffffffffu, x.w, off);
+      }
+      cluster_store(total + at, k, x);
+    }
+    cluster_sync();
     // A thread has four digits, the largest first, and scans over the cluster's counts.
     const int top = kBins - 1 - 4 * tid;
-    uint4 got[kEvictCluster];  // all on their way together
-#pragma unroll
-    for (int r = 0; r < kEvictCluster; ++r)
-      got[r] = r < cluster ? cluster_load(count + top - 3, r) : make_uint4(0u, 0u, 0u, 0u);
-    uint32_t c[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int r = 0; r < kEvictCluster; ++r) {
-      c[0] += got[r].w;
-      c[1] += got[r].z;
-      c[2] += got[r].y;
-      c[3] += got[r].x;
-    }
+    const uint4 got = *reinterpret_cast<const uint4*>(total + top - 3);
+    const uint32_t c[4] = {got.w, got.z, got.y, got.x};
     const uint32_t sum = c[0] + c[1] + c[2] + c[3];
     uint32_t incl = sum;
 #pragma unroll
@@ -182,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
     want -= above;
     more += own[0];
     equal = own[1];
-    cluster_sync();  // the others have read this CTA's counts
+    // (The others have read this CTA's counts before they gave it their sums.)
   }
   // Of the CTAs before this one: what lies above the limit, what equals it.
   if (tid == 0) {
@@ -204,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
     uint32_t above_in[kHeld], equal_in[kHeld];  // ballots
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
+      if (r0 + j * kThreads >= m1) break;
       const bool in = r0 + j * kThreads + tid < m1;
       above_in[j] = __ballot_sync(0xffffffffu, in && first[j] > prefix);
       equal_in[j] = __ballot_sync(0xffffffffu, in && first[j] == prefix);
@@ -212,31 +239,30 @@ __global__ void __launch_bounds__(kThreads, 2) evict_choose_kernel(const EvictPa
             (uint32_t)__popc(above_in[j]) | (uint32_t)__popc(equal_in[j]) << 16;
     }
     __syncthreads();
-    // Each warp scans all counts of the run (kHeld x kWarps, in order), eight a lane.
-    constexpr int kEach = kHeld * kWarps / 32;
-    uint32_t part[kEach], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      part[i] = sum;
-      sum += scan[lane * kEach + i];
-    }
-    uint32_t incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += up;
-    }
-    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-    const uint32_t before = incl - sum, under = (1u << lane) - 1;
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const int e = j * kWarps + warp;  // whose count comes before
-      uint32_t off = __shfl_sync(0xffffffffu, before, e / kEach);
+    if (warp == 0) {  // scans all counts of the run (kHeld x kWarps, in order), eight a lane
+      constexpr int kEach = kHeld * kWarps / 32;
+      const int n = min(kHeld, (m1 - r0 + kThreads - 1) / kThreads) * kWarps;
+      uint32_t part[kEach], sum = 0;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const uint32_t x = __shfl_sync(0xffffffffu, part[i], e / kEach);
-        if (e % kEach == i) off += x;
+        part[i] = sum;
+        sum += lane * kEach + i < n ? scan[lane * kEach + i] : 0u;
       }
+      uint32_t incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += up;
+      }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) scan[lane * kEach + i] = incl - sum + part[i];
+      if (lane == 31) all = incl;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (r0 + j * kThreads >= m1) break;
+      const uint32_t off = scan[j * kWarps + warp], under = (1u << lane) - 1;
       const uint32_t g = gt + (off & 0xFFFFu) + __popc(above_in[j] & under);
       const uint32_t q = eq + (off >> 16) + __popc(equal_in[j] & under);
       const bool is_gt = above_in[j] >> lane & 1, is_eq = equal_in[j] >> lane & 1;
