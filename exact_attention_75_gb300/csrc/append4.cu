@@ -13,8 +13,9 @@
 // bytes, so extremes are taken two values at a time in 16 bits (of 16-bit values they
 // are exact), and quotients by multiplying with the group's reciprocal and a
 // correction (divide).  A prompt of 16384 tokens, 16 + 8 + 8 heads of 128 in bf16: 132 us
-// with __fdiv_rn, 70 with divide, 62 with two heads between barriers and six blocks an SM
-// (four heads and four blocks, as in the 16-bit append, 65).
+// with __fdiv_rn, 70 with divide, 60 with two heads between barriers and six blocks an SM
+// (four heads and four blocks, as in the 16-bit append, 65): 3.9 TB/s, 0.58 of a copy's
+// rate, at 0.58 of the issue slots.  Reading it back takes 17 us.
 #include <cuda_runtime.h>
 #include <cstdint>
 

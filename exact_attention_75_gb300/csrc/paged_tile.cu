@@ -29,7 +29,13 @@
 // terms (three products).  The scale of an fp16 cache has 11 bits; its upper 8 and
 // its lower 3 make a tile of keys each.  Powers of two bring every 32 keys, and each
 // query, into fp16's range; the scores are scaled back where they are scaled anyway.
-// The softmax threads prepare their queries' rows.
+// The softmax threads prepare their queries' rows.  A pair of query tiles widens its
+// keys again: with 32 pairs to a head, 2.7 us a key block for the 1.9 of 16 bits, of which
+// widening's share of the issue slots is 0.45 and the longer softmax (half a row held,
+// 16 columns more) 0.25.  Measured: 4096 tokens over 16384 keys 502 us (fp16, with its two
+// tiles of keys, 775), 4 chunks of up to 509 tokens with 12 single ones 98.  640 threads
+// with registers moved between roles took 552 to 746, a whole row held in 168 registers
+// 617.
 //
 // Bound, like the dense forward, by the softmax and products of 128-row tiles:
 // a key block of two tiles takes 1.55 to 1.75 us (d = 128; d = 96 1.65), of one
