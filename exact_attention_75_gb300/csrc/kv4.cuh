@@ -9,7 +9,8 @@
 // so m is a value of the group and x is off by s / 2 at most, but at the
 // largest, where the rounding of s may add 15 half steps of s.  A group with an
 // infinity or a NaN, or whose range passes fp32, has s = m = NaN: all of it
-// stands for NaN.
+// stands for NaN.  Where s rounded up would carry code 15 past the range of T, it is
+// the number below.
 //
 // Values take part in products as RN_T(m + c s), one fused multiply-add of two
 // 16-bit values at a time, or as m and RN_T(c s): half a step of T, the error that a
@@ -171,6 +172,37 @@ __device__ __forceinline__ float kv4_query(uint4 (&q)[C], float* sums) {
     sums[c] = sum + __shfl_xor_sync(0xffffffffu, sum, 2);
   }
   return f.y;
+}
+
+// What the minima of the groups add to a score, sum over groups of m sum q, as a product
+// of its own in the cache's type, 16 deep: the sum of a query over a group is cut into
+// three terms, which meet the group's minimum one by one.  Each quad of lanes has a query
+// (operand B) and a key (A, both its registers alike); what no term needs is 0 in B.
+template <bool BF16, int C>
+__device__ __forceinline__ uint2 kv4_sum_terms(const float (&sums)[C], int t) {
+  const bool odd = C > 2 && t & 1;  // groups 2 and 3, not 0 and 1
+  float a = sums[0], b = sums[1];
+  if (odd) {
+    a = sums[C > 2 ? 2 : 0];
+    b = C > 3 ? sums[C > 3 ? 3 : 0] : 0.f;
+  }
+  uint32_t term[3];
+#pragma unroll
+  for (int n = 0; n < 3; ++n) {
+    term[n] = BF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+    const float2 had = unpack2<BF16>(term[n]);
+    a = isfinite(a) ? a - had.x : 0.f;
+    b = isfinite(b) ? b - had.y : 0.f;
+  }
+  if constexpr (C == 2) return make_uint2(t == 0 ? term[0] : (t == 1 ? term[1] : (t == 2 ? term[2] : 0u)), 0u);
+  return make_uint2(t < 2 ? term[0] : term[1], t < 2 ? term[2] : 0u);
+}
+// par: s and m of the key's groups.
+template <int C>
+__device__ __forceinline__ uint32_t kv4_minima(const uint32_t (&par)[C], int t) {
+  const uint32_t low = __byte_perm(par[0], par[1], 0x7632);
+  if constexpr (C == 2) return low;
+  return t & 1 ? __byte_perm(par[C > 2 ? 2 : 0], C > 3 ? par[C > 3 ? 3 : 0] : 0u, 0x7632) : low;
 }
 
 // The eight values of a code word, in channel order or (ORDER false) as channels 0, 4,

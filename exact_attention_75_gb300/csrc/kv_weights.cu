@@ -18,16 +18,17 @@
 // from the second time on the keys come from L2.
 //
 // Of a cache in 4 bits (kv4.cuh) the product is taken with the codes in fp16, as in the
-// decoding kernel.
+// decoding kernel, and what the groups' minima add is one more product for all of them.
 //
 // Work.  A block of 16 keys costs kRead + its tiles of 8 rows; the blocks of all
 // sequences and heads laid end to end are shared out evenly over the grid, and
 // the warps of a CTA take its blocks in turn.
 //
 // Single tokens are bound by HBM: 64 of them over 2048 to 8192 keys, 16 query heads on 4
-// of 128, 58 us in 16 bits, 6.0 TB/s, 0.90 of a copy's rate; 39 in 4 bits.  Windows are
+// of 128, 57 us in 16 bits, 6.0 TB/s, 0.90 of a copy's rate; 37 in 4 bits.  Windows are
 // bound by the product's latencies and the operands read for it: 4 of 32 tokens over up to
-// 16384 keys, 16 heads on 8, 49 us in 4 bits, 40 in 16.
+// 16384 keys, 16 heads on 8, 38 us in 4 bits (49 with the minima added to the scores one by
+// one), 35 in 16; of 256 tokens in 4 bits 233.
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -151,18 +152,18 @@ struct Keys {
   }
 };
 
-// A row of queries beside its operand: the sums over its groups and what takes its
-// products to base 2 (KV4), its log-sum-exp in base 2, the last key it sees.
+// A row of queries beside its operand: what takes its products to base 2, its
+// log-sum-exp in base 2, the last key it sees, and the last that all of its tile see.
 struct RowInfo {
-  float qsum[4];
   float to2, lse;
-  int lim, unused;
+  int lim, all;
 };
 
 template <int D, bool BF16, bool KV4>
 __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsParams a) {
   constexpr int C = D / 32;
   __shared__ uint4 tiles[kWarps][C][32];  // operand B of 8 rows: by lane
+  __shared__ uint2 minima[KV4 ? kWarps : 1][32];  // operand B of what the minima add
   __shared__ __align__(16) RowInfo info[kWarps * 8];
   const PagedParams& p = a.paged;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -212,19 +213,27 @@ __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsPa
           RowInfo ri = {};
           ri.to2 = p.scale_log2;
           if constexpr (KV4) {
-            const float undo = kv4_query<BF16, C>(q, ri.qsum);
+            float sums[C];
+            const float undo = kv4_query<BF16, C>(q, sums);
+            minima[warp][lane] = kv4_sum_terms<BF16, C>(sums, t);
             ri.to2 = fminf(fmaxf(p.scale_log2 * undo, 1e-37f), 1e37f);
           }
 #pragma unroll
           for (int c = 0; c < C; ++c) tiles[warp][c][lane] = q[c];
           ri.lim = live ? last_key(p, sq, i) : -1;
+          ri.all = ri.lim;
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            ri.all = min(ri.all, __shfl_xor_sync(0xffffffffu, ri.all, off));
           ri.lse = live ? 1.4426950408889634f * __ldg(p.lse + row) : 0.f;
           if (t == 0) info[8 * warp + g] = ri;
         }
         __syncthreads();
         uint4 q[C];
+        uint2 qm = {};
         RowInfo ri[2];
         auto load_tile = [&](int n) {
+          if constexpr (KV4) qm = minima[n][lane];
 #pragma unroll
           for (int c = 0; c < C; ++c) q[c] = tiles[n][c][lane];
           ri[0] = info[8 * n + 2 * t];
@@ -239,20 +248,24 @@ __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsPa
           if (!cur.valid) continue;
           const int key0 = u * kKeys;
           uint32_t v[KV4 ? C : 1][2][4];  // 4 bits: the codes, and s and m
-          float2 par[KV4 ? C : 1][2];
+          float scale[KV4 ? C : 1][2];
+          uint32_t am[4] = {};  // the minima
           if constexpr (KV4) {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                par[c][h] = unpack2<BF16>(cur.par[h][c]);
+              for (int c = 0; c < C; ++c) {
+                scale[c][h] = unpack2<BF16>(cur.par[h][c]).x;
                 kv4_halves(cur.code[h][c], v[c][h]);
               }
+              am[h] = am[h + 2] = kv4_minima(cur.par[h], t);
+            }
           }
           float sum[2] = {0.f, 0.f};
           for (int n = 0; n < n_tiles; ++n) {
             if (n_tiles > 1) load_tile(n);
             float x[4] = {0.f, 0.f, 0.f, 0.f};  // key g + 8 (e / 2), row 2 t + e % 2 of the tile
+            if constexpr (KV4) mma16816<BF16>(x, am, qm.x, qm.y);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
               if constexpr (KV4) {
@@ -262,9 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsPa
                 mma16816<false>(y, a0, q[c].x, q[c].y);
                 mma16816<false>(y, a1, q[c].z, q[c].w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  x[e] = fmaf(par[c][e >> 1].y, ri[e & 1].qsum[c],
-                              fmaf(par[c][e >> 1].x, y[e], x[e]));
+                for (int e = 0; e < 4; ++e) x[e] = fmaf(scale[c][e >> 1], y[e], x[e]);
               } else {
                 const uint32_t a0[4] = {cur.x[0][c].x, cur.x[1][c].x, cur.x[0][c].y, cur.x[1][c].y};
                 const uint32_t a1[4] = {cur.x[0][c].z, cur.x[1][c].z, cur.x[0][c].w, cur.x[1][c].w};
@@ -273,11 +284,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsPa
               }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float w = ex2_approx(fmaf(x[e], ri[e & 1].to2, -ri[e & 1].lse));
-              // (a select: an unseen key may hold anything)
-              if (key0 + g + 8 * (e >> 1) <= ri[e & 1].lim) sum[e >> 1] += w;
+            for (int e = 0; e < 4; ++e)
+              x[e] = ex2_approx(fmaf(x[e], ri[e & 1].to2, -ri[e & 1].lse));
+            // (An unseen key may hold anything.  In 16 bits a test for none costs more than
+            // it saves: the window 37.7 us, not 35.2.)
+            if (!KV4 || key0 + kKeys - 1 > ri[0].all) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key0 + g + 8 * (e >> 1) > ri[e & 1].lim) x[e] = 0.f;
             }
+            sum[0] += x[0] + x[1];
+            sum[1] += x[2] + x[3];
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

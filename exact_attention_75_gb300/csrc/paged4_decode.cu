@@ -20,8 +20,8 @@
 //   V: it reads channels g D/8 .. of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9; two keys'
 //      half words side by side give the pairs of keys that an operand holds.
 // A group's product is taken with the codes in fp16, the query scaled into its range by
-// a power of two, and s and m of its keys are applied to it and to the sum of the
-// query's channels in 32 bits: keys lose nothing.
+// a power of two, and s of its keys is applied to it in 32 bits; what m adds is one more
+// product for all groups, with the query's sums in three terms: keys lose nothing.
 // Values are m + c s rounded to 16 bits, or, in bf16, c s rounded, and m by a product of
 // its own: (128 + c) s - 128 s is one instruction where c s + m takes two.
 // P leaves the softmax by keys and is wanted by rows: one 8 x 8 transpose for 8
@@ -214,11 +214,12 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     const int nbw = warp_blocks(w, warp);
     const PagedSeq sq = w.sq;
     const int rows = min(kPagedRows, sq.qlen * p.G);
-    // Q^T: of row 8 nt + g the channels that the lane has of the keys (kv4_query); of
-    // rows 8 nt + 2 t and the next the sums over each group, and what takes their
-    // products to base 2 (1e-37 .. 1e37, as in the tile kernel).
+    // Q^T: of row 8 nt + g the channels that the lane has of the keys (kv4_query) and the
+    // terms of the sums over each group; of rows 8 nt + 2 t and the next what takes
+    // their products to base 2 (1e-37 .. 1e37, as in the tile kernel).
     uint32_t qb[NT][KS][2];
-    float2 qsum[NT][C], to2[NT];
+    uint2 qm[NT];
+    float2 to2[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = 8 * nt + g;
@@ -236,9 +237,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
         qb[nt][2 * c][1] = x[c].y;
         qb[nt][2 * c + 1][0] = x[c].z;
         qb[nt][2 * c + 1][1] = x[c].w;
-        qsum[nt][c] = make_float2(__shfl_sync(0xffffffffu, sums[c], 8 * t),
-                                  __shfl_sync(0xffffffffu, sums[c], 8 * t + 4));
       }
+      qm[nt] = kv4_sum_terms<BF16, C>(sums, t);
       const float by = fminf(fmaxf(p.scale_log2 * undo, 1e-37f), 1e37f);
       to2[nt] = make_float2(__shfl_sync(0xffffffffu, by, 8 * t),
                             __shfl_sync(0xffffffffu, by, 8 * t + 4));
@@ -282,10 +282,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
       // S^T: x[nt][2 u + h] is rows 8 nt + 2 t and the next, key key0 + 16 u + 8 h + g.
       float2 x[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[nt][i] = make_float2(0.f, 0.f);
-#pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t kw[2][C], kp[2][C];
 #pragma unroll
@@ -295,13 +291,24 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
           for (int c = 0; c < C; ++c) kw[h][c] = load_word(row + 16 * c + 4 * t);
           load_words<C>(row + D / 2, kp[h]);
         }
+        {
+          const uint32_t m0 = kv4_minima(kp[0], t), m1 = kv4_minima(kp[1], t);
+          const uint32_t a[4] = {m0, m1, m0, m1};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816<BF16>(y, a, qm[nt].x, qm[nt].y);
+            x[nt][2 * u] = make_float2(y[0], y[1]);
+            x[nt][2 * u + 1] = make_float2(y[2], y[3]);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           uint32_t v[2][4];
-          float2 par[2];  // s, m
+          float s[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            par[h] = unpack2<BF16>(kp[h][c]);
+            s[h] = unpack2<BF16>(kp[h][c]).x;
             kv4_halves(kw[h][c], v[h]);
           }
           const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]};
@@ -314,8 +321,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float2& z = x[nt][2 * u + h];
-              z.x = fmaf(par[h].y, qsum[nt][c].x, fmaf(par[h].x, y[2 * h], z.x));
-              z.y = fmaf(par[h].y, qsum[nt][c].y, fmaf(par[h].x, y[2 * h + 1], z.y));
+              z.x = fmaf(s[h], y[2 * h], z.x);
+              z.y = fmaf(s[h], y[2 * h + 1], z.y);
             }
           }
         }
