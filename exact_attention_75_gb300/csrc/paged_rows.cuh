@@ -21,9 +21,12 @@ template <int D>
 constexpr int kRowStride = D + 4;  // floats of a row there
 
 // An item is a sequence's key/value head; the W warps of a CTA take the blocks (K
-// keys each) of its cost blocks (one block for each warp) in turn.
+// keys each) of its cost blocks (one block for each warp) in turn.  An item's borders cost
+// as much as 128 keys in 16 bits, as 512 in 4 (whose keys take less; 64 single tokens with 16
+// rows over up to 8192 keys 66.5 us, with 128 70.4, with 1024 69.4; 3 sequences of 16 rows
+// over up to 65536 24.8, 27.2 and 24.7).
 template <int W, int K>
-using Cost = PagedCost<W * K, 1, 1, 128, true>;
+using Cost = PagedCost<W * K, 1, 1, K == 32 ? 512 : 128, true>;
 template <int W, int K>
 struct Walk : PagedWalk<Cost<W, K>> {};
 

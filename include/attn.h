@@ -372,9 +372,8 @@ attn_status attn_fwd_paged(const void* q, const void* k_pages, const void* v_pag
  * Over the 32 values x of a group: m = min x, s = RN16((max x - m) / 15),
  * c = min(RN((x - m) / s), 15) in fp32 (0 where s = 0), so that a value is off
  * by s / 2, the largest by 15 half steps of s's rounding more.  A group that
- * holds an infinity or a NaN, or whose range passes fp32, stands for NaN; the
- * largest of a group, where s was rounded up, comes back as an infinity if what
- * it stands for passes the type's range (fp16: from 65472 up).
+ * holds an infinity or a NaN, or whose range passes fp32, stands for NaN.  Where
+ * s rounded up would carry code 15 past the type's range, s is the number below.
  * The other arrays of the batch are those of the 16-bit cache (attn_append_kv).
  *
  * attn_append_kv4: as attn_append_kv, with the same arguments.  What that
