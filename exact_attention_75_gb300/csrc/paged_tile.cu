@@ -30,10 +30,10 @@
 // its lower 3 make a tile of keys each.  Powers of two bring every 32 keys, and each
 // query, into fp16's range; the scores are scaled back where they are scaled anyway.
 // The softmax threads prepare their queries' rows.  A pair of query tiles widens its
-// keys again: with 32 pairs to a head, 2.7 us a key block for the 1.9 of 16 bits, of which
+// keys again: with 32 pairs to a head, 2.6 us a key block for the 1.9 of 16 bits, of which
 // widening's share of the issue slots is 0.45 and the longer softmax (half a row held,
-// 16 columns more) 0.25.  Measured: 4096 tokens over 16384 keys 502 us (fp16, with its two
-// tiles of keys, 775), 4 chunks of up to 509 tokens with 12 single ones 98.  640 threads
+// 16 columns more) 0.25.  Measured: 4096 tokens over 16384 keys 487 us (fp16, with its two
+// tiles of keys, 755), 4 chunks of up to 509 tokens with 12 single ones 90.  640 threads
 // with registers moved between roles took 552 to 746, a whole row held in 168 registers
 // 617.
 //
@@ -105,9 +105,15 @@ struct PagedTileLayout {
 // A walk along the CTA's share; an item is a pair of tiles of TT tokens each.
 // Weights: a key block of one tile was measured at 1.06 us, of a pair at 1.55,
 // an item's borders at 3 to 4 us; 3 : 4 and two blocks an item balance best (a
-// mixed batch 58.5 us, with 2 : 3 59.8, with equal weights 60.4).
-using Cost = PagedCost<128, 3, 4, 1024, false>;
-struct Walk : PagedWalk<Cost> {
+// mixed batch 58.5 us, with 2 : 3 59.8, with equal weights 60.4).  Over a 4-bit cache, where
+// queries are prepared and the first keys widened at a border, four blocks an item (a mixed
+// batch 90 us for 94, 32 chunks of 24 tokens 59 for 62; six blocks 89 and 62).
+template <bool KV4>
+using Cost = PagedCost<128, 3, 4, KV4 ? 2048 : 1024, false>;
+template <bool KV4>
+struct Walk : PagedWalk<Cost<KV4>> {
+  using Base = PagedWalk<Cost<KV4>>;
+  using Base::advance, Base::item, Base::left, Base::nb, Base::sq, Base::two, Base::u0, Base::u1;
   int n[2];  // key blocks of the piece that tile 0 / 1 sees (two: tile 1 has rows)
 
   __device__ __forceinline__ void tiles(const PagedParams& p, int TT) {
@@ -144,13 +150,33 @@ __device__ __forceinline__ uint32_t two_terms(float x) {
   return pack_f16x2(x, x - hi);
 }
 
+// Shared memory by its own addresses (a pointer into the dynamic part is generic: it
+// costs 64-bit arithmetic and a look at what it points to).
+__device__ __forceinline__ uint4 load_smem16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_smem16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+// Piece c of row `row` of a tile (128-byte swizzle; the tile begins at a multiple of 1024).
+__device__ __forceinline__ uint32_t tile_piece(uint32_t tile, int row, int c) {
+  const uint32_t first = tile + row * 128 + ((row & 7) << 4);
+  return (first ^ ((c & 7) << 4)) + (c >> 3) * 16384;
+}
+
 // Row `row` of a tile's 16 further columns (32 bytes a row, 32-byte swizzle): columns
 // 0-7, then 8-11; the last four are 0.
-__device__ __forceinline__ void store_extra(uint8_t* extra, int row, uint4 a, uint2 b) {
-  uint4* const x = reinterpret_cast<uint4*>(extra + row * 32);
-  const int swap = row >> 2 & 1;
-  x[swap] = a;
-  x[swap ^ 1] = make_uint4(b.x, b.y, 0u, 0u);
+__device__ __forceinline__ void store_extra(uint32_t extra, int row, uint4 a, uint2 b) {
+  const uint32_t x = extra + row * 32, swap = (row >> 2 & 1) * 16;
+  store_smem16(x + swap, a);
+  store_smem16(x + (swap ^ 16), make_uint4(b.x, b.y, 0u, 0u));
 }
 
 // N words from global memory, aligned as rows of a 4-bit cache are.
@@ -199,15 +225,10 @@ struct Row4 {
     }
     return b;
   }
-  // Where word c lies in row `row` of a tile.
-  static __device__ __forceinline__ uint4* place(uint8_t* tile, int row, int c) {
-    return reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
-                                    (((c & 7) ^ (row & 7)) << 4));
-  }
   // Row `row` of a tile of keys times f: the codes less 8, times the upper 8 bits of the
   // scale or what these leave of it (LOW).
   template <bool BF16, bool LOW>
-  __device__ __forceinline__ void key(uint8_t* tile, int row, float f) const {
+  __device__ __forceinline__ void key(uint32_t tile, int row, float f) const {
 #pragma unroll
     for (int g = 0; g < D / 32; ++g) {
       const float s = unpack2<BF16>(par[g]).x * f;
@@ -216,12 +237,12 @@ struct Row4 {
       const uint32_t even = pack_f16x2(by, by), odd = pack_f16x2(by * 0.0625f, by * 0.0625f);
 #pragma unroll
       for (int c = 4 * g; c < 4 * g + 4; ++c)
-        *place(tile, row, c) = kv4_scaled_word(w[c], even, odd);
+        store_smem16(tile_piece(tile, row, c), kv4_scaled_word(w[c], even, odd));
     }
   }
   // Its columns behind: m + 8 s in two terms, the first of them once more.
   template <bool BF16>
-  __device__ __forceinline__ void key_extra(uint8_t* extra, int row, float f) const {
+  __device__ __forceinline__ void key_extra(uint32_t extra, int row, float f) const {
     uint32_t two[4] = {0u, 0u, 0u, 0u};  // first and second term
 #pragma unroll
     for (int g = 0; g < D / 32; ++g) {
@@ -234,9 +255,10 @@ struct Row4 {
   }
   // Widened values.
   template <bool BF16>
-  __device__ __forceinline__ void value(uint8_t* tile, int row) const {
+  __device__ __forceinline__ void value(uint32_t tile, int row) const {
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) *place(tile, row, c) = kv4_word<BF16, false>(w[c], par[c / 4]);
+    for (int c = 0; c < D / 8; ++c)
+      store_smem16(tile_piece(tile, row, c), kv4_word<BF16, false>(w[c], par[c / 4]));
   }
 };
 
@@ -244,15 +266,11 @@ struct Row4 {
 // of 32, and the sums over its groups as the columns behind: the first term twice,
 // the second.  The factor that undoes the scaling.
 template <int D, bool BF16>
-__device__ __forceinline__ float query_row(uint8_t* tile, uint8_t* extra, int row) {
-  auto piece = [&](int c) {
-    return reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + row * 128 +
-                                    (((c & 7) ^ (row & 7)) << 4));
-  };
+__device__ __forceinline__ float query_row(uint32_t tile, uint32_t extra, int row) {
   uint32_t top = 0u;
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
-    const uint4 x = *piece(c);
+    const uint4 x = load_smem16(tile_piece(tile, row, c));
     const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -264,7 +282,7 @@ __device__ __forceinline__ float query_row(uint8_t* tile, uint8_t* extra, int ro
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
-    const uint4 x = *piece(c);
+    const uint4 x = load_smem16(tile_piece(tile, row, c));
     uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -275,8 +293,9 @@ __device__ __forceinline__ float query_row(uint8_t* tile, uint8_t* extra, int ro
       y[i] = pack_f16x2(v.x, v.y);
     }
     // channels (0, 1) (2, 3) (4, 5) (6, 7) as (0, 4) (1, 5) (2, 6) (3, 7)
-    *piece(c) = make_uint4(__byte_perm(y[0], y[2], 0x5410), __byte_perm(y[0], y[2], 0x7632),
-                           __byte_perm(y[1], y[3], 0x5410), __byte_perm(y[1], y[3], 0x7632));
+    store_smem16(tile_piece(tile, row, c),
+                 make_uint4(__byte_perm(y[0], y[2], 0x5410), __byte_perm(y[0], y[2], 0x7632),
+                            __byte_perm(y[1], y[3], 0x5410), __byte_perm(y[1], y[3], 0x7632)));
   }
   uint32_t two[4];
 #pragma unroll
@@ -343,9 +362,10 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
   }
   tc_fence_before();
   if (threadIdx.x == 0) paged_clear(p);
-  Walk w;
+  Walk<KV4> w;
   // (a CTA barrier)
-  static_cast<PagedWalk<Cost>&>(w) = paged_start<Cost, kTileThreads<KV4>>(p, 2 * TT);
+  static_cast<PagedWalk<Cost<KV4>>&>(w) =
+      paged_start<Cost<KV4>, kTileThreads<KV4>>(p, 2 * TT);
   if (w.left > 0) w.tiles(p, TT);
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
@@ -440,6 +460,7 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
       for (; w.left > 0 && ok; w.next(p, TT)) {
         const int nbmax = max(w.n[0], w.n[1]);
         if (nbmax == 0) continue;  // the same skip in every role
+        const uint32_t page_bytes = (uint32_t)(p.page * kv4_row(D));
         // The page of the thread's key of the piece's block j: -2 past the sequence
         // or the piece.
         auto key_page = [&](int j) {
@@ -451,9 +472,9 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
         // Where its row lies in the cache; -1 past the sequence and for a page outside
         // the cache, which give zeros.
         auto find = [&](int page, int j) -> int64_t {
-          if (page >= 0 && page < p.n_pages)
-            return ((((int64_t)page * p.Hkv + w.head) << p.page_log2) +
-                    (((w.u0 + j) * 128 + row) & (p.page - 1))) * kv4_row(D);
+          if (page >= 0 && page < p.n_pages)  // (n_pages Hkv is a number of 32 bits)
+            return (uint64_t)(uint32_t)(page * p.Hkv + w.head) * page_bytes +
+                   (uint32_t)(((w.u0 + j) * 128 + row) & (p.page - 1)) * kv4_row(D);
           if (page != -2)
             atomicCAS(p.status, 0u, 1u | (64u << 8) | ((uint32_t)min(w.b, 0xFFFF) << 16));
           return -1;
@@ -464,7 +485,7 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kKvEmpty + slot),
                                                      ((it / L::kSlots) & 1) ^ 1, wd, 78));
           if (!ok) return;
-          write(smem + L::kKvOff + slot * L::kTileBytes);
+          write(sbase + L::kKvOff + slot * L::kTileBytes);
           fence_proxy_async_smem();  // before the products read it
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kKvFull + slot));
@@ -477,20 +498,20 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
         v.load(at < 0 ? nullptr : p.v4 + at);
         for (int j = 0; j < nbmax && ok; ++j, ++block) {
           at = find(page, j + 1);
-          page = key_page(j + 2);
           const float2 f =
               to_fp16_range<14>(__reduce_max_sync(0xffffffffu, k.template top<BF16>()));
-          put(0, [&](uint8_t* tile) {
+          put(0, [&](uint32_t tile) {
             if (lane == 0) reinterpret_cast<float*>(scales + block % L::kScales)[row >> 5] = f.y;
             k.template key_extra<BF16>(
-                smem + L::kKExtraOff + block % L::kExtras * kExtraBytes, row, f.x);
+                sbase + L::kKExtraOff + block % L::kExtras * kExtraBytes, row, f.x);
             k.template key<BF16, false>(tile, row, f.x);
           });
           if (kKeyTiles == 2 && ok)
-            put(1, [&](uint8_t* tile) { k.template key<BF16, true>(tile, row, f.x); });
+            put(1, [&](uint32_t tile) { k.template key<BF16, true>(tile, row, f.x); });
           k.load(at < 0 ? nullptr : p.k4 + at);
           if (!ok) break;
-          put(kKeyTiles, [&](uint8_t* tile) { v.template value<BF16>(tile, row); });
+          page = key_page(j + 2);
+          put(kKeyTiles, [&](uint32_t tile) { v.template value<BF16>(tile, row); });
           v.load(at < 0 ? nullptr : p.v4 + at);
         }
       }
@@ -714,8 +735,8 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
         if (!aborted)
           aborted = !__all_sync(0xffffffffu, mbar_wait(bar(L::kQFull + t), o_it & 1, wd, 79));
         if (!aborted) {
-          sl2 = p.scale_log2 * query_row<D, BF16>(smem + L::kQOff + t * L::kTileBytes,
-                                                  smem + L::kQExtraOff + t * kExtraBytes, r);
+          sl2 = p.scale_log2 * query_row<D, BF16>(sbase + L::kQOff + t * L::kTileBytes,
+                                                  sbase + L::kQExtraOff + t * kExtraBytes, r);
           fence_proxy_async_smem();  // before the products read it
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kQReady + t));
@@ -752,10 +773,11 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           // score times 0 would be NaN (a product that needs more is 0 or inf anyway).
           float to2[4] = {sl2, sl2, sl2, sl2};
           if constexpr (KV4) {
-            const float4 f = scales[(block0 + j) % L::kScales];
-            const float by[4] = {f.x, f.y, f.z, f.w};
+            const uint4 f = load_smem16(sbase + L::kScaleOff + (block0 + j) % L::kScales * 16);
+            const uint32_t by[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) to2[c] = fminf(fmaxf(sl2 * by[c], 1e-37f), 1e37f);
+            for (int c = 0; c < 4; ++c)
+              to2[c] = fminf(fmaxf(sl2 * __uint_as_float(by[c]), 1e-37f), 1e37f);
           }
           float m_blk;
           if constexpr (KV4) {
