@@ -194,7 +194,8 @@ __device__ __forceinline__ uint2 kv4_sum_terms(const float (&sums)[C], int t) {
     a = isfinite(a) ? a - had.x : 0.f;
     b = isfinite(b) ? b - had.y : 0.f;
   }
-  if constexpr (C == 2) return make_uint2(t == 0 ? term[0] : (t == 1 ? term[1] : (t == 2 ? term[2] : 0u)), 0u);
+  if constexpr (C == 2)
+    return make_uint2(t == 0 ? term[0] : (t == 1 ? term[1] : (t == 2 ? term[2] : 0u)), 0u);
   return make_uint2(t < 2 ? term[0] : term[1], t < 2 ? term[2] : 0u);
 }
 // par: s and m of the key's groups.

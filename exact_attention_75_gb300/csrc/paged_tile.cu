@@ -30,12 +30,14 @@
 // its lower 3 make a tile of keys each.  Powers of two bring every 32 keys, and each
 // query, into fp16's range; the scores are scaled back where they are scaled anyway.
 // The softmax threads prepare their queries' rows.  A pair of query tiles widens its
-// keys again: with 32 pairs to a head, 2.6 us a key block for the 1.9 of 16 bits, of which
-// widening's share of the issue slots is 0.45 and the longer softmax (half a row held,
-// 16 columns more) 0.25.  Measured: 4096 tokens over 16384 keys 487 us (fp16, with its two
-// tiles of keys, 755), 4 chunks of up to 509 tokens with 12 single ones 90.  640 threads
-// with registers moved between roles took 552 to 746, a whole row held in 168 registers
-// 617.
+// keys again: with 32 pairs to a head, 2.35 us a key block for the 1.9 of 16 bits.  Widening,
+// a longer softmax and what each border of an item runs once share the instruction
+// cache, so the loops are kept short: with the halves of a row of scores unrolled, the
+// words of a row and the preparation of queries too, the mixed batch took 84 us and the long
+// chunk 463.  Measured: 4096 tokens over 16384 keys 446 us (fp16, with its two tiles of
+// keys, 715), 4 chunks of up to 509 tokens with 12 single ones 71.  640 threads with
+// registers moved between roles took 552 to 746 for the first, a whole row of scores
+// held in 168 registers 617.
 //
 // Bound, like the dense forward, by the softmax and products of 128-row tiles:
 // a key block of two tiles takes 1.55 to 1.75 us (d = 128; d = 96 1.65), of one
@@ -106,10 +108,10 @@ struct PagedTileLayout {
 // Weights: a key block of one tile was measured at 1.06 us, of a pair at 1.55,
 // an item's borders at 3 to 4 us; 3 : 4 and two blocks an item balance best (a
 // mixed batch 58.5 us, with 2 : 3 59.8, with equal weights 60.4).  Over a 4-bit cache, where
-// queries are prepared and the first keys widened at a border, four blocks an item (a mixed
-// batch 90 us for 94, 32 chunks of 24 tokens 59 for 62; six blocks 89 and 62).
+// queries are prepared and the first keys widened at a border, three blocks an item (a mixed
+// batch 70.6 us, 32 chunks of 24 tokens 52.4; two blocks 72.1 and 53.4, four 70.1 and 54.0).
 template <bool KV4>
-using Cost = PagedCost<128, 3, 4, KV4 ? 2048 : 1024, false>;
+using Cost = PagedCost<128, 3, 4, KV4 ? 1536 : 1024, false>;
 template <bool KV4>
 struct Walk : PagedWalk<Cost<KV4>> {
   using Base = PagedWalk<Cost<KV4>>;
@@ -205,6 +207,15 @@ template <int D>
 struct Row4 {
   uint32_t w[D / 8], par[D / 32];
 
+  // Rows of 128 are widened in two turns of a loop: all roles' instructions have to fit
+  // their cache.
+  static constexpr int kParts = D == 128 ? 2 : 1, kGroups = D / 32 / kParts;
+  // Number i of part h of x, whose parts have n.
+  template <int N>
+  static __device__ __forceinline__ uint32_t part(const uint32_t (&x)[N], int n, int h, int i) {
+    return kParts == 1 ? x[i] : (h ? x[n + i] : x[i]);
+  }
+
   __device__ __forceinline__ void load(const uint8_t* x) {  // null: a row of zeros
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) w[i] = 0u;
@@ -229,15 +240,19 @@ struct Row4 {
   // scale or what these leave of it (LOW).
   template <bool BF16, bool LOW>
   __device__ __forceinline__ void key(uint32_t tile, int row, float f) const {
+#pragma unroll 1
+    for (int h = 0; h < kParts; ++h) {
 #pragma unroll
-    for (int g = 0; g < D / 32; ++g) {
-      const float s = unpack2<BF16>(par[g]).x * f;
-      const float hi = __uint_as_float(__float_as_uint(s) & 0xFFFF0000u);
-      const float by = LOW ? s - hi : hi;
-      const uint32_t even = pack_f16x2(by, by), odd = pack_f16x2(by * 0.0625f, by * 0.0625f);
+      for (int g = 0; g < kGroups; ++g) {
+        const float s = unpack2<BF16>(part(par, kGroups, h, g)).x * f;
+        const float hi = __uint_as_float(__float_as_uint(s) & 0xFFFF0000u);
+        const float by = LOW ? s - hi : hi;
+        const uint32_t even = pack_f16x2(by, by), odd = pack_f16x2(by * 0.0625f, by * 0.0625f);
 #pragma unroll
-      for (int c = 4 * g; c < 4 * g + 4; ++c)
-        store_smem16(tile_piece(tile, row, c), kv4_scaled_word(w[c], even, odd));
+        for (int c = 4 * g; c < 4 * g + 4; ++c)
+          store_smem16(tile_piece(tile, row, c) + h * 16384,
+                       kv4_scaled_word(part(w, 4 * kGroups, h, c), even, odd));
+      }
     }
   }
   // Its columns behind: m + 8 s in two terms, the first of them once more.
@@ -256,9 +271,14 @@ struct Row4 {
   // Widened values.
   template <bool BF16>
   __device__ __forceinline__ void value(uint32_t tile, int row) const {
+#pragma unroll 1
+    for (int h = 0; h < kParts; ++h) {
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-      store_smem16(tile_piece(tile, row, c), kv4_word<BF16, false>(w[c], par[c / 4]));
+      for (int c = 0; c < 4 * kGroups; ++c)
+        store_smem16(tile_piece(tile, row, c) + h * 16384,
+                     kv4_word<BF16, false>(part(w, 4 * kGroups, h, c),
+                                           part(par, kGroups, h, c / 4)));
+    }
   }
 };
 
@@ -267,43 +287,65 @@ struct Row4 {
 // the second.  The factor that undoes the scaling.
 template <int D, bool BF16>
 __device__ __forceinline__ float query_row(uint32_t tile, uint32_t extra, int row) {
-  uint32_t top = 0u;
-#pragma unroll
+  // The largest of the row, by the bits of |x| two at a time; a number by number look at a
+  // row that is not finite.
+  uint32_t both = 0u;
+#pragma unroll 4
   for (int c = 0; c < D / 8; ++c) {
     const uint4 x = load_smem16(tile_piece(tile, row, c));
     const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = unpack2<BF16>(y[i]);
-      top = max(top, max(finite_bits(v.x), finite_bits(v.y)));
+    for (int i = 0; i < 4; ++i)
+      asm("max.u16x2 %0, %0, %1;" : "+r"(both) : "r"(y[i] & 0x7FFF7FFFu));
+  }
+  const uint32_t most = max(both & 0xFFFFu, both >> 16);
+  uint32_t top = __float_as_uint(unpack2<BF16>(most).x);
+  if (most >= (BF16 ? 0x7F80u : 0x7C00u)) {
+    top = 0u;
+#pragma unroll 1
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = load_smem16(tile_piece(tile, row, c));
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2<BF16>(y[i]);
+        top = max(top, max(finite_bits(v.x), finite_bits(v.y)));
+      }
     }
   }
   const float2 f = to_fp16_range<9>(top);
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    const uint4 x = load_smem16(tile_piece(tile, row, c));
-    uint32_t y[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t x32 = extra + row * 32, swap = (row >> 2 & 1) * 16;  // (as store_extra)
+  store_smem16(x32 + swap, make_uint4(0u, 0u, 0u, 0u));
+  store_smem16(x32 + (swap ^ 16), make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll 1
+  for (int g = 0; g < D / 32; ++g) {
+    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float2 v = unpack2<BF16>(y[i]);
-      v.x *= f.x;
-      v.y *= f.x;
-      sum[c / 4] += v.x + v.y;
-      y[i] = pack_f16x2(v.x, v.y);
-    }
-    // channels (0, 1) (2, 3) (4, 5) (6, 7) as (0, 4) (1, 5) (2, 6) (3, 7)
-    store_smem16(tile_piece(tile, row, c),
-                 make_uint4(__byte_perm(y[0], y[2], 0x5410), __byte_perm(y[0], y[2], 0x7632),
-                            __byte_perm(y[1], y[3], 0x5410), __byte_perm(y[1], y[3], 0x7632)));
-  }
-  uint32_t two[4];
+      const uint32_t at = tile_piece(tile, row, 4 * g + i);
+      const uint4 x = load_smem16(at);
+      uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int g = 0; g < 4; ++g) two[g] = two_terms(sum[g]);
-  store_extra(extra, row,
-              make_uint4(__byte_perm(two[0], 0u, 0x1010), __byte_perm(two[1], 0u, 0x1010),
-                         __byte_perm(two[2], 0u, 0x1010), __byte_perm(two[3], 0u, 0x1010)),
-              make_uint2(__byte_perm(two[0], two[1], 0x7632), __byte_perm(two[2], two[3], 0x7632)));
+      for (int e = 0; e < 4; ++e) {
+        float2 v = unpack2<BF16>(y[e]);
+        v.x *= f.x;
+        v.y *= f.x;
+        sum += v.x + v.y;
+        y[e] = pack_f16x2(v.x, v.y);
+      }
+      // channels (0, 1) (2, 3) (4, 5) (6, 7) as (0, 4) (1, 5) (2, 6) (3, 7)
+      store_smem16(at,
+                   make_uint4(__byte_perm(y[0], y[2], 0x5410), __byte_perm(y[0], y[2], 0x7632),
+                              __byte_perm(y[1], y[3], 0x5410), __byte_perm(y[1], y[3], 0x7632)));
+    }
+    const uint32_t two = two_terms(sum);
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(x32 + swap + 4 * g),
+                 "r"(__byte_perm(two, 0u, 0x1010))
+                 : "memory");
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(x32 + (swap ^ 16) + 2 * g),
+                 "h"((uint16_t)(two >> 16))
+                 : "memory");
+  }
   return f.y;
 }
 
@@ -754,6 +796,10 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           const int kbase = (w.u0 + j) * 128;
           // Scores 32 c .. of the row, those that it does not see -inf.
           constexpr int kHeld = KV4 ? 2 : 4;  // chunks of 32 in registers at a time
+          // Their halves are turns of a loop where the roles' instructions do not fit their
+          // cache otherwise (d = 128: the mixed batch 74 us for 84, the long chunk 443 for
+          // 463; d = 96 the latter 420 for 471, but d = 64 389 for 355).
+          constexpr int kTurns = D == 64 ? 2 : 1;
           uint32_t sr[kHeld][32];
           auto read_scores = [&](int c0) {
 #pragma unroll
@@ -781,13 +827,13 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
           }
           float m_blk;
           if constexpr (KV4) {
-            auto held_max = [&](int c0) {
-              return fmaxf(row_max32(sr[0]) * to2[c0], row_max32(sr[1]) * to2[c0 + 1]);
-            };
-            read_scores(2);
-            m_blk = held_max(2);
-            read_scores(0);
-            m_blk = fmaxf(m_blk, held_max(0));
+            m_blk = -INFINITY;
+#pragma unroll (kTurns)
+            for (int c0 = 2; c0 >= 0; c0 -= 2) {
+              read_scores(c0);
+              m_blk = fmaxf(m_blk, fmaxf(row_max32(sr[0]) * (c0 ? to2[2] : to2[0]),
+                                         row_max32(sr[1]) * (c0 ? to2[3] : to2[1])));
+            }
           } else {
             read_scores(0);
             float x[kHeld * 32];
@@ -821,7 +867,8 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
 #pragma unroll
             for (int c = 0; c < kHeld; ++c) {
               uint32_t pk[16];
-              const float2 sc2 = make_float2(to2[c0 + c], to2[c0 + c]);
+              const float by = KV4 && c0 ? to2[2 + c % 2] : to2[c];
+              const float2 sc2 = make_float2(by, by);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[c][2 * i]),
@@ -835,10 +882,14 @@ __global__ void __launch_bounds__(kTileThreads<KV4>, 1)
               tmem_st16(s_addr + (c0 + c) * 16, pk);
             }
           };
-          exponentials(0);
           if constexpr (KV4) {
-            read_scores(2);
-            exponentials(2);
+#pragma unroll (kTurns)
+            for (int c0 = 0; c0 < 4; c0 += 2) {
+              if (c0 > 0) read_scores(2);
+              exponentials(c0);
+            }
+          } else {
+            exponentials(0);
           }
           const float2 rsum =
               __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
