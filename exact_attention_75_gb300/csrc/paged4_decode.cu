@@ -30,9 +30,9 @@
 // The running maximum is a reference that is raised only where a score passes
 // it by 2^8 (P stays below that), so that most blocks need no maximum across lanes.
 //
-// Bound by those instructions (350 for 16 keys and 8 rows at d = 128; issue 52 % and
-// ALU 48 % of the time, DRAM 47 %) and, in small batches, by the 11 us around them: 4 to
-// the first key, 2 of meeting, 3 to 6 of join.  64 single tokens over 2048 to 8192 keys,
+// Bound by those instructions (350 for 16 keys and 8 rows at d = 128; issue 54 % and
+// ALU 48 % of the time, DRAM 49 %) and by the 15 us around them: 4 to the first key, the
+// borders of items, 2 of meeting, 3 to 6 of join.  64 single tokens over 2048 to 8192 keys,
 // 16 query heads on 4 of 128, 50 us, 196 MB, 3.9 TB/s; over up to 65536 keys 295 us,
 // 5.3 TB/s, 0.80 of a copy's rate (the 16-bit cache's: 101 us and 0.90 for 3.2 times the
 // bytes).  d = 96 takes 47, d = 64 37, 16 rows 66.  Six warps a CTA, two CTAs an
