@@ -23,7 +23,7 @@
 // a power of two, and s of its keys is applied to it in 32 bits; what m adds is one more
 // product for all groups, with the query's sums in three terms: keys lose nothing.
 // Values are m + c s rounded to 16 bits, or, in bf16, c s rounded, and m by a product of
-// its own: (128 + c) s - 128 s is one instruction where c s + m takes two.
+// its own: (8 + c / 16) s - 8 s is one instruction where c s + m takes two.
 // P leaves the softmax by keys and is wanted by rows: one 8 x 8 transpose for 8
 // keys.
 //
@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
         for (int i = 0; i < KS; ++i) {
           const int n = kSplit ? i / 2 : 0;  // the lane's group of tile i
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][i][e] += om[nt][n / 2][(e & 1) + 2 * (n & 1)];
+          for (int e = 0; e < 4; ++e)
+            o[nt][i][e] = fmaf(o[nt][i][e], kKv4Steps, om[nt][n / 2][(e & 1) + 2 * (n & 1)]);
         }
       }
     }

@@ -406,7 +406,10 @@ attn_status attn_read_kv4(const void* k_pages, const void* v_pages, void* k, voi
 /*
  * attn_fwd_paged over a 4-bit cache, with the same arguments, workspace
  * (attn_fwd_paged_workspace_bytes), masking and promises.  Values take part as
- * RN16(m + c s), or as m + RN16(c s); keys as m + c s unrounded (a channel may be off
+ * RN16(m + c s), or as m + RN16(c s) (within 2^-130 where c s is below 2^-122).  Sums
+ * over them are fp32 before they are divided, with probabilities scaled by 2^8 at most, as
+ * over a 16-bit cache: where a sequence's keys times its largest value pass 2^119
+ * (bf16), O may be infinite.  Keys take part as m + c s unrounded (a channel may be off
  * by 2^-34 of its query's largest and, in chunks of more than 16 query rows a
  * key/value head, by 2^-38 of the largest of the 32 cached positions 32 i .. 32 i + 31;
  * keys and queries of a bf16 cache stay below 2^100, or their scores may be NaN).
