@@ -177,6 +177,14 @@ __device__ __forceinline__ float kv4_query(uint4 (&q)[C], float* sums) {
   return f.y;
 }
 
+// What takes a scaled row's products to base 2.  Neither 0 nor infinite, since a masked
+// product, -inf, times 0 would be NaN, and so would 0 times infinity.  Products are below
+// 2^124 (keys below 2^100), so that one with the least number, 2^-149, counts nothing;
+// one that 1e37 is too little for is infinite as an exponent anyway.
+__device__ __forceinline__ float kv4_to_base2(float scale_log2, float undo) {
+  return fminf(fmaxf(scale_log2 * undo, 0x1p-149f), 1e37f);
+}
+
 // What the minima of the groups add to a score, sum over groups of m sum q, as a product
 // of its own in the cache's type, 16 deep: the sum of a query over a group is cut into
 // three terms, which meet the group's minimum one by one.  Each quad of lanes has a query

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_weights_kernel(const WeightsPa
             float sums[C];
             const float undo = kv4_query<BF16, C>(q, sums);
             minima[warp][lane] = kv4_sum_terms<BF16, C>(sums, t);
-            ri.to2 = fminf(fmaxf(p.scale_log2 * undo, 1e-37f), 1e37f);
+            ri.to2 = kv4_to_base2(p.scale_log2, undo);
           }
 #pragma unroll
           for (int c = 0; c < C; ++c) tiles[warp][c][lane] = q[c];

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     const int rows = min(kPagedRows, sq.qlen * p.G);
     // Q^T: of row 8 nt + g the channels that the lane has of the keys (kv4_query) and the
     // terms of the sums over each group; of rows 8 nt + 2 t and the next what takes
-    // their products to base 2 (1e-37 .. 1e37, as in the tile kernel).
+    // their products to base 2.
     uint32_t qb[NT][KS][2];
     uint2 qm[NT];
     float2 to2[NT];
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
         qb[nt][2 * c + 1][1] = x[c].w;
       }
       qm[nt] = kv4_sum_terms<BF16, C>(sums, t);
-      const float by = fminf(fmaxf(p.scale_log2 * undo, 1e-37f), 1e37f);
+      const float by = kv4_to_base2(p.scale_log2, undo);
       to2[nt] = make_float2(__shfl_sync(0xffffffffu, by, 8 * t),
                             __shfl_sync(0xffffffffu, by, 8 * t + 4));
     }
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
             const float by = e ? to2[nt].y : to2[nt].x, n = b * by;
             const float alpha = ex2_approx(m[nt][e] - n);
             m[nt][e] = ref[nt][e] = n;
-            limit[nt][e] = b + kRaise / by;
+            limit[nt][e] = b + kRaise / by;  // (infinite where no product can be that much more)
             (e ? l[nt].y : l[nt].x) *= alpha;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {

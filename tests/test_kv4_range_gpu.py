@@ -38,3 +38,41 @@ def test_far_values_of_bf16(four, amp, lens, reach, Hq, Hkv, d):
     o, lse = paged.run(four, x, True)
     assert four.poll_status() == (0, 0)
     check4(x, o, lse, True)
+
+
+def weights_with(attn, x, causal, scale):
+    """kv_weights over the 4-bit keys k4 of x at a scale, from weights of 1, against the
+    oracle.  The tolerance is that of test_retain_gpu.py, with the exponential of a
+    score's error (scores reach 10^4 here), and n 2^-126: a term below 2^-126 is a
+    subnormal number, which fp32 holds to 2^-149 and the exponential may take for 0."""
+    dt, args = x["q"].dtype, (x["table"].cpu().numpy(), x["cu"].cpu().numpy(), x["kv"].cpu().numpy(), causal, scale)
+    k = to64(exact4(x["k4"], dt))
+    _, L, _, big = oracle.attention_paged(to64(x["q"]), k, np.nan_to_num(to64(x["v"])), *args)
+    lse = torch.tensor(L, dtype=torch.float32).cuda()
+    one = torch.ones(x["k4"].shape[:3], device="cuda")
+    ref, new = oracle.weights_paged(to64(x["q"]), k, to64(lse), to64(one), *args)
+    got = to64(attn.kv_weights(x["q"], x["k4"], x["table"], x["cu"], x["kv"], lse, one, x["max_q"], causal=causal,
+                               scale=scale))
+    s, m, _ = parts4(x["k4"], dt)
+    err = 48 * 2.0 ** -24 * largest(x, causal, scale, m.abs() + 15 * s)
+    L = np.max(np.abs(L), where=np.isfinite(L), initial=0.0) + big
+    n = x["max_q"] * (x["q"].shape[0] // k.shape[1])
+    tol = (np.expm1(err + 2 * L * 2.0 ** -24) + 2.0 ** -21 + n * 2.0 ** -24) * new
+    tol += 2.0 ** -24 * np.abs(ref) + n * 2.0 ** -126
+    assert np.isfinite(got).all()
+    assert (np.abs(got - ref) <= tol).all(), float(np.max(np.abs(got - ref) - tol))
+
+
+@pytest.mark.parametrize("lens,reach", [([(1, 1), (2, 64)], 16), ([(1, 70), (1, 1)] * 12, 5000),
+                                        ([(40, 70), (33, 33)], 16)])
+@pytest.mark.parametrize("q_amp,scale", [(2.0 ** -60, 2.0 ** -100), (1.0, 2.0 ** -125), (2.0 ** -110, 0.0625),
+                                         (2.0 ** -60, 2.0 ** -30)])
+def test_small_scales_and_large_keys(four, lens, reach, q_amp, scale):
+    """Scales and queries so small that their product is a subnormal number, or none,
+    beside keys near the largest that are allowed (2^100): the scores are all but 0."""
+    x = widen(paged.make(lens, 4, 2, 128, 32, "bf16", seed=113), reach)
+    x["k4"], x["q"] = pack4(x["k"].abs() * 2.0 ** 97), x["q"].abs() * q_amp
+    o, lse = paged.run(four, x, True, scale=scale)
+    check4(x, o, lse, True, scale)
+    weights_with(four, x, True, scale)
+    assert four.poll_status() == (0, 0)
