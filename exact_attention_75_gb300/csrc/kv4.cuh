@@ -140,7 +140,10 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
 
 // A row of queries as the operand that meets kv4_halves: a quad of lanes has the row,
 // lane t channels 32 c + 8 t .. of each group in q[c], which become fp16 in channel
-// pairs (i, i + 4), scaled into its range by a power of two, those of odd i over 16.
+// pairs (i, i + 4), scaled into its range by a power of two, those of odd i over 16:
+// half a step of fp16's least numbers, 2^-25, is 2^-34 of the row's largest (even i) or
+// 2^-30 where that is brought to 2^9, as the sums of an fp16 cache need to stay in range
+// (kv4_sum_terms), and 2^-35 where it is brought to 2^14.
 // sums: of the scaled row over each group.  Returns the factor that undoes the
 // scaling.  All lanes of the warp call this.
 template <bool BF16, int C>
@@ -157,7 +160,7 @@ __device__ __forceinline__ float kv4_query(uint4 (&q)[C], float* sums) {
   }
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const float2 f = to_fp16_range<9>(top);
+  const float2 f = to_fp16_range<BF16 ? 14 : 9>(top);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const uint32_t y[4] = {q[c].x, q[c].y, q[c].z, q[c].w};

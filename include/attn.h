@@ -409,10 +409,13 @@ attn_status attn_read_kv4(const void* k_pages, const void* v_pages, void* k, voi
  * RN16(m + c s), or as m + RN16(c s) (within 2^-130 where c s is below 2^-122).  Sums
  * over them are fp32 before they are divided, with probabilities scaled by 2^8 at most, as
  * over a 16-bit cache: where a sequence's keys times its largest value pass 2^119
- * (bf16), O may be infinite.  Keys take part as m + c s unrounded (a channel may be off
- * by 2^-34 of its query's largest and, in chunks of more than 16 query rows a
- * key/value head, by 2^-38 of the largest of the 32 cached positions 32 i .. 32 i + 31;
- * keys and queries of a bf16 cache stay below 2^100, or their scores may be NaN).
+ * (bf16), O may be infinite.  Keys take part as m + c s, not rounded to 16 bits:
+ *   - a channel of a query is off by at most 2^-34 of its row's largest (fp16 with at
+ *     most 16 query rows a key/value head: 2^-30);
+ *   - in chunks of more rows a channel of a key is off by at most 2^-30 of the largest
+ *     of the 32 cached positions 32 i .. 32 i + 31, and what m + 8 s of a group adds to a
+ *     score by 2^-20 of that;
+ *   - keys and queries of a bf16 cache stay below 2^100, or their scores may be NaN.
  * Cite: as attn_fwd_paged, and "8.3 FlashAttention-3", section 5.1.
  */
 attn_status attn_fwd_paged4(const void* q, const void* k_pages, const void* v_pages, void* o,
@@ -432,7 +435,8 @@ attn_status attn_fwd_paged4(const void* q, const void* k_pages, const void* v_pa
  *   q, lse  : [Hq, total, d] and what attn_fwd_paged (attn_fwd_paged4) wrote for
  *             them, [Hq, total]; or the last rows of a prompt alone with
  *             their lse, packed by a cu_seqlens of their own.
- *   k_pages : a cache in 16 bits (bits = 16) or 4 (bits = 4).
+ *   k_pages : a cache in 16 bits (bits = 16) or 4 (bits = 4; keys take part as in
+ *             attn_fwd_paged4 with few rows, however many there are).
  * Sequences without new rows, and positions behind a length, are left as they
  * were.  Masking, the other arguments and the device checks are those of
  * attn_fwd_paged; a row that sees no key adds nothing.  Sums are fp32 and their

@@ -76,3 +76,64 @@ def test_small_scales_and_large_keys(four, lens, reach, q_amp, scale):
     check4(x, o, lse, True, scale)
     weights_with(four, x, True, scale)
     assert four.poll_status() == (0, 0)
+
+
+def one_channel(dtype, top, least, amp, n_new, keys, Hq=2):
+    """Queries of one large channel, which no key has, and a small odd one at 33; keys of
+    that channel alone, up to amp."""
+    x = paged.make([(n_new, keys)], Hq, 1, 64, 16, dtype, seed=1)
+    q, k = torch.zeros_like(x["q"]), torch.where(torch.isnan(x["k"]), x["k"], x["k"].new_zeros(()))
+    q[:, :, 0], q[:, :, 33] = top, least
+    for j in range(keys):
+        k[int(x["table"][0, j // 16]), :, j % 16, 33] = amp * (j % 3) / 2
+    x["q"], x["k4"] = q, pack4(k)
+    x["v4"] = pack4(x["v"])
+    return x
+
+
+def lse_error(x, lse, scale):
+    args = x["table"].cpu().numpy(), x["cu"].cpu().numpy(), x["kv"].cpu().numpy(), False, scale
+    k = to64(exact4(x["k4"], x["q"].dtype))
+    _, L, _, big = oracle.attention_paged(to64(x["q"]), k, np.nan_to_num(to64(x["v"])), *args)
+    rounding = 2.0 ** -20 + int(x["kv"].max()) * 2.0 ** -24 + 64 * 2.0 ** -24 * big + 2.0 ** -23 * np.abs(L)
+    return np.max(np.abs(to64(lse) - L) - rounding), L
+
+
+@pytest.mark.parametrize("reach", [16, 5000])
+@pytest.mark.parametrize("dtype,top,least,amp,share", [
+    ("bf16", 1.0, 1.5 * 2.0 ** -29, 2.0 ** 30, 2.0 ** -34), ("bf16", 2.0 ** -40, 1.5 * 2.0 ** -74, 2.0 ** 74, 2.0 ** -34),
+    ("fp16", 2.0 ** 15, 1.5 * 2.0 ** -14, 2.0 ** 14, 2.0 ** -30)])
+def test_queries_of_a_wide_range_in_few_rows(four, reach, dtype, top, least, amp, share):
+    """A channel of a query is off by at most the share of its row's largest that the
+    header states, whatever the keys."""
+    x = widen(one_channel(dtype, top, least, amp, 1, 3), reach)
+    _, lse = paged.run(four, x, False, scale=1.0)
+    error, L = lse_error(x, lse, 1.0)
+    assert error <= share * top * amp, error
+    # the weights: each exp(s - lse) by that in the score
+    one = torch.zeros(x["k4"].shape[:3], device="cuda")
+    exact = torch.tensor(L, dtype=torch.float32).cuda()
+    four.kv_weights(x["q"], x["k4"], x["table"], x["cu"], x["kv"], exact, one, 1, scale=1.0)
+    got = torch.stack([one[int(x["table"][0, 0]), 0, j] for j in range(3)]).double().cpu().numpy()
+    ref = 2 * np.exp(least * amp * np.arange(3) / 2 - L[0, 0])
+    assert (np.abs(got - ref) <= np.expm1(share * top * amp + 2.0 ** -18) * ref).all(), (got, ref)
+    assert four.poll_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,big,small", [("bf16", 2.0 ** 27, 1.5 * 2.0 ** -4), ("bf16", 2.0 ** 27, 1.5 * 2.0 ** -5),
+                                             ("fp16", 2.0 ** 12, 1.5 * 2.0 ** -19)])
+def test_keys_of_a_wide_range_in_chunks(four, dtype, big, small):
+    """Among 32 cached positions one of a scale of `big`, in channels that the queries do not
+    have, and others of `small`: their channels are off by at most 2^-30 of the
+    largest.  (s / 16, or in fp16 its upper bits and what they leave over 16, is rounded
+    to 2^-25 at worst, times 16 |c - 8|: 2^-18, twice, where the largest of 8 s and
+    |m + 8 s|, at most 16/15 of the largest value, is brought to 2^14.)"""
+    x = one_channel(dtype, 0.0, 1.0 if dtype == "bf16" else 2.0 ** 15, 15 * small, 40, 40, Hq=1)
+    rows = exact4(x["k4"], x["q"].dtype)
+    rows[int(x["table"][0, 0]), :, 1, :32] = 15 * big * (torch.arange(32, device="cuda") % 2)
+    x["k4"] = pack4(rows.to(x["q"].dtype))
+    scale = 1.0 if dtype == "bf16" else 2.0 ** -2
+    _, lse = paged.run(four, x, False, scale=scale)
+    assert four.poll_status() == (0, 0)
+    error, _ = lse_error(x, lse, scale)
+    assert error <= 2.0 ** -30 * 15 * big * float(x["q"].max()) * scale + 2.0 ** -20, error
