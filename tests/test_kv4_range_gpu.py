@@ -40,25 +40,31 @@ def test_far_values_of_bf16(four, amp, lens, reach, Hq, Hkv, d):
     check4(x, o, lse, True)
 
 
-def weights_with(attn, x, causal, scale):
-    """kv_weights over the 4-bit keys k4 of x at a scale, from weights of 1, against the
-    oracle.  The tolerance is that of test_retain_gpu.py, with the exponential of a
-    score's error (scores reach 10^4 here), and n 2^-126: a term below 2^-126 is a
-    subnormal number, which fp32 holds to 2^-149 and the exponential may take for 0."""
+def weights_with(attn, x, causal, scale, n_bits=4):
+    """kv_weights over the keys k4 of x (or its 16-bit keys k) at a scale, from weights of
+    1, against the oracle.  The tolerance is that of test_retain_gpu.py, with
+    * the exponential of a score's error (scores reach 10^4 here);
+    * n 2^-126: a term below 2^-126 is a subnormal number, which fp32 holds to 2^-149 and
+      the exponential may take for 0;
+    * 2^-24 of the weight for each of the passes of 64 rows that add to it."""
     dt, args = x["q"].dtype, (x["table"].cpu().numpy(), x["cu"].cpu().numpy(), x["kv"].cpu().numpy(), causal, scale)
-    k = to64(exact4(x["k4"], dt))
+    pages = x["k4"] if n_bits == 4 else x["k"]
+    k = to64(exact4(pages, dt)) if n_bits == 4 else to64(pages)
     _, L, _, big = oracle.attention_paged(to64(x["q"]), k, np.nan_to_num(to64(x["v"])), *args)
     lse = torch.tensor(L, dtype=torch.float32).cuda()
-    one = torch.ones(x["k4"].shape[:3], device="cuda")
+    one = torch.ones(pages.shape[:3], device="cuda")
     ref, new = oracle.weights_paged(to64(x["q"]), k, to64(lse), to64(one), *args)
-    got = to64(attn.kv_weights(x["q"], x["k4"], x["table"], x["cu"], x["kv"], lse, one, x["max_q"], causal=causal,
+    got = to64(attn.kv_weights(x["q"], pages, x["table"], x["cu"], x["kv"], lse, one, x["max_q"], causal=causal,
                                scale=scale))
-    s, m, _ = parts4(x["k4"], dt)
-    err = 48 * 2.0 ** -24 * largest(x, causal, scale, m.abs() + 15 * s)
+    if n_bits == 4:
+        s, m, _ = parts4(pages, dt)
+        err = 48 * 2.0 ** -24 * largest(x, causal, scale, m.abs() + 15 * s)
+    else:
+        err = k.shape[3] * 2.0 ** -24 * largest(x, causal, scale, pages.double().abs())
     L = np.max(np.abs(L), where=np.isfinite(L), initial=0.0) + big
     n = x["max_q"] * (x["q"].shape[0] // k.shape[1])
     tol = (np.expm1(err + 2 * L * 2.0 ** -24) + 2.0 ** -21 + n * 2.0 ** -24) * new
-    tol += 2.0 ** -24 * np.abs(ref) + n * 2.0 ** -126
+    tol += -(-n // 64) * 2.0 ** -24 * np.abs(ref) + n * 2.0 ** -126
     assert np.isfinite(got).all()
     assert (np.abs(got - ref) <= tol).all(), float(np.max(np.abs(got - ref) - tol))
 
@@ -137,3 +143,63 @@ def test_keys_of_a_wide_range_in_chunks(four, dtype, big, small):
     assert four.poll_status() == (0, 0)
     error, _ = lse_error(x, lse, scale)
     assert error <= 2.0 ** -30 * 15 * big * float(x["q"].max()) * scale + 2.0 ** -20, error
+
+
+@pytest.mark.parametrize("lens,reach", [([(1, 700), (2, 64)], 16), ([(40, 700), (33, 64)], 16), ([(1, 70)] * 40, 16)])
+@pytest.mark.parametrize("k_amp,q_amp", [(2.0 ** 40, 2.0 ** -40), (2.0 ** -60, 2.0 ** 60), (2.0 ** -70, 2.0 ** -40),
+                                         (2.0 ** 17, 2.0 ** -17)])
+def test_weights_of_far_exponents(four, lens, reach, k_amp, q_amp):
+    x = widen(paged.make(lens, 4, 2, 128, 32, "bf16", seed=107), reach)
+    x["k4"], x["q"] = pack4(x["k"] * k_amp), x["q"] * q_amp
+    weights_with(four, x, True, 128 ** -0.5)
+    assert four.poll_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("lens", [[(1, 700), (2, 64)], [(40, 700), (33, 64)]])
+@pytest.mark.parametrize("scale", [0.01, 0.3, 1.0])
+@pytest.mark.parametrize("n_bits", [4, 16])
+def test_weights_at_other_scales(four, dtype, d, lens, scale, n_bits):
+    """The scale is the caller's, in either cache."""
+    x = paged.make(lens, 4, 2, d, 32, dtype, seed=5)
+    x["k4"] = pack4(x["k"])
+    weights_with(four, x, True, scale, n_bits)
+    assert four.poll_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64), ("bf16", 96)])
+def test_weights_of_a_key_that_stands_for_nan(four, dtype, d):
+    """A group of NaN makes the weight of its own position NaN, and no other's; in a
+    position that no row sees it reaches nothing."""
+    lens = [(3, 90), (1, 40), (20, 70)]
+    x = paged.make(lens, 4, 2, d, 16, dtype, seed=31)
+    x["k4"] = pack4(x["k"])
+    args = x["table"].cpu().numpy(), x["cu"].cpu().numpy(), x["kv"].cpu().numpy(), True, d ** -0.5
+    L = oracle.attention_paged(to64(x["q"]), to64(exact4(x["k4"], x["q"].dtype)), np.nan_to_num(to64(x["v"])),
+                               *args)[1]
+    lse = torch.tensor(L, dtype=torch.float32).cuda()
+
+    def weights(k):
+        w = torch.ones(k.shape[:3], device="cuda")
+        four.kv_weights(x["q"], k, x["table"], x["cu"], x["kv"], lse, w, x["max_q"], causal=True)
+        return w
+
+    clean = weights(x["k4"])
+    k, table, hit = x["k4"].clone(), x["table"].tolist(), torch.zeros_like(clean, dtype=torch.bool)
+    for b, at, head in ((0, 17, 0), (1, 39, 1), (2, 3, 1), (2, 69, 0)):
+        k[table[b][at // 16], head, at % 16, d // 2:d // 2 + 4] = 0xFF
+        hit[table[b][at // 16], head, at % 16] = True
+    got = weights(k)
+    assert four.poll_status() == (0, 0)
+    assert torch.isnan(got[hit]).all()
+    assert torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("n_bits", [4, 16])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([(700, 700)], 4, 1), ([(513, 900), (1, 40)], 2, 2), ([(1100, 1100)], 1, 1)])
+def test_weights_of_whole_prompts(four, n_bits, lens, Hq, Hkv):
+    """Many passes over the keys: every further 64 rows of a head add to the same weights."""
+    x = paged.make(lens, Hq, Hkv, 64, 32, "bf16", seed=41)
+    x["k4"] = pack4(x["k"])
+    weights_with(four, x, True, 0.125, n_bits)
+    assert four.poll_status() == (0, 0)
