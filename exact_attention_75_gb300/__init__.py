@@ -601,8 +601,7 @@ def fwd_paged4(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """fwd_paged over a cache held in 4 bits (see append_kv4).  Values m + c s take
-    part to half a step (of q's dtype, which is the one that was appended) of
-    themselves or of c s, keys unrounded.
+    part rounded to q's dtype, which is the one that was appended, keys unrounded.
     Arguments, masking and workspace (fwd_paged_workspace_bytes) as there."""
     return _binding().fwd_paged(q, k_pages, v_pages, block_table, cu_seqlens, kv_lens, max_q,
                                 causal, scale, out, lse, workspace, True)

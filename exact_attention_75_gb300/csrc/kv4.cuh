@@ -13,8 +13,8 @@
 // the number below.
 //
 // Values take part in products as RN_T(m + c s), one fused multiply-add of two
-// 16-bit values at a time, or as m and RN_T(c s) (bf16, few rows): half a step of the
-// value or of c s, the kind of error that a 16-bit cache has in the first place.  Keys do not: an error of 2^-9 a channel, even
+// 16-bit values at a time: half a step of T, the error that a 16-bit cache has in the
+// first place.  Keys do not: an error of 2^-9 a channel, even
 // of 2^-12, shows in the log-sum-exp of a short sequence.  A code's product with a
 // query is exact, and so is that of c - 8, which has three significant bits, with a
 // scale of 8 bits; so
@@ -96,21 +96,6 @@ __device__ __forceinline__ void kv4_values(uint32_t w, uint32_t s, uint32_t m, u
       asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(c), "r"(s), "r"(m));
     }
   }
-}
-
-// c s / 16 of a word's codes in bf16, nibbles i and i + 4 side by side, each rounded
-// once: (8 + c / 16) s - 8 s, the second product being exact.  s is below 2^124.1, as a
-// finite range is below 2^128, so no product leaves the range (128 s would from 2^121
-// on); numbers below 2^-126 have steps of 2^-133.
-constexpr float kKv4Steps = 16.f;
-__device__ __forceinline__ void kv4_steps(uint32_t w, uint32_t s, uint32_t (&v)[4]) {
-  uint32_t base;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(base) : "r"(s), "r"(0xC100C100u));
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
-        : "=r"(v[i])
-        : "r"(and_or(w >> (4 * i), 0x000F000Fu, 0x41004100u)), "r"(s), "r"(base));
 }
 
 // Two 16-bit values in 32 bits.

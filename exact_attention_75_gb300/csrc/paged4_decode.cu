@@ -22,8 +22,10 @@
 // A group's product is taken with the codes in fp16, the query scaled into its range by
 // a power of two, and s of its keys is applied to it in 32 bits; what m adds is one more
 // product for all groups, with the query's sums in three terms: keys lose nothing.
-// Values are m + c s rounded to 16 bits, or, in bf16, c s rounded, and m by a product of
-// its own: (8 + c / 16) s - 8 s is one instruction where c s + m takes two.
+// Values are m + c s rounded to 16 bits.  (In bf16 c s rounded by itself and m by a
+// product of its own took an instruction less a pair of values, 50.1 us for the 50.5
+// below, but what cancels between the two is lost: 2.5 times the error of O over a few
+// keys.)
 // P leaves the softmax by keys and is wanted by rows: one 8 x 8 transpose for 8
 // keys.
 //
@@ -150,7 +152,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
   constexpr int NS = L::kSlots;
   constexpr bool kSplit = D == 96;  // a lane's channels of V lie in more than one group
   constexpr int G = kSplit ? C : 1;  // scales and minima of them
-  constexpr int M = BF16 ? (G + 1) / 2 : 0;  // products of the minima: two to a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                              ~static_cast<uintptr_t>(127));
@@ -252,7 +253,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     const int lim0 = last_key_of(p, sq, 0);
 
     float o[NT][KS][4];
-    float om[NT][BF16 ? M : 1][4];  // what the minima add to the lane's channels
     // The reference of a row's exponentials, what it is subtracted as (0 before there
     // is one), the product beyond which it is raised; the sum of the exponentials.
     float m[NT][2], ref[NT][2], limit[NT][2];
@@ -261,8 +261,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-#pragma unroll
-      for (int i = 0; i < M; ++i) om[nt][i][0] = om[nt][i][1] = om[nt][i][2] = om[nt][i][3] = 0.f;
       m[nt][0] = m[nt][1] = limit[nt][0] = limit[nt][1] = -INFINITY;
       ref[nt][0] = ref[nt][1] = 0.f;
       l[nt] = make_float2(0.f, 0.f);
@@ -367,11 +365,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
               o[nt][i][e] *= alpha;
               o[nt][i][e + 2] *= alpha;
             }
-#pragma unroll
-            for (int i = 0; i < M; ++i) {
-              om[nt][i][e] *= alpha;
-              om[nt][i][e + 2] *= alpha;
-            }
           }
       }
       // P is rounded to 16 bits for its product, as in the 16-bit kernel; l sums
@@ -425,23 +418,12 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
             lo[h][n] = __byte_perm(vp[h][0][n], vp[h][1][n], 0x7632);
           }
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-          // row g of the tile: group 2 i of the lane's, row g + 8: the next
-          const int n = 2 * i + 1;
-          const uint32_t a[4] = {lo[0][2 * i], n < G ? lo[0][n % G] : 0u, lo[1][2 * i],
-                                 n < G ? lo[1][n % G] : 0u};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816<BF16>(om[nt][i], a, pb[nt][2 * u], pb[nt][2 * u + 1]);
-        }
-#pragma unroll
         for (int c = 0; c < C; ++c) {
           uint32_t v[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int n = kSplit ? c : 0;
-            if constexpr (BF16) kv4_steps(vw[h][c], sc[h][n], v[h]);
-            else kv4_values<BF16>(vw[h][c], sc[h][n], lo[h][n], v[h]);
+            kv4_values<BF16>(vw[h][c], sc[h][n], lo[h][n], v[h]);
           }
           const uint32_t a0[4] = {v[0][0], v[0][1], v[1][0], v[1][1]};
           const uint32_t a1[4] = {v[0][2], v[0][3], v[1][2], v[1][3]};
@@ -473,15 +455,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 32, 2) paged4_decode_kernel(const
       for (int off = 4; off < 32; off <<= 1) {
         l[nt].x += __shfl_xor_sync(0xffffffffu, l[nt].x, off);
         l[nt].y += __shfl_xor_sync(0xffffffffu, l[nt].y, off);
-      }
-      if constexpr (BF16) {
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const int n = kSplit ? i / 2 : 0;  // the lane's group of tile i
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[nt][i][e] = fmaf(o[nt][i][e], kKv4Steps, om[nt][n / 2][(e & 1) + 2 * (n & 1)]);
-        }
       }
     }
 

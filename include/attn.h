@@ -406,10 +406,10 @@ attn_status attn_read_kv4(const void* k_pages, const void* v_pages, void* k, voi
 /*
  * attn_fwd_paged over a 4-bit cache, with the same arguments, workspace
  * (attn_fwd_paged_workspace_bytes), masking and promises.  Values take part as
- * RN16(m + c s), or as m + RN16(c s) (within 2^-130 where c s is below 2^-122).  Sums
- * over them are fp32 before they are divided, with probabilities scaled by 2^8 at most, as
- * over a 16-bit cache: where a sequence's keys times its largest value pass 2^119
- * (bf16), O may be infinite.  Keys take part as m + c s, not rounded to 16 bits:
+ * RN16(m + c s).  Sums over them are fp32 before they are divided, with probabilities
+ * scaled by 2^8 at most, as over a 16-bit cache: where a sequence's keys times its
+ * largest value pass 2^119 (bf16), O may be infinite.  Keys take part as m + c s, not
+ * rounded to 16 bits:
  *   - a channel of a query is off by at most 2^-34 of its row's largest (fp16 with at
  *     most 16 query rows a key/value head: 2^-30);
  *   - in chunks of more rows a channel of a key is off by at most 2^-30 of the largest

@@ -26,10 +26,8 @@ CHUNK = [([(20, 20), (1, 4)], 16, 4, 2)]
 @pytest.mark.parametrize("d", [64, 96, 128])
 def test_far_values_of_bf16(four, amp, lens, reach, Hq, Hkv, d):
     """Values up to a fifth of bf16's largest number, whose scales pass 2^121, and
-    least ones: finite, and as precise as others.  (In few rows c s / 16 is rounded to a
-    bf16 number, which may be subnormal: half a step of those times 16, 2^-130, a
-    value.)  Scores are all but equal, so that sums of 5 values (20 of the smaller ones)
-    stay in the range of fp32."""
+    least ones: finite, and as precise as others.  Scores are all but equal, so that sums
+    of 5 values (20 of the smaller ones) stay in the range of fp32."""
     x = widen(paged.make(lens, Hq, Hkv, d, 32, "bf16", seed=d, amp=2.0 ** -6), reach)
     x["v4"] = pack4(x["v"] * amp)
     s = parts4(x["v4"], torch.bfloat16)[0]
@@ -203,3 +201,25 @@ def test_weights_of_whole_prompts(four, n_bits, lens, Hq, Hkv):
     x["k4"] = pack4(x["k"])
     weights_with(four, x, True, 0.125, n_bits)
     assert four.poll_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("lens,reach,Hq,Hkv", [([(1, 1)] * 3, 16, 4, 2), ([(1, 1)] * 30, 5000, 2, 1),
+                                               ([(1, 1)] * 3, 16, 12, 1)])
+@pytest.mark.parametrize("shift", [0.0, 30.0])
+def test_values_of_one_key(four, dtype, d, lens, reach, Hq, Hkv, shift):
+    """O of a sequence of one key is its value: P is 1 but for 2^-20, so that what is left
+    is a rounding of m + c s, u |O|, and none of c s or m by themselves, which are both
+    far larger than a value in the middle of its group."""
+    x = widen(paged.make(lens, Hq, Hkv, d, 16, dtype, seed=d), reach)
+    x["v4"] = pack4(x["v"] + shift)
+    o, lse = paged.run(four, x, True)
+    assert four.poll_status() == (0, 0)
+    s, m, c = (t.cpu().numpy() for t in parts4(x["v4"], x["q"].dtype))
+    u = torch.finfo(x["q"].dtype).eps / 2
+    for b, page in enumerate(x["table"][:, 0].tolist()):
+        for h in range(Hq):
+            at = page, h // (Hq // Hkv), 0
+            want, got = (m + c * s)[at], to64(o)[h, b]
+            assert (np.abs(got - want) <= (u + 2.0 ** -20) * (1 + u) * np.abs(want)).all()
