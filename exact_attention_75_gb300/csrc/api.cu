@@ -466,7 +466,17 @@ bool same_layout(const int64_t* s, const int64_t* t, const int64_t* n, int dims)
 //   160 items (1)           256 keys 7.0 / 9.9, 1024 16.9 / 16.1
 //   300 items (1)           256 keys 7.6 / 11.8, 1024 28.4 / 32.2
 // and with lengths of a quarter of the table's up to it 300 items of 1024 keys
-// 23.2 / 25.5.  Without a graph a call in shares takes the host 9 to 10 us at
+// 23.2 / 25.5.  The rule was taken on the 16-bit cache's kernel; over 4 bits, whose blocks
+// are longer, it is on the faster side at its borders.  (Past them clusters are again
+// faster for 36 items of 8192 equal keys and 300 of 2048, in 16 bits too.)
+//   4 items (8)     256 keys 6.4 / 7.4 us, 1024 6.8 / 8.0, 2048 8.0 / 8.1, 4096 9.4 / 8.3
+//   16 items (8)    1024 keys 7.7 / 9.1, 2048 9.4 / 9.6, 4096 11.0 / 11.2, 8192 15.8 / 13.1
+//   36 items (8)    1024 keys 8.2 / 9.6, 2048 9.6 / 11.4, 4096 11.6 / 13.1, 8192 19.2 / 21.0
+//   40 items (4)    1024 keys 9.1 / 10.6, 2048 10.8 / 11.4, 4096 16.3 / 14.5
+//   80 items (2)    256 keys 7.6 / 9.4, 1024 10.9 / 11.8, 2048 15.4 / 14.4
+//   160 items (1)   256 keys 7.2 / 9.9, 1024 14.1 / 15.3, 2048 24.7 / 22.5
+//   300 items (1)   1024 keys 17.5 / 22.6, 2048 26.3 / 32.0, 8192 78.7 / 85.5
+// Without a graph a call in shares takes the host 9 to 10 us at
 // least (two launches and a workspace), in clusters 6.
 constexpr int kPagedClusterWide = 288;  // resident CTAs in clusters of 8 or 4
 constexpr int kPagedClusterCtas = 300;

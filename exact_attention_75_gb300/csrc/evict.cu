@@ -22,9 +22,11 @@
 // latency (2.3 us) with few.
 //
 // 16 sequences of up to 8192 positions on 4 heads of 128 in 16 bits, half of them
-// kept, 58 us: choice 18, and 240 MB in 40, half of them from HBM.  One sequence of 65536 on 8 heads of 64
-// in 4 bits, a quarter kept, 36 us: choice 17, five rounds.  Measured on the way:
-// every CTA reading all the CTAs' counts, 64 and 38; equal digits of a warp counted
+// kept, cold and for the first time 57 us (alone, the choice 20, the move of 240 MB 42).
+// One sequence of 65536 on 8 heads of 64 in 4 bits, a quarter kept, 45 (choice 34, five
+// rounds 22).  From L2 and over a cache that was cut before, whose heavy rows lie in
+// front, 33 and 35; three such caches in turn 58 and 36, of which the choice has 18 and
+// 17.  Measured on the way, in that last form: every CTA reading all the CTAs' counts, 64 and 38; equal digits of a warp counted
 // together, 70 and 50; 16 vectors of a row's a thread in place of 8, 45 for the move
 // of the second, not 38.
 #include <cuda_runtime.h>

@@ -25,10 +25,13 @@
 // the warps of a CTA take its blocks in turn.
 //
 // Single tokens are bound by HBM: 64 of them over 2048 to 8192 keys, 16 query heads on 4
-// of 128, 57 us in 16 bits, 6.0 TB/s, 0.90 of a copy's rate; 37 in 4 bits.  Windows are
+// of 128, 57 us in 16 bits, 6.0 TB/s, 0.90 of a copy's rate.  In 4 bits 37, 2.1 times
+// their bytes' time: a block ahead is 88 bytes a key, 22 KB on their way for an SM's 16
+// warps, where HBM's rate and latency want some 35 (in 16 bits it is 67).  Windows are
 // bound by the product's latencies and the operands read for it: 4 of 32 tokens over up to
 // 16384 keys, 16 heads on 8, 38 us in 4 bits (49 with the minima added to the scores one by
-// one), 35 in 16; of 256 tokens in 4 bits 233.
+// one), 35 in 16; of 256 tokens 235 and 203; a whole prompt of 4096, whose keys are read
+// again for every 64 rows of a head, 893 and 582.
 #include <cuda_runtime.h>
 #include <cstdint>
 

@@ -32,12 +32,14 @@
 // The running maximum is a reference that is raised only where a score passes
 // it by 2^8 (P stays below that), so that most blocks need no maximum across lanes.
 //
-// Bound by those instructions (350 for 16 keys and 8 rows at d = 128; issue 54 % and
-// ALU 48 % of the time, DRAM 49 %) and by the 15 us around them: 4 to the first key, the
+// No unit is full (some 370 instructions for 16 keys and 8 rows at d = 128: issue 58 % of
+// the time, ALU 46 %, DRAM 50 %, tensor 17 %): what is left are waits between dependent
+// instructions of 12 warps an SM, and the 15 us around them: 4 to the first key, the
 // borders of items, 2 of meeting, 3 to 6 of join.  64 single tokens over 2048 to 8192 keys,
-// 16 query heads on 4 of 128, 50 us, 196 MB, 3.9 TB/s; over up to 65536 keys 295 us,
-// 5.3 TB/s, 0.80 of a copy's rate (the 16-bit cache's: 101 us and 0.90 for 3.2 times the
-// bytes).  d = 96 takes 47, d = 64 37, 16 rows 66.  Six warps a CTA, two CTAs an
+// 16 query heads on 4 of 128, 50.5 us, 196 MB, 3.9 TB/s; over up to 65536 keys 297 us,
+// 5.3 TB/s, 0.79 of a copy's rate (the 16-bit cache's: 102 us and 0.90 for 3.2 times the
+// bytes).  d = 96 takes 47, d = 64 37, 16 rows 68.  Drafts of 16 rows (8 warps an SM: issue
+// 39 %, DRAM 20 %) are such waits altogether.  Six warps a CTA, two CTAs an
 // SM; four, five and eight took 1, 9 and 7 % longer.
 #include <cuda_runtime.h>
 #include <cstdint>
