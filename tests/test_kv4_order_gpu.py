@@ -2,7 +2,6 @@
 written: every kernel here may start before the work ahead of it has finished, and reads
 lengths, pages, tokens, weights and caches that this work writes.  Bits are compared with
 those of calls on idle streams."""
-import numpy as np
 import pytest
 import torch
 
@@ -148,3 +147,39 @@ def test_eviction(attn_lib, n_bits, lens):
         return out
 
     alternate(attn_lib, xs, ("v", "k", "w"), step)
+
+
+@pytest.mark.parametrize("lens,reach", BATCHES)
+def test_captured_step_with_weights_and_eviction(attn_lib, lens, reach):
+    """Append, attention, weights and eviction in one graph, replayed on other lengths,
+    pages and tokens: the bits of the calls by themselves."""
+    rope = attn_lib.rope_table(D)
+    xs = batches(lens, reach)
+    for i, x in enumerate(xs):
+        x["w"] = torch.rand(x["k"].shape[:3], generator=torch.Generator().manual_seed(i)).cuda()
+    keys = xs[0]["table"].shape[1] * PAGE
+    room = attn_lib.fwd_paged_workspace_bytes(len(lens), xs[0]["max_q"], keys, HQ, HKV, D)
+    ws = torch.empty(max(1, room), dtype=torch.uint8, device="cuda")
+
+    def step(x):
+        args = x["table"], x["cu"], x["kv"]
+        q = attn_lib.append_kv4(x["nk"], x["nv"], x["k"], x["v"], *args, table=rope, q=x["q"])
+        o, lse = attn_lib.fwd_paged4(q, x["k"], x["v"], *args, x["max_q"], causal=True, workspace=ws)
+        attn_lib.kv_weights(q, x["k"], *args, lse, x["w"], x["max_q"], causal=True)
+        kept, new = attn_lib.evict_kv(x["k"], x["v"], x["w"], x["table"], x["kv"], 48, sinks=2, recent=8)
+        return q, o, lse, kept, new, x["k"], x["v"], x["w"]
+
+    copy = lambda x: {k: v.clone() if torch.is_tensor(v) else v for k, v in x.items()}  # noqa: E731
+    want = [[t.clone() for t in step(copy(x))] for x in xs]
+    hold, side, graph = copy(xs[0]), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        out = step(hold)
+    for i in (0, 1, 1, 0):
+        for n, t in xs[i].items():
+            if torch.is_tensor(t):
+                hold[n].copy_(t)
+        graph.replay()
+        assert all(torch.equal(bits(a), bits(b)) for a, b in zip(out, want[i]))
+    assert want[0][4].max() == 48
+    assert attn_lib.poll_status() == (0, 0)
